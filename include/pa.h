@@ -90,6 +90,12 @@ enum {
     PA_DEV_BAD_TEMPERATURE = 7 /* sampler: temperature not > 1e-10; where = row */
 };
 
+/* Code formats of an 8-bit KV pool (pa_store_kvcache_q8 and what reads it). */
+enum {
+    PA_Q8_E4M3 = 0,            /* OCP FP8 E4M3: 4 exponent and 3 mantissa bits */
+    PA_Q8_INT8 = 1             /* two's-complement integers, -127..127 */
+};
+
 /* Library version (major*10000 + minor*100 + patch). */
 PA_API int pa_version(void);
 
@@ -393,6 +399,80 @@ PA_API pa_status pa_prefill_store_varlen(void *out, const void *q, int64_t q_row
 PA_API pa_status pa_sample_gumbel(int32_t *out_tokens, const void *logits, int64_t logits_row_stride,
                                   int32_t logits_is_fp32, const float *temperatures, const float *exp_noise,
                                   int64_t noise_row_stride, int32_t batch, int32_t vocab, pa_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * 8-bit KV pool.  (An addition of this library: the source pages keep the
+ * pool in bf16.)  Decode is bound by the bytes of the cache; an 8-bit pool
+ * halves them and doubles the tokens that fit.
+ *
+ * Layout (head-major, unlike the bf16 pool: the keys of one block and head are
+ * contiguous, which 128-byte rows need to be streamed at full rate):
+ *   k_cache, v_cache   1-byte codes [num_blocks, num_kv_heads, block_size, 128]
+ *   k_scale, v_scale   1 byte       [num_blocks, num_kv_heads, block_size]
+ * Slots, block tables and block_size are those of the bf16 pool: slot s is
+ * token s % block_size of block s / block_size.
+ *
+ * A row (one token and head) stands for code * 2^(scale - 127), scale 0..254;
+ * scale 255 marks a row that held a NaN or an infinity: it reads as NaN.  The
+ * scale is the smallest power of two (at least 2^-126) with
+ * max|x| <= 448 * 2^e (PA_Q8_E4M3) or 127 * 2^e (PA_Q8_INT8), and a code is
+ * x * 2^-e rounded once, to nearest, ties to even.  The result is a function
+ * of the row alone: it depends on no other token, so appending a token never
+ * touches older ones.  An error of a value is at most 2^-4 of it (E4M3, above
+ * 2^-15 of the row's largest magnitude) or 1/126 of the row's largest
+ * magnitude (INT8).
+ * Pointers 16-byte aligned; num_blocks * block_size * num_kv_heads < 2^31.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pa_store_kvcache_q8 -- pa_store_kvcache into an 8-bit pool: each row is
+ * quantised as it is written.  Arguments, padding (negative slots) and bad
+ * slots (PA_DEV_BAD_SLOT) as there; non-negative slots must be distinct.
+ *   format   PA_Q8_E4M3 or PA_Q8_INT8.
+ */
+PA_API pa_status pa_store_kvcache_q8(const void *key, int64_t key_row_stride, const void *value,
+                                     int64_t value_row_stride, void *k_cache, void *v_cache, void *k_scale,
+                                     void *v_scale, const int32_t *slot_mapping, int32_t num_tokens,
+                                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                     int32_t num_blocks, int32_t format, pa_stream_t stream);
+
+/*
+ * pa_load_kvcache_q8 -- read rows of an 8-bit pool back as bf16, exactly.
+ * Token i's rows are written to key + i*key_row_stride and value + i*
+ * value_row_stride ([Hkv, 128] each, strides in elements, multiples of 8): the
+ * rows of slot slot_mapping[i], zeros for a negative slot (and for a slot >=
+ * num_blocks*block_size, recorded as PA_DEV_BAD_SLOT).  Slots may repeat.
+ * With the slots of whole contexts (pa_slot_mapping_prefill with
+ * cu_seqlens_q = cu_seqlens_k) the result is what pa_prefill_varlen takes as
+ * contiguous k / v.
+ */
+PA_API pa_status pa_load_kvcache_q8(void *key, int64_t key_row_stride, void *value, int64_t value_row_stride,
+                                    const void *k_cache, const void *v_cache, const void *k_scale,
+                                    const void *v_scale, const int32_t *slot_mapping, int32_t num_tokens,
+                                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                    int32_t num_blocks, int32_t format, pa_stream_t stream);
+
+/*
+ * pa_decode_q8 -- pa_decode over an 8-bit pool (one query token per sequence;
+ * store its own key first).  Same definition, with K and V the values the
+ * pool stands for; q and out bf16.  The scores use q and the codes exactly
+ * (fp32 accumulation); the softmax weights, each times its value row's scale,
+ * are rounded to fp16.  A key or value row that reads as NaN makes its
+ * sequence's outputs of that kv head NaN.
+ *   workspace   device scratch of >= pa_decode_q8_workspace_size(...) bytes,
+ *               16-byte aligned, ZERO-FILLED before its first use; contract as
+ *               for pa_decode (every call leaves it ready for the next; not
+ *               shared by calls that may run at the same time).
+ * Other arguments and limits as pa_decode.
+ */
+PA_API size_t pa_decode_q8_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
+PA_API pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const void *k_cache,
+                              const void *v_cache, const void *k_scale, const void *v_scale,
+                              const int32_t *block_tables, int32_t max_blocks_per_seq,
+                              const int32_t *context_lens, int32_t batch, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                              int32_t format, float softmax_scale, void *workspace, size_t workspace_bytes,
+                              pa_stream_t stream);
 
 /* --------------------------------------------------------------------------
  * Host block manager: the pool's allocator and prefix cache, whose block

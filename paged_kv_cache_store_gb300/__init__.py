@@ -11,6 +11,8 @@ Entry points (same names as the C ABI without the ``pa_`` prefix):
   store_kvcache, slot_mapping_decode, slot_mapping_prefill,
   decode_workspace_size, decode, decode_static, prefill_varlen,
   sample_gumbel, set_checked, get_device_error;
+  kvcache_q8, store_kvcache_q8, load_kvcache_q8, decode_q8_workspace,
+  decode_q8 (the 8-bit pool);
   block_manager.BlockManager wraps the host block manager (pa_bm_*).
 """
 from __future__ import annotations
@@ -27,6 +29,7 @@ LIB_PATH = os.path.join(_PKG, "libpa.so")
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA, PA_ERR_DEVICE_CHECK = range(6)
 (PA_DEV_TIMEOUT, PA_DEV_BAD_SLOT, PA_DEV_BAD_CONTEXT, PA_DEV_BAD_BLOCK, PA_DEV_BAD_SEQLENS, PA_DEV_SMEM_ALIGN,
  PA_DEV_BAD_TEMPERATURE) = range(1, 8)
+PA_Q8_E4M3, PA_Q8_INT8 = range(2)
 
 # Every symbol include/pa.h declares, with its ctypes signature.
 _i32, _i64, _sz, _f32, _vp = C.c_int32, C.c_int64, C.c_size_t, C.c_float, C.c_void_p
@@ -55,6 +58,13 @@ SIGNATURES = {
                                           _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp,
                                           C.c_size_t, _vp]),
     "pa_sample_gumbel": (C.c_int, [_vp, _vp, _i64, _i32, _vp, _vp, _i64, _i32, _i32, _vp]),
+    "pa_store_kvcache_q8": (C.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                      _i32, _vp]),
+    "pa_load_kvcache_q8": (C.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                     _i32, _vp]),
+    "pa_decode_q8_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "pa_decode_q8": (C.c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
+                               _i32, _i32, _f32, _vp, _sz, _vp]),
     "pa_set_checked": (C.c_int, [_i32]),
     # host block manager
     "pa_bm_create": (C.c_int, [_i32, _i32, C.POINTER(_vp)]),
@@ -357,6 +367,157 @@ def sample_gumbel(logits, temperatures, exp_noise, out=None, stream=None):
                                   _ptr(temperatures), _ptr(exp_noise), exp_noise.stride(0), batch, vocab,
                                   _stream(stream)),
            "pa_sample_gumbel")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The 8-bit pool: codes [num_blocks, Hkv, B, 128] (float8_e4m3fn or int8) and
+# one scale byte per token and head [num_blocks, Hkv, B] (uint8).
+# ---------------------------------------------------------------------------
+_Q8_FORMATS = {torch.float8_e4m3fn: PA_Q8_E4M3, torch.int8: PA_Q8_INT8}
+
+
+def kvcache_q8(num_blocks, block_size, num_kv_heads, head_dim=128, dtype=torch.float8_e4m3fn, device="cuda"):
+    """Allocate one layer's 8-bit pool, zero-filled: (k_cache, v_cache, k_scale, v_scale)."""
+    if dtype not in _Q8_FORMATS:
+        raise TypeError(f"dtype must be float8_e4m3fn or int8, got {dtype}")
+    shape = (num_blocks, num_kv_heads, block_size, head_dim)
+    return (*(torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2)),
+            *(torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+def _q8_pool(k_cache, v_cache, k_scale, v_scale):
+    """Checks the four tensors of an 8-bit pool; returns its format."""
+    fmt = _Q8_FORMATS.get(k_cache.dtype)
+    if fmt is None or k_cache.dim() != 4:
+        raise TypeError("k_cache must be a [num_blocks, Hkv, B, D] tensor of float8_e4m3fn or int8")
+    _need(k_cache, k_cache.dtype, "k_cache")
+    _need(v_cache, k_cache.dtype, "v_cache")
+    _need(k_scale, torch.uint8, "k_scale")
+    _need(v_scale, torch.uint8, "v_scale")
+    if v_cache.shape != k_cache.shape or not (k_scale.shape == v_scale.shape == k_cache.shape[:3]):
+        raise ValueError("k_cache / v_cache must be [num_blocks, Hkv, B, D] and k_scale / v_scale [num_blocks, Hkv, B]")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous()):
+        raise ValueError("caches and scales must be contiguous")
+    return fmt
+
+
+class _Launch:
+    """Where a call runs: on the tensors' device (all must share it) and on
+    `stream`, default that device's current stream.  Inside the `with`, both
+    are current, so that what the call allocates belongs to that stream."""
+
+    def __init__(self, stream, first, *others):
+        self.device = first.device
+        for t in others:
+            if t is not None and t.device != self.device:
+                raise ValueError(f"tensors on different devices: {self.device} and {t.device}")
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"stream of {stream.device}, tensors on {self.device}")
+        self.contexts = []
+        if stream is not None:
+            self.contexts.append(torch.cuda.stream(stream))  # also makes its device current
+        elif self.device.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(self.device))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return C.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _q8_slots(slot_mapping, n=None):
+    _need(slot_mapping, torch.int32, "slot_mapping")
+    if slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or (n is not None and slot_mapping.numel() != n):
+        raise ValueError("slot_mapping must be contiguous with one entry per token")
+
+
+def store_kvcache_q8(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping, stream=None):
+    """Quantise key/value [N, Hkv, 128] (bf16, rows may be strided) into the
+    8-bit pool at slot_mapping (int32 [N], negatives skipped)."""
+    fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
+    nb, hkv, B, d = k_cache.shape
+    _need(key, torch.bfloat16, "key")
+    _need(value, torch.bfloat16, "value")
+    if tuple(key.shape[1:]) != (hkv, d) or value.shape != key.shape:
+        raise ValueError(f"key and value must be [N, {hkv}, {d}]")
+    n = key.shape[0]
+    _q8_slots(slot_mapping, n)
+    with _Launch(stream, key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping) as s:
+        _check(lib().pa_store_kvcache_q8(_ptr(key), _row_stride(key, "key"), _ptr(value), _row_stride(value, "value"),
+                                         _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                         _ptr(slot_mapping), n, hkv, d, B, nb, fmt, s), "pa_store_kvcache_q8")
+
+
+def load_kvcache_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k=None, out_v=None, stream=None):
+    """Read rows of the 8-bit pool back: (k, v), bf16 [N, Hkv, 128], the rows of
+    slots slot_mapping (int32 [N], may repeat; zeros for negatives).  out_k /
+    out_v may be given (rows may be strided)."""
+    fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
+    nb, hkv, B, d = k_cache.shape
+    _q8_slots(slot_mapping)
+    n = slot_mapping.numel()
+    with _Launch(stream, k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k, out_v) as s:
+        if out_k is None:
+            out_k = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device)
+        if out_v is None:
+            out_v = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device)
+        for t, name in ((out_k, "out_k"), (out_v, "out_v")):
+            _need(t, torch.bfloat16, name)
+            if tuple(t.shape) != (n, hkv, d):
+                raise ValueError(f"{name} must be [{n}, {hkv}, {d}]")
+        _check(lib().pa_load_kvcache_q8(_ptr(out_k), _row_stride(out_k, "out_k"), _ptr(out_v),
+                                        _row_stride(out_v, "out_v"), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                        _ptr(v_scale), _ptr(slot_mapping), n, hkv, d, B, nb, fmt, s),
+               "pa_load_kvcache_q8")
+    return out_k, out_v
+
+
+def decode_q8_workspace(num_q_heads, num_kv_heads, head_dim=128, device="cuda"):
+    """Zero-filled workspace for decode_q8 (it depends only on the GQA group);
+    the calls leave it ready for the next one on the same stream."""
+    n = int(lib().pa_decode_q8_workspace_size(num_q_heads, num_kv_heads, head_dim))
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, softmax_scale=None, workspace=None,
+              out=None, stream=None):
+    """Paged decode attention over the 8-bit pool.  q [batch, Hq, 128] bf16
+    (rows may be strided); block_tables int32 [batch, max_blocks];
+    context_lens int32 [batch].  Returns out [batch, Hq, 128] bf16."""
+    fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
+    nb, hkv, B, d = k_cache.shape
+    _need(q, torch.bfloat16, "q")
+    _need(block_tables, torch.int32, "block_tables")
+    _need(context_lens, torch.int32, "context_lens")
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [batch, Hq, {d}]")
+    batch, hq, _ = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != batch or tuple(context_lens.shape) != (batch,):
+        raise ValueError("block_tables must be [batch, max_blocks] and context_lens [batch]")
+    if not (block_tables.is_contiguous() and context_lens.is_contiguous()):
+        raise ValueError("block_tables and context_lens must be contiguous")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(d)
+    with _Launch(stream, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace, out) as s:
+        if workspace is None:
+            workspace = decode_q8_workspace(hq, hkv, d, q.device)
+        elif not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        if out is None:
+            out = torch.empty(batch, hq, d, dtype=torch.bfloat16, device=q.device)
+        _need(out, torch.bfloat16, "out")
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous and of q's shape")
+        _check(lib().pa_decode_q8(_ptr(out), _ptr(q), _row_stride(q, "q"), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
+                                  _ptr(context_lens), batch, hq, hkv, d, B, nb, fmt, float(softmax_scale),
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(), s), "pa_decode_q8")
     return out
 
 

@@ -133,6 +133,22 @@ pa_status encode_kv_tensor_map_halves(CUtensorMap *map, const void *base, int64_
     return encode_halves_map(map, base, num_slots, (int64_t)num_kv_heads * 256, num_kv_heads, box_rows, 2);
 }
 
+pa_status encode_row_map_u8(CUtensorMap *map, const void *base, int64_t num_rows, int32_t box_rows) {
+    pa_status st = get_encoder();
+    if (st != PA_OK) return st;
+    const cuuint64_t dims[2] = {128u, (cuuint64_t)num_rows};
+    const cuuint64_t strides[1] = {128u};
+    const cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %lld rows of 128 bytes", (int)r,
+                    (long long)num_rows);
+    return PA_OK;
+}
+
 }  // namespace pa
 
 extern "C" {

@@ -227,6 +227,9 @@ pa_status encode_halves_map(CUtensorMap *map, const void *base, int64_t num_rows
 pa_status encode_tensor_map_3d(CUtensorMap *map, const void *base, int64_t dim0, int64_t dim1, int64_t dim2,
                                int64_t stride1_bytes, int64_t stride2_bytes, int32_t box0, int32_t box2,
                                bool swizzle128);
+// 2-D map over an 8-bit pool's [num_rows][128] one-byte rows with box
+// {128, box_rows} and 128-byte swizzle.
+pa_status encode_row_map_u8(CUtensorMap *map, const void *base, int64_t num_rows, int32_t box_rows);
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
