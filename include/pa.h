@@ -87,7 +87,9 @@ enum {
                                   where = sequence index */
     PA_DEV_SMEM_ALIGN = 6,     /* a kernel could not align its shared-memory tiles
                                   (no work done); where = bytes of padding needed */
-    PA_DEV_BAD_TEMPERATURE = 7 /* sampler: temperature not > 1e-10; where = row */
+    PA_DEV_BAD_TEMPERATURE = 7, /* sampler, log probabilities: temperature not > 1e-10;
+                                  where = row */
+    PA_DEV_BAD_TOKEN = 8       /* log probabilities: token >= vocab; where = row */
 };
 
 /* Code formats of an 8-bit KV pool (pa_store_kvcache_q8 and what reads it). */
@@ -399,6 +401,37 @@ PA_API pa_status pa_prefill_store_varlen(void *out, const void *q, int64_t q_row
 PA_API pa_status pa_sample_gumbel(int32_t *out_tokens, const void *logits, int64_t logits_row_stride,
                                   int32_t logits_is_fp32, const float *temperatures, const float *exp_noise,
                                   int64_t noise_row_stride, int32_t batch, int32_t vocab, pa_stream_t stream);
+
+/*
+ * pa_logprobs -- log probabilities of given tokens, entropy, top alternatives:
+ * what a server answers beside the tokens pa_sample_gumbel picks.  (An addition
+ * of this library: the source pages stop at the token.)
+ *
+ * Per row, with z = float(logits) / T:
+ *   logprobs[r]  = z_t - ln sum_i e^{z_i}   for t = tokens[r],
+ *   entropy[r]   = -sum_i p_i ln p_i, p = softmax(z)   (0 ln 0 = 0),
+ *   top_ids[r], top_logprobs[r]: the top_k largest logits in order (the lower
+ *   index first among equals; NaN last) and their log probabilities.
+ * All in fp32.  Logits of -inf have probability 0 and log probability -inf; a
+ * row of nothing else has log probabilities -inf and entropy 0.  A NaN or
+ * +inf logit makes its row's log probabilities and entropy NaN (top_ids still
+ * follow the order).  A negative token (none given) has log probability -inf;
+ * one >= vocab likewise, recorded as PA_DEV_BAD_TOKEN.
+ *   logprobs, entropy      fp32 [rows].
+ *   top_ids, top_logprobs  int32 / fp32 [rows, top_k]; unused for top_k == 0.
+ *   logits                 [rows, vocab] bf16 (logits_is_fp32 = 0) or fp32 (1);
+ *                          row stride in elements, >= vocab and a multiple of 8
+ *                          (bf16) or 4 (fp32); 16-byte aligned.
+ *   temperatures           fp32 [rows], each > 1e-10, or NULL (1).  A row whose
+ *                          temperature is not gets NaN and ids -1
+ *                          (PA_DEV_BAD_TEMPERATURE).
+ *   tokens                 int32 [rows].
+ *   top_k                  0..32, at most vocab.
+ */
+PA_API pa_status pa_logprobs(float *logprobs, float *entropy, int32_t *top_ids, float *top_logprobs,
+                             const void *logits, int64_t logits_row_stride, int32_t logits_is_fp32,
+                             const float *temperatures, const int32_t *tokens, int32_t rows, int32_t vocab,
+                             int32_t top_k, pa_stream_t stream);
 
 /* --------------------------------------------------------------------------
  * 8-bit KV pool.  (An addition of this library: the source pages keep the

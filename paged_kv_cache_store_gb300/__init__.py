@@ -12,7 +12,7 @@ Entry points (same names as the C ABI without the ``pa_`` prefix):
   decode_workspace_size, decode, decode_static, prefill_varlen,
   sample_gumbel, set_checked, get_device_error;
   kvcache_q8, store_kvcache_q8, load_kvcache_q8, decode_q8_workspace,
-  decode_q8 (the 8-bit pool);
+  decode_q8 (the 8-bit pool); logprobs;
   block_manager.BlockManager wraps the host block manager (pa_bm_*).
 """
 from __future__ import annotations
@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes as C
 import math
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -28,7 +29,7 @@ LIB_PATH = os.path.join(_PKG, "libpa.so")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA, PA_ERR_DEVICE_CHECK = range(6)
 (PA_DEV_TIMEOUT, PA_DEV_BAD_SLOT, PA_DEV_BAD_CONTEXT, PA_DEV_BAD_BLOCK, PA_DEV_BAD_SEQLENS, PA_DEV_SMEM_ALIGN,
- PA_DEV_BAD_TEMPERATURE) = range(1, 8)
+ PA_DEV_BAD_TEMPERATURE, PA_DEV_BAD_TOKEN) = range(1, 9)
 PA_Q8_E4M3, PA_Q8_INT8 = range(2)
 
 # Every symbol include/pa.h declares, with its ctypes signature.
@@ -58,6 +59,7 @@ SIGNATURES = {
                                           _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp,
                                           C.c_size_t, _vp]),
     "pa_sample_gumbel": (C.c_int, [_vp, _vp, _i64, _i32, _vp, _vp, _i64, _i32, _i32, _vp]),
+    "pa_logprobs": (C.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp]),
     "pa_store_kvcache_q8": (C.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
                                       _i32, _vp]),
     "pa_load_kvcache_q8": (C.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
@@ -518,6 +520,57 @@ def decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
                                   _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
                                   _ptr(context_lens), batch, hq, hkv, d, B, nb, fmt, float(softmax_scale),
                                   _ptr(workspace), workspace.numel() * workspace.element_size(), s), "pa_decode_q8")
+    return out
+
+
+class Logprobs(NamedTuple):
+    """What logprobs returns; the last two are None for top_k == 0."""
+    logprobs: torch.Tensor                # fp32 [rows]
+    entropy: torch.Tensor                 # fp32 [rows]
+    top_ids: Optional[torch.Tensor]       # int32 [rows, top_k]
+    top_logprobs: Optional[torch.Tensor]  # fp32 [rows, top_k]
+
+
+def logprobs(logits, tokens, top_k=0, temperatures=None, out=None, stream=None):
+    """Log probabilities of tokens (int32 [rows]) under softmax(logits / T),
+    the entropy and the top_k largest entries per row.  logits [rows, vocab]
+    bf16 or fp32 (rows may be strided); temperatures fp32 [rows] or None.
+    `out`, a Logprobs of contiguous tensors, is filled and returned."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("logits must be a bfloat16 or float32 tensor")
+    _need(logits, logits.dtype, "logits")
+    _need(tokens, torch.int32, "tokens")
+    if logits.dim() != 2 or tuple(tokens.shape) != (logits.shape[0],):
+        raise ValueError("logits must be [rows, vocab] and tokens [rows]")
+    rows, vocab = logits.shape
+    top_k = int(top_k)
+    if not tokens.is_contiguous() or (vocab > 1 and logits.stride(1) != 1):
+        raise ValueError("rows must be contiguous")
+    if temperatures is not None:
+        _need(temperatures, torch.float32, "temperatures")
+        if tuple(temperatures.shape) != (rows,) or not temperatures.is_contiguous():
+            raise ValueError("temperatures must be contiguous [rows]")
+    # A lone row's stride does not matter; the library wants it well-formed.
+    stride = logits.stride(0) if rows > 1 else -(-vocab // 8) * 8
+    with _Launch(stream, logits, tokens, temperatures, *(out or ())) as s:
+        if out is None:
+            k = max(top_k, 0)
+            out = Logprobs(*torch.empty(2, rows, dtype=torch.float32, device=logits.device).unbind(0),
+                           torch.empty(rows, k, dtype=torch.int32, device=logits.device) if k else None,
+                           torch.empty(rows, k, dtype=torch.float32, device=logits.device) if k else None)
+        else:
+            for t, dtype, shape, name in ((out[0], torch.float32, (rows,), "logprobs"),
+                                          (out[1], torch.float32, (rows,), "entropy"),
+                                          (out[2], torch.int32, (rows, top_k), "top_ids"),
+                                          (out[3], torch.float32, (rows, top_k), "top_logprobs")):
+                if t is None and top_k == 0 and len(shape) == 2:
+                    continue
+                _need(t, dtype, name)
+                if tuple(t.shape) != shape or not t.is_contiguous():
+                    raise ValueError(f"out.{name} must be contiguous {list(shape)}")
+        _check(lib().pa_logprobs(_ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), _ptr(logits), stride,
+                                 1 if logits.dtype == torch.float32 else 0, _ptr(temperatures), _ptr(tokens), rows,
+                                 vocab, top_k, s), "pa_logprobs")
     return out
 
 

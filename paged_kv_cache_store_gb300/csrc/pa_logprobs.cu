@@ -1,0 +1,504 @@
+// pa_logprobs.cu -- log probabilities of given tokens, entropy, top alternatives.
+//
+// What it computes, per row of logits x with temperature T (z = x / T):
+//   lse = ln sum_i e^{z_i},  logprob(i) = z_i - lse,
+//   entropy = lse - sum_i p_i z_i  (p = softmax z),
+//   the k largest logits in order, the lower index first among equals.
+//
+// How (GB300 design): a row is split over the CTAs of a thread-block cluster
+// (one CTA when there are many rows) and read from HBM once.
+//  * Sums: each thread keeps a reference m and S = sum 2^y, E = sum 2^y y with
+//    y = (x - m) * log2(e) / T, in fp32 pairs (packed add, mul and fma), one
+//    ex2 per element.  m is in logit units and y a product of a difference, so
+//    rows of the type's lowest value or of very large logits do not overflow.
+//    m only moves when a logit exceeds it by 32 in base 2.  Threads, warps
+//    and CTAs combine as (m, S, E) triples.
+//  * Top k: a thread also keeps the largest logit it has seen and the vector
+//    (8 logits) that first held it.  The threads form P >= k groups (P = 8, 16
+//    or 32 by lane); the smallest of the P group maxima, with its vector as
+//    the tie-break, is a threshold that at least k entries of the CTA's chunk
+//    reach.  Only threads whose own maximum reaches it re-read their vectors
+//    (from L2) and collect the entries that reach it: about P ln P of them
+//    for logits in random order.  The collected keys (logit, then index) are
+//    ranked by counting.  A chunk with more than CAP such entries, or with
+//    NaNs that hid some, is selected by k passes of a plain maximum instead.
+//    The CTAs' lists meet in the cluster's first CTA, where an entry's rank is
+//    its place in its own list plus the entries above it in the others'.
+#include <math.h>
+
+#include <algorithm>
+
+#include "pa_internal.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int LP_THREADS = 256;
+constexpr int LP_WARPS = LP_THREADS / 32;
+constexpr int LP_MAX_CLUSTER = 8;
+constexpr int LP_MAX_TOP = 32;
+constexpr int LP_CAP = 2048;      // collected entries of a chunk
+constexpr int LP_UNROLL = 4;      // vectors in flight per thread
+constexpr float LP_LAZY = 32.f;   // log2 headroom before the reference moves
+constexpr float LP_FLOOR = -200.f;  // 2^-200 is 0: keeps 0 * y finite for y = -inf
+constexpr unsigned FULL = 0xffffffffu;
+typedef unsigned long long u64;
+
+struct LpArgs {
+    float *logprobs, *entropy;
+    int32_t *top_ids;
+    float *top_logprobs;
+    const void *logits;
+    int64_t stride;
+    const float *temperatures;  // null: 1
+    const int32_t *tokens;
+    int32_t vocab, top, cluster;
+    DevError *err;
+};
+
+// (m, S, E) of a set of logits; m = -inf when it holds nothing finite.
+struct Stat {
+    float m, s, e;
+};
+
+__device__ __forceinline__ void join(Stat &a, const Stat &b, float kk) {
+    const float m = fmaxf(a.m, b.m);
+    auto moved = [&](const Stat &x) -> Stat {
+        if (x.m == m || x.s == 0.f) return Stat{m, x.s, x.e};
+        const float d = fmaxf((x.m - m) * kk, LP_FLOOR), f = exp2f(d);
+        return Stat{m, x.s * f, (x.e + x.s * d) * f};
+    };
+    const Stat x = moved(a), y = moved(b);
+    a = Stat{m, x.s + y.s, x.e + y.e};
+}
+
+// A float as an unsigned integer in the same order (-0 as +0); NaN lowest.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return x != x ? 0u : (b >> 31) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+    return o == 0 ? NAN : __uint_as_float((o >> 31) ? o & 0x7fffffffu : ~o);
+}
+// Larger logits first, then lower indices (or vectors).  0: nothing.
+__device__ __forceinline__ u64 key_of(float x, uint32_t i) { return ((u64)ordered(x) << 32) | (uint32_t)~i; }
+
+__device__ __forceinline__ uint4 ld16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Packed pairs of fp32.
+__device__ __forceinline__ u64 pack2(float a, float b) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(u64 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // keeps a NaN
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // drops a NaN
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight consecutive logits.
+template <bool FP32>
+struct Vec {
+    uint4 a, b;  // b: fp32 only
+    __device__ __forceinline__ void load(const void *row, int i) {
+        const char *p = static_cast<const char *>(row) + (int64_t)i * (FP32 ? 4 : 2);
+        a = ld16(p);
+        if (FP32) b = ld16(p + 16);
+    }
+    // The pair of logits 2j, 2j+1.
+    __device__ __forceinline__ void pair(int j, float &x, float &y) const {
+        if (FP32) {
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            x = __uint_as_float(w[2 * j]);
+            y = __uint_as_float(w[2 * j + 1]);
+        } else {
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+            x = bf16lo(w[j]);
+            y = bf16hi(w[j]);
+        }
+    }
+    __device__ __forceinline__ float top() const {  // the largest, NaNs dropped
+        if (FP32) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float x, y;
+                pair(j, x, y);
+                m = fmaxf(m, fmaxf(x, y));
+            }
+            return m;
+        }
+        const uint32_t w = max_bf16x2(max_bf16x2(a.x, a.y), max_bf16x2(a.z, a.w));
+        return fmaxf(bf16lo(w), bf16hi(w));
+    }
+};
+
+template <bool FP32>
+__device__ __forceinline__ float logit(const void *row, int i) {
+    if (FP32) return __ldg(static_cast<const float *>(row) + i);
+    return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(row) + i) << 16);
+}
+
+// A thread's running state over its vectors.
+struct Run {
+    float m, limit;   // reference, and the logit above which it moves
+    u64 s, e;         // packed pairs
+    float top;        // largest logit so far and the vector that first held it
+    uint32_t top_vec; // 0xffffffff: none
+};
+
+__device__ __forceinline__ void move_reference(Run &r, float to, float kk) {
+    if (r.m != -INFINITY) {
+        float s0, s1, e0, e1;
+        unpack2(r.s, s0, s1);
+        unpack2(r.e, e0, e1);
+        const float d = fmaxf((r.m - to) * kk, LP_FLOOR), f = fast_exp2(d);
+        r.s = pack2(s0 * f, s1 * f);
+        r.e = pack2((e0 + s0 * d) * f, (e1 + s1 * d) * f);
+    }
+    r.m = to;
+    r.limit = to + LP_LAZY / kk;
+}
+
+// Sums of a pair (a lone logit: its partner is -inf).
+__device__ __forceinline__ void add_pair(Run &r, float x, float y, u64 negm, u64 kk2) {
+    float a, b;
+    unpack2(mul2(add2(pack2(x, y), negm), kk2), a, b);
+    a = max_nan(a, LP_FLOOR);
+    b = max_nan(b, LP_FLOOR);
+    const u64 ex = pack2(fast_exp2(a), fast_exp2(b));
+    r.s = add2(r.s, ex);
+    r.e = fma2(ex, pack2(a, b), r.e);
+}
+
+__device__ __forceinline__ void see(Run &r, float t, uint32_t vec) {
+    if (t > r.top || r.top_vec == 0xffffffffu) {
+        r.top = t != t ? -INFINITY : t;
+        r.top_vec = vec;
+    }
+}
+
+template <bool FP32>
+__global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a) {
+    pdl_wait_then_release();
+    // Distributed shared memory is written only once every CTA of the cluster runs.
+    if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    __shared__ u64 buf[LP_CAP];
+    __shared__ u64 group[LP_WARPS][32];
+    __shared__ Stat stats[LP_WARPS];
+    __shared__ int count;
+    __shared__ u64 lists[LP_MAX_CLUSTER][LP_MAX_TOP];  // in the cluster's first CTA
+    __shared__ Stat cstats[LP_MAX_CLUSTER];            // likewise
+    __shared__ u64 mine[LP_MAX_TOP];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = a.cluster;
+    const int64_t row = blockIdx.x / (unsigned)S;
+    const int rank = (int)(blockIdx.x % (unsigned)S);
+    const float T = a.temperatures ? __ldg(a.temperatures + row) : 1.f;
+    const bool bad_t = !(T > 1e-10f);
+    const float kk = bad_t ? 1.f : 1.4426950408889634f / T;
+    const char *x = static_cast<const char *>(a.logits) + row * a.stride * (FP32 ? 4 : 2);
+    // This CTA's chunk of the row, a multiple of 8 logits except at the end.
+    const int chunk = (int)((((int64_t)a.vocab + S - 1) / S + 7) & ~7ll);
+    const int lo = (int)min((int64_t)a.vocab, (int64_t)rank * chunk), hi = (int)min((int64_t)a.vocab, (int64_t)lo + chunk);
+    const int nvec = (hi - lo) / 8;
+    if (tid < LP_MAX_TOP) mine[tid] = 0;
+    if (tid == 0) count = 0;
+
+    // ---- one pass: sums, and each thread's largest logit
+    Run r;
+    r.m = r.limit = r.top = -INFINITY;
+    r.s = r.e = pack2(0.f, 0.f);
+    r.top_vec = 0xffffffffu;
+    const u64 kk2 = pack2(kk, kk);
+    for (int v0 = tid; v0 < nvec; v0 += LP_UNROLL * LP_THREADS) {
+        Vec<FP32> v[LP_UNROLL];
+#pragma unroll
+        for (int u = 0; u < LP_UNROLL; ++u)
+            v[u].load(x, lo + 8 * min(v0 + u * LP_THREADS, nvec - 1));  // a repeat past the end is ignored below
+#pragma unroll
+        for (int u = 0; u < LP_UNROLL; ++u) {
+            const int vec = v0 + u * LP_THREADS;
+            if (vec >= nvec) break;
+            const float t = v[u].top();
+            see(r, t, (uint32_t)vec);
+            if (t > r.limit) move_reference(r, t, kk);
+            const float nm = r.m == -INFINITY ? 0.f : -r.m;
+            const u64 negm = pack2(nm, nm);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float p, q;
+                v[u].pair(j, p, q);
+                add_pair(r, p, q, negm, kk2);
+            }
+        }
+    }
+    // The ragged end of the row: one logit per thread.
+    const int tail = lo + 8 * nvec + tid;
+    if (tail < hi) {
+        const float t = logit<FP32>(x, tail);
+        see(r, t, (uint32_t)nvec);
+        if (t > r.limit) move_reference(r, t, kk);
+        const float nm = r.m == -INFINITY ? 0.f : -r.m;
+        add_pair(r, t, -INFINITY, pack2(nm, nm), kk2);
+    }
+    // References become the largest logits themselves: ln of the final sum is
+    // then small where one entry holds the row, and exact to fp32.
+    if (r.top > r.m) move_reference(r, r.top, kk);
+    Stat st;
+    {
+        float s0, s1, e0, e1;
+        unpack2(r.s, s0, s1);
+        unpack2(r.e, e0, e1);
+        st = Stat{r.m, s0 + s1, e0 + e1};
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Stat t;
+        t.m = __shfl_xor_sync(FULL, st.m, o);
+        t.s = __shfl_xor_sync(FULL, st.s, o);
+        t.e = __shfl_xor_sync(FULL, st.e, o);
+        // The same order on both sides, so that every lane holds the same bits.
+        Stat l = (lane & o) ? t : st;
+        join(l, (lane & o) ? st : t, kk);
+        st = l;
+    }
+    if (lane == 0) stats[warp] = st;
+
+    // ---- the chunk's k largest, in order, in mine[]
+    if (a.top > 0) {
+        const int want = min(a.top, hi - lo);
+        const int P = a.top <= 8 ? 8 : a.top <= 16 ? 16 : 32;
+        const u64 own = r.top_vec == 0xffffffffu ? 0ull : key_of(r.top, r.top_vec);
+        u64 g = own;
+        for (int o = P; o < 32; o <<= 1) g = max(g, __shfl_xor_sync(FULL, g, o));
+        group[warp][lane] = g;
+        __syncthreads();
+        u64 thr = group[0][lane];
+#pragma unroll
+        for (int w = 1; w < LP_WARPS; ++w) thr = max(thr, group[w][lane]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) thr = min(thr, __shfl_xor_sync(FULL, thr, o));
+        if (own != 0 && own >= thr) {
+            auto collect = [&](float t, uint32_t vec, int i) {
+                if (key_of(t, vec) >= thr) {
+                    const int at = atomicAdd(&count, 1);
+                    if (at < LP_CAP) buf[at] = key_of(t, (uint32_t)i);
+                }
+            };
+            for (int v0 = tid; v0 < nvec; v0 += LP_UNROLL * LP_THREADS) {
+                Vec<FP32> v[LP_UNROLL];
+#pragma unroll
+                for (int u = 0; u < LP_UNROLL; ++u) v[u].load(x, lo + 8 * min(v0 + u * LP_THREADS, nvec - 1));
+#pragma unroll
+                for (int u = 0; u < LP_UNROLL; ++u) {
+                    const int vec = v0 + u * LP_THREADS;
+                    if (vec >= nvec || key_of(v[u].top(), (uint32_t)vec) < thr) continue;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float p, q;
+                        v[u].pair(j, p, q);
+                        collect(p, (uint32_t)vec, lo + 8 * vec + 2 * j);
+                        collect(q, (uint32_t)vec, lo + 8 * vec + 2 * j + 1);
+                    }
+                }
+            }
+            if (tail < hi) collect(logit<FP32>(x, tail), (uint32_t)nvec, tail);
+        }
+        __syncthreads();
+        const int n = count;
+        if (n >= want && n <= LP_CAP) {
+            for (int i = tid; i < n; i += LP_THREADS) {
+                const u64 k = buf[i];
+                int above = 0;
+                for (int j = 0; j < n; ++j) above += buf[j] > k;
+                if (above < want) mine[above] = k;
+            }
+        } else {  // k passes: the largest key below the last one
+            u64 last = ~0ull;
+            for (int i = 0; i < want; ++i) {
+                u64 best = 0;
+                for (int e = lo + tid; e < hi; e += LP_THREADS) {
+                    const u64 k = key_of(logit<FP32>(x, e), (uint32_t)e);
+                    if (k < last && k > best) best = k;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(FULL, best, o));
+                __syncthreads();
+                if (lane == 0) group[0][warp] = best;
+                __syncthreads();
+                best = group[0][0];
+#pragma unroll
+                for (int w = 1; w < LP_WARPS; ++w) best = max(best, group[0][w]);
+                if (tid == 0) mine[i] = best;
+                last = best;
+            }
+        }
+    }
+    __syncthreads();
+    // ---- to the cluster's first CTA
+    if (tid == 0) {
+        Stat c = stats[0];
+        for (int w = 1; w < LP_WARPS; ++w) join(c, stats[w], kk);
+        stats[0] = c;
+    }
+    if (S > 1) {
+        __syncthreads();
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (tid < a.top) {
+            uint32_t dst;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_addr(&lists[rank][tid])), "r"(0u));
+            asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(dst), "l"(mine[tid]) : "memory");
+        }
+        if (tid >= 32 && tid < 35) {
+            const int f = tid - 32;
+            const Stat c = stats[0];
+            uint32_t dst;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_addr(&cstats[rank])), "r"(0u));
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst + 4 * f),
+                         "r"(__float_as_uint(f == 0 ? c.m : f == 1 ? c.s : c.e))
+                         : "memory");
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+    }
+    // ---- the row's answers
+    Stat all = S > 1 ? cstats[0] : stats[0];
+    for (int c = 1; c < S; ++c) join(all, cstats[c], kk);
+    const float lsum = logf(all.s);
+    auto logprob = [&](float t) -> float {
+        if (all.s == 0.f) return -INFINITY;  // a row without a finite logit
+        return (t - all.m) / T - lsum;
+    };
+    if (tid == 0) {
+        const int32_t tok = __ldg(a.tokens + row);
+        float lp = -INFINITY;
+        if (bad_t) {
+            record_error(a.err, PA_DEV_BAD_TEMPERATURE, row);
+            lp = NAN;
+        } else if (tok >= a.vocab) {
+            record_error(a.err, PA_DEV_BAD_TOKEN, row);
+        } else if (tok >= 0) {
+            lp = logprob(logit<FP32>(x, tok));
+        }
+        a.logprobs[row] = lp;
+        a.entropy[row] = bad_t ? NAN : all.s == 0.f ? 0.f : lsum - 0.6931471805599453f * (all.e / all.s);
+    }
+    for (int i = tid; i < S * a.top; i += LP_THREADS) {
+        const int c = i / a.top, at = i - c * a.top;
+        const u64 k = S > 1 ? lists[c][at] : mine[at];
+        if (k == 0) continue;
+        int place = at;
+        for (int o = 0; o < S; ++o) {
+            if (o == c) continue;
+            int l = 0, h = a.top;  // entries of list o above k
+            while (l < h) {
+                const int mid = (l + h) >> 1;
+                if (lists[o][mid] > k) l = mid + 1; else h = mid;
+            }
+            place += l;
+        }
+        if (place < a.top) {
+            a.top_ids[row * a.top + place] = bad_t ? -1 : (int32_t)~(uint32_t)k;
+            a.top_logprobs[row * a.top + place] = bad_t ? NAN : logprob(from_ordered((uint32_t)(k >> 32)));
+        }
+    }
+}
+
+// CTAs per row: the smallest power of two that gives ~4 CTAs per SM over the
+// rows, at most 8 (a portable cluster) and at least 2048 logits per CTA.
+int lp_ctas_per_row(int rows, int vocab, int sms) {
+    int S = 1;
+    while (S < LP_MAX_CLUSTER && (int64_t)rows * S < 4LL * sms && vocab / (2 * S) >= 2048) S *= 2;
+    return S;
+}
+
+template <bool FP32>
+pa_status launch_logprobs(const LpArgs &a, int32_t rows, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.cluster * (unsigned)rows);
+    cfg.blockDim = dim3(LP_THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, logprobs_kernel<FP32>, a);
+    if (e != cudaSuccess) return cuda_fail(e, "logprobs_kernel");
+    return check_launch("logprobs_kernel");
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status pa_logprobs(float *logprobs, float *entropy, int32_t *top_ids, float *top_logprobs,
+                                 const void *logits, int64_t logits_row_stride, int32_t logits_is_fp32,
+                                 const float *temperatures, const int32_t *tokens, int32_t rows, int32_t vocab,
+                                 int32_t top_k, pa_stream_t stream) {
+    using namespace pa;
+    if (rows < 0 || vocab < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
+    if (rows == 0) return PA_OK;
+    if (vocab == 0) return fail(PA_ERR_INVALID_ARG, "vocab must be positive");
+    if (top_k < 0 || top_k > vocab) return fail(PA_ERR_INVALID_ARG, "top_k must be in [0, vocab]");
+    if (top_k > LP_MAX_TOP) return fail(PA_ERR_UNSUPPORTED, "top_k %d (at most %d)", top_k, LP_MAX_TOP);
+    if (!logprobs || !entropy || !logits || !tokens || (top_k > 0 && (!top_ids || !top_logprobs)))
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    if (logits_is_fp32 != 0 && logits_is_fp32 != 1) return fail(PA_ERR_INVALID_ARG, "logits_is_fp32 must be 0 or 1");
+    const int align = logits_is_fp32 ? 4 : 8;  // elements per 16 bytes
+    if (logits_row_stride < vocab || logits_row_stride % align)
+        return fail(PA_ERR_INVALID_ARG, "logits_row_stride must be >= vocab and a multiple of %d", align);
+    if (!aligned16(logits)) return fail(PA_ERR_INVALID_ARG, "logits must be 16-byte aligned");
+    const int sms = sm_count();
+    if (sms <= 0) return fail(PA_ERR_CUDA, "no CUDA device");
+    LpArgs a = {};
+    a.logprobs = logprobs;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.logits = logits;
+    a.stride = logits_row_stride;
+    a.temperatures = temperatures;
+    a.tokens = tokens;
+    a.vocab = vocab;
+    a.top = top_k;
+    a.cluster = lp_ctas_per_row(rows, vocab, sms);
+    a.err = device_error_ptr();
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return logits_is_fp32 ? launch_logprobs<true>(a, rows, s) : launch_logprobs<false>(a, rows, s);
+}
