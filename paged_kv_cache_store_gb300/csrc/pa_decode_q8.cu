@@ -5,14 +5,15 @@
 //   K[p] = kc[p] * 2^(ks[p]-127),  V[p] = vc[p] * 2^(vs[p]-127),  p < ctx_b.
 //
 // How (GB300 design):
-//  * The work is a flat list of 32-key tiles ordered (sequence, kv head, tile).
-//    It is cut into equal contiguous ranges, one per WARP of a persistent grid
-//    (one CTA per SM).  A warp is its own producer: its lane 0 issues the TMA
-//    copies of its next tiles into the warp's own ring of shared memory (K and
-//    V codes, 4 KB each, 128-byte swizzled, and the 32 + 32 scale bytes) and
-//    the warp waits on its own mbarriers.  No barrier between warps while it
-//    streams: with half the bytes per key of a bf16 pool, the merges and
-//    hand-overs of a CTA-wide pipeline would weigh twice as much.
+//  * The work is a flat list of 32-key tiles ordered (sequence, kv head, tile),
+//    cut into equal contiguous ranges, one per CTA of a persistent grid (one
+//    CTA per SM), and each CTA's range into equal contiguous ranges of its
+//    WARPS.  A warp is its own producer: its lane 0 issues the TMA copies of
+//    its next tiles into the warp's own ring of shared memory (K and V codes,
+//    4 KB each, 128-byte swizzled) and the warp waits on its own mbarriers;
+//    the scale bytes, one per lane, are plain loads a ring ahead.  No barrier between warps while they stream:
+//    with half the bytes per key of a bf16 pool, the merges and hand-overs of
+//    a CTA-wide pipeline would weigh twice as much.
 //  * Q.K and P.V run as mma.sync m16n8k16 (fp16 in, fp32 accumulate) with the
 //    KEYS (Q.K) and the VALUE DIMS (P.V) as the M side and the G <= 8 query
 //    heads as N = 8: half the MMAs of the layout with heads as M.  The codes
@@ -28,9 +29,12 @@
 //    kept between 2^7 and 2^15 (a weight 2^-21 below it is still a normal
 //    fp16 number, one 2^-32 below it rounds to 0); the softmax sum uses the
 //    plain weights 2^(x_p - m) in fp32.
-//  * Segment end: a pair (b, g) inside the warp's range is written directly; a
-//    part goes to the workspace and the last arriving warp merges the pair's
-//    parts in order, so the result does not depend on timing.
+//  * A pair (b, g) inside a warp's range is written directly.  The pieces of
+//    the others meet when the CTA's warps are done, one (pair, head) per warp
+//    at a time; pairs that span CTAs leave a part in the workspace and the
+//    CTA that arrives last merges them.  Pieces are combined in list order,
+//    so the result does not depend on timing.  A pair is cut between at most
+//    kMaxParts CTAs (or so), since its parts are read by one CTA.
 //  * All waits are bounded; a timeout records PA_DEV_TIMEOUT and ends the warp.
 #include <math.h>
 
@@ -46,37 +50,53 @@ constexpr int KT = 32;            // keys per tile
 constexpr int NW = 12;            // warps per CTA
 constexpr int ST = 2;             // tiles in a warp's ring
 constexpr int NT = NW * 32;
+constexpr int NG = KT / 16;       // MMA key groups of a tile
 constexpr int TILE_BYTES = KT * Q8_D;                 // K or V codes of a tile
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;
 constexpr int kMaxBatch = 2048;
 constexpr int kMaxGrid = 160;     // CTAs of the persistent grid (min(SMs, this))
-constexpr int kMaxWorkers = kMaxGrid * NW;
+constexpr uint32_t kMaxParts = 32;     // CTAs that share a pair, about
+constexpr uint32_t kMinTilesPerCta = 2;
 constexpr float kLazyRescale = 8.f;  // log2 headroom before a running reference must move
 constexpr float kWeightTop = 7.f;    // log2 of the largest fp16 weight when its reference moves
 constexpr unsigned FULL = 0xffffffffu;
 
-constexpr int OFF_SC = NW * ST * STAGE_BYTES;         // scale bytes [NW][ST][2][KT]
-constexpr int OFF_BAR = OFF_SC + NW * ST * 2 * KT;    // mbarriers [NW][ST]
+constexpr int OFF_BAR = NW * ST * STAGE_BYTES;        // mbarriers [NW][ST]
 constexpr int OFF_ZERO = OFF_BAR + NW * ST * 8;       // a row of zeros
-constexpr int OFF_WSUM = OFF_ZERO + Q8_D;             // scan scratch [NW]
-constexpr int OFF_CUM = OFF_WSUM + 64;                // tile prefix sum [batch + 1]
-static_assert(OFF_SC % 16 == 0 && OFF_BAR % 8 == 0 && OFF_ZERO % 16 == 0 && NW * 4 <= 64, "shared-memory layout");
+constexpr int OFF_WSUM = OFF_ZERO + Q8_D;             // scan scratch [NW], then a maximum [NW]
+constexpr int OFF_PIECE = OFF_WSUM + 128;             // pair of each warp's two pieces [2 * NW] (-1: none)
+constexpr int OFF_TODO = OFF_PIECE + 128;             // pairs this CTA merges across CTAs [2], abort flag
+constexpr int OFF_SPAN = OFF_TODO + 16;               // the range's end pairs: {pair or -1, first CTA, CTAs, -} [2]
+constexpr int OFF_CUM = OFF_SPAN + 32;                // tile prefix sum [batch + 1]
+static_assert(OFF_BAR % 16 == 0 && OFF_ZERO % 16 == 0 && NW * 8 <= 128, "shared-memory layout");
+static_assert(NW <= 16, "a warp's lanes hold the CTA's pieces");
 __host__ __device__ constexpr size_t off_ctx(int batch) { return OFF_CUM + 4 * (size_t)(batch + 1); }
-constexpr size_t smem_bytes(int batch) { return off_ctx(batch) + 4 * (size_t)batch + 1024; }
-static_assert(smem_bytes(kMaxBatch) <= 232448, "shared memory budget");
+__host__ __device__ constexpr size_t off_stash(int batch) { return (off_ctx(batch) + 4 * (size_t)batch + 15) / 16 * 16; }
+constexpr size_t smem_bytes(int batch) { return off_stash(batch) + 1024; }
+constexpr size_t kMaxSmem = 232448;
+static_assert(smem_bytes(kMaxBatch) <= kMaxSmem, "shared memory budget");
 
-// Workspace: per worker two parts (its first and its last segment) of G heads:
-// o [2 * kMaxWorkers][G][128] fp32, (m, mv, l, -) [2 * kMaxWorkers][G] float4,
-// then the arrival counters [kMaxWorkers].
+// A piece of a pair: o [G][128] fp32, then (m, mv, l, -) [G].  Of each warp,
+// the last piece waits in the warp's own ring (free by then) and the first, if
+// it is another, in a stash: shared memory where it fits beside the batch's
+// tables (G = 8 does not, nor do the largest batches of G = 4), else the
+// workspace.  A CTA's parts of pairs that span CTAs are in the workspace.
+template <int G>
+constexpr int kPiece = G * (Q8_D + 4);  // floats
+static_assert(kPiece<8> * 4 <= ST * STAGE_BYTES, "a piece fits a ring");
+
+// Workspace: the warps' first pieces [kMaxGrid][NW], the CTAs' parts [kMaxGrid][2]
+// (of the pair at the range's start, of a later one), the arrival counters
+// [kMaxGrid] (of the pair that spans CTAs and starts in this one's range).
 struct WsLayout {
-    size_t ml_off, o_off, cnt_off, total;
+    size_t part_off, cnt_off, total;
 };
 WsLayout ws_layout(int G) {
+    const size_t piece = (size_t)G * (Q8_D + 4) * 4;
     WsLayout w;
-    w.o_off = 0;
-    w.ml_off = (size_t)2 * kMaxWorkers * G * Q8_D * 4;
-    w.cnt_off = w.ml_off + (size_t)2 * kMaxWorkers * G * 16;
-    w.total = w.cnt_off + (size_t)kMaxWorkers * 4;
+    w.part_off = piece * kMaxGrid * NW;
+    w.cnt_off = w.part_off + piece * kMaxGrid * 2;
+    w.total = w.cnt_off + (size_t)kMaxGrid * 4;
     return w;
 }
 
@@ -90,9 +110,9 @@ struct Args {
     int32_t max_blocks, batch, Hq, Hkv, block_size, box_rows, num_blocks;
     float scale_log2;
     int32_t ctx_limit;
-    float *ws_o;
-    float4 *ws_ml;
+    float *ws_piece, *ws_part;
     int *ws_cnt;
+    int32_t stash;  // first pieces are stashed in shared memory
     DevError *err;
     int32_t checked;
 };
@@ -133,16 +153,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
 // The bytes (d0 k0, d1 k0, d0 k1, d1 k1) of a transposed V register as the two
 // fp16 pairs (k0, k1) of dim d0 and of dim d1.
 template <int FMT>
 __device__ __forceinline__ void v_to_f16(uint32_t w, uint32_t &d0, uint32_t &d1) {
-    q8_to_f16<FMT>(__byte_perm(w, 0, 0x3120), d0, d1);
+    if (FMT == PA_Q8_INT8) q8_int8_to_f16<0x4240, 0x4341>(w, d0, d1);
+    else q8_to_f16<FMT>(__byte_perm(w, 0, 0x3120), d0, d1);
 }
 
 // A position of the flat list.
@@ -155,8 +171,8 @@ struct Shared {
     const int *ctx;
 };
 
-__device__ __forceinline__ Pos locate(const Args &a, const Shared &s, long long x) {
-    const uint32_t qv = (uint32_t)(x / a.Hkv);
+__device__ __forceinline__ Pos locate(const Args &a, const Shared &s, uint32_t x) {
+    const uint32_t qv = x / (uint32_t)a.Hkv;
     int lo = 0, hi = a.batch - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -165,9 +181,9 @@ __device__ __forceinline__ Pos locate(const Args &a, const Shared &s, long long 
     Pos p;
     p.b = lo;
     p.nt = (int)(s.cum[lo + 1] - s.cum[lo]);
-    const long long off = x - (long long)a.Hkv * s.cum[lo];
-    p.g = (int)(off / p.nt);
-    p.t = (int)(off - (long long)p.g * p.nt);
+    const uint32_t off = x - (uint32_t)a.Hkv * s.cum[lo];
+    p.g = (int)(off / (uint32_t)p.nt);
+    p.t = (int)(off - (uint32_t)p.g * p.nt);
     return p;
 }
 
@@ -181,6 +197,89 @@ __device__ __forceinline__ void advance(const Args &a, const Shared &s, Pos &p) 
     if (p.b < a.batch) p.nt = (s.ctx[p.b] + KT - 1) / KT;
 }
 
+// Merges pieces of one pair and head: lane i of `mask` holds piece i's address.
+// Every lane returns dims 4*lane .. +3 and the totals.  FAR: the pieces are
+// other CTAs' (read from L2); else this CTA's, in shared memory or not.
+struct Merged {
+    float m, mv, l;
+    float4 o;
+};
+template <bool FAR>
+__device__ __forceinline__ float4 ld_piece(const float *p) {
+    const float4 *v = reinterpret_cast<const float4 *>(p);
+    return FAR ? __ldcg(v) : *v;
+}
+template <int G, bool FAR>
+__device__ __forceinline__ Merged merge_pieces(const float *piece, unsigned mask, int h) {
+    const int lane = threadIdx.x & 31;
+    float4 ml = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+    if (mask >> lane & 1) ml = ld_piece<FAR>(piece + G * Q8_D + 4 * h);
+    const unsigned long long at = reinterpret_cast<unsigned long long>(piece + h * Q8_D);
+    constexpr int PF = 4;  // pieces whose loads are in flight
+    float4 v[PF];
+    int from[PF];
+    auto load = [&](unsigned left) -> unsigned {
+#pragma unroll
+        for (int u = 0; u < PF; ++u) {
+            from[u] = left ? __ffs(left) - 1 : -1;
+            const float *src = reinterpret_cast<const float *>(__shfl_sync(FULL, at, max(from[u], 0)));
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (left) v[u] = ld_piece<FAR>(src + 4 * lane);
+            left &= left - 1;
+        }
+        return left;
+    };
+    unsigned left = load(mask);
+    Merged r;
+    r.m = ml.x;
+    r.mv = ml.y;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        r.m = fmaxf(r.m, __shfl_xor_sync(FULL, r.m, d));
+        r.mv = fmaxf(r.mv, __shfl_xor_sync(FULL, r.mv, d));
+    }
+    // 2^(own - max): a piece without a finite score has l = 0 or NaN.
+    float l = ml.z * (ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - r.m));
+    const float f = ml.y == -INFINITY ? 1.f : fast_exp2(ml.y - r.mv);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) l += __shfl_xor_sync(FULL, l, d);
+    r.l = l;
+    r.o = make_float4(0.f, 0.f, 0.f, 0.f);
+    while (true) {
+#pragma unroll
+        for (int u = 0; u < PF; ++u) {
+            const float w = __shfl_sync(FULL, f, max(from[u], 0));
+            if (from[u] < 0) continue;
+            r.o.x = fmaf(v[u].x, w, r.o.x);
+            r.o.y = fmaf(v[u].y, w, r.o.y);
+            r.o.z = fmaf(v[u].z, w, r.o.z);
+            r.o.w = fmaf(v[u].w, w, r.o.w);
+        }
+        if (!left) break;
+        left = load(left);
+    }
+    return r;
+}
+
+__device__ __forceinline__ void write_out(const Args &a, const Merged &r, int64_t row) {
+    const float f = fast_exp2(r.mv - r.m) / r.l;
+    __nv_bfloat162 *od = reinterpret_cast<__nv_bfloat162 *>(a.out + row * Q8_D + 4 * (threadIdx.x & 31));
+    od[0] = __floats2bfloat162_rn(r.o.x * f, r.o.y * f);
+    od[1] = __floats2bfloat162_rn(r.o.z * f, r.o.w * f);
+}
+
+// Equal contiguous shares of n items (fewer than 2^31; the list's length is
+// bounded on the host, so that positions are 32-bit).
+struct Split {
+    uint32_t base, rem;
+    __device__ Split(uint32_t n, uint32_t parts) : base(n / parts), rem(n - n / parts * parts) {}
+    __device__ uint32_t start(uint32_t i) const { return i * base + min(i, rem); }
+    __device__ uint32_t owner(uint32_t x) const {
+        const uint32_t cut = rem * (base + 1);
+        return x < cut ? x / (base + 1) : rem + (x - cut) / base;
+    }
+};
+
 template <int G, int FMT>
 __global__ void __launch_bounds__(NT, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const Args a) {
@@ -189,25 +288,33 @@ __global__ void __launch_bounds__(NT, 1)
     uint32_t *cum = reinterpret_cast<uint32_t *>(smem + OFF_CUM);
     int *ctx_s = reinterpret_cast<int *>(smem + off_ctx(a.batch));
     uint32_t *wsum = reinterpret_cast<uint32_t *>(smem + OFF_WSUM);
+    int *piece_pair = reinterpret_cast<int *>(smem + OFF_PIECE);
+    volatile int *todo = reinterpret_cast<volatile int *>(smem + OFF_TODO);
+    int4 *span = reinterpret_cast<int4 *>(smem + OFF_SPAN);
+    // The warps' first pieces.
+    float *stash = a.stash ? reinterpret_cast<float *>(smem + off_stash(a.batch))
+                           : a.ws_piece + (int64_t)blockIdx.x * NW * kPiece<G>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + OFF_BAR) + warp * ST;
     uint8_t *ring = smem + warp * ST * STAGE_BYTES;
-    uint8_t *ring_sc = smem + OFF_SC + warp * ST * 2 * KT;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NW * ST; ++i) mbar_init(reinterpret_cast<uint64_t *>(smem + OFF_BAR) + i, 1);
         fence_mbar_init();
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
+        todo[2] = 0;
     }
     if (threadIdx.x < Q8_D / 16) *reinterpret_cast<uint4 *>(smem + OFF_ZERO + 16 * threadIdx.x) = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x < 2 * NW) piece_pair[threadIdx.x] = -1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // Context lengths and the exclusive prefix sum of the tile counts (per kv head).
+    // Context lengths, their maximum, and the exclusive prefix sum of the tile
+    // counts (per kv head).
     {
         const int per = (a.batch + NT - 1) / NT;
         const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
-        uint32_t run = 0;
+        uint32_t run = 0, top = 0;
         for (int b = b0; b < b1; ++b) {
             int ctx = __ldg(a.ctx_lens + b);
             if (ctx < 0 || ctx > a.ctx_limit) {
@@ -215,7 +322,9 @@ __global__ void __launch_bounds__(NT, 1)
                 ctx = ctx < 0 ? 0 : a.ctx_limit;
             }
             ctx_s[b] = ctx;
-            run += (uint32_t)((ctx + KT - 1) / KT);
+            const uint32_t nt = (uint32_t)((ctx + KT - 1) / KT);
+            run += nt;
+            top = max(top, nt);
         }
         uint32_t x = run;
 #pragma unroll
@@ -223,7 +332,11 @@ __global__ void __launch_bounds__(NT, 1)
             const uint32_t y = __shfl_up_sync(FULL, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) wsum[warp] = x;
+        top = __reduce_max_sync(FULL, top);
+        if (lane == 31) {
+            wsum[warp] = x;
+            wsum[NW + warp] = top;
+        }
         __syncthreads();
         uint32_t excl = x - run;
         for (int w = 0; w < warp; ++w) excl += wsum[w];
@@ -244,170 +357,195 @@ __global__ void __launch_bounds__(NT, 1)
         for (int j = threadIdx.x; j < a.Hq * Q8_D / 8; j += NT) o[j] = make_uint4(0, 0, 0, 0);
     }
 
-    // This worker's range.  Workers are numbered across the CTAs first, so a
-    // short list spreads over the SMs.
-    const long long total = (long long)a.Hkv * cum[a.batch];
-    const int workers = (int)gridDim.x * NW, me = warp * (int)gridDim.x + (int)blockIdx.x;
-    const long long base = total / workers, rem = total % workers;
-    auto start_of = [&](int w) -> long long { return (long long)w * base + min((long long)w, rem); };
-    auto owner_of = [&](long long x) -> int {
-        const long long cut = rem * (base + 1);
-        return (int)(x < cut ? x / (base + 1) : rem + (x - cut) / base);
-    };
-    const long long x_begin = start_of(me), x_end = start_of(me + 1);
-    if (x_begin >= x_end) return;
+    // The CTAs that work, and this one's range; then this warp's.
+    const uint32_t total = (uint32_t)a.Hkv * cum[a.batch];
+    uint32_t nt_max = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) nt_max = max(nt_max, wsum[NW + w]);
+    const uint32_t least = max(kMinTilesPerCta, (nt_max + kMaxParts - 1) / kMaxParts);
+    const uint32_t ctas = min(gridDim.x, (total + least - 1) / least), cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const Split by_cta(total, ctas);
+    const uint32_t c_begin = by_cta.start(cta), c_end = by_cta.start(cta + 1);
+    const Split by_warp(c_end - c_begin, NW);
+    const uint32_t x_begin = c_begin + by_warp.start(warp), x_end = c_begin + by_warp.start(warp + 1);
 
-    // ---- producer side: the tile at `ip` is issued next, its block ids are in
-    // `blk` (lane 0: the first box, lane 1: the second when boxes have 16 rows).
-    const uint64_t pol = policy_evict_first();
-    Pos ip = locate(a, sh, x_begin);
-    long long ix = x_begin;
-    const int nbox = KT / a.box_rows;
-    auto fetch = [&](const Pos &p) -> int {
-        const int key = p.t * KT + (lane < nbox ? lane : 0) * a.box_rows;
-        return key < ctx_s[p.b] ? __ldg(a.block_tables + (int64_t)p.b * a.max_blocks + key / a.block_size) : -1;
-    };
-    int blk = fetch(ip);
-    auto issue = [&](int stage) {
-        const int live = ctx_s[ip.b] - ip.t * KT;  // keys of the tile
-        const int n = min(nbox, (live + a.box_rows - 1) / a.box_rows);
-        const int blk1 = __shfl_sync(FULL, blk, 1);
-        if (lane == 0) {
-            uint8_t *st = ring + stage * STAGE_BYTES, *sc = ring_sc + stage * 2 * KT;
-            uint32_t bytes = 0;
-            for (int i = 0; i < n; ++i) {
-                const int id = i ? blk1 : blk;
-                bytes += 2 * a.box_rows * Q8_D + (id >= 0 && id < a.num_blocks ? 2 * a.box_rows : 0);
+    if (x_begin < x_end) {
+        // ---- producer side: the tile at `ip` is issued next.  Lane i stands for its
+        // key i; `blk` is the block that holds it.
+        const uint64_t pol = policy_evict_first();
+        Pos p = locate(a, sh, x_begin), ip = p;
+        uint32_t ix = x_begin;
+        const bool two = a.box_rows < KT;  // boxes of 16 keys: lane 16 issues the second
+        auto fetch = [&](const Pos &q) -> int {
+            const int key = q.t * KT + (two ? lane & 16 : 0);
+            return key < ctx_s[q.b]
+                       ? __ldg(a.block_tables + (int64_t)q.b * a.max_blocks + (int)((uint32_t)key / (uint32_t)a.block_size))
+                       : -1;
+        };
+        int blk = fetch(ip);
+        // The scale bytes of the tile being consumed and of the one behind it
+        // (tile n's are loaded when its copy is issued, ST tiles ahead).
+        uint32_t k_byte[ST], v_byte[ST];
+        auto issue = [&](int stage, uint32_t &kb, uint32_t &vb) {
+            const int key = ip.t * KT + lane, ctx = ctx_s[ip.b];
+            const bool good = blk >= 0 && blk < a.num_blocks;
+            const int off = (int)((uint32_t)key % (uint32_t)a.block_size);
+            // An invalid block reads as zeros: TMA fills rows out of range.
+            const int64_t row = good ? ((int64_t)blk * a.Hkv + ip.g) * a.block_size + off : -2LL * KT;
+            kb = vb = 127;
+            if (good && key < ctx) {
+                kb = __ldg(a.k_scale + row);
+                vb = __ldg(a.v_scale + row);
             }
-            // Expected before any copy is issued.
-            mbar_arrive_expect_tx(&bar[stage], bytes);
-            for (int i = 0; i < n; ++i) {
-                const int id = i ? blk1 : blk, key = ip.t * KT + i * a.box_rows;
-                const bool good = id >= 0 && id < a.num_blocks;
+            uint8_t *kd = ring + stage * STAGE_BYTES + lane * Q8_D;
+            if (lane == 0) {  // expected before any copy is issued
+                const int boxes = two && key + 16 < ctx ? 2 : 1;
+                mbar_arrive_expect_tx(&bar[stage], (uint32_t)(boxes * 2 * a.box_rows * Q8_D));
+            }
+            if (two) __syncwarp();
+            if (lane == 0 || (two && lane == 16 && key < ctx)) {
                 if (!good && a.checked)
                     record_error(a.err, PA_DEV_BAD_BLOCK, (long long)ip.b * a.max_blocks + key / a.block_size);
-                // An invalid block reads as zeros: TMA fills rows out of range.
-                const int64_t row = good ? ((int64_t)id * a.Hkv + ip.g) * a.block_size + key % a.block_size
-                                         : -2LL * a.box_rows;
-                uint8_t *kd = st + i * a.box_rows * Q8_D;
                 tma_load_2d(kd, &tmk, 0, (int)row, &bar[stage], pol);
                 tma_load_2d(kd + TILE_BYTES, &tmv, 0, (int)row, &bar[stage], pol);
-                if (good) {
-                    bulk_load(sc + i * a.box_rows, a.k_scale + row, (uint32_t)a.box_rows, &bar[stage]);
-                    bulk_load(sc + KT + i * a.box_rows, a.v_scale + row, (uint32_t)a.box_rows, &bar[stage]);
-                } else {
-                    for (int j = 0; j < a.box_rows; j += 16) {
-                        *reinterpret_cast<uint4 *>(sc + i * a.box_rows + j) = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(sc + KT + i * a.box_rows + j) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();  // a later copy overwrites these bytes
+            }
+            __syncwarp();
+            if (++ix < x_end) {
+                advance(a, sh, ip);
+                blk = fetch(ip);
+            }
+        };
+        int issued = 0;
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+            if (ix < x_end) issue(issued++, k_byte[i], v_byte[i]);
+        // While the first tiles travel: the pairs at the range's ends, if they
+        // span CTAs (a range inside one pair counts it once).
+        if (threadIdx.x < 2) {
+            const Pos e = threadIdx.x == 0 ? p : locate(a, sh, c_end - 1);
+            const uint32_t x0 = (threadIdx.x == 0 ? c_begin : c_end - 1) - (uint32_t)e.t, x1 = x0 + (uint32_t)e.nt - 1;
+            int4 sp = make_int4(-1, 0, 0, 0);
+            if ((x0 < c_begin || x1 >= c_end) && (threadIdx.x == 0 || x0 > c_begin)) {
+                sp.x = e.b * a.Hkv + e.g;
+                sp.y = (int)by_cta.owner(x0);
+                sp.z = (int)by_cta.owner(x1) - sp.y + 1;
+            }
+            span[threadIdx.x] = sp;
+        }
+
+        // ---- consumer side.  Fragment coordinates (m16n8k16): g4 = lane / 4 is a
+        // key (Q.K) or a dim (P.V) row, t4 = lane % 4; columns 2*t4, 2*t4+1 are the
+        // heads of the accumulators, column g4 the head of a B fragment.
+        const int g4 = lane >> 2, t4 = lane & 3, r8 = lane & 7, mi = lane >> 3;
+        const uint32_t zero_row = smem_addr(smem + OFF_ZERO);
+        const bool h0 = 2 * t4 < G, h1 = 2 * t4 + 1 < G;  // this lane's two heads exist
+        uint32_t x = x_begin;
+        int n = 0;  // tiles consumed
+        bool ok = true;
+        while (ok && x < x_end) {
+            const int take = (int)min((uint32_t)(p.nt - p.t), x_end - x);
+            const int ctx = ctx_s[p.b];
+            // q: chunk c's registers hold dims 16c + 4*t4 .. +3 of head g4.
+            uint32_t qb[8][2];
+            float qs0, qs1;
+            {
+                uint2 w[8];
+                uint32_t mx = 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    w[c] = make_uint2(0, 0);
+                    if (g4 < G)
+                        w[c] = __ldg(reinterpret_cast<const uint2 *>(a.q + (int64_t)p.b * a.q_row_stride +
+                                                                     ((int64_t)p.g * G + g4) * Q8_D + 16 * c + 4 * t4));
+                    // Finite magnitudes order as their bits, NaN and infinity above.
+                    mx = max(max(mx, w[c].x & 0x7fffu), max((w[c].x >> 16) & 0x7fffu,
+                             max(w[c].y & 0x7fffu, (w[c].y >> 16) & 0x7fffu)));
                 }
+                mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+                mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+                // 2^-e brings the largest magnitude to [1, 2) ([2, 4) at the top of the range).
+                const int e = min(max((int)(mx >> 7), 1), 253) - 127;
+                const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    qb[c][0] = pack_f16(bf16lo(w[c].x) * f, bf16hi(w[c].x) * f);
+                    qb[c][1] = pack_f16(bf16lo(w[c].y) * f, bf16hi(w[c].y) * f);
+                }
+                // The factor of heads 2*t4, 2*t4+1 (head h is held by lanes 4h..4h+3).
+                const float s = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
+                qs0 = __shfl_sync(FULL, s, 8 * t4);
+                qs1 = __shfl_sync(FULL, s, 8 * t4 + 4);
             }
-        }
-        __syncwarp();
-        if (++ix < x_end) {
-            advance(a, sh, ip);
-            blk = fetch(ip);
-        }
-    };
-    int issued = 0;
-    for (; issued < ST && ix < x_end; ++issued) issue(issued);
+            float o[8][4];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+            float m0 = -INFINITY, m1 = -INFINITY, mv0 = -INFINITY, mv1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-    // ---- consumer side.  Fragment coordinates (m16n8k16): g4 = lane / 4 is a
-    // key (Q.K) or a dim (P.V) row, t4 = lane % 4; columns 2*t4, 2*t4+1 are the
-    // heads of the accumulators, column g4 the head of a B fragment.
-    const int g4 = lane >> 2, t4 = lane & 3, r8 = lane & 7, mi = lane >> 3;
-    const uint32_t zero_row = smem_addr(smem + OFF_ZERO);
-    const bool h0 = 2 * t4 < G, h1 = 2 * t4 + 1 < G;  // this lane's two heads exist
-    Pos p = locate(a, sh, x_begin);
-    long long x = x_begin;
-    int n = 0;  // tiles consumed
-    while (x < x_end) {
-        const int take = (int)min((long long)(p.nt - p.t), x_end - x);
-        const int ctx = ctx_s[p.b];
-        const int64_t bh0 = (int64_t)p.b * a.Hq + (int64_t)p.g * G;
-        // q: chunk c's registers hold dims 16c + 4*t4 .. +3 of head g4.
-        uint32_t qb[8][2];
-        float qs0, qs1;
-        {
-            uint2 w[8];
-            uint32_t mx = 0;
+            for (int i = 0; i < take; ++i, ++n) {
+                const int stage = n % ST;
+                if (!mbar_wait(&bar[stage], (n / ST) & 1)) {
+                    if (lane == 0) record_error(a.err, PA_DEV_TIMEOUT, 500 + warp);
+                    // Let the copies already issued land before shared memory goes away.
+                    for (int j = n + 1; j < issued; ++j) (void)mbar_wait(&bar[j % ST], (j / ST) & 1);
+                    ok = false;
+                    break;
+                }
+                const uint32_t ks = smem_addr(ring + stage * STAGE_BYTES), vs = ks + TILE_BYTES;
+                const int nvalid = min(KT, ctx - (p.t + i) * KT);
+                // Lane j holds key j's scale, and the exponent of its value's.
+                const float k_sc = q8_scale(k_byte[0]);
+                const float v_ex = v_byte[0] == 255 ? NAN : (float)((int)v_byte[0] - 127);
+                // ---- S^T = K.Q^T, 16 keys per MMA; the two chains are independent
+                float s[NG][4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                w[c] = make_uint2(0, 0);
-                if (g4 < G)
-                    w[c] = __ldg(reinterpret_cast<const uint2 *>(a.q + (int64_t)p.b * a.q_row_stride +
-                                                                 ((int64_t)p.g * G + g4) * Q8_D + 16 * c + 4 * t4));
-                // Finite magnitudes order as their bits, NaN and infinity above.
-                mx = max(max(mx, w[c].x & 0x7fffu), max((w[c].x >> 16) & 0x7fffu, max(w[c].y & 0x7fffu, (w[c].y >> 16) & 0x7fffu)));
-            }
-            mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
-            mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
-            // 2^-e brings the largest magnitude to [1, 2) ([2, 4) at the top of the range).
-            const int e = min(max((int)(mx >> 7), 1), 253) - 127;
-            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                qb[c][0] = pack_f16(bf16lo(w[c].x) * f, bf16hi(w[c].x) * f);
-                qb[c][1] = pack_f16(bf16lo(w[c].y) * f, bf16hi(w[c].y) * f);
-            }
-            // The factor of heads 2*t4, 2*t4+1 (head h is held by lanes 4h..4h+3).
-            const float s = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
-            qs0 = __shfl_sync(FULL, s, 8 * t4);
-            qs1 = __shfl_sync(FULL, s, 8 * t4 + 4);
-        }
-        float o[8][4];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, mv0 = -INFINITY, mv1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-
-        for (int i = 0; i < take; ++i, ++n) {
-            const int stage = n % ST;
-            if (!mbar_wait(&bar[stage], (n / ST) & 1)) {
-                if (lane == 0) record_error(a.err, PA_DEV_TIMEOUT, 500 + warp);
-                // Let the copies already issued land before shared memory goes away.
-                for (int j = n + 1; j < issued; ++j) (void)mbar_wait(&bar[j % ST], (j / ST) & 1);
-                return;
-            }
-            const uint32_t ks = smem_addr(ring + stage * STAGE_BYTES), vs = ks + TILE_BYTES;
-            const uint32_t scs = smem_addr(ring_sc + stage * 2 * KT);
-            const int nvalid = min(KT, ctx - (p.t + i) * KT);
-#pragma unroll
-            for (int grp = 0; grp < KT / 16; ++grp) {
-                if (grp * 16 >= nvalid) break;
-                // ---- S^T = K.Q^T for 16 keys
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
-                const uint32_t krow = ks + (uint32_t)(grp * 16 + (mi & 1) * 8 + r8) * Q8_D;
+                for (int u = 0; u < NG; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
 #pragma unroll
                 for (int c = 0; c < 8; c += 2) {
-                    uint32_t r[4], a0, a1, a2, a3;
-                    ldsm_x4(krow + (uint32_t)(((c + (mi >> 1)) ^ r8) << 4), r);
-                    q8_to_f16<FMT>(r[0], a0, a2);
-                    q8_to_f16<FMT>(r[1], a1, a3);
-                    mma16816(s, a0, a1, a2, a3, qb[c][0], qb[c][1]);
-                    q8_to_f16<FMT>(r[2], a0, a2);
-                    q8_to_f16<FMT>(r[3], a1, a3);
-                    mma16816(s, a0, a1, a2, a3, qb[c + 1][0], qb[c + 1][1]);
+#pragma unroll
+                    for (int u = 0; u < NG; ++u) {
+                        uint32_t r[4], a0, a1, a2, a3;
+                        ldsm_x4(ks + (uint32_t)(u * 16 + (mi & 1) * 8 + r8) * Q8_D + (uint32_t)(((c + (mi >> 1)) ^ r8) << 4), r);
+                        q8_to_f16<FMT>(r[0], a0, a2);
+                        q8_to_f16<FMT>(r[1], a1, a3);
+                        mma16816(s[u], a0, a1, a2, a3, qb[c][0], qb[c][1]);
+                        q8_to_f16<FMT>(r[2], a0, a2);
+                        q8_to_f16<FMT>(r[3], a1, a3);
+                        mma16816(s[u], a0, a1, a2, a3, qb[c + 1][0], qb[c + 1][1]);
+                    }
                 }
-                // ---- scores and weights of keys key0 (s[0], s[1]) and key0 + 8
-                const int key0 = grp * 16 + g4, key1 = key0 + 8;
-                const float k0 = q8_scale(ld_shared_u8(scs + key0)), k1 = q8_scale(ld_shared_u8(scs + key1));
-                const uint32_t e0 = ld_shared_u8(scs + KT + key0), e1 = ld_shared_u8(scs + KT + key1);
-                const float v0 = e0 == 255 ? NAN : (float)((int)e0 - 127), v1 = e1 == 255 ? NAN : (float)((int)e1 - 127);
-                const bool ok0 = key0 < nvalid, ok1 = key1 < nvalid;
-                float xx[4], yy[4];
-                xx[0] = ok0 ? s[0] * k0 * qs0 : -INFINITY;
-                xx[1] = ok0 ? s[1] * k0 * qs1 : -INFINITY;
-                xx[2] = ok1 ? s[2] * k1 * qs0 : -INFINITY;
-                xx[3] = ok1 ? s[3] * k1 * qs1 : -INFINITY;
-                yy[0] = ok0 ? xx[0] + v0 : -INFINITY;
-                yy[1] = ok0 ? xx[1] + v0 : -INFINITY;
-                yy[2] = ok1 ? xx[2] + v1 : -INFINITY;
-                yy[3] = ok1 ? xx[3] + v1 : -INFINITY;
-                float tx0 = fmaxf(xx[0], xx[2]), tx1 = fmaxf(xx[1], xx[3]);
-                float ty0 = fmaxf(yy[0], yy[2]), ty1 = fmaxf(yy[1], yy[3]);
-                const bool move = (h0 && (tx0 > m0 + kLazyRescale || ty0 > mv0 + (kWeightTop + kLazyRescale))) ||
-                                  (h1 && (tx1 > m1 + kLazyRescale || ty1 > mv1 + (kWeightTop + kLazyRescale)));
+                // ---- scores x and weighted exponents y of keys 16u + g4 (elements 0, 1)
+                // and 16u + g4 + 8 (2, 3), heads 2*t4 (0, 2) and 2*t4 + 1 (1, 3)
+                float xx[NG][4], yy[NG][4];
+#pragma unroll
+                for (int u = 0; u < NG; ++u) {
+                    const int key0 = u * 16 + g4, key1 = key0 + 8;
+                    const float k0 = __shfl_sync(FULL, k_sc, key0), k1 = __shfl_sync(FULL, k_sc, key1);
+                    const float v0 = __shfl_sync(FULL, v_ex, key0), v1 = __shfl_sync(FULL, v_ex, key1);
+                    xx[u][0] = s[u][0] * k0 * qs0;
+                    xx[u][1] = s[u][1] * k0 * qs1;
+                    xx[u][2] = s[u][2] * k1 * qs0;
+                    xx[u][3] = s[u][3] * k1 * qs1;
+                    yy[u][0] = xx[u][0] + v0;
+                    yy[u][1] = xx[u][1] + v0;
+                    yy[u][2] = xx[u][2] + v1;
+                    yy[u][3] = xx[u][3] + v1;
+                    if (nvalid < KT) {  // the context's last tile
+                        if (key0 >= nvalid) xx[u][0] = xx[u][1] = yy[u][0] = yy[u][1] = -INFINITY;
+                        if (key1 >= nvalid) xx[u][2] = xx[u][3] = yy[u][2] = yy[u][3] = -INFINITY;
+                    }
+                }
+                float tx0 = -INFINITY, tx1 = -INFINITY, ty0 = -INFINITY, ty1 = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < NG; ++u) {
+                    tx0 = fmaxf(tx0, fmaxf(xx[u][0], xx[u][2]));
+                    tx1 = fmaxf(tx1, fmaxf(xx[u][1], xx[u][3]));
+                    ty0 = fmaxf(ty0, fmaxf(yy[u][0], yy[u][2]));
+                    ty1 = fmaxf(ty1, fmaxf(yy[u][1], yy[u][3]));
+                }
+                const bool move =
+                    (h0 && (tx0 > m0 + kLazyRescale || ty0 > mv0 + (kWeightTop + kLazyRescale))) ||
+                    (h1 && (tx1 > m1 + kLazyRescale || ty1 > mv1 + (kWeightTop + kLazyRescale)));
                 if (__any_sync(FULL, move)) {
 #pragma unroll
                     for (int d = 4; d <= 16; d <<= 1) {
@@ -435,108 +573,169 @@ __global__ void __launch_bounds__(NT, 1)
                 // A head with nothing finite yet keeps the reference 0 (its weights are 0 or NaN).
                 const float um0 = m0 == -INFINITY ? 0.f : m0, um1 = m1 == -INFINITY ? 0.f : m1;
                 const float uv0 = mv0 == -INFINITY ? 0.f : mv0, uv1 = mv1 == -INFINITY ? 0.f : mv1;
-                l0 += fast_exp2(xx[0] - um0) + fast_exp2(xx[2] - um0);
-                l1 += fast_exp2(xx[1] - um1) + fast_exp2(xx[3] - um1);
-                // ---- O^T += V^T.P'^T; the weights become the B fragment by a transpose
-                const uint32_t b0 = transpose8x8(pack_f16(fast_exp2(yy[0] - uv0), fast_exp2(yy[1] - uv1)));
-                const uint32_t b1 = transpose8x8(pack_f16(fast_exp2(yy[2] - uv0), fast_exp2(yy[3] - uv1)));
-                // Rows past the context may hold anything (NaN codes included) and
-                // 0 * NaN is not 0: their lanes read the row of zeros.
-                const int vk = grp * 16 + (mi & 1) * 8 + r8;
-                const uint32_t vrow = vk < nvalid ? vs + (uint32_t)vk * Q8_D : zero_row;
+                // ---- O^T += V^T.P'^T; the weights become the B fragments by transposes
+                uint32_t b0[NG], b1[NG];
 #pragma unroll
-                for (int c = 0; c < 8; c += 2) {
-                    uint32_t r[4], a0, a1, a2, a3;
-                    ldsm_x4_t(vrow + (uint32_t)(((c + (mi >> 1)) ^ r8) << 4), r);
-                    v_to_f16<FMT>(r[0], a0, a1);
-                    v_to_f16<FMT>(r[1], a2, a3);
-                    mma16816(o[c], a0, a1, a2, a3, b0, b1);
-                    v_to_f16<FMT>(r[2], a0, a1);
-                    v_to_f16<FMT>(r[3], a2, a3);
-                    mma16816(o[c + 1], a0, a1, a2, a3, b0, b1);
+                for (int u = 0; u < NG; ++u) {
+                    l0 += fast_exp2(xx[u][0] - um0) + fast_exp2(xx[u][2] - um0);
+                    l1 += fast_exp2(xx[u][1] - um1) + fast_exp2(xx[u][3] - um1);
+                    b0[u] = transpose8x8(pack_f16(fast_exp2(yy[u][0] - uv0), fast_exp2(yy[u][1] - uv1)));
+                    b1[u] = transpose8x8(pack_f16(fast_exp2(yy[u][2] - uv0), fast_exp2(yy[u][3] - uv1)));
+                }
+#pragma unroll
+                for (int u = 0; u < NG; ++u) {
+                    // Rows past the context may hold anything (NaN codes included) and
+                    // 0 * NaN is not 0: their lanes read the row of zeros.
+                    const int vk = u * 16 + (mi & 1) * 8 + r8;
+                    const uint32_t vrow = vk < nvalid ? vs + (uint32_t)vk * Q8_D : zero_row;
+#pragma unroll
+                    for (int c = 0; c < 8; c += 2) {
+                        uint32_t r[4], a0, a1, a2, a3;
+                        ldsm_x4_t(vrow + (uint32_t)(((c + (mi >> 1)) ^ r8) << 4), r);
+                        v_to_f16<FMT>(r[0], a0, a1);
+                        v_to_f16<FMT>(r[1], a2, a3);
+                        mma16816(o[c], a0, a1, a2, a3, b0[u], b1[u]);
+                        v_to_f16<FMT>(r[2], a0, a1);
+                        v_to_f16<FMT>(r[3], a2, a3);
+                        mma16816(o[c + 1], a0, a1, a2, a3, b0[u], b1[u]);
+                    }
+                }
+                __syncwarp();  // every lane has read the stage
+#pragma unroll
+                for (int j = 1; j < ST; ++j) {
+                    k_byte[j - 1] = k_byte[j];
+                    v_byte[j - 1] = v_byte[j];
+                }
+                if (ix < x_end) {
+                    issue(stage, k_byte[ST - 1], v_byte[ST - 1]);
+                    ++issued;
                 }
             }
-            __syncwarp();  // every lane has read the stage
-            if (ix < x_end) {
-                issue(stage);
-                ++issued;
+            if (!ok) break;
+            // ---- segment end.  This lane holds dims 16c + 2*g4, +1 of heads 2*t4, 2*t4+1.
+#pragma unroll
+            for (int d = 4; d <= 16; d <<= 1) {
+                l0 += __shfl_xor_sync(FULL, l0, d);
+                l1 += __shfl_xor_sync(FULL, l1, d);
+            }
+            const bool last = x + take == x_end;
+            if (p.t == 0 && take == p.nt) {
+                const float f0 = fast_exp2(mv0 - m0) / l0, f1 = fast_exp2(mv1 - m1) / l1;
+                __nv_bfloat16 *dst = a.out + ((int64_t)p.b * a.Hq + (int64_t)p.g * G + 2 * t4) * Q8_D + 2 * g4;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    if (h0) *reinterpret_cast<__nv_bfloat162 *>(dst + 16 * c) = __floats2bfloat162_rn(o[c][0] * f0, o[c][2] * f0);
+                    if (h1) *reinterpret_cast<__nv_bfloat162 *>(dst + Q8_D + 16 * c) = __floats2bfloat162_rn(o[c][1] * f1, o[c][3] * f1);
+                }
+            } else {
+                // A piece of the pair: only a range's first and last segments can be.
+                float *piece = last ? reinterpret_cast<float *>(ring)
+                                    : stash + warp * kPiece<G>;
+                float *dst = piece + 2 * t4 * Q8_D + 2 * g4;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    if (h0) *reinterpret_cast<float2 *>(dst + 16 * c) = make_float2(o[c][0], o[c][2]);
+                    if (h1) *reinterpret_cast<float2 *>(dst + Q8_D + 16 * c) = make_float2(o[c][1], o[c][3]);
+                }
+                if (g4 == 0) {
+                    float4 *ml = reinterpret_cast<float4 *>(piece + G * Q8_D);
+                    if (h0) ml[2 * t4] = make_float4(m0, mv0, l0, 0.f);
+                    if (h1) ml[2 * t4 + 1] = make_float4(m1, mv1, l1, 0.f);
+                }
+                if (lane == 0) piece_pair[2 * warp + (last ? 1 : 0)] = p.b * a.Hkv + p.g;
+            }
+            x += take;
+            if (x < x_end) {
+                p.t += take - 1;
+                advance(a, sh, p);
             }
         }
-        // ---- segment end.  This lane holds dims 16c + 2*g4, +1 of heads 2*t4, 2*t4+1.
-#pragma unroll
-        for (int d = 4; d <= 16; d <<= 1) {
-            l0 += __shfl_xor_sync(FULL, l0, d);
-            l1 += __shfl_xor_sync(FULL, l1, d);
+        if (!ok && lane == 0) todo[2] = 1;
+    }
+
+    // ---- the CTA's pieces, pair by pair.  Lane i stands for piece i; a pair's
+    // pieces are neighbours, since the warps' ranges follow the list.
+    __syncthreads();
+    if (todo[2]) return;  // a wait ran out: the call's result is void
+    auto first_tile = [&](int pair, uint32_t &nt) -> uint32_t {
+        const int b = pair / a.Hkv;
+        nt = cum[b + 1] - cum[b];
+        return (uint32_t)a.Hkv * cum[b] + (uint32_t)(pair - b * a.Hkv) * nt;
+    };
+    auto part_of = [&](uint32_t c, uint32_t x0) -> float * {
+        return a.ws_part + ((int64_t)2 * c + (x0 > by_cta.start(c) ? 1 : 0)) * kPiece<G>;
+    };
+    {
+        const int pair = lane < 2 * NW ? piece_pair[lane] : -1;
+        const float *piece = (lane & 1) ? reinterpret_cast<const float *>(smem + (lane >> 1) * ST * STAGE_BYTES)
+                                        : stash + (lane >> 1) * kPiece<G>;
+        const unsigned valid = __ballot_sync(FULL, pair >= 0);
+        const unsigned before = valid & ((1u << lane) - 1);
+        const int prev = __shfl_sync(FULL, pair, before ? 31 - __clz(before) : 0);
+        const unsigned heads = __ballot_sync(FULL, pair >= 0 && (!before || prev != pair));
+        for (int item = warp; item < __popc(heads) * G; item += NW) {
+            const int h = item % G;
+            unsigned rest = heads;
+            for (int k = item / G; k > 0; --k) rest &= rest - 1;
+            const int i0 = __ffs(rest) - 1;  // the pair's first piece
+            rest &= rest - 1;
+            const unsigned mask = valid & ~((1u << i0) - 1) & (rest ? (1u << (__ffs(rest) - 1)) - 1 : FULL);
+            const int pr = __shfl_sync(FULL, pair, i0);
+            const Merged r = merge_pieces<G, false>(piece, mask, h);
+            uint32_t nt;
+            const uint32_t x0 = first_tile(pr, nt);
+            if (x0 >= c_begin && x0 + nt <= c_end) {
+                write_out(a, r, (int64_t)(pr / a.Hkv) * a.Hq + (int64_t)(pr % a.Hkv) * G + h);
+            } else {
+                float *part = part_of(cta, x0);
+                *reinterpret_cast<float4 *>(part + h * Q8_D + 4 * lane) = r.o;
+                if (lane == 0) *reinterpret_cast<float4 *>(part + G * Q8_D + 4 * h) = make_float4(r.m, r.mv, r.l, 0.f);
+            }
         }
-        if (p.t == 0 && take == p.nt) {
-            const float f0 = fast_exp2(mv0 - m0) / l0, f1 = fast_exp2(mv1 - m1) / l1;
-            __nv_bfloat16 *dst = a.out + (bh0 + 2 * t4) * Q8_D + 2 * g4;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if (h0) *reinterpret_cast<__nv_bfloat162 *>(dst + 16 * c) = __floats2bfloat162_rn(o[c][0] * f0, o[c][2] * f0);
-                if (h1) *reinterpret_cast<__nv_bfloat162 *>(dst + Q8_D + 16 * c) = __floats2bfloat162_rn(o[c][1] * f1, o[c][3] * f1);
-            }
-        } else {
-            // A part of the pair: only a range's first and last segments can be.
-            const int slot = 2 * me + (x == x_begin ? 0 : 1);
-            float *dst = a.ws_o + ((int64_t)slot * G + 2 * t4) * Q8_D + 2 * g4;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if (h0) *reinterpret_cast<float2 *>(dst + 16 * c) = make_float2(o[c][0], o[c][2]);
-                if (h1) *reinterpret_cast<float2 *>(dst + Q8_D + 16 * c) = make_float2(o[c][1], o[c][3]);
-            }
-            if (g4 == 0) {
-                if (h0) a.ws_ml[(int64_t)slot * G + 2 * t4] = make_float4(m0, mv0, l0, 0.f);
-                if (h1) a.ws_ml[(int64_t)slot * G + 2 * t4 + 1] = make_float4(m1, mv1, l1, 0.f);
-            }
-            const long long x0 = x - p.t;  // the pair's first tile
-            const int w0 = owner_of(x0), w1 = owner_of(x0 + p.nt - 1);
+    }
+    // ---- pairs that span CTAs: at most the first and the last of the range.
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        const int4 sp = span[threadIdx.x];
+        int mine = -1;
+        if (sp.x >= 0) {
             __threadfence();
-            __syncwarp();
-            int arrived = 0;
-            if (lane == 0) arrived = atomicAdd(&a.ws_cnt[w0], 1);
-            arrived = __shfl_sync(FULL, arrived, 0);
-            if (arrived == w1 - w0) {  // the last part: merge them all, in order
+            if (atomicAdd(&a.ws_cnt[sp.y], 1) == sp.z - 1) {
                 __threadfence();
-                const int s0 = 2 * w0 + (x0 == start_of(w0) ? 0 : 1);
-                for (int h = 0; h < G; ++h) {
-                    float M = -INFINITY, MV = -INFINITY;
-                    for (int w = w0 + lane; w <= w1; w += 32) {
-                        const float4 ml = __ldcg(a.ws_ml + (int64_t)(w == w0 ? s0 : 2 * w) * G + h);
-                        M = fmaxf(M, ml.x);
-                        MV = fmaxf(MV, ml.y);
-                    }
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        M = fmaxf(M, __shfl_xor_sync(FULL, M, d));
-                        MV = fmaxf(MV, __shfl_xor_sync(FULL, MV, d));
-                    }
-                    float L = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int w = w0; w <= w1; ++w) {
-                        const int64_t row = (int64_t)(w == w0 ? s0 : 2 * w) * G + h;
-                        const float4 ml = __ldcg(a.ws_ml + row);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.ws_o + row * Q8_D) + lane);
-                        const float fv = fast_exp2(ml.y - MV);
-                        L = fmaf(ml.z, fast_exp2(ml.x - M), L);
-                        acc.x = fmaf(v.x, fv, acc.x);
-                        acc.y = fmaf(v.y, fv, acc.y);
-                        acc.z = fmaf(v.z, fv, acc.z);
-                        acc.w = fmaf(v.w, fv, acc.w);
-                    }
-                    const float f = fast_exp2(MV - M) / L;
-                    __nv_bfloat162 *od = reinterpret_cast<__nv_bfloat162 *>(a.out + (bh0 + h) * Q8_D + 4 * lane);
-                    od[0] = __floats2bfloat162_rn(acc.x * f, acc.y * f);
-                    od[1] = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-                }
-                if (lane == 0) a.ws_cnt[w0] = 0;  // ready for the next call
+                a.ws_cnt[sp.y] = 0;  // ready for the next call
+                mine = sp.x;
             }
         }
-        x += take;
-        if (x < x_end) {
-            p.t += take - 1;
-            advance(a, sh, p);
+        todo[threadIdx.x] = mine;
+    }
+    __syncthreads();
+    for (int item = warp; item < 2 * G; item += NW) {
+        const int pr = todo[item / G], h = item % G;
+        if (pr < 0) continue;
+        uint32_t nt;
+        const uint32_t x0 = first_tile(pr, nt);
+        const uint32_t c0 = (uint32_t)span[item / G].y, c1 = c0 + (uint32_t)span[item / G].z - 1;
+        Merged r;
+        for (uint32_t c = c0; c <= c1; c += 32) {
+            const float *part = part_of(min(c + lane, c1), x0);
+            const uint32_t left = c1 - c + 1;
+            const Merged q = merge_pieces<G, true>(part, left >= 32 ? FULL : (1u << left) - 1, h);
+            if (c == c0) {
+                r = q;
+                continue;
+            }
+            const float m = fmaxf(r.m, q.m), mv = fmaxf(r.mv, q.mv);
+            const float fr = r.m == -INFINITY ? 1.f : fast_exp2(r.m - m), fq = q.m == -INFINITY ? 1.f : fast_exp2(q.m - m);
+            const float gr = r.mv == -INFINITY ? 1.f : fast_exp2(r.mv - mv), gq = q.mv == -INFINITY ? 1.f : fast_exp2(q.mv - mv);
+            r.l = r.l * fr + q.l * fq;
+            r.o.x = r.o.x * gr + q.o.x * gq;
+            r.o.y = r.o.y * gr + q.o.y * gq;
+            r.o.z = r.o.z * gr + q.o.z * gq;
+            r.o.w = r.o.w * gr + q.o.w * gq;
+            r.m = m;
+            r.mv = mv;
         }
+        write_out(a, r, (int64_t)(pr / a.Hkv) * a.Hq + (int64_t)(pr % a.Hkv) * G + h);
     }
 }
 
@@ -549,12 +748,16 @@ pa_status launch(const Args &a, const CUtensorMap &tk, const CUtensorMap &tv, in
     const int gi = (G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3) + 4 * FMT;
     if (dev >= 0 && dev < 64 && !g_attr_done[dev][gi].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<G, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)smem_bytes(kMaxBatch));
+                                                   (int)kMaxSmem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_q8_kernel)");
         g_attr_done[dev][gi].store(1, std::memory_order_release);
     }
-    return launch_pdl(decode_q8_kernel<G, FMT>, dim3((unsigned)grid), dim3(NT), smem_bytes(a.batch), st,
-                      "decode_q8_kernel", tk, tv, a);
+    Args b = a;
+    size_t smem = smem_bytes(a.batch);
+    constexpr size_t kStash = (size_t)NW * kPiece<G> * 4;
+    b.stash = smem + kStash <= kMaxSmem;
+    if (b.stash) smem += kStash;
+    return launch_pdl(decode_q8_kernel<G, FMT>, dim3((unsigned)grid), dim3(NT), smem, st, "decode_q8_kernel", tk, tv, b);
 }
 
 template <int FMT>
@@ -605,8 +808,8 @@ pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const voi
     if (max_blocks_per_seq <= 0) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq must be positive");
     if ((int64_t)max_blocks_per_seq * block_size > 0x7fffffffLL - KT)
         return fail(PA_ERR_UNSUPPORTED, "table too large for 32-bit positions");
-    // The per-head tile prefix sum is 32-bit: batch * ceil(max_blocks * B / 32) must fit.
-    if ((int64_t)batch * (((int64_t)max_blocks_per_seq * block_size + KT - 1) / KT) >= 0x7fffffffLL)
+    // The list of tiles is numbered in 32 bits: batch * Hkv * ceil(max_blocks * B / 32) must fit.
+    if ((int64_t)batch * (((int64_t)max_blocks_per_seq * block_size + KT - 1) / KT) >= 0x7fffffffLL / num_kv_heads)
         return fail(PA_ERR_UNSUPPORTED, "batch x block-table capacity too large (%d x %lld tokens)", batch,
                     (long long)max_blocks_per_seq * block_size);
     if (q_row_stride < (int64_t)num_q_heads * Q8_D || q_row_stride % 8)
@@ -648,8 +851,8 @@ pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const voi
     A.scale_log2 = softmax_scale * 1.4426950408889634f;
     A.ctx_limit = max_blocks_per_seq * block_size;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    A.ws_o = reinterpret_cast<float *>(ws + W.o_off);
-    A.ws_ml = reinterpret_cast<float4 *>(ws + W.ml_off);
+    A.ws_piece = reinterpret_cast<float *>(ws);
+    A.ws_part = reinterpret_cast<float *>(ws + W.part_off);
     A.ws_cnt = reinterpret_cast<int *>(ws + W.cnt_off);
     A.err = device_error_ptr();
     A.checked = checked_mode() ? 1 : 0;

@@ -54,9 +54,18 @@ __device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float 
     return r;
 }
 
+// Two pairs of INT8 codes of a word as f16x2, exactly: the byte (offset by 128)
+// is put under the exponent of 1024 and 1152 is subtracted, one permute and one
+// packed subtract per pair.  A selector names its pair's bytes (0x4140: 0 and 1).
+template <uint32_t LO, uint32_t HI>
+__device__ __forceinline__ void q8_int8_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, LO), b = __byte_perm(u, 0x64646464u, HI);
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+}
+
 // The codes in bytes 0, 1 (lo) and 2, 3 (hi) of a word as f16x2, exactly.
-// For int8 the byte (offset by 128) is put under the exponent of 1024 and
-// 1152 is subtracted: one permute and one packed add per pair.
 template <int FMT>
 __device__ __forceinline__ void q8_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     if (FMT == PA_Q8_E4M3) {
@@ -67,10 +76,7 @@ __device__ __forceinline__ void q8_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi
             : "=r"(lo), "=r"(hi)
             : "r"(w));
     } else {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
-        asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+        q8_int8_to_f16<0x4140, 0x4342>(w, lo, hi);
     }
 }
 
