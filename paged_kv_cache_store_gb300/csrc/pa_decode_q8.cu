@@ -13,7 +13,12 @@
 //    4 KB each, 128-byte swizzled) and the warp waits on its own mbarriers;
 //    the scale bytes, one per lane, are plain loads a ring ahead.  No barrier between warps while they stream:
 //    with half the bytes per key of a bf16 pool, the merges and hand-overs of
-//    a CTA-wide pipeline would weigh twice as much.
+//    a CTA-wide pipeline would weigh twice as much.  Eight warps with two tiles
+//    each (128 KB in flight per SM) fill the bandwidth; twelve only lengthen
+//    the memory's queues, whose service then differs more between warps (long
+//    contexts, E4M3: 93 us instead of 85).  Chunks of the last eighth, taken
+//    from a counter by the warps that are done, even out the ends to 5 us but
+//    cost more in pieces and merges than that (95 us).
 //  * Q.K and P.V run as mma.sync m16n8k16 (fp16 in, fp32 accumulate) with the
 //    KEYS (Q.K) and the VALUE DIMS (P.V) as the M side and the G <= 8 query
 //    heads as N = 8: half the MMAs of the layout with heads as M.  The codes
@@ -47,7 +52,7 @@ namespace pa {
 namespace {
 
 constexpr int KT = 32;            // keys per tile
-constexpr int NW = 12;            // warps per CTA
+constexpr int NW = 8;             // warps per CTA
 constexpr int ST = 2;             // tiles in a warp's ring
 constexpr int NT = NW * 32;
 constexpr int NG = KT / 16;       // MMA key groups of a tile
@@ -72,30 +77,27 @@ static_assert(OFF_BAR % 16 == 0 && OFF_ZERO % 16 == 0 && NW * 8 <= 128, "shared-
 static_assert(NW <= 16, "a warp's lanes hold the CTA's pieces");
 __host__ __device__ constexpr size_t off_ctx(int batch) { return OFF_CUM + 4 * (size_t)(batch + 1); }
 __host__ __device__ constexpr size_t off_stash(int batch) { return (off_ctx(batch) + 4 * (size_t)batch + 15) / 16 * 16; }
-constexpr size_t smem_bytes(int batch) { return off_stash(batch) + 1024; }
-constexpr size_t kMaxSmem = 232448;
-static_assert(smem_bytes(kMaxBatch) <= kMaxSmem, "shared memory budget");
 
-// A piece of a pair: o [G][128] fp32, then (m, mv, l, -) [G].  Of each warp,
-// the last piece waits in the warp's own ring (free by then) and the first, if
-// it is another, in a stash: shared memory where it fits beside the batch's
-// tables (G = 8 does not, nor do the largest batches of G = 4), else the
-// workspace.  A CTA's parts of pairs that span CTAs are in the workspace.
+// A piece of a pair: o [G][128] fp32, then (m, mv, l, -) [G].  The pieces of the
+// warps' ranges (first and last segment) are stashed in shared memory, a CTA's
+// parts of pairs that span CTAs in the workspace.
 template <int G>
 constexpr int kPiece = G * (Q8_D + 4);  // floats
-static_assert(kPiece<8> * 4 <= ST * STAGE_BYTES, "a piece fits a ring");
+constexpr size_t smem_bytes(int batch, int G) {
+    return off_stash(batch) + (size_t)2 * NW * G * (Q8_D + 4) * 4 + 1024;
+}
+constexpr size_t kMaxSmem = 232448;
+static_assert(smem_bytes(kMaxBatch, 8) <= kMaxSmem, "shared memory budget");
 
-// Workspace: the warps' first pieces [kMaxGrid][NW], the CTAs' parts [kMaxGrid][2]
-// (of the pair at the range's start, of a later one), the arrival counters
-// [kMaxGrid] (of the pair that spans CTAs and starts in this one's range).
+// Workspace: the CTAs' parts [kMaxGrid][2] (of the pair at the range's start, of
+// its last one), then the arrival counters [kMaxGrid] (of the pair that spans
+// CTAs and starts in this one's range).
 struct WsLayout {
-    size_t part_off, cnt_off, total;
+    size_t cnt_off, total;
 };
 WsLayout ws_layout(int G) {
-    const size_t piece = (size_t)G * (Q8_D + 4) * 4;
     WsLayout w;
-    w.part_off = piece * kMaxGrid * NW;
-    w.cnt_off = w.part_off + piece * kMaxGrid * 2;
+    w.cnt_off = (size_t)2 * kMaxGrid * G * (Q8_D + 4) * 4;
     w.total = w.cnt_off + (size_t)kMaxGrid * 4;
     return w;
 }
@@ -110,9 +112,8 @@ struct Args {
     int32_t max_blocks, batch, Hq, Hkv, block_size, box_rows, num_blocks;
     float scale_log2;
     int32_t ctx_limit;
-    float *ws_piece, *ws_part;
+    float *ws_part;
     int *ws_cnt;
-    int32_t stash;  // first pieces are stashed in shared memory
     DevError *err;
     int32_t checked;
 };
@@ -199,7 +200,7 @@ __device__ __forceinline__ void advance(const Args &a, const Shared &s, Pos &p) 
 
 // Merges pieces of one pair and head: lane i of `mask` holds piece i's address.
 // Every lane returns dims 4*lane .. +3 and the totals.  FAR: the pieces are
-// other CTAs' (read from L2); else this CTA's, in shared memory or not.
+// CTAs' parts (read from L2); else in this CTA's shared memory.
 struct Merged {
     float m, mv, l;
     float4 o;
@@ -215,7 +216,7 @@ __device__ __forceinline__ Merged merge_pieces(const float *piece, unsigned mask
     float4 ml = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
     if (mask >> lane & 1) ml = ld_piece<FAR>(piece + G * Q8_D + 4 * h);
     const unsigned long long at = reinterpret_cast<unsigned long long>(piece + h * Q8_D);
-    constexpr int PF = 4;  // pieces whose loads are in flight
+    constexpr int PF = FAR ? 8 : 4;  // pieces whose loads are in flight
     float4 v[PF];
     int from[PF];
     auto load = [&](unsigned left) -> unsigned {
@@ -291,9 +292,7 @@ __global__ void __launch_bounds__(NT, 1)
     int *piece_pair = reinterpret_cast<int *>(smem + OFF_PIECE);
     volatile int *todo = reinterpret_cast<volatile int *>(smem + OFF_TODO);
     int4 *span = reinterpret_cast<int4 *>(smem + OFF_SPAN);
-    // The warps' first pieces.
-    float *stash = a.stash ? reinterpret_cast<float *>(smem + off_stash(a.batch))
-                           : a.ws_piece + (int64_t)blockIdx.x * NW * kPiece<G>;
+    float *stash = reinterpret_cast<float *>(smem + off_stash(a.batch));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + OFF_BAR) + warp * ST;
     uint8_t *ring = smem + warp * ST * STAGE_BYTES;
@@ -377,22 +376,23 @@ __global__ void __launch_bounds__(NT, 1)
         Pos p = locate(a, sh, x_begin), ip = p;
         uint32_t ix = x_begin;
         const bool two = a.box_rows < KT;  // boxes of 16 keys: lane 16 issues the second
-        auto fetch = [&](const Pos &q) -> int {
-            const int key = q.t * KT + (two ? lane & 16 : 0);
-            return key < ctx_s[q.b]
-                       ? __ldg(a.block_tables + (int64_t)q.b * a.max_blocks + (int)((uint32_t)key / (uint32_t)a.block_size))
-                       : -1;
+        const int sub16 = two ? lane & 16 : 0;
+        // The logical block and the offset in it of this lane's box, kept up tile
+        // by tile: divisions only here (a pair starts at block 0).
+        int lb = (int)((uint32_t)(ip.t * KT + sub16) / (uint32_t)a.block_size);
+        int off = ip.t * KT + sub16 - lb * a.block_size;
+        auto fetch = [&]() -> int {
+            return ip.t * KT + sub16 < ctx_s[ip.b] ? __ldg(a.block_tables + (int64_t)ip.b * a.max_blocks + lb) : -1;
         };
-        int blk = fetch(ip);
+        int blk = fetch();
         // The scale bytes of the tile being consumed and of the one behind it
         // (tile n's are loaded when its copy is issued, ST tiles ahead).
         uint32_t k_byte[ST], v_byte[ST];
         auto issue = [&](int stage, uint32_t &kb, uint32_t &vb) {
             const int key = ip.t * KT + lane, ctx = ctx_s[ip.b];
             const bool good = blk >= 0 && blk < a.num_blocks;
-            const int off = (int)((uint32_t)key % (uint32_t)a.block_size);
             // An invalid block reads as zeros: TMA fills rows out of range.
-            const int64_t row = good ? ((int64_t)blk * a.Hkv + ip.g) * a.block_size + off : -2LL * KT;
+            const int64_t row = good ? ((int64_t)blk * a.Hkv + ip.g) * a.block_size + off + (lane - sub16) : -2LL * KT;
             kb = vb = 127;
             if (good && key < ctx) {
                 kb = __ldg(a.k_scale + row);
@@ -406,14 +406,23 @@ __global__ void __launch_bounds__(NT, 1)
             if (two) __syncwarp();
             if (lane == 0 || (two && lane == 16 && key < ctx)) {
                 if (!good && a.checked)
-                    record_error(a.err, PA_DEV_BAD_BLOCK, (long long)ip.b * a.max_blocks + key / a.block_size);
+                    record_error(a.err, PA_DEV_BAD_BLOCK, (long long)ip.b * a.max_blocks + lb);
                 tma_load_2d(kd, &tmk, 0, (int)row, &bar[stage], pol);
                 tma_load_2d(kd + TILE_BYTES, &tmv, 0, (int)row, &bar[stage], pol);
             }
             __syncwarp();
             if (++ix < x_end) {
                 advance(a, sh, ip);
-                blk = fetch(ip);
+                off += KT;
+                while (off >= a.block_size) {
+                    off -= a.block_size;
+                    ++lb;
+                }
+                if (ip.t == 0) {  // another pair
+                    lb = sub16 < a.block_size ? 0 : 1;
+                    off = sub16 - lb * a.block_size;
+                }
+                blk = fetch();
             }
         };
         int issued = 0;
@@ -440,6 +449,17 @@ __global__ void __launch_bounds__(NT, 1)
         const int g4 = lane >> 2, t4 = lane & 3, r8 = lane & 7, mi = lane >> 3;
         const uint32_t zero_row = smem_addr(smem + OFF_ZERO);
         const bool h0 = 2 * t4 < G, h1 = 2 * t4 + 1 < G;  // this lane's two heads exist
+        uint2 qw[8];
+        auto load_q = [&](const Pos &q) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                qw[c] = make_uint2(0, 0);
+                if (g4 < G)
+                    qw[c] = __ldg(reinterpret_cast<const uint2 *>(a.q + (int64_t)q.b * a.q_row_stride +
+                                                                  ((int64_t)q.g * G + g4) * Q8_D + 16 * c + 4 * t4));
+            }
+        };
+        load_q(p);
         uint32_t x = x_begin;
         int n = 0;  // tiles consumed
         bool ok = true;
@@ -450,18 +470,12 @@ __global__ void __launch_bounds__(NT, 1)
             uint32_t qb[8][2];
             float qs0, qs1;
             {
-                uint2 w[8];
                 uint32_t mx = 0;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    w[c] = make_uint2(0, 0);
-                    if (g4 < G)
-                        w[c] = __ldg(reinterpret_cast<const uint2 *>(a.q + (int64_t)p.b * a.q_row_stride +
-                                                                     ((int64_t)p.g * G + g4) * Q8_D + 16 * c + 4 * t4));
+                for (int c = 0; c < 8; ++c)
                     // Finite magnitudes order as their bits, NaN and infinity above.
-                    mx = max(max(mx, w[c].x & 0x7fffu), max((w[c].x >> 16) & 0x7fffu,
-                             max(w[c].y & 0x7fffu, (w[c].y >> 16) & 0x7fffu)));
-                }
+                    mx = max(max(mx, qw[c].x & 0x7fffu), max((qw[c].x >> 16) & 0x7fffu,
+                             max(qw[c].y & 0x7fffu, (qw[c].y >> 16) & 0x7fffu)));
                 mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
                 mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
                 // 2^-e brings the largest magnitude to [1, 2) ([2, 4) at the top of the range).
@@ -469,13 +483,20 @@ __global__ void __launch_bounds__(NT, 1)
                 const float f = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    qb[c][0] = pack_f16(bf16lo(w[c].x) * f, bf16hi(w[c].x) * f);
-                    qb[c][1] = pack_f16(bf16lo(w[c].y) * f, bf16hi(w[c].y) * f);
+                    qb[c][0] = pack_f16(bf16lo(qw[c].x) * f, bf16hi(qw[c].x) * f);
+                    qb[c][1] = pack_f16(bf16lo(qw[c].y) * f, bf16hi(qw[c].y) * f);
                 }
                 // The factor of heads 2*t4, 2*t4+1 (head h is held by lanes 4h..4h+3).
                 const float s = __uint_as_float((uint32_t)(127 + e) << 23) * a.scale_log2;
                 qs0 = __shfl_sync(FULL, s, 8 * t4);
                 qs1 = __shfl_sync(FULL, s, 8 * t4 + 4);
+            }
+            // The next segment's q travels while this one streams.
+            Pos pn = p;
+            pn.t = p.nt - 1;
+            if (x + take < x_end) {
+                advance(a, sh, pn);
+                load_q(pn);
             }
             float o[8][4];
 #pragma unroll
@@ -618,7 +639,6 @@ __global__ void __launch_bounds__(NT, 1)
                 l0 += __shfl_xor_sync(FULL, l0, d);
                 l1 += __shfl_xor_sync(FULL, l1, d);
             }
-            const bool last = x + take == x_end;
             if (p.t == 0 && take == p.nt) {
                 const float f0 = fast_exp2(mv0 - m0) / l0, f1 = fast_exp2(mv1 - m1) / l1;
                 __nv_bfloat16 *dst = a.out + ((int64_t)p.b * a.Hq + (int64_t)p.g * G + 2 * t4) * Q8_D + 2 * g4;
@@ -629,8 +649,8 @@ __global__ void __launch_bounds__(NT, 1)
                 }
             } else {
                 // A piece of the pair: only a range's first and last segments can be.
-                float *piece = last ? reinterpret_cast<float *>(ring)
-                                    : stash + warp * kPiece<G>;
+                const int slot = 2 * warp + (x == x_begin ? 0 : 1);
+                float *piece = stash + slot * kPiece<G>;
                 float *dst = piece + 2 * t4 * Q8_D + 2 * g4;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -642,13 +662,10 @@ __global__ void __launch_bounds__(NT, 1)
                     if (h0) ml[2 * t4] = make_float4(m0, mv0, l0, 0.f);
                     if (h1) ml[2 * t4 + 1] = make_float4(m1, mv1, l1, 0.f);
                 }
-                if (lane == 0) piece_pair[2 * warp + (last ? 1 : 0)] = p.b * a.Hkv + p.g;
+                if (lane == 0) piece_pair[slot] = p.b * a.Hkv + p.g;
             }
             x += take;
-            if (x < x_end) {
-                p.t += take - 1;
-                advance(a, sh, p);
-            }
+            p = pn;
         }
         if (!ok && lane == 0) todo[2] = 1;
     }
@@ -667,8 +684,7 @@ __global__ void __launch_bounds__(NT, 1)
     };
     {
         const int pair = lane < 2 * NW ? piece_pair[lane] : -1;
-        const float *piece = (lane & 1) ? reinterpret_cast<const float *>(smem + (lane >> 1) * ST * STAGE_BYTES)
-                                        : stash + (lane >> 1) * kPiece<G>;
+        const float *piece = stash + lane * kPiece<G>;
         const unsigned valid = __ballot_sync(FULL, pair >= 0);
         const unsigned before = valid & ((1u << lane) - 1);
         const int prev = __shfl_sync(FULL, pair, before ? 31 - __clz(before) : 0);
@@ -752,12 +768,8 @@ pa_status launch(const Args &a, const CUtensorMap &tk, const CUtensorMap &tv, in
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_q8_kernel)");
         g_attr_done[dev][gi].store(1, std::memory_order_release);
     }
-    Args b = a;
-    size_t smem = smem_bytes(a.batch);
-    constexpr size_t kStash = (size_t)NW * kPiece<G> * 4;
-    b.stash = smem + kStash <= kMaxSmem;
-    if (b.stash) smem += kStash;
-    return launch_pdl(decode_q8_kernel<G, FMT>, dim3((unsigned)grid), dim3(NT), smem, st, "decode_q8_kernel", tk, tv, b);
+    return launch_pdl(decode_q8_kernel<G, FMT>, dim3((unsigned)grid), dim3(NT), smem_bytes(a.batch, G), st,
+                      "decode_q8_kernel", tk, tv, a);
 }
 
 template <int FMT>
@@ -825,7 +837,7 @@ pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const voi
                     workspace ? workspace_bytes : (size_t)0);
     if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
 
-    const int box = block_size % 32 ? 16 : 32;  // a TMA box stays inside a block
+    const int box = block_size % KT ? 16 : KT;  // a TMA box stays inside a block
     const int64_t rows = (int64_t)num_blocks * num_kv_heads * block_size;
     CUtensorMap tk, tv;
     st = encode_row_map_u8(&tk, k_cache, rows, box);
@@ -851,8 +863,7 @@ pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const voi
     A.scale_log2 = softmax_scale * 1.4426950408889634f;
     A.ctx_limit = max_blocks_per_seq * block_size;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    A.ws_piece = reinterpret_cast<float *>(ws);
-    A.ws_part = reinterpret_cast<float *>(ws + W.part_off);
+    A.ws_part = reinterpret_cast<float *>(ws);
     A.ws_cnt = reinterpret_cast<int *>(ws + W.cnt_off);
     A.err = device_error_ptr();
     A.checked = checked_mode() ? 1 : 0;
