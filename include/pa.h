@@ -497,7 +497,7 @@ PA_API pa_status pa_load_kvcache_q8(void *key, int64_t key_row_stride, void *val
  *               for pa_decode (every call leaves it ready for the next; not
  *               shared by calls that may run at the same time).
  * Other arguments and limits as pa_decode, and batch * num_kv_heads *
- * max_blocks_per_seq * block_size / 32 < 2^31.
+ * max_blocks_per_seq * block_size < 2^35.
  */
 PA_API size_t pa_decode_q8_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim);
 PA_API pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const void *k_cache,

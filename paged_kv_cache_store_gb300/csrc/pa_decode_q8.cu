@@ -6,9 +6,10 @@
 //
 // How (GB300 design):
 //  * The work is a flat list of 32-key tiles ordered (sequence, kv head, tile),
-//    cut into equal contiguous ranges, one per CTA of a persistent grid (one
-//    CTA per SM), and each CTA's range into equal contiguous ranges of its
-//    WARPS.  A warp is its own producer: its lane 0 issues the TMA copies of
+//    cut into contiguous ranges of equal cost, one per CTA of a persistent grid
+//    (one CTA per SM), and each CTA's range likewise between its WARPS.  A pair
+//    costs half a tile on top of its tiles (measured: 0.7 us where a tile takes
+//    a warp 1.5 us).  A warp is its own producer: its lane 0 issues the TMA copies of
 //    its next tiles into the warp's own ring of shared memory (K and V codes,
 //    4 KB each, 128-byte swizzled) and the warp waits on its own mbarriers;
 //    the scale bytes, one per lane, are plain loads a ring ahead.  No barrier between warps while they stream:
@@ -68,14 +69,15 @@ constexpr unsigned FULL = 0xffffffffu;
 
 constexpr int OFF_BAR = NW * ST * STAGE_BYTES;        // mbarriers [NW][ST]
 constexpr int OFF_ZERO = OFF_BAR + NW * ST * 8;       // a row of zeros
-constexpr int OFF_WSUM = OFF_ZERO + Q8_D;             // scan scratch [NW], then a maximum [NW]
+constexpr int OFF_WSUM = OFF_ZERO + Q8_D;             // scan scratch [3][NW]
 constexpr int OFF_PIECE = OFF_WSUM + 128;             // pair of each warp's two pieces [2 * NW] (-1: none)
 constexpr int OFF_TODO = OFF_PIECE + 128;             // pairs this CTA merges across CTAs [2], abort flag
 constexpr int OFF_SPAN = OFF_TODO + 16;               // the range's end pairs: {pair or -1, first CTA, CTAs, -} [2]
 constexpr int OFF_CUM = OFF_SPAN + 32;                // tile prefix sum [batch + 1]
-static_assert(OFF_BAR % 16 == 0 && OFF_ZERO % 16 == 0 && NW * 8 <= 128, "shared-memory layout");
+static_assert(OFF_BAR % 16 == 0 && OFF_ZERO % 16 == 0 && NW * 12 <= 128, "shared-memory layout");
 static_assert(NW <= 16, "a warp's lanes hold the CTA's pieces");
-__host__ __device__ constexpr size_t off_ctx(int batch) { return OFF_CUM + 4 * (size_t)(batch + 1); }
+__host__ __device__ constexpr size_t off_cost(int batch) { return OFF_CUM + 4 * (size_t)(batch + 1); }  // cost prefix sum [batch + 1]
+__host__ __device__ constexpr size_t off_ctx(int batch) { return off_cost(batch) + 4 * (size_t)(batch + 1); }
 __host__ __device__ constexpr size_t off_stash(int batch) { return (off_ctx(batch) + 4 * (size_t)batch + 15) / 16 * 16; }
 
 // A piece of a pair: o [G][128] fp32, then (m, mv, l, -) [G].  The pieces of the
@@ -167,25 +169,46 @@ struct Pos {
     int b, g, t, nt;
 };
 
+// Per sequence, in shared memory: prefix sums (per kv head) of the tiles and of
+// the costs, and the context lengths.  Cost unit: half a tile; pair (b, g) has
+// 2 * nt + 1 units, of which the first is its own and tile t begins at 1 + 2t.
 struct Shared {
-    const uint32_t *cum;
+    const uint32_t *cum, *cost;
     const int *ctx;
 };
 
-__device__ __forceinline__ Pos locate(const Args &a, const Shared &s, uint32_t x) {
+// The first tile that begins at unit x or later: its position (b = batch past
+// the end) and its index in the list.
+__device__ __forceinline__ Pos locate(const Args &a, const Shared &s, uint32_t x, uint32_t &tile) {
+    Pos p = {a.batch, 0, 0, 0};
+    tile = (uint32_t)a.Hkv * s.cum[a.batch];
+    if (x >= (uint32_t)a.Hkv * s.cost[a.batch]) return p;
     const uint32_t qv = x / (uint32_t)a.Hkv;
     int lo = 0, hi = a.batch - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (s.cum[mid] <= qv) lo = mid; else hi = mid - 1;
+        if (s.cost[mid] <= qv) lo = mid; else hi = mid - 1;
     }
-    Pos p;
     p.b = lo;
     p.nt = (int)(s.cum[lo + 1] - s.cum[lo]);
-    const uint32_t off = x - (uint32_t)a.Hkv * s.cum[lo];
-    p.g = (int)(off / (uint32_t)p.nt);
-    p.t = (int)(off - (uint32_t)p.g * p.nt);
+    const uint32_t off = x - (uint32_t)a.Hkv * s.cost[lo], units = 2 * p.nt + 1;
+    p.g = (int)(off / units);
+    p.t = (int)(off - (uint32_t)p.g * units) / 2;
+    tile = (uint32_t)a.Hkv * s.cum[lo] + (uint32_t)(p.g * p.nt + p.t);
+    if (p.t == p.nt) {  // the pair's last tile begins before x
+        p.t = 0;
+        if (++p.g == a.Hkv) {
+            p.g = 0;
+            do ++p.b; while (p.b < a.batch && s.ctx[p.b] == 0);
+            p.nt = p.b < a.batch ? (s.ctx[p.b] + KT - 1) / KT : 0;
+        }
+    }
     return p;
+}
+
+// The unit at which tile t of a pair begins.
+__device__ __forceinline__ uint32_t unit_of(const Args &a, const Shared &s, const Pos &p, uint32_t t) {
+    return (uint32_t)a.Hkv * s.cost[p.b] + (uint32_t)p.g * (2 * p.nt + 1) + 1 + 2 * t;
 }
 
 // The next tile's position (not past the list's end: the caller counts).
@@ -269,8 +292,8 @@ __device__ __forceinline__ void write_out(const Args &a, const Merged &r, int64_
     od[1] = __floats2bfloat162_rn(r.o.z * f, r.o.w * f);
 }
 
-// Equal contiguous shares of n items (fewer than 2^31; the list's length is
-// bounded on the host, so that positions are 32-bit).
+// Equal contiguous shares of n items (the list's length is bounded on the host,
+// so that units fit 32 bits).
 struct Split {
     uint32_t base, rem;
     __device__ Split(uint32_t n, uint32_t parts) : base(n / parts), rem(n - n / parts * parts) {}
@@ -287,6 +310,7 @@ __global__ void __launch_bounds__(NT, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint32_t *cum = reinterpret_cast<uint32_t *>(smem + OFF_CUM);
+    uint32_t *cost = reinterpret_cast<uint32_t *>(smem + off_cost(a.batch));
     int *ctx_s = reinterpret_cast<int *>(smem + off_ctx(a.batch));
     uint32_t *wsum = reinterpret_cast<uint32_t *>(smem + OFF_WSUM);
     int *piece_pair = reinterpret_cast<int *>(smem + OFF_PIECE);
@@ -313,7 +337,7 @@ __global__ void __launch_bounds__(NT, 1)
     {
         const int per = (a.batch + NT - 1) / NT;
         const int b0 = min(a.batch, (int)threadIdx.x * per), b1 = min(a.batch, b0 + per);
-        uint32_t run = 0, top = 0;
+        uint32_t run = 0, live = 0, top = 0;  // tiles, sequences that have some, most tiles
         for (int b = b0; b < b1; ++b) {
             int ctx = __ldg(a.ctx_lens + b);
             if (ctx < 0 || ctx > a.ctx_limit) {
@@ -323,31 +347,45 @@ __global__ void __launch_bounds__(NT, 1)
             ctx_s[b] = ctx;
             const uint32_t nt = (uint32_t)((ctx + KT - 1) / KT);
             run += nt;
+            live += nt ? 1u : 0u;
             top = max(top, nt);
         }
-        uint32_t x = run;
+        uint32_t x = run, z = live;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(FULL, x, o);
-            if (lane >= o) x += y;
+            const uint32_t y = __shfl_up_sync(FULL, x, o), w = __shfl_up_sync(FULL, z, o);
+            if (lane >= o) {
+                x += y;
+                z += w;
+            }
         }
         top = __reduce_max_sync(FULL, top);
         if (lane == 31) {
             wsum[warp] = x;
             wsum[NW + warp] = top;
+            wsum[2 * NW + warp] = z;
         }
         __syncthreads();
-        uint32_t excl = x - run;
-        for (int w = 0; w < warp; ++w) excl += wsum[w];
+        uint32_t excl = x - run, seqs = z - live;
+        for (int w = 0; w < warp; ++w) {
+            excl += wsum[w];
+            seqs += wsum[2 * NW + w];
+        }
         for (int b = b0; b < b1; ++b) {
             cum[b] = excl;
-            excl += (uint32_t)((ctx_s[b] + KT - 1) / KT);
+            cost[b] = 2 * excl + seqs;
+            const uint32_t nt = (uint32_t)((ctx_s[b] + KT - 1) / KT);
+            excl += nt;
+            seqs += nt ? 1u : 0u;
         }
-        if (threadIdx.x == NT - 1) cum[a.batch] = excl;
+        if (threadIdx.x == NT - 1) {
+            cum[a.batch] = excl;
+            cost[a.batch] = 2 * excl + seqs;
+        }
     }
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Shared sh{cum, ctx_s};
+    const Shared sh{cum, cost, ctx_s};
 
     // Sequences with no context produce zeros.
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -364,16 +402,44 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t least = max(kMinTilesPerCta, (nt_max + kMaxParts - 1) / kMaxParts);
     const uint32_t ctas = min(gridDim.x, (total + least - 1) / least), cta = blockIdx.x;
     if (cta >= ctas) return;
-    const Split by_cta(total, ctas);
-    const uint32_t c_begin = by_cta.start(cta), c_end = by_cta.start(cta + 1);
-    const Split by_warp(c_end - c_begin, NW);
-    const uint32_t x_begin = c_begin + by_warp.start(warp), x_end = c_begin + by_warp.start(warp + 1);
+    const Split by_cta((uint32_t)a.Hkv * cost[a.batch], ctas);
+    const uint32_t cu = by_cta.start(cta), cu_end = by_cta.start(cta + 1);
+    const Split by_warp(cu_end - cu, NW);
+    // Lanes 0 and 1 find the warp's first tile and the one after its last, lanes
+    // 2 and 3 the CTA's.  A range of three units or more holds a tile; a CTA's
+    // has more, a warp's may not.
+    Pos ip;
+    uint32_t x_begin, x_end, c_begin, c_end;
+    {
+        const uint32_t u = lane == 0 ? cu + by_warp.start(warp) : lane == 1 ? cu + by_warp.start(warp + 1) : lane == 2 ? cu : cu_end;
+        uint32_t tile;
+        const Pos e = locate(a, sh, u, tile);
+        x_begin = __shfl_sync(FULL, tile, 0);
+        x_end = __shfl_sync(FULL, tile, 1);
+        c_begin = __shfl_sync(FULL, tile, 2);
+        c_end = __shfl_sync(FULL, tile, 3);
+        ip.b = __shfl_sync(FULL, e.b, 0);
+        ip.g = __shfl_sync(FULL, e.g, 0);
+        ip.t = __shfl_sync(FULL, e.t, 0);
+        ip.nt = __shfl_sync(FULL, e.nt, 0);
+        // The pairs that span CTAs: the one the range begins inside of, and the one
+        // it ends inside of, if that began in this range.
+        if (warp == 0 && (lane == 2 || lane == 3)) {
+            int4 sp = make_int4(-1, 0, 0, 0);
+            if (e.t > 0 && (lane == 2 || tile - (uint32_t)e.t >= c_begin)) {
+                sp.x = e.b * a.Hkv + e.g;
+                sp.y = (int)by_cta.owner(unit_of(a, sh, e, 0));
+                sp.z = (int)by_cta.owner(unit_of(a, sh, e, (uint32_t)e.nt - 1)) - sp.y + 1;
+            }
+            span[lane - 2] = sp;
+        }
+    }
 
     if (x_begin < x_end) {
         // ---- producer side: the tile at `ip` is issued next.  Lane i stands for its
         // key i; `blk` is the block that holds it.
         const uint64_t pol = policy_evict_first();
-        Pos p = locate(a, sh, x_begin), ip = p;
+        Pos p = ip;
         uint32_t ix = x_begin;
         const bool two = a.box_rows < KT;  // boxes of 16 keys: lane 16 issues the second
         const int sub16 = two ? lane & 16 : 0;
@@ -429,19 +495,6 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
         for (int i = 0; i < ST; ++i)
             if (ix < x_end) issue(issued++, k_byte[i], v_byte[i]);
-        // While the first tiles travel: the pairs at the range's ends, if they
-        // span CTAs (a range inside one pair counts it once).
-        if (threadIdx.x < 2) {
-            const Pos e = threadIdx.x == 0 ? p : locate(a, sh, c_end - 1);
-            const uint32_t x0 = (threadIdx.x == 0 ? c_begin : c_end - 1) - (uint32_t)e.t, x1 = x0 + (uint32_t)e.nt - 1;
-            int4 sp = make_int4(-1, 0, 0, 0);
-            if ((x0 < c_begin || x1 >= c_end) && (threadIdx.x == 0 || x0 > c_begin)) {
-                sp.x = e.b * a.Hkv + e.g;
-                sp.y = (int)by_cta.owner(x0);
-                sp.z = (int)by_cta.owner(x1) - sp.y + 1;
-            }
-            span[threadIdx.x] = sp;
-        }
 
         // ---- consumer side.  Fragment coordinates (m16n8k16): g4 = lane / 4 is a
         // key (Q.K) or a dim (P.V) row, t4 = lane % 4; columns 2*t4, 2*t4+1 are the
@@ -679,9 +732,6 @@ __global__ void __launch_bounds__(NT, 1)
         nt = cum[b + 1] - cum[b];
         return (uint32_t)a.Hkv * cum[b] + (uint32_t)(pair - b * a.Hkv) * nt;
     };
-    auto part_of = [&](uint32_t c, uint32_t x0) -> float * {
-        return a.ws_part + ((int64_t)2 * c + (x0 > by_cta.start(c) ? 1 : 0)) * kPiece<G>;
-    };
     {
         const int pair = lane < 2 * NW ? piece_pair[lane] : -1;
         const float *piece = stash + lane * kPiece<G>;
@@ -703,7 +753,7 @@ __global__ void __launch_bounds__(NT, 1)
             if (x0 >= c_begin && x0 + nt <= c_end) {
                 write_out(a, r, (int64_t)(pr / a.Hkv) * a.Hq + (int64_t)(pr % a.Hkv) * G + h);
             } else {
-                float *part = part_of(cta, x0);
+                float *part = a.ws_part + ((int64_t)2 * cta + (x0 > c_begin ? 1 : 0)) * kPiece<G>;
                 *reinterpret_cast<float4 *>(part + h * Q8_D + 4 * lane) = r.o;
                 if (lane == 0) *reinterpret_cast<float4 *>(part + G * Q8_D + 4 * h) = make_float4(r.m, r.mv, r.l, 0.f);
             }
@@ -728,12 +778,17 @@ __global__ void __launch_bounds__(NT, 1)
     for (int item = warp; item < 2 * G; item += NW) {
         const int pr = todo[item / G], h = item % G;
         if (pr < 0) continue;
-        uint32_t nt;
-        const uint32_t x0 = first_tile(pr, nt);
+        // In its first CTA the pair may follow another one; in later ones it is first.
         const uint32_t c0 = (uint32_t)span[item / G].y, c1 = c0 + (uint32_t)span[item / G].z - 1;
+        const int b = pr / a.Hkv;
+        const Pos e = {b, pr - b * a.Hkv, 0, (int)(cum[b + 1] - cum[b])};
+        uint32_t first;
+        locate(a, sh, by_cta.start(c0), first);
+        const uint32_t s0 = 2 * c0 + ((uint32_t)a.Hkv * cum[b] + (uint32_t)(e.g * e.nt) > first ? 1 : 0);
         Merged r;
         for (uint32_t c = c0; c <= c1; c += 32) {
-            const float *part = part_of(min(c + lane, c1), x0);
+            const uint32_t at = min(c + lane, c1);
+            const float *part = a.ws_part + (int64_t)(at == c0 ? s0 : 2 * at) * kPiece<G>;
             const uint32_t left = c1 - c + 1;
             const Merged q = merge_pieces<G, true>(part, left >= 32 ? FULL : (1u << left) - 1, h);
             if (c == c0) {
@@ -820,8 +875,8 @@ pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const voi
     if (max_blocks_per_seq <= 0) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq must be positive");
     if ((int64_t)max_blocks_per_seq * block_size > 0x7fffffffLL - KT)
         return fail(PA_ERR_UNSUPPORTED, "table too large for 32-bit positions");
-    // The list of tiles is numbered in 32 bits: batch * Hkv * ceil(max_blocks * B / 32) must fit.
-    if ((int64_t)batch * (((int64_t)max_blocks_per_seq * block_size + KT - 1) / KT) >= 0x7fffffffLL / num_kv_heads)
+    // The list's units (up to three per tile) are numbered in 32 bits.
+    if ((int64_t)batch * (((int64_t)max_blocks_per_seq * block_size + KT - 1) / KT) >= (1LL << 30) / num_kv_heads)
         return fail(PA_ERR_UNSUPPORTED, "batch x block-table capacity too large (%d x %lld tokens)", batch,
                     (long long)max_blocks_per_seq * block_size);
     if (q_row_stride < (int64_t)num_q_heads * Q8_D || q_row_stride % 8)
