@@ -389,95 +389,112 @@ def kvcache_q8(num_blocks, block_size, num_kv_heads, head_dim=128, dtype=torch.f
 
 
 def _q8_pool(k_cache, v_cache, k_scale, v_scale):
-    """Checks the four tensors of an 8-bit pool; returns its format."""
-    fmt = _Q8_FORMATS.get(k_cache.dtype)
-    if fmt is None or k_cache.dim() != 4:
+    """Checks the four tensors of an 8-bit pool; returns its shape and format."""
+    dtype = k_cache.dtype
+    fmt = _Q8_FORMATS.get(dtype)
+    shape = k_cache.shape
+    if fmt is None or len(shape) != 4:
         raise TypeError("k_cache must be a [num_blocks, Hkv, B, D] tensor of float8_e4m3fn or int8")
-    _need(k_cache, k_cache.dtype, "k_cache")
-    _need(v_cache, k_cache.dtype, "v_cache")
+    _need(v_cache, dtype, "v_cache")
     _need(k_scale, torch.uint8, "k_scale")
     _need(v_scale, torch.uint8, "v_scale")
-    if v_cache.shape != k_cache.shape or not (k_scale.shape == v_scale.shape == k_cache.shape[:3]):
+    if v_cache.shape != shape or not (k_scale.shape == v_scale.shape == shape[:3]):
         raise ValueError("k_cache / v_cache must be [num_blocks, Hkv, B, D] and k_scale / v_scale [num_blocks, Hkv, B]")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
             and v_scale.is_contiguous()):
         raise ValueError("caches and scales must be contiguous")
-    return fmt
+    return shape, fmt
 
 
-class _Launch:
-    """Where a call runs: on the tensors' device (all must share it) and on
-    `stream`, default that device's current stream.  Inside the `with`, both
-    are current, so that what the call allocates belongs to that stream."""
-
-    def __init__(self, stream, first, *others):
-        self.device = first.device
-        for t in others:
-            if t is not None and t.device != self.device:
-                raise ValueError(f"tensors on different devices: {self.device} and {t.device}")
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"stream of {stream.device}, tensors on {self.device}")
-        self.contexts = []
-        if stream is not None:
-            self.contexts.append(torch.cuda.stream(stream))  # also makes its device current
-        elif self.device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(self.device))
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-        return C.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
+def _placed(stream, first, *others):
+    """Where a call runs: on its tensors' device (which all must share) and on
+    `stream`, default that device's current stream.  Returns None when both are
+    current already, else a context in which they are, so that what the call
+    allocates belongs to the stream that it runs on."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    if dev < 0:
+        raise TypeError("tensors must be CUDA tensors")
+    if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError(f"stream of device {stream.device_index}, tensors on {first.device}")
+        return torch.cuda.stream(stream)  # makes its device current as well
+    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _q8_slots(slot_mapping, n=None):
+def _rows(t, name, n, heads, d):
+    """Elements between the rows of a bf16 [n, heads, d] tensor (n None: any),
+    each contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or (n is not None and shape[0] != n):
+        raise ValueError(f"{name} must be [{'N' if n is None else n}, {heads}, {d}], got {list(shape)}")
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (heads > 1 and s1 != d):
+        raise ValueError(f"{name}: each row must be contiguous")
+    return s0 if shape[0] > 1 else heads * d
+
+
+def _slots(slot_mapping, n=None):
     _need(slot_mapping, torch.int32, "slot_mapping")
-    if slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or (n is not None and slot_mapping.numel() != n):
+    if slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or (n is not None and slot_mapping.shape[0] != n):
         raise ValueError("slot_mapping must be contiguous with one entry per token")
+
+
+def _raw_stream():
+    """The current device's current stream (torch's raw getter takes 0.1 us,
+    building a Stream object 3 us)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
 
 
 def store_kvcache_q8(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping, stream=None):
     """Quantise key/value [N, Hkv, 128] (bf16, rows may be strided) into the
     8-bit pool at slot_mapping (int32 [N], negatives skipped)."""
-    fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
-    nb, hkv, B, d = k_cache.shape
-    _need(key, torch.bfloat16, "key")
-    _need(value, torch.bfloat16, "value")
-    if tuple(key.shape[1:]) != (hkv, d) or value.shape != key.shape:
-        raise ValueError(f"key and value must be [N, {hkv}, {d}]")
+    (nb, hkv, B, d), fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
+    ks = _rows(key, "key", None, hkv, d)
     n = key.shape[0]
-    _q8_slots(slot_mapping, n)
-    with _Launch(stream, key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping) as s:
-        _check(lib().pa_store_kvcache_q8(_ptr(key), _row_stride(key, "key"), _ptr(value), _row_stride(value, "value"),
-                                         _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                         _ptr(slot_mapping), n, hkv, d, B, nb, fmt, s), "pa_store_kvcache_q8")
+    vs = _rows(value, "value", n, hkv, d)
+    _slots(slot_mapping, n)
+    ctx = _placed(stream, key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping)
+
+    def call():
+        _check(lib().pa_store_kvcache_q8(key.data_ptr(), ks, value.data_ptr(), vs, k_cache.data_ptr(),
+                                         v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                         slot_mapping.data_ptr(), n, hkv, d, B, nb, fmt, _raw_stream()),
+               "pa_store_kvcache_q8")
+
+    if ctx is None:
+        return call()
+    with ctx:
+        return call()
 
 
 def load_kvcache_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k=None, out_v=None, stream=None):
     """Read rows of the 8-bit pool back: (k, v), bf16 [N, Hkv, 128], the rows of
     slots slot_mapping (int32 [N], may repeat; zeros for negatives).  out_k /
     out_v may be given (rows may be strided)."""
-    fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
-    nb, hkv, B, d = k_cache.shape
-    _q8_slots(slot_mapping)
-    n = slot_mapping.numel()
-    with _Launch(stream, k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k, out_v) as s:
-        if out_k is None:
-            out_k = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device)
-        if out_v is None:
-            out_v = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device)
-        for t, name in ((out_k, "out_k"), (out_v, "out_v")):
-            _need(t, torch.bfloat16, name)
-            if tuple(t.shape) != (n, hkv, d):
-                raise ValueError(f"{name} must be [{n}, {hkv}, {d}]")
-        _check(lib().pa_load_kvcache_q8(_ptr(out_k), _row_stride(out_k, "out_k"), _ptr(out_v),
-                                        _row_stride(out_v, "out_v"), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                        _ptr(v_scale), _ptr(slot_mapping), n, hkv, d, B, nb, fmt, s),
-               "pa_load_kvcache_q8")
-    return out_k, out_v
+    (nb, hkv, B, d), fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
+    _slots(slot_mapping)
+    n = slot_mapping.shape[0]
+    ctx = _placed(stream, k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k, out_v)
+
+    def call():
+        k = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device) if out_k is None else out_k
+        v = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device) if out_v is None else out_v
+        _check(lib().pa_load_kvcache_q8(k.data_ptr(), _rows(k, "out_k", n, hkv, d), v.data_ptr(),
+                                        _rows(v, "out_v", n, hkv, d), k_cache.data_ptr(), v_cache.data_ptr(),
+                                        k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(), n, hkv, d, B,
+                                        nb, fmt, _raw_stream()), "pa_load_kvcache_q8")
+        return k, v
+
+    if ctx is None:
+        return call()
+    with ctx:
+        return call()
 
 
 def decode_q8_workspace(num_q_heads, num_kv_heads, head_dim=128, device="cuda"):
@@ -492,35 +509,40 @@ def decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
     """Paged decode attention over the 8-bit pool.  q [batch, Hq, 128] bf16
     (rows may be strided); block_tables int32 [batch, max_blocks];
     context_lens int32 [batch].  Returns out [batch, Hq, 128] bf16."""
-    fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
-    nb, hkv, B, d = k_cache.shape
-    _need(q, torch.bfloat16, "q")
+    (nb, hkv, B, d), fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
     _need(block_tables, torch.int32, "block_tables")
     _need(context_lens, torch.int32, "context_lens")
-    if q.dim() != 3 or q.shape[2] != d:
+    if q.dim() != 3:
         raise ValueError(f"q must be [batch, Hq, {d}]")
     batch, hq, _ = q.shape
-    if block_tables.dim() != 2 or block_tables.shape[0] != batch or tuple(context_lens.shape) != (batch,):
+    qs = _rows(q, "q", batch, hq, d)
+    if block_tables.dim() != 2 or block_tables.shape[0] != batch or context_lens.shape != (batch,):
         raise ValueError("block_tables must be [batch, max_blocks] and context_lens [batch]")
     if not (block_tables.is_contiguous() and context_lens.is_contiguous()):
         raise ValueError("block_tables and context_lens must be contiguous")
-    if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(d)
-    with _Launch(stream, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace, out) as s:
-        if workspace is None:
-            workspace = decode_q8_workspace(hq, hkv, d, q.device)
-        elif not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        if out is None:
-            out = torch.empty(batch, hq, d, dtype=torch.bfloat16, device=q.device)
+    if out is not None:
         _need(out, torch.bfloat16, "out")
         if out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous and of q's shape")
-        _check(lib().pa_decode_q8(_ptr(out), _ptr(q), _row_stride(q, "q"), _ptr(k_cache), _ptr(v_cache),
-                                  _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
-                                  _ptr(context_lens), batch, hq, hkv, d, B, nb, fmt, float(softmax_scale),
-                                  _ptr(workspace), workspace.numel() * workspace.element_size(), s), "pa_decode_q8")
-    return out
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
+    ctx = _placed(stream, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace, out)
+
+    def call():
+        ws = decode_q8_workspace(hq, hkv, d, q.device) if workspace is None else workspace
+        o = torch.empty(batch, hq, d, dtype=torch.bfloat16, device=q.device) if out is None else out
+        _check(lib().pa_decode_q8(o.data_ptr(), q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
+                                  k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
+                                  block_tables.shape[1], context_lens.data_ptr(), batch, hq, hkv, d, B, nb, fmt,
+                                  scale, ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream()),
+               "pa_decode_q8")
+        return o
+
+    if ctx is None:
+        return call()
+    with ctx:
+        return call()
 
 
 class Logprobs(NamedTuple):
@@ -538,9 +560,8 @@ def logprobs(logits, tokens, top_k=0, temperatures=None, out=None, stream=None):
     `out`, a Logprobs of contiguous tensors, is filled and returned."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("logits must be a bfloat16 or float32 tensor")
-    _need(logits, logits.dtype, "logits")
     _need(tokens, torch.int32, "tokens")
-    if logits.dim() != 2 or tuple(tokens.shape) != (logits.shape[0],):
+    if logits.dim() != 2 or tokens.shape != logits.shape[:1]:
         raise ValueError("logits must be [rows, vocab] and tokens [rows]")
     rows, vocab = logits.shape
     top_k = int(top_k)
@@ -548,30 +569,41 @@ def logprobs(logits, tokens, top_k=0, temperatures=None, out=None, stream=None):
         raise ValueError("rows must be contiguous")
     if temperatures is not None:
         _need(temperatures, torch.float32, "temperatures")
-        if tuple(temperatures.shape) != (rows,) or not temperatures.is_contiguous():
+        if temperatures.shape != (rows,) or not temperatures.is_contiguous():
             raise ValueError("temperatures must be contiguous [rows]")
-    # A lone row's stride does not matter; the library wants it well-formed.
-    stride = logits.stride(0) if rows > 1 else -(-vocab // 8) * 8
-    with _Launch(stream, logits, tokens, temperatures, *(out or ())) as s:
-        if out is None:
-            k = max(top_k, 0)
-            out = Logprobs(*torch.empty(2, rows, dtype=torch.float32, device=logits.device).unbind(0),
-                           torch.empty(rows, k, dtype=torch.int32, device=logits.device) if k else None,
-                           torch.empty(rows, k, dtype=torch.float32, device=logits.device) if k else None)
-        else:
-            for t, dtype, shape, name in ((out[0], torch.float32, (rows,), "logprobs"),
-                                          (out[1], torch.float32, (rows,), "entropy"),
-                                          (out[2], torch.int32, (rows, top_k), "top_ids"),
-                                          (out[3], torch.float32, (rows, top_k), "top_logprobs")):
-                if t is None and top_k == 0 and len(shape) == 2:
-                    continue
-                _need(t, dtype, name)
-                if tuple(t.shape) != shape or not t.is_contiguous():
-                    raise ValueError(f"out.{name} must be contiguous {list(shape)}")
-        _check(lib().pa_logprobs(_ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), _ptr(logits), stride,
-                                 1 if logits.dtype == torch.float32 else 0, _ptr(temperatures), _ptr(tokens), rows,
-                                 vocab, top_k, s), "pa_logprobs")
-    return out
+    if out is not None:
+        for t, dtype, shape, name in ((out[0], torch.float32, (rows,), "logprobs"),
+                                      (out[1], torch.float32, (rows,), "entropy"),
+                                      (out[2], torch.int32, (rows, top_k), "top_ids"),
+                                      (out[3], torch.float32, (rows, top_k), "top_logprobs")):
+            if t is None and top_k == 0 and len(shape) == 2:
+                continue
+            _need(t, dtype, name)
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"out.{name} must be contiguous {list(shape)}")
+    ctx = _placed(stream, logits, tokens, temperatures, *(out or ()))
+
+    def call():
+        r = out
+        if r is None:
+            dev, k = logits.device, max(top_k, 0)
+            r = Logprobs(torch.empty(rows, dtype=torch.float32, device=dev),
+                         torch.empty(rows, dtype=torch.float32, device=dev),
+                         torch.empty(rows, k, dtype=torch.int32, device=dev) if k else None,
+                         torch.empty(rows, k, dtype=torch.float32, device=dev) if k else None)
+        # A lone row's stride does not matter; the library wants it well-formed.
+        stride = logits.stride(0) if rows > 1 else -(-vocab // 8) * 8
+        _check(lib().pa_logprobs(r[0].data_ptr(), r[1].data_ptr(), r[2].data_ptr() if top_k > 0 else None,
+                                 r[3].data_ptr() if top_k > 0 else None, logits.data_ptr(), stride,
+                                 1 if logits.dtype == torch.float32 else 0,
+                                 None if temperatures is None else temperatures.data_ptr(), tokens.data_ptr(), rows,
+                                 vocab, top_k, _raw_stream()), "pa_logprobs")
+        return r
+
+    if ctx is None:
+        return call()
+    with ctx:
+        return call()
 
 
 def set_checked(enabled: bool):

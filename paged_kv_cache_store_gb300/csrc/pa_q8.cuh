@@ -35,9 +35,11 @@ __device__ __forceinline__ float q8_scale(uint32_t s) {
     return __uint_as_float(s == 255 ? 0x7fc00000u : bits);
 }
 
-// Four codes (one word) from four scaled values.
+// Four codes (one word) from two words of bf16 pairs and 2^-e.  The products are
+// exact; the conversion (for INT8: adding 1.5 * 2^23, which leaves the integer
+// in the low bits) is the one rounding.
 template <int FMT>
-__device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t q8_encode4(uint32_t lo, uint32_t hi, float inv) {
     uint32_t r;
     if (FMT == PA_Q8_E4M3) {
         asm("{\n\t.reg .b16 lo, hi;\n\t"
@@ -45,11 +47,12 @@ __device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float 
             "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
             "mov.b32 %0, {lo, hi};\n\t}"
             : "=r"(r)
-            : "f"(a), "f"(b), "f"(c), "f"(d));
+            : "f"(bf16lo(lo) * inv), "f"(bf16hi(lo) * inv), "f"(bf16lo(hi) * inv), "f"(bf16hi(hi) * inv));
     } else {
-        const uint32_t ab = __byte_perm((uint32_t)__float2int_rn(a), (uint32_t)__float2int_rn(b), 0x0040);
-        const uint32_t cd = __byte_perm((uint32_t)__float2int_rn(c), (uint32_t)__float2int_rn(d), 0x0040);
-        r = __byte_perm(ab, cd, 0x5410);
+        constexpr float kMagic = 12582912.f;
+        const uint32_t a = __float_as_uint(fmaf(bf16lo(lo), inv, kMagic)), b = __float_as_uint(fmaf(bf16hi(lo), inv, kMagic));
+        const uint32_t c = __float_as_uint(fmaf(bf16lo(hi), inv, kMagic)), d = __float_as_uint(fmaf(bf16hi(hi), inv, kMagic));
+        r = __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
     }
     return r;
 }
@@ -78,6 +81,39 @@ __device__ __forceinline__ void q8_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi
     } else {
         q8_int8_to_f16<0x4140, 0x4342>(w, lo, hi);
     }
+}
+
+// Four codes of a word as two bf16 pairs, in order, times 2^e (a bf16 pair):
+// exact wherever the value is a normal bf16 number.  INT8: bf16 holds 128 + the
+// low seven bits, and 128 or 256 by the sign bit is subtracted.
+template <int FMT>
+__device__ __forceinline__ uint2 q8_to_bf16(uint32_t w, uint32_t scale) {
+    uint32_t p[2];
+    if (FMT == PA_Q8_E4M3) {
+        uint32_t f[2];
+        q8_to_f16<FMT>(w, f[0], f[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&f[j]));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[j]) : "f"(x.y), "f"(x.x));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t t = __byte_perm(w, 0x43434343u, j ? 0x4342 : 0x4140);
+            asm("sub.bf16x2 %0, %1, %2;" : "=r"(p[j]) : "r"(t & 0xff7fff7fu), "r"(t & 0xff80ff80u));
+        }
+    }
+    uint2 r;
+    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(p[0]), "r"(scale));
+    asm("mul.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(p[1]), "r"(scale));
+    return r;
+}
+
+// 2^(s - 127) as a bf16 pair; NaN for 255.
+__device__ __forceinline__ uint32_t q8_scale_bf16x2(uint32_t s) {
+    const uint32_t h = s == 255 ? 0x7fc0u : s == 0 ? 0x0040u : s << 7;
+    return h | (h << 16);
 }
 
 // Host checks shared by the entry points over an 8-bit pool.

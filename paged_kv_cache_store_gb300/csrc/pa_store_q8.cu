@@ -6,11 +6,14 @@
 // of scattered blocks by TMA measured 7.1-7.3 TB/s this way and 4.7-4.8 TB/s
 // from 128-byte rows a token apart, [num_blocks, block_size, Hkv, 128].)
 //
-// Store: a half-warp takes one (token, K or V, head) row: 16 lanes x 16 bytes
-// of bf16, the row's largest magnitude by four shuffles, then 8 codes a lane.
-// Load: the same units the other way.  Both are pure streams (store: 256 bytes
-// read and 129 written a row; load: 129 and 256), so a half-warp keeps UNITS
-// rows' loads in flight before it works on the first.
+// Store: a half-warp takes up to H heads' rows of one (token, K or V): 16
+// lanes x 16 bytes of bf16 a row, the row's largest magnitude by four shuffles,
+// then 8 codes a lane.  Load: the same the other way.  Both are pure streams
+// (store: 256 bytes read and 129 written a row; load: 129 and 256) that would
+// be bound by instructions if each row found its own slot, block and offset
+// (three divisions; 2.8 TB/s): the unit's rows share them, and the next unit's
+// slot travels while this one's rows do.  H is 8 for calls that fill the GPU
+// with such units, else 2, which spreads short calls over more SMs.
 #include <algorithm>
 
 #include "pa_q8.cuh"
@@ -19,46 +22,45 @@ namespace pa {
 namespace {
 
 constexpr int Q8_THREADS = 256;
-constexpr int UNITS = 4;  // rows in flight per half-warp
 
 struct Q8Rows {
     uint4 *key, *value;             // the bf16 rows (store: read, load: written)
     int64_t key16, value16;         // 16-byte units between tokens
     uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
     const int32_t *slots;
-    uint32_t num_tokens, hkv, block;
+    uint32_t num_tokens, hkv, block, groups;  // groups of H heads
     int64_t num_slots;
     DevError *err;
 };
 
-// Row r of the call: token, K or V, head (heads innermost, as the rows lie).
+// Up to H heads' rows of a token's K or V.
 struct Unit {
-    uint4 *rows;             // the unit's 256 bytes of bf16
-    uint8_t *codes, *scale;  // its codes and scale byte (null: nothing to read or write)
-    bool live;
+    uint4 *rows;             // this lane's 16 bytes of the first row
+    uint8_t *codes, *scale;  // its 8 codes, and the row's scale byte
+    uint32_t n;              // rows
+    bool live;               // a slot of the pool
 };
 
-__device__ __forceinline__ Unit unit_of(const Q8Rows &a, uint64_t r, uint64_t n, int lane16) {
-    Unit u;
-    u.live = r < n;
-    if (!u.live) r = 0;
-    const uint32_t per = 2 * a.hkv;
-    const uint32_t token = n <= 0xffffffffull ? (uint32_t)r / per : (uint32_t)(r / per);
-    const uint32_t rest = (uint32_t)(r - (uint64_t)token * per);
-    const bool is_v = rest >= a.hkv;
-    const uint32_t head = is_v ? rest - a.hkv : rest;
-    u.rows = (is_v ? a.value + token * a.value16 : a.key + token * a.key16) + head * (Q8_D / 8) + lane16;
-    u.codes = u.scale = nullptr;
-    const int32_t slot = __ldg(a.slots + token);
-    if (slot >= 0 && slot < a.num_slots) {
-        const uint32_t blk = (uint32_t)slot / a.block, off = (uint32_t)slot - blk * a.block;
-        const int64_t row = ((int64_t)blk * a.hkv + head) * a.block + off;
-        u.codes = (is_v ? a.v_codes : a.k_codes) + row * Q8_D + 8 * lane16;
-        u.scale = (is_v ? a.v_scales : a.k_scales) + row;
-    } else if (slot >= 0 && u.live && rest == 0 && lane16 == 0) {
-        record_error(a.err, PA_DEV_BAD_SLOT, token);
-    }
-    return u;
+// Unit u: token, K or V, group of heads (innermost).
+__device__ __forceinline__ uint32_t token_of(const Q8Rows &a, uint64_t u) {
+    const uint32_t per = 2 * a.groups;
+    return u <= 0xffffffffull ? (uint32_t)u / per : (uint32_t)(u / per);
+}
+template <uint32_t H>
+__device__ __forceinline__ Unit unit_of(const Q8Rows &a, uint64_t u, uint32_t token, int32_t slot, int lane16) {
+    const uint32_t rest = (uint32_t)(u - (uint64_t)token * (2 * a.groups));
+    const bool is_v = rest >= a.groups;
+    const uint32_t head = (is_v ? rest - a.groups : rest) * H;
+    Unit r;
+    r.n = min(H, a.hkv - head);
+    r.rows = (is_v ? a.value + token * a.value16 : a.key + token * a.key16) + head * (Q8_D / 8) + lane16;
+    r.live = slot >= 0 && slot < a.num_slots;
+    if (slot >= 0 && !r.live && rest == 0 && lane16 == 0) record_error(a.err, PA_DEV_BAD_SLOT, token);
+    const uint32_t at = r.live ? (uint32_t)slot : 0u, blk = at / a.block, off = at - blk * a.block;
+    const int64_t row = ((int64_t)blk * a.hkv + head) * a.block + off;
+    r.codes = (is_v ? a.v_codes : a.k_codes) + row * Q8_D + 8 * lane16;
+    r.scale = (is_v ? a.v_scales : a.k_scales) + row;
+    return r;
 }
 
 __device__ __forceinline__ uint4 ld_stream16(const uint4 *p) {
@@ -76,110 +78,109 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-template <int FMT>
+template <int FMT, uint32_t H>
 __global__ void __launch_bounds__(Q8_THREADS) store_kvcache_q8_kernel(const Q8Rows a) {
     pdl_wait_then_release();
     const int lane16 = threadIdx.x & 15;
-    const uint64_t n = 2ull * a.num_tokens * a.hkv;
-    const uint64_t hw = ((uint64_t)blockIdx.x * Q8_THREADS + threadIdx.x) >> 4;
-    const uint64_t nhw = (uint64_t)gridDim.x * (Q8_THREADS / 16);
-    // Both halves of a warp run the same trips (the shuffles need them).
-    for (uint64_t r0 = hw; (r0 & ~1ull) < n; r0 += nhw * UNITS) {
-        Unit u[UNITS];
-        uint4 v[UNITS];
+    const unsigned half = 0xffffu << (threadIdx.x & 16);  // this half-warp's lanes
+    const uint64_t n = 2ull * a.num_tokens * a.groups;
+    const uint64_t step = (uint64_t)gridDim.x * (Q8_THREADS / 16);
+    uint64_t i = ((uint64_t)blockIdx.x * Q8_THREADS + threadIdx.x) >> 4;
+    uint32_t token = i < n ? token_of(a, i) : 0;
+    int32_t slot = i < n ? __ldg(a.slots + token) : -1;
+    for (; i < n; i += step) {
+        const Unit u = unit_of<H>(a, i, token, slot, lane16);
+        uint4 v[H];
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            u[i] = unit_of(a, r0 + i * nhw, n, lane16);
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (u[i].live && u[i].codes) v[i] = ld_stream16(u[i].rows);
+        for (uint32_t h = 0; h < H; ++h) {
+            v[h] = make_uint4(0, 0, 0, 0);
+            if (u.live && h < u.n) v[h] = ld_stream16(u.rows + h * (Q8_D / 8));
         }
+        if (i + step < n) {
+            token = token_of(a, i + step);
+            slot = __ldg(a.slots + token);
+        }
+        if (!u.live) continue;  // padding (the half-warp as one)
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (uint32_t h = 0; h < H; ++h) {
+            const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
             uint32_t mx = w[0] & 0x7fff7fffu;
 #pragma unroll
             for (int j = 1; j < 4; ++j) mx = max_nan_bf16x2(mx, w[j] & 0x7fff7fffu);
 #pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) mx = max_nan_bf16x2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            for (int o = 8; o >= 1; o >>= 1) mx = max_nan_bf16x2(mx, __shfl_xor_sync(half, mx, o));
             // Magnitudes order as their bits (a NaN above all).
             const uint32_t amax = max(mx & 0xffffu, mx >> 16);
             const bool finite = amax < 0x7f80u;
             const int e = q8_exponent<FMT>(amax);
             const float inv = __uint_as_float((uint32_t)(127 - (finite ? e : 0)) << 23);
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[2 * j] = finite ? bf16lo(w[j]) * inv : 0.f;
-                f[2 * j + 1] = finite ? bf16hi(w[j]) * inv : 0.f;
-            }
-            if (u[i].live && u[i].codes) {
-                uint2 c;
-                c.x = q8_encode4<FMT>(f[0], f[1], f[2], f[3]);
-                c.y = q8_encode4<FMT>(f[4], f[5], f[6], f[7]);
-                *reinterpret_cast<uint2 *>(u[i].codes) = c;
-                if (lane16 == 0) *u[i].scale = (uint8_t)(finite ? e + 127 : 255);
+            uint2 c;
+            c.x = q8_encode4<FMT>(w[0], w[1], inv);
+            c.y = q8_encode4<FMT>(w[2], w[3], inv);
+            if (!finite) c = make_uint2(0, 0);
+            if (h < u.n) {
+                *reinterpret_cast<uint2 *>(u.codes + (int64_t)h * a.block * Q8_D) = c;
+                if (lane16 == 0) u.scale[(int64_t)h * a.block] = (uint8_t)(finite ? e + 127 : 255);
             }
         }
     }
 }
 
-template <int FMT>
+template <int FMT, uint32_t H>
 __global__ void __launch_bounds__(Q8_THREADS) load_kvcache_q8_kernel(const Q8Rows a) {
     pdl_wait_then_release();
     const int lane16 = threadIdx.x & 15;
-    const uint64_t n = 2ull * a.num_tokens * a.hkv;
-    const uint64_t hw = ((uint64_t)blockIdx.x * Q8_THREADS + threadIdx.x) >> 4;
-    const uint64_t nhw = (uint64_t)gridDim.x * (Q8_THREADS / 16);
-    for (uint64_t r0 = hw; r0 < n; r0 += nhw * UNITS) {
-        Unit u[UNITS];
-        uint2 c[UNITS];
-        uint32_t s[UNITS];
+    const uint64_t n = 2ull * a.num_tokens * a.groups;
+    const uint64_t step = (uint64_t)gridDim.x * (Q8_THREADS / 16);
+    uint64_t i = ((uint64_t)blockIdx.x * Q8_THREADS + threadIdx.x) >> 4;
+    uint32_t token = i < n ? token_of(a, i) : 0;
+    int32_t slot = i < n ? __ldg(a.slots + token) : -1;
+    for (; i < n; i += step) {
+        const Unit u = unit_of<H>(a, i, token, slot, lane16);
+        uint2 c[H];
+        uint32_t s[H];
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            u[i] = unit_of(a, r0 + i * nhw, n, lane16);
-            c[i] = make_uint2(0, 0);
-            s[i] = 127;
-            if (u[i].live && u[i].codes) {
-                c[i] = __ldg(reinterpret_cast<const uint2 *>(u[i].codes));
-                s[i] = __ldg(u[i].scale);
+        for (uint32_t h = 0; h < H; ++h) {
+            c[h] = make_uint2(0, 0);  // a negative (or bad) slot reads as zeros
+            s[h] = 127;
+            if (u.live && h < u.n) {
+                c[h] = __ldg(reinterpret_cast<const uint2 *>(u.codes + (int64_t)h * a.block * Q8_D));
+                s[h] = __ldg(u.scale + (int64_t)h * a.block);
             }
         }
+        if (i + step < n) {
+            token = token_of(a, i + step);
+            slot = __ldg(a.slots + token);
+        }
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i) {
-            if (!u[i].live) continue;
-            uint4 o = make_uint4(0, 0, 0, 0);  // a negative (or bad) slot reads as zeros
-            if (u[i].codes) {
-                const float sc = q8_scale(s[i]);
-                uint32_t h[4];
-                q8_to_f16<FMT>(c[i].x, h[0], h[1]);
-                q8_to_f16<FMT>(c[i].y, h[2], h[3]);
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-                    w[j] = *reinterpret_cast<const uint32_t *>(&b);
-                }
-                o = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            *u[i].rows = o;
+        for (uint32_t h = 0; h < H; ++h) {
+            if (h >= u.n) break;
+            const uint32_t sc = q8_scale_bf16x2(s[h]);
+            const uint2 x = q8_to_bf16<FMT>(c[h].x, sc), y = q8_to_bf16<FMT>(c[h].y, sc);
+            u.rows[h * (Q8_D / 8)] = make_uint4(x.x, x.y, y.x, y.y);
         }
     }
 }
 
-pa_status launch_rows(const Q8Rows &a, int32_t format, bool store, cudaStream_t stream) {
+template <int FMT, uint32_t H>
+pa_status launch_rows(Q8Rows a, bool store, int sms, cudaStream_t stream) {
+    a.groups = (a.hkv + H - 1) / H;
+    // A half-warp per unit and step; at most 8 (load: 16) CTAs of 16 half-warps
+    // per SM.  Sixteen shorten a long load, whose time is in its writes (262144
+    // tokens 250 us instead of 266), and not a store (16384 tokens 21.4, 20.7).
+    const int64_t units = 2LL * a.num_tokens * a.groups, per = Q8_THREADS / 16;
+    const int64_t most = (store ? 8LL : 16LL) * sms;
+    const dim3 grid((unsigned)std::min<int64_t>((units + per - 1) / per, most)), block(Q8_THREADS);
+    return store ? launch_pdl(store_kvcache_q8_kernel<FMT, H>, grid, block, 0, stream, "store_kvcache_q8_kernel", a)
+                 : launch_pdl(load_kvcache_q8_kernel<FMT, H>, grid, block, 0, stream, "load_kvcache_q8_kernel", a);
+}
+
+template <int FMT>
+pa_status launch_rows(const Q8Rows &a, bool store, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms <= 0) return fail(PA_ERR_CUDA, "no CUDA device");
-    // A half-warp per row and step; at most 8 CTAs of 16 half-warps per SM.
-    const int64_t rows = 2LL * a.num_tokens * a.hkv, per = Q8_THREADS / 16;
-    const dim3 grid((unsigned)std::min<int64_t>((rows + per - 1) / per, 8LL * sms)), block(Q8_THREADS);
-    if (store)
-        return format == PA_Q8_E4M3
-                   ? launch_pdl(store_kvcache_q8_kernel<PA_Q8_E4M3>, grid, block, 0, stream, "store_kvcache_q8_kernel", a)
-                   : launch_pdl(store_kvcache_q8_kernel<PA_Q8_INT8>, grid, block, 0, stream, "store_kvcache_q8_kernel", a);
-    return format == PA_Q8_E4M3
-               ? launch_pdl(load_kvcache_q8_kernel<PA_Q8_E4M3>, grid, block, 0, stream, "load_kvcache_q8_kernel", a)
-               : launch_pdl(load_kvcache_q8_kernel<PA_Q8_INT8>, grid, block, 0, stream, "load_kvcache_q8_kernel", a);
+    const bool fills = 2LL * a.num_tokens * ((a.hkv + 7) / 8) >= 64LL * sms;
+    return fills ? launch_rows<FMT, 8>(a, store, sms, stream) : launch_rows<FMT, 2>(a, store, sms, stream);
 }
 
 pa_status rows_impl(const void *key, int64_t key_row_stride, const void *value, int64_t value_row_stride,
@@ -215,7 +216,8 @@ pa_status rows_impl(const void *key, int64_t key_row_stride, const void *value, 
     a.block = (uint32_t)block_size;
     a.num_slots = (int64_t)num_blocks * block_size;
     a.err = device_error_ptr();
-    return launch_rows(a, format, store, reinterpret_cast<cudaStream_t>(stream));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return format == PA_Q8_E4M3 ? launch_rows<PA_Q8_E4M3>(a, store, s) : launch_rows<PA_Q8_INT8>(a, store, s);
 }
 
 }  // namespace
