@@ -13,15 +13,18 @@
 //    rows of the type's lowest value or of very large logits do not overflow.
 //    m only moves when a logit exceeds it by 32 in base 2.  Threads, warps
 //    and CTAs combine as (m, S, E) triples.
-//  * Top k: a thread also keeps the largest logit it has seen and the vector
-//    (8 logits) that first held it.  The threads form P >= k groups (P = 8, 16
-//    or 32 by lane); the smallest of the P group maxima, with its vector as
-//    the tie-break, is a threshold that at least k entries of the CTA's chunk
-//    reach.  Only threads whose own maximum reaches it re-read their vectors
-//    (from L2) and collect the entries that reach it: about P ln P of them
-//    for logits in random order.  The collected keys (logit, then index) are
-//    ranked by counting.  A chunk with more than CAP such entries, or with
-//    NaNs that hid some, is selected by k passes of a plain maximum instead.
+//  * Top k: a thread also keeps the largest logit it has seen, the vector (8
+//    logits) that first held it, and the largest of each eighth of its
+//    vectors.  The threads form P >= k groups (P = 8, 16 or 32 by lane); the
+//    smallest of the P group maxima, with its vector as the tie-break, is a
+//    threshold that at least k entries of the CTA's chunk reach.  The eighths
+//    whose maximum reaches it are listed and re-read by all threads, which
+//    collect the entries that do: about P ln P of them for logits in random
+//    order.  (Re-reading a thread's whole share cost 42 % more DRAM traffic: a
+//    row has left L2 by then.  Re-reading by the owners alone cost 13 us a
+//    row: a warp's lanes had different eighths to wait for.)  The collected
+//    keys (logit, then index) are ranked by counting.  A chunk with more than CAP such entries, or with NaNs that
+//    hid some, is selected by k passes of a plain maximum instead.
 //    The CTAs' lists meet in the cluster's first CTA, where an entry's rank is
 //    its place in its own list plus the entries above it in the others'.
 #include <math.h>
@@ -37,8 +40,8 @@ constexpr int LP_THREADS = 256;
 constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_MAX_CLUSTER = 8;
 constexpr int LP_MAX_TOP = 32;
-constexpr int LP_CAP = 2048;      // collected entries of a chunk
-constexpr int LP_UNROLL = 4;      // vectors in flight per thread
+constexpr int LP_CAP = 1024;      // collected entries of a chunk
+constexpr int LP_SEGS = 8;        // parts of a thread's vectors with a maximum of their own
 constexpr float LP_LAZY = 32.f;   // log2 headroom before the reference moves
 constexpr float LP_FLOOR = -200.f;  // 2^-200 is 0: keeps 0 * y finite for y = -inf
 constexpr unsigned FULL = 0xffffffffu;
@@ -60,17 +63,6 @@ struct LpArgs {
 struct Stat {
     float m, s, e;
 };
-
-__device__ __forceinline__ void join(Stat &a, const Stat &b, float kk) {
-    const float m = fmaxf(a.m, b.m);
-    auto moved = [&](const Stat &x) -> Stat {
-        if (x.m == m || x.s == 0.f) return Stat{m, x.s, x.e};
-        const float d = fmaxf((x.m - m) * kk, LP_FLOOR), f = exp2f(d);
-        return Stat{m, x.s * f, (x.e + x.s * d) * f};
-    };
-    const Stat x = moved(a), y = moved(b);
-    a = Stat{m, x.s + y.s, x.e + y.e};
-}
 
 // A float as an unsigned integer in the same order (-0 as +0); NaN lowest.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -188,7 +180,8 @@ __device__ __forceinline__ void move_reference(Run &r, float to, float kk) {
     r.limit = to + LP_LAZY / kk;
 }
 
-// Sums of a pair (a lone logit: its partner is -inf).
+// Sums of a pair (a lone logit: its partner is -inf).  The floor keeps 0 * y
+// finite for y = -inf.
 __device__ __forceinline__ void add_pair(Run &r, float x, float y, u64 negm, u64 kk2) {
     float a, b;
     unpack2(mul2(add2(pack2(x, y), negm), kk2), a, b);
@@ -206,18 +199,65 @@ __device__ __forceinline__ void see(Run &r, float t, uint32_t vec) {
     }
 }
 
+// A vector's logits into the sums; returns the largest.
+template <bool FP32>
+__device__ __forceinline__ float take(Run &r, const Vec<FP32> &v, uint32_t vec, float kk, u64 kk2) {
+    const float t = v.top();
+    see(r, t, vec);
+    if (t > r.limit) move_reference(r, t, kk);
+    const float nm = r.m == -INFINITY ? 0.f : -r.m;
+    const u64 negm = pack2(nm, nm);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float p, q;
+        v.pair(j, p, q);
+        add_pair(r, p, q, negm, kk2);
+    }
+    return t;
+}
+
+// The smallest and the largest 64-bit key of a warp, word by word.
+__device__ __forceinline__ u64 warp_min(u64 k) {
+    const uint32_t hi = (uint32_t)(k >> 32), m = __reduce_min_sync(FULL, hi);
+    return ((u64)m << 32) | __reduce_min_sync(FULL, hi == m ? (uint32_t)k : 0xffffffffu);
+}
+__device__ __forceinline__ u64 warp_max(u64 k) {
+    const uint32_t hi = (uint32_t)(k >> 32), m = __reduce_max_sync(FULL, hi);
+    return ((u64)m << 32) | __reduce_max_sync(FULL, hi == m ? (uint32_t)k : 0u);
+}
+
+// Joins the lanes' statistics; every lane holds the same bits afterwards.
+__device__ __forceinline__ Stat warp_join(Stat a, float kk) {
+    const float m = from_ordered(__reduce_max_sync(FULL, ordered(a.m)));
+    if (a.m != m && a.s != 0.f) {
+        const float d = fmaxf((a.m - m) * kk, LP_FLOOR), f = fast_exp2(d);
+        a.e = (a.e + a.s * d) * f;
+        a.s *= f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a.s += __shfl_xor_sync(FULL, a.s, o);
+        a.e += __shfl_xor_sync(FULL, a.e, o);
+    }
+    return Stat{m, a.s, a.e};
+}
+
 template <bool FP32>
 __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a) {
     pdl_wait_then_release();
     // Distributed shared memory is written only once every CTA of the cluster runs.
     if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     __shared__ u64 buf[LP_CAP];
+    __shared__ float seg_top[LP_SEGS][LP_THREADS];
     __shared__ u64 group[LP_WARPS][32];
     __shared__ Stat stats[LP_WARPS];
-    __shared__ int count;
+    __shared__ uint16_t items[LP_SEGS * LP_THREADS];  // segment, thread
+    __shared__ int count, nitems;
     __shared__ u64 lists[LP_MAX_CLUSTER][LP_MAX_TOP];  // in the cluster's first CTA
     __shared__ Stat cstats[LP_MAX_CLUSTER];            // likewise
     __shared__ u64 mine[LP_MAX_TOP];
+    constexpr int UNROLL = FP32 ? 2 : 4;  // vectors of a thread in flight (64 bytes)
+    constexpr int BATCH = UNROLL * LP_THREADS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.cluster;
     const int64_t row = blockIdx.x / (unsigned)S;
@@ -231,67 +271,64 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
     const int lo = (int)min((int64_t)a.vocab, (int64_t)rank * chunk), hi = (int)min((int64_t)a.vocab, (int64_t)lo + chunk);
     const int nvec = (hi - lo) / 8;
     if (tid < LP_MAX_TOP) mine[tid] = 0;
-    if (tid == 0) count = 0;
+    if (tid == 0) count = nitems = 0;
 
-    // ---- one pass: sums, and each thread's largest logit
+    // ---- one pass: sums, and the largest logits
     Run r;
     r.m = r.limit = r.top = -INFINITY;
     r.s = r.e = pack2(0.f, 0.f);
     r.top_vec = 0xffffffffu;
     const u64 kk2 = pack2(kk, kk);
-    for (int v0 = tid; v0 < nvec; v0 += LP_UNROLL * LP_THREADS) {
-        Vec<FP32> v[LP_UNROLL];
+    auto fetch = [&](Vec<FP32>(&v)[UNROLL], int v0) {  // a repeat past the end is ignored later
 #pragma unroll
-        for (int u = 0; u < LP_UNROLL; ++u)
-            v[u].load(x, lo + 8 * min(v0 + u * LP_THREADS, nvec - 1));  // a repeat past the end is ignored below
+        for (int u = 0; u < UNROLL; ++u) v[u].load(x, lo + 8 * min(v0 + u * LP_THREADS, nvec - 1));
+    };
+    // Batches of a segment; segment s holds batches [s * per, (s + 1) * per).
+    const int batches = (nvec + BATCH - 1) / BATCH, per = (batches + LP_SEGS - 1) / LP_SEGS;
+    {
+        Vec<FP32> v[UNROLL];
+        if (batches > 0) fetch(v, tid);
+        float top = -INFINITY;
+        int left = per, seg = 0;
+        for (int i = 0; i < batches; ++i) {
+            const int v0 = i * BATCH + tid;
+            Vec<FP32> next[UNROLL];
+            if (i + 1 < batches) fetch(next, v0 + BATCH);
 #pragma unroll
-        for (int u = 0; u < LP_UNROLL; ++u) {
-            const int vec = v0 + u * LP_THREADS;
-            if (vec >= nvec) break;
-            const float t = v[u].top();
-            see(r, t, (uint32_t)vec);
-            if (t > r.limit) move_reference(r, t, kk);
-            const float nm = r.m == -INFINITY ? 0.f : -r.m;
-            const u64 negm = pack2(nm, nm);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float p, q;
-                v[u].pair(j, p, q);
-                add_pair(r, p, q, negm, kk2);
+            for (int u = 0; u < UNROLL; ++u) {
+                const int vec = v0 + u * LP_THREADS;
+                if (vec < nvec) top = fmaxf(top, take<FP32>(r, v[u], (uint32_t)vec, kk, kk2));
             }
+            if (--left == 0 || i + 1 == batches) {
+                if (a.top > 0) seg_top[seg][tid] = top;
+                top = -INFINITY;
+                left = per;
+                ++seg;
+            }
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) v[u] = next[u];
         }
     }
     // The ragged end of the row: one logit per thread.
     const int tail = lo + 8 * nvec + tid;
+    float tail_logit = 0.f;
     if (tail < hi) {
-        const float t = logit<FP32>(x, tail);
-        see(r, t, (uint32_t)nvec);
-        if (t > r.limit) move_reference(r, t, kk);
+        tail_logit = logit<FP32>(x, tail);
+        see(r, tail_logit, (uint32_t)nvec);
+        if (tail_logit > r.limit) move_reference(r, tail_logit, kk);
         const float nm = r.m == -INFINITY ? 0.f : -r.m;
-        add_pair(r, t, -INFINITY, pack2(nm, nm), kk2);
+        add_pair(r, tail_logit, -INFINITY, pack2(nm, nm), kk2);
     }
     // References become the largest logits themselves: ln of the final sum is
     // then small where one entry holds the row, and exact to fp32.
     if (r.top > r.m) move_reference(r, r.top, kk);
-    Stat st;
     {
         float s0, s1, e0, e1;
         unpack2(r.s, s0, s1);
         unpack2(r.e, e0, e1);
-        st = Stat{r.m, s0 + s1, e0 + e1};
+        const Stat st = warp_join(Stat{r.m, s0 + s1, e0 + e1}, kk);
+        if (lane == 0) stats[warp] = st;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stat t;
-        t.m = __shfl_xor_sync(FULL, st.m, o);
-        t.s = __shfl_xor_sync(FULL, st.s, o);
-        t.e = __shfl_xor_sync(FULL, st.e, o);
-        // The same order on both sides, so that every lane holds the same bits.
-        Stat l = (lane & o) ? t : st;
-        join(l, (lane & o) ? st : t, kk);
-        st = l;
-    }
-    if (lane == 0) stats[warp] = st;
 
     // ---- the chunk's k largest, in order, in mine[]
     if (a.top > 0) {
@@ -305,33 +342,47 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         u64 thr = group[0][lane];
 #pragma unroll
         for (int w = 1; w < LP_WARPS; ++w) thr = max(thr, group[w][lane]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) thr = min(thr, __shfl_xor_sync(FULL, thr, o));
+        thr = warp_min(thr);
+        auto collect = [&](float t, uint32_t vec, int i) {
+            if (key_of(t, vec) >= thr) {
+                const int at = atomicAdd(&count, 1);
+                if (at < LP_CAP) buf[at] = key_of(t, (uint32_t)i);
+            }
+        };
         if (own != 0 && own >= thr) {
-            auto collect = [&](float t, uint32_t vec, int i) {
-                if (key_of(t, vec) >= thr) {
-                    const int at = atomicAdd(&count, 1);
-                    if (at < LP_CAP) buf[at] = key_of(t, (uint32_t)i);
+            const float thr_top = thr >> 32 ? from_ordered((uint32_t)(thr >> 32)) : -INFINITY;
+            for (int seg = 0; seg * per < batches; ++seg)
+                if (seg_top[seg][tid] >= thr_top) items[atomicAdd(&nitems, 1)] = (uint16_t)(seg * LP_THREADS + tid);
+            if (tail < hi) collect(tail_logit, (uint32_t)nvec, tail);
+        }
+        __syncthreads();
+        // An item's vectors: segment's batches, UNROLL of the thread's in each.
+        const int vecs = per * UNROLL, work = nitems * vecs;
+        for (int w0 = tid; w0 < work; w0 += 2 * LP_THREADS) {
+            Vec<FP32> v[2];
+            int at[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int w = w0 + u * LP_THREADS;
+                at[u] = nvec;
+                if (w < work) {
+                    const int item = w / vecs, j = w - item * vecs;
+                    at[u] = (items[item] / LP_THREADS * per + j / UNROLL) * BATCH + j % UNROLL * LP_THREADS +
+                            items[item] % LP_THREADS;
                 }
-            };
-            for (int v0 = tid; v0 < nvec; v0 += LP_UNROLL * LP_THREADS) {
-                Vec<FP32> v[LP_UNROLL];
+                if (at[u] < nvec) v[u].load(x, lo + 8 * at[u]);
+            }
 #pragma unroll
-                for (int u = 0; u < LP_UNROLL; ++u) v[u].load(x, lo + 8 * min(v0 + u * LP_THREADS, nvec - 1));
+            for (int u = 0; u < 2; ++u) {
+                if (at[u] >= nvec || key_of(v[u].top(), (uint32_t)at[u]) < thr) continue;
 #pragma unroll
-                for (int u = 0; u < LP_UNROLL; ++u) {
-                    const int vec = v0 + u * LP_THREADS;
-                    if (vec >= nvec || key_of(v[u].top(), (uint32_t)vec) < thr) continue;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float p, q;
-                        v[u].pair(j, p, q);
-                        collect(p, (uint32_t)vec, lo + 8 * vec + 2 * j);
-                        collect(q, (uint32_t)vec, lo + 8 * vec + 2 * j + 1);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    float p, q;
+                    v[u].pair(j, p, q);
+                    collect(p, (uint32_t)at[u], lo + 8 * at[u] + 2 * j);
+                    collect(q, (uint32_t)at[u], lo + 8 * at[u] + 2 * j + 1);
                 }
             }
-            if (tail < hi) collect(logit<FP32>(x, tail), (uint32_t)nvec, tail);
         }
         __syncthreads();
         const int n = count;
@@ -339,7 +390,11 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
             for (int i = tid; i < n; i += LP_THREADS) {
                 const u64 k = buf[i];
                 int above = 0;
-                for (int j = 0; j < n; ++j) above += buf[j] > k;
+                int j = 0;
+                for (; j + 8 <= n; j += 8)
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) above += buf[j + u] > k;
+                for (; j < n; ++j) above += buf[j] > k;
                 if (above < want) mine[above] = k;
             }
         } else {  // k passes: the largest key below the last one
@@ -350,8 +405,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
                     const u64 k = key_of(logit<FP32>(x, e), (uint32_t)e);
                     if (k < last && k > best) best = k;
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(FULL, best, o));
+                best = warp_max(best);
                 __syncthreads();
                 if (lane == 0) group[0][warp] = best;
                 __syncthreads();
@@ -364,14 +418,9 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         }
     }
     __syncthreads();
-    // ---- to the cluster's first CTA
-    if (tid == 0) {
-        Stat c = stats[0];
-        for (int w = 1; w < LP_WARPS; ++w) join(c, stats[w], kk);
-        stats[0] = c;
-    }
+    // ---- the CTA's statistics (each warp joins them), to the cluster's first CTA
+    Stat all = warp_join(lane < LP_WARPS ? stats[lane] : Stat{-INFINITY, 0.f, 0.f}, kk);
     if (S > 1) {
-        __syncthreads();
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         if (tid < a.top) {
             uint32_t dst;
@@ -380,28 +429,24 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         }
         if (tid >= 32 && tid < 35) {
             const int f = tid - 32;
-            const Stat c = stats[0];
             uint32_t dst;
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_addr(&cstats[rank])), "r"(0u));
             asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst + 4 * f),
-                         "r"(__float_as_uint(f == 0 ? c.m : f == 1 ? c.s : c.e))
+                         "r"(__float_as_uint(f == 0 ? all.m : f == 1 ? all.s : all.e))
                          : "memory");
         }
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (rank != 0) return;
-    } else {
-        __syncthreads();
+        all = warp_join(lane < S ? cstats[lane] : Stat{-INFINITY, 0.f, 0.f}, kk);
     }
     // ---- the row's answers
-    Stat all = S > 1 ? cstats[0] : stats[0];
-    for (int c = 1; c < S; ++c) join(all, cstats[c], kk);
     const float lsum = logf(all.s);
     auto logprob = [&](float t) -> float {
         if (all.s == 0.f) return -INFINITY;  // a row without a finite logit
         return (t - all.m) / T - lsum;
     };
-    if (tid == 0) {
+    if (tid == LP_THREADS - 1) {
         const int32_t tok = __ldg(a.tokens + row);
         float lp = -INFINITY;
         if (bad_t) {
