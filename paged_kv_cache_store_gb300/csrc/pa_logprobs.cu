@@ -15,12 +15,12 @@
 //    and CTAs combine as (m, S, E) triples.
 //  * Top k: a thread also keeps the largest logit it has seen, the vector (8
 //    logits) that first held it, and the largest of each eighth of its
-//    vectors.  The threads form P >= k groups (P = 8, 16 or 32 by lane); the
-//    smallest of the P group maxima, with its vector as the tie-break, is a
-//    threshold that at least k entries of the CTA's chunk reach.  The eighths
-//    whose maximum reaches it are listed and re-read by all threads, which
-//    collect the entries that do: about P ln P of them for logits in random
-//    order.  (Re-reading a thread's whole share cost 42 % more DRAM traffic: a
+//    vectors.  The threads form 32 groups by lane (64 by lane and the warp's
+//    parity for k > 16); the k-th largest of the groups' maxima, with its
+//    vector as the tie-break, is a threshold that at least k entries of the
+//    CTA's chunk reach.  The eighths whose maximum reaches it are listed and
+//    re-read by all threads, which collect the entries that do: for logits in
+//    random order 6 of them at k = 5, 24 at 20 and 44 at 32.  (Re-reading a thread's whole share cost 42 % more DRAM traffic: a
 //    row has left L2 by then.  Re-reading by the owners alone cost 13 us a
 //    row: a warp's lanes had different eighths to wait for.)  The collected
 //    keys (logit, then index) are ranked by counting.  A chunk with more than CAP such entries, or with NaNs that
@@ -216,11 +216,7 @@ __device__ __forceinline__ float take(Run &r, const Vec<FP32> &v, uint32_t vec, 
     return t;
 }
 
-// The smallest and the largest 64-bit key of a warp, word by word.
-__device__ __forceinline__ u64 warp_min(u64 k) {
-    const uint32_t hi = (uint32_t)(k >> 32), m = __reduce_min_sync(FULL, hi);
-    return ((u64)m << 32) | __reduce_min_sync(FULL, hi == m ? (uint32_t)k : 0xffffffffu);
-}
+// The largest 64-bit key of a warp, word by word.
 __device__ __forceinline__ u64 warp_max(u64 k) {
     const uint32_t hi = (uint32_t)(k >> 32), m = __reduce_max_sync(FULL, hi);
     return ((u64)m << 32) | __reduce_max_sync(FULL, hi == m ? (uint32_t)k : 0u);
@@ -333,16 +329,32 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
     // ---- the chunk's k largest, in order, in mine[]
     if (a.top > 0) {
         const int want = min(a.top, hi - lo);
-        const int P = a.top <= 8 ? 8 : a.top <= 16 ? 16 : 32;
         const u64 own = r.top_vec == 0xffffffffu ? 0ull : key_of(r.top, r.top_vec);
-        u64 g = own;
-        for (int o = P; o < 32; o <<= 1) g = max(g, __shfl_xor_sync(FULL, g, o));
-        group[warp][lane] = g;
+        group[warp][lane] = own;
         __syncthreads();
-        u64 thr = group[0][lane];
+        u64 g0 = group[0][lane], g1 = group[1][lane];  // even and odd warps' lanes
 #pragma unroll
-        for (int w = 1; w < LP_WARPS; ++w) thr = max(thr, group[w][lane]);
-        thr = warp_min(thr);
+        for (int w = 2; w < LP_WARPS; w += 2) {
+            g0 = max(g0, group[w][lane]);
+            g1 = max(g1, group[w + 1][lane]);
+        }
+        // Keys above this lane's; keys are distinct but for 0 (an empty group).
+        int above0 = 0, above1 = 0;
+        u64 thr;
+        if (a.top <= 16) {
+            g0 = max(g0, g1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) above0 += __shfl_sync(FULL, g0, i) > g0;
+            thr = warp_max(above0 >= a.top - 1 ? g0 : 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const u64 o0 = __shfl_sync(FULL, g0, i), o1 = __shfl_sync(FULL, g1, i);
+                above0 += (o0 > g0) + (o1 > g0);
+                above1 += (o0 > g1) + (o1 > g1);
+            }
+            thr = warp_max(max(above0 >= a.top - 1 ? g0 : 0, above1 >= a.top - 1 ? g1 : 0));
+        }
         auto collect = [&](float t, uint32_t vec, int i) {
             if (key_of(t, vec) >= thr) {
                 const int at = atomicAdd(&count, 1);
@@ -375,13 +387,19 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 if (at[u] >= nvec || key_of(v[u].top(), (uint32_t)at[u]) < thr) continue;
+                float t[8];
+                unsigned hit = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float p, q;
-                    v[u].pair(j, p, q);
-                    collect(p, (uint32_t)at[u], lo + 8 * at[u] + 2 * j);
-                    collect(q, (uint32_t)at[u], lo + 8 * at[u] + 2 * j + 1);
-                }
+                for (int j = 0; j < 4; ++j) v[u].pair(j, t[2 * j], t[2 * j + 1]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) hit |= (key_of(t[j], (uint32_t)at[u]) >= thr ? 1u : 0u) << j;
+                int to = atomicAdd(&count, __popc(hit));
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (hit >> j & 1) {
+                        if (to < LP_CAP) buf[to] = key_of(t[j], (uint32_t)(lo + 8 * at[u] + j));
+                        ++to;
+                    }
             }
         }
         __syncthreads();
@@ -465,14 +483,18 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         const u64 k = S > 1 ? lists[c][at] : mine[at];
         if (k == 0) continue;
         int place = at;
-        for (int o = 0; o < S; ++o) {
-            if (o == c) continue;
-            int l = 0, h = a.top;  // entries of list o above k
-            while (l < h) {
-                const int mid = (l + h) >> 1;
-                if (lists[o][mid] > k) l = mid + 1; else h = mid;
-            }
-            place += l;
+        if (S > 1) {  // the entries above k in the other lists, searched side by side
+            int pos[LP_MAX_CLUSTER];
+#pragma unroll
+            for (int o = 0; o < LP_MAX_CLUSTER; ++o) pos[o] = 0;
+#pragma unroll
+            for (int step = LP_MAX_TOP; step > 0; step >>= 1)
+#pragma unroll
+                for (int o = 0; o < LP_MAX_CLUSTER; ++o)
+                    if (o < S && pos[o] + step <= a.top && lists[o][pos[o] + step - 1] > k) pos[o] += step;
+            place = 0;  // (its own list counts the entries before it)
+#pragma unroll
+            for (int o = 0; o < LP_MAX_CLUSTER; ++o) place += pos[o];
         }
         if (place < a.top) {
             a.top_ids[row * a.top + place] = bad_t ? -1 : (int32_t)~(uint32_t)k;
