@@ -15,12 +15,11 @@
 //    and CTAs combine as (m, S, E) triples.
 //  * Top k: a thread also keeps the largest logit it has seen, the vector (8
 //    logits) that first held it, and the largest of each eighth of its
-//    vectors.  The threads form 32 groups by lane (64 by lane and the warp's
-//    parity for k > 16); the k-th largest of the groups' maxima, with its
-//    vector as the tie-break, is a threshold that at least k entries of the
-//    CTA's chunk reach.  The eighths whose maximum reaches it are listed and
+//    vectors.  The threads form 64 groups, by lane and the warp's parity; the
+//    k-th largest of the groups' maxima, with its vector as the tie-break, is
+//    a threshold that at least k entries of the CTA's chunk reach.  The eighths whose maximum reaches it are listed and
 //    re-read by all threads, which collect the entries that do: for logits in
-//    random order 6 of them at k = 5, 24 at 20 and 44 at 32.  (Re-reading a thread's whole share cost 42 % more DRAM traffic: a
+//    random order 5 of them at k = 5, 24 at 20 and 44 at 32.  (Re-reading a thread's whole share cost 42 % more DRAM traffic: a
 //    row has left L2 by then.  Re-reading by the owners alone cost 13 us a
 //    row: a warp's lanes had different eighths to wait for.)  The collected
 //    keys (logit, then index) are ranked by counting.  A chunk with more than CAP such entries, or with NaNs that
@@ -249,6 +248,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
     __shared__ Stat stats[LP_WARPS];
     __shared__ uint16_t items[LP_SEGS * LP_THREADS];  // segment, thread
     __shared__ int count, nitems;
+    __shared__ u64 threshold;
     __shared__ u64 lists[LP_MAX_CLUSTER][LP_MAX_TOP];  // in the cluster's first CTA
     __shared__ Stat cstats[LP_MAX_CLUSTER];            // likewise
     __shared__ u64 mine[LP_MAX_TOP];
@@ -267,7 +267,14 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
     const int lo = (int)min((int64_t)a.vocab, (int64_t)rank * chunk), hi = (int)min((int64_t)a.vocab, (int64_t)lo + chunk);
     const int nvec = (hi - lo) / 8;
     if (tid < LP_MAX_TOP) mine[tid] = 0;
-    if (tid == 0) count = nitems = 0;
+    if (tid == 0) {
+        count = nitems = 0;
+        threshold = 0;
+    }
+    // The given token's logit, ahead of its use.
+    const bool answers = rank == 0 && tid == LP_THREADS - 1;
+    const int32_t tok = answers ? __ldg(a.tokens + row) : -1;
+    const float tok_logit = tok >= 0 && tok < a.vocab ? logit<FP32>(x, tok) : 0.f;
 
     // ---- one pass: sums, and the largest logits
     Run r;
@@ -338,23 +345,16 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
             g0 = max(g0, group[w][lane]);
             g1 = max(g1, group[w + 1][lane]);
         }
-        // Keys above this lane's; keys are distinct but for 0 (an empty group).
-        int above0 = 0, above1 = 0;
-        u64 thr;
-        if (a.top <= 16) {
-            g0 = max(g0, g1);
+        // Each warp ranks eight of the 64 groups; keys are distinct but for 0 (an
+        // empty group), which the threshold is if fewer than k groups hold any.
 #pragma unroll
-            for (int i = 0; i < 32; ++i) above0 += __shfl_sync(FULL, g0, i) > g0;
-            thr = warp_max(above0 >= a.top - 1 ? g0 : 0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const u64 o0 = __shfl_sync(FULL, g0, i), o1 = __shfl_sync(FULL, g1, i);
-                above0 += (o0 > g0) + (o1 > g0);
-                above1 += (o0 > g1) + (o1 > g1);
-            }
-            thr = warp_max(max(above0 >= a.top - 1 ? g0 : 0, above1 >= a.top - 1 ? g1 : 0));
+        for (int j = 0; j < 8; ++j) {
+            const u64 k = __shfl_sync(FULL, j < 4 ? g0 : g1, warp * 4 + (j & 3));
+            const int above = __popc(__ballot_sync(FULL, g0 > k)) + __popc(__ballot_sync(FULL, g1 > k));
+            if (above == a.top - 1 && lane == 0) threshold = k;
         }
+        __syncthreads();
+        const u64 thr = threshold;
         auto collect = [&](float t, uint32_t vec, int i) {
             if (key_of(t, vec) >= thr) {
                 const int at = atomicAdd(&count, 1);
@@ -464,8 +464,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         if (all.s == 0.f) return -INFINITY;  // a row without a finite logit
         return (t - all.m) / T - lsum;
     };
-    if (tid == LP_THREADS - 1) {
-        const int32_t tok = __ldg(a.tokens + row);
+    if (answers) {
         float lp = -INFINITY;
         if (bad_t) {
             record_error(a.err, PA_DEV_BAD_TEMPERATURE, row);
@@ -473,7 +472,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         } else if (tok >= a.vocab) {
             record_error(a.err, PA_DEV_BAD_TOKEN, row);
         } else if (tok >= 0) {
-            lp = logprob(logit<FP32>(x, tok));
+            lp = logprob(tok_logit);
         }
         a.logprobs[row] = lp;
         a.entropy[row] = bad_t ? NAN : all.s == 0.f ? 0.f : lsum - 0.6931471805599453f * (all.e / all.s);
@@ -487,8 +486,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
             int pos[LP_MAX_CLUSTER];
 #pragma unroll
             for (int o = 0; o < LP_MAX_CLUSTER; ++o) pos[o] = 0;
-#pragma unroll
-            for (int step = LP_MAX_TOP; step > 0; step >>= 1)
+            for (int step = 1 << (31 - __clz(a.top)); step > 0; step >>= 1)
 #pragma unroll
                 for (int o = 0; o < LP_MAX_CLUSTER; ++o)
                     if (o < S && pos[o] + step <= a.top && lists[o][pos[o] + step - 1] > k) pos[o] += step;
