@@ -71,8 +71,8 @@ constexpr int OFF_BAR = NW * ST * STAGE_BYTES;        // mbarriers [NW][ST]
 constexpr int OFF_ZERO = OFF_BAR + NW * ST * 8;       // a row of zeros
 constexpr int OFF_WSUM = OFF_ZERO + Q8_D;             // scan scratch [3][NW]
 constexpr int OFF_PIECE = OFF_WSUM + 128;             // pair of each warp's two pieces [2 * NW] (-1: none)
-constexpr int OFF_TODO = OFF_PIECE + 128;             // pairs this CTA merges across CTAs [2], abort flag
-constexpr int OFF_SPAN = OFF_TODO + 16;               // the range's end pairs: {pair or -1, first CTA, CTAs, -} [2]
+constexpr int OFF_ABORT = OFF_PIECE + 128;            // a wait ran out
+constexpr int OFF_SPAN = OFF_ABORT + 16;              // the pairs that span CTAs: {-, first CTA, CTAs, -} [2]
 constexpr int OFF_CUM = OFF_SPAN + 32;                // tile prefix sum [batch + 1]
 static_assert(OFF_BAR % 16 == 0 && OFF_ZERO % 16 == 0 && NW * 12 <= 128, "shared-memory layout");
 static_assert(NW <= 16, "a warp's lanes hold the CTA's pieces");
@@ -91,16 +91,16 @@ constexpr size_t smem_bytes(int batch, int G) {
 constexpr size_t kMaxSmem = 232448;
 static_assert(smem_bytes(kMaxBatch, 8) <= kMaxSmem, "shared memory budget");
 
-// Workspace: the CTAs' parts [kMaxGrid][2] (of the pair at the range's start, of
-// its last one), then the arrival counters [kMaxGrid] (of the pair that spans
-// CTAs and starts in this one's range).
+// Workspace: the CTAs' parts [kMaxGrid][2] (of the pair that began in an earlier
+// range, of the one that begins in this range and ends in a later one), then
+// the arrival counters [kMaxGrid][8] (of the latter pair's heads).
 struct WsLayout {
     size_t cnt_off, total;
 };
 WsLayout ws_layout(int G) {
     WsLayout w;
     w.cnt_off = (size_t)2 * kMaxGrid * G * (Q8_D + 4) * 4;
-    w.total = w.cnt_off + (size_t)kMaxGrid * 4;
+    w.total = w.cnt_off + (size_t)kMaxGrid * 8 * 4;
     return w;
 }
 
@@ -292,6 +292,34 @@ __device__ __forceinline__ void write_out(const Args &a, const Merged &r, int64_
     od[1] = __floats2bfloat162_rn(r.o.z * f, r.o.w * f);
 }
 
+// Merges the parts of a pair that n CTAs from c0 on share (it begins in c0's
+// range) for head h.
+template <int G>
+__device__ void merge_parts(const Args &a, int pair, int c0, int n, int h) {
+    const int lane = threadIdx.x & 31;
+    Merged r;
+    for (int i = 0; i < n; i += 32) {
+        const int at = min(i + lane, n - 1), left = n - i;
+        const float *part = a.ws_part + (int64_t)(2 * (c0 + at) + (at == 0 ? 1 : 0)) * kPiece<G>;
+        const Merged q = merge_pieces<G, true>(part, left >= 32 ? FULL : (1u << left) - 1, h);
+        if (i == 0) {
+            r = q;
+            continue;
+        }
+        const float m = fmaxf(r.m, q.m), mv = fmaxf(r.mv, q.mv);
+        const float fr = r.m == -INFINITY ? 1.f : fast_exp2(r.m - m), fq = q.m == -INFINITY ? 1.f : fast_exp2(q.m - m);
+        const float gr = r.mv == -INFINITY ? 1.f : fast_exp2(r.mv - mv), gq = q.mv == -INFINITY ? 1.f : fast_exp2(q.mv - mv);
+        r.l = r.l * fr + q.l * fq;
+        r.o.x = r.o.x * gr + q.o.x * gq;
+        r.o.y = r.o.y * gr + q.o.y * gq;
+        r.o.z = r.o.z * gr + q.o.z * gq;
+        r.o.w = r.o.w * gr + q.o.w * gq;
+        r.m = m;
+        r.mv = mv;
+    }
+    write_out(a, r, (int64_t)(pair / a.Hkv) * a.Hq + (int64_t)(pair % a.Hkv) * G + h);
+}
+
 // Equal contiguous shares of n items (the list's length is bounded on the host,
 // so that units fit 32 bits).
 struct Split {
@@ -314,7 +342,7 @@ __global__ void __launch_bounds__(NT, 1)
     int *ctx_s = reinterpret_cast<int *>(smem + off_ctx(a.batch));
     uint32_t *wsum = reinterpret_cast<uint32_t *>(smem + OFF_WSUM);
     int *piece_pair = reinterpret_cast<int *>(smem + OFF_PIECE);
-    volatile int *todo = reinterpret_cast<volatile int *>(smem + OFF_TODO);
+    int *abort = reinterpret_cast<int *>(smem + OFF_ABORT);
     int4 *span = reinterpret_cast<int4 *>(smem + OFF_SPAN);
     float *stash = reinterpret_cast<float *>(smem + off_stash(a.batch));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -326,7 +354,7 @@ __global__ void __launch_bounds__(NT, 1)
         fence_mbar_init();
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
-        todo[2] = 0;
+        *abort = 0;
     }
     if (threadIdx.x < Q8_D / 16) *reinterpret_cast<uint4 *>(smem + OFF_ZERO + 16 * threadIdx.x) = make_uint4(0, 0, 0, 0);
     if (threadIdx.x < 2 * NW) piece_pair[threadIdx.x] = -1;
@@ -425,9 +453,8 @@ __global__ void __launch_bounds__(NT, 1)
         // The pairs that span CTAs: the one the range begins inside of, and the one
         // it ends inside of, if that began in this range.
         if (warp == 0 && (lane == 2 || lane == 3)) {
-            int4 sp = make_int4(-1, 0, 0, 0);
+            int4 sp = make_int4(0, 0, 0, 0);
             if (e.t > 0 && (lane == 2 || tile - (uint32_t)e.t >= c_begin)) {
-                sp.x = e.b * a.Hkv + e.g;
                 sp.y = (int)by_cta.owner(unit_of(a, sh, e, 0));
                 sp.z = (int)by_cta.owner(unit_of(a, sh, e, (uint32_t)e.nt - 1)) - sp.y + 1;
             }
@@ -720,13 +747,13 @@ __global__ void __launch_bounds__(NT, 1)
             x += take;
             p = pn;
         }
-        if (!ok && lane == 0) todo[2] = 1;
+        if (!ok && lane == 0) *abort = 1;
     }
 
     // ---- the CTA's pieces, pair by pair.  Lane i stands for piece i; a pair's
     // pieces are neighbours, since the warps' ranges follow the list.
     __syncthreads();
-    if (todo[2]) return;  // a wait ran out: the call's result is void
+    if (*abort) return;  // a wait ran out: the call's result is void
     auto first_tile = [&](int pair, uint32_t &nt) -> uint32_t {
         const int b = pair / a.Hkv;
         nt = cum[b + 1] - cum[b];
@@ -752,61 +779,30 @@ __global__ void __launch_bounds__(NT, 1)
             const uint32_t x0 = first_tile(pr, nt);
             if (x0 >= c_begin && x0 + nt <= c_end) {
                 write_out(a, r, (int64_t)(pr / a.Hkv) * a.Hq + (int64_t)(pr % a.Hkv) * G + h);
-            } else {
-                float *part = a.ws_part + ((int64_t)2 * cta + (x0 > c_begin ? 1 : 0)) * kPiece<G>;
-                *reinterpret_cast<float4 *>(part + h * Q8_D + 4 * lane) = r.o;
-                if (lane == 0) *reinterpret_cast<float4 *>(part + G * Q8_D + 4 * h) = make_float4(r.m, r.mv, r.l, 0.f);
-            }
-        }
-    }
-    // ---- pairs that span CTAs: at most the first and the last of the range.
-    __syncthreads();
-    if (threadIdx.x < 2) {
-        const int4 sp = span[threadIdx.x];
-        int mine = -1;
-        if (sp.x >= 0) {
-            __threadfence();
-            if (atomicAdd(&a.ws_cnt[sp.y], 1) == sp.z - 1) {
-                __threadfence();
-                a.ws_cnt[sp.y] = 0;  // ready for the next call
-                mine = sp.x;
-            }
-        }
-        todo[threadIdx.x] = mine;
-    }
-    __syncthreads();
-    for (int item = warp; item < 2 * G; item += NW) {
-        const int pr = todo[item / G], h = item % G;
-        if (pr < 0) continue;
-        // In its first CTA the pair may follow another one; in later ones it is first.
-        const uint32_t c0 = (uint32_t)span[item / G].y, c1 = c0 + (uint32_t)span[item / G].z - 1;
-        const int b = pr / a.Hkv;
-        const Pos e = {b, pr - b * a.Hkv, 0, (int)(cum[b + 1] - cum[b])};
-        uint32_t first;
-        locate(a, sh, by_cta.start(c0), first);
-        const uint32_t s0 = 2 * c0 + ((uint32_t)a.Hkv * cum[b] + (uint32_t)(e.g * e.nt) > first ? 1 : 0);
-        Merged r;
-        for (uint32_t c = c0; c <= c1; c += 32) {
-            const uint32_t at = min(c + lane, c1);
-            const float *part = a.ws_part + (int64_t)(at == c0 ? s0 : 2 * at) * kPiece<G>;
-            const uint32_t left = c1 - c + 1;
-            const Merged q = merge_pieces<G, true>(part, left >= 32 ? FULL : (1u << left) - 1, h);
-            if (c == c0) {
-                r = q;
                 continue;
             }
-            const float m = fmaxf(r.m, q.m), mv = fmaxf(r.mv, q.mv);
-            const float fr = r.m == -INFINITY ? 1.f : fast_exp2(r.m - m), fq = q.m == -INFINITY ? 1.f : fast_exp2(q.m - m);
-            const float gr = r.mv == -INFINITY ? 1.f : fast_exp2(r.mv - mv), gq = q.mv == -INFINITY ? 1.f : fast_exp2(q.mv - mv);
-            r.l = r.l * fr + q.l * fq;
-            r.o.x = r.o.x * gr + q.o.x * gq;
-            r.o.y = r.o.y * gr + q.o.y * gq;
-            r.o.z = r.o.z * gr + q.o.z * gq;
-            r.o.w = r.o.w * gr + q.o.w * gq;
-            r.m = m;
-            r.mv = mv;
+            // The pair spans CTAs: leave this head's part and count it.
+            const int began = x0 >= c_begin;
+            float *part = a.ws_part + ((int64_t)2 * cta + began) * kPiece<G>;
+            *reinterpret_cast<float4 *>(part + h * Q8_D + 4 * lane) = r.o;
+            if (lane == 0) *reinterpret_cast<float4 *>(part + G * Q8_D + 4 * h) = make_float4(r.m, r.mv, r.l, 0.f);
+            __syncwarp();
+            const int c0 = span[began].y, n = span[began].z;
+            int last = 0;
+            if (lane == 0) {
+                __threadfence();
+                int *cnt = a.ws_cnt + c0 * 8 + h;
+                last = atomicAdd(cnt, 1) == n - 1;
+                if (last) {
+                    __threadfence();
+                    *cnt = 0;  // ready for the next call
+                }
+            }
+            if (__shfl_sync(FULL, last, 0)) {
+                __syncwarp();
+                merge_parts<G>(a, pr, c0, n, h);
+            }
         }
-        write_out(a, r, (int64_t)(pr / a.Hkv) * a.Hq + (int64_t)(pr % a.Hkv) * G + h);
     }
 }
 
