@@ -70,9 +70,9 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int OFF_BAR = NW * ST * STAGE_BYTES;        // mbarriers [NW][ST]
 constexpr int OFF_ZERO = OFF_BAR + NW * ST * 8;       // a row of zeros
 constexpr int OFF_WSUM = OFF_ZERO + Q8_D;             // scan scratch [3][NW]
-constexpr int OFF_PIECE = OFF_WSUM + 128;             // pair of each warp's two pieces [2 * NW] (-1: none)
-constexpr int OFF_ABORT = OFF_PIECE + 128;            // a wait ran out
-constexpr int OFF_SPAN = OFF_ABORT + 16;              // the pairs that span CTAs: {-, first CTA, CTAs, -} [2]
+constexpr int OFF_PIECE = OFF_WSUM + 128;             // (b, g) of each warp's two pieces [2 * NW] (-1: none)
+constexpr int OFF_ABORT = OFF_PIECE + 256;            // a wait ran out
+constexpr int OFF_SPAN = OFF_ABORT + 16;              // the pairs that span CTAs: {first CTA, CTAs} [2]
 constexpr int OFF_CUM = OFF_SPAN + 32;                // tile prefix sum [batch + 1]
 static_assert(OFF_BAR % 16 == 0 && OFF_ZERO % 16 == 0 && NW * 12 <= 128, "shared-memory layout");
 static_assert(NW <= 16, "a warp's lanes hold the CTA's pieces");
@@ -183,11 +183,10 @@ __device__ __forceinline__ Pos locate(const Args &a, const Shared &s, uint32_t x
     Pos p = {a.batch, 0, 0, 0};
     tile = (uint32_t)a.Hkv * s.cum[a.batch];
     if (x >= (uint32_t)a.Hkv * s.cost[a.batch]) return p;
-    const uint32_t qv = x / (uint32_t)a.Hkv;
     int lo = 0, hi = a.batch - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (s.cost[mid] <= qv) lo = mid; else hi = mid - 1;
+        if ((uint32_t)a.Hkv * s.cost[mid] <= x) lo = mid; else hi = mid - 1;
     }
     p.b = lo;
     p.nt = (int)(s.cum[lo + 1] - s.cum[lo]);
@@ -293,9 +292,9 @@ __device__ __forceinline__ void write_out(const Args &a, const Merged &r, int64_
 }
 
 // Merges the parts of a pair that n CTAs from c0 on share (it begins in c0's
-// range) for head h.
+// range) for head h, output row `row`.
 template <int G>
-__device__ void merge_parts(const Args &a, int pair, int c0, int n, int h) {
+__device__ void merge_parts(const Args &a, int64_t row, int c0, int n, int h) {
     const int lane = threadIdx.x & 31;
     Merged r;
     for (int i = 0; i < n; i += 32) {
@@ -317,7 +316,7 @@ __device__ void merge_parts(const Args &a, int pair, int c0, int n, int h) {
         r.m = m;
         r.mv = mv;
     }
-    write_out(a, r, (int64_t)(pair / a.Hkv) * a.Hq + (int64_t)(pair % a.Hkv) * G + h);
+    write_out(a, r, row);
 }
 
 // Equal contiguous shares of n items (the list's length is bounded on the host,
@@ -341,9 +340,9 @@ __global__ void __launch_bounds__(NT, 1)
     uint32_t *cost = reinterpret_cast<uint32_t *>(smem + off_cost(a.batch));
     int *ctx_s = reinterpret_cast<int *>(smem + off_ctx(a.batch));
     uint32_t *wsum = reinterpret_cast<uint32_t *>(smem + OFF_WSUM);
-    int *piece_pair = reinterpret_cast<int *>(smem + OFF_PIECE);
+    int2 *piece_pair = reinterpret_cast<int2 *>(smem + OFF_PIECE);
     int *abort = reinterpret_cast<int *>(smem + OFF_ABORT);
-    int4 *span = reinterpret_cast<int4 *>(smem + OFF_SPAN);
+    int2 *span = reinterpret_cast<int2 *>(smem + OFF_SPAN);
     float *stash = reinterpret_cast<float *>(smem + off_stash(a.batch));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + OFF_BAR) + warp * ST;
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__(NT, 1)
         *abort = 0;
     }
     if (threadIdx.x < Q8_D / 16) *reinterpret_cast<uint4 *>(smem + OFF_ZERO + 16 * threadIdx.x) = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x < 2 * NW) piece_pair[threadIdx.x] = -1;
+    if (threadIdx.x < 2 * NW) piece_pair[threadIdx.x] = make_int2(-1, 0);
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // Context lengths, their maximum, and the exclusive prefix sum of the tile
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
     for (int w = 0; w < NW; ++w) nt_max = max(nt_max, wsum[NW + w]);
     const uint32_t least = max(kMinTilesPerCta, (nt_max + kMaxParts - 1) / kMaxParts);
-    const uint32_t ctas = min(gridDim.x, (total + least - 1) / least), cta = blockIdx.x;
+    const uint32_t ctas = total >= gridDim.x * (uint64_t)least ? gridDim.x : min(gridDim.x, (total + least - 1) / least), cta = blockIdx.x;
     if (cta >= ctas) return;
     const Split by_cta((uint32_t)a.Hkv * cost[a.batch], ctas);
     const uint32_t cu = by_cta.start(cta), cu_end = by_cta.start(cta + 1);
@@ -438,6 +437,8 @@ __global__ void __launch_bounds__(NT, 1)
     // has more, a warp's may not.
     Pos ip;
     uint32_t x_begin, x_end, c_begin, c_end;
+    Pos edge;            // lanes 2 and 3: the first tile at or after the CTA's ends
+    uint32_t edge_pair;  // and the first tile of its pair
     {
         const uint32_t u = lane == 0 ? cu + by_warp.start(warp) : lane == 1 ? cu + by_warp.start(warp + 1) : lane == 2 ? cu : cu_end;
         uint32_t tile;
@@ -450,19 +451,21 @@ __global__ void __launch_bounds__(NT, 1)
         ip.g = __shfl_sync(FULL, e.g, 0);
         ip.t = __shfl_sync(FULL, e.t, 0);
         ip.nt = __shfl_sync(FULL, e.nt, 0);
-        // The pairs that span CTAs: the one the range begins inside of, and the one
-        // it ends inside of, if that began in this range.
-        if (warp == 0 && (lane == 2 || lane == 3)) {
-            int4 sp = make_int4(0, 0, 0, 0);
-            if (e.t > 0 && (lane == 2 || tile - (uint32_t)e.t >= c_begin)) {
-                sp.y = (int)by_cta.owner(unit_of(a, sh, e, 0));
-                sp.z = (int)by_cta.owner(unit_of(a, sh, e, (uint32_t)e.nt - 1)) - sp.y + 1;
-            }
-            span[lane - 2] = sp;
-        }
+        edge = e;
+        edge_pair = tile - (uint32_t)e.t;
     }
 
-    if (x_begin < x_end) {
+    // The pairs that span CTAs: the one the range begins inside of, and the one it
+    // ends inside of, if that began in it.
+    auto note_spans = [&]() {
+        if (warp == 0 && (lane == 2 || lane == 3) && edge.t > 0 && (lane == 2 || edge_pair >= c_begin)) {
+            const int c0 = (int)by_cta.owner(unit_of(a, sh, edge, 0));
+            span[lane - 2] = make_int2(c0, (int)by_cta.owner(unit_of(a, sh, edge, (uint32_t)edge.nt - 1)) - c0 + 1);
+        }
+    };
+    if (x_begin >= x_end) {
+        note_spans();
+    } else {
         // ---- producer side: the tile at `ip` is issued next.  Lane i stands for its
         // key i; `blk` is the block that holds it.
         const uint64_t pol = policy_evict_first();
@@ -522,6 +525,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
         for (int i = 0; i < ST; ++i)
             if (ix < x_end) issue(issued++, k_byte[i], v_byte[i]);
+        note_spans();  // while the first tiles travel
 
         // ---- consumer side.  Fragment coordinates (m16n8k16): g4 = lane / 4 is a
         // key (Q.K) or a dim (P.V) row, t4 = lane % 4; columns 2*t4, 2*t4+1 are the
@@ -742,7 +746,7 @@ __global__ void __launch_bounds__(NT, 1)
                     if (h0) ml[2 * t4] = make_float4(m0, mv0, l0, 0.f);
                     if (h1) ml[2 * t4 + 1] = make_float4(m1, mv1, l1, 0.f);
                 }
-                if (lane == 0) piece_pair[slot] = p.b * a.Hkv + p.g;
+                if (lane == 0) piece_pair[slot] = make_int2(p.b, p.g);
             }
             x += take;
             p = pn;
@@ -754,18 +758,14 @@ __global__ void __launch_bounds__(NT, 1)
     // pieces are neighbours, since the warps' ranges follow the list.
     __syncthreads();
     if (*abort) return;  // a wait ran out: the call's result is void
-    auto first_tile = [&](int pair, uint32_t &nt) -> uint32_t {
-        const int b = pair / a.Hkv;
-        nt = cum[b + 1] - cum[b];
-        return (uint32_t)a.Hkv * cum[b] + (uint32_t)(pair - b * a.Hkv) * nt;
-    };
     {
-        const int pair = lane < 2 * NW ? piece_pair[lane] : -1;
+        const int2 bg = lane < 2 * NW ? piece_pair[lane] : make_int2(-1, 0);
         const float *piece = stash + lane * kPiece<G>;
-        const unsigned valid = __ballot_sync(FULL, pair >= 0);
+        const unsigned valid = __ballot_sync(FULL, bg.x >= 0);
         const unsigned before = valid & ((1u << lane) - 1);
-        const int prev = __shfl_sync(FULL, pair, before ? 31 - __clz(before) : 0);
-        const unsigned heads = __ballot_sync(FULL, pair >= 0 && (!before || prev != pair));
+        const int from = before ? 31 - __clz(before) : 0;
+        const int pb = __shfl_sync(FULL, bg.x, from), pg = __shfl_sync(FULL, bg.y, from);
+        const unsigned heads = __ballot_sync(FULL, bg.x >= 0 && (!before || pb != bg.x || pg != bg.y));
         for (int item = warp; item < __popc(heads) * G; item += NW) {
             const int h = item % G;
             unsigned rest = heads;
@@ -773,12 +773,12 @@ __global__ void __launch_bounds__(NT, 1)
             const int i0 = __ffs(rest) - 1;  // the pair's first piece
             rest &= rest - 1;
             const unsigned mask = valid & ~((1u << i0) - 1) & (rest ? (1u << (__ffs(rest) - 1)) - 1 : FULL);
-            const int pr = __shfl_sync(FULL, pair, i0);
+            const int b = __shfl_sync(FULL, bg.x, i0), g = __shfl_sync(FULL, bg.y, i0);
             const Merged r = merge_pieces<G, false>(piece, mask, h);
-            uint32_t nt;
-            const uint32_t x0 = first_tile(pr, nt);
+            const uint32_t nt = cum[b + 1] - cum[b], x0 = (uint32_t)a.Hkv * cum[b] + (uint32_t)g * nt;
+            const int64_t row = (int64_t)b * a.Hq + (int64_t)g * G + h;
             if (x0 >= c_begin && x0 + nt <= c_end) {
-                write_out(a, r, (int64_t)(pr / a.Hkv) * a.Hq + (int64_t)(pr % a.Hkv) * G + h);
+                write_out(a, r, row);
                 continue;
             }
             // The pair spans CTAs: leave this head's part and count it.
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(NT, 1)
             *reinterpret_cast<float4 *>(part + h * Q8_D + 4 * lane) = r.o;
             if (lane == 0) *reinterpret_cast<float4 *>(part + G * Q8_D + 4 * h) = make_float4(r.m, r.mv, r.l, 0.f);
             __syncwarp();
-            const int c0 = span[began].y, n = span[began].z;
+            const int c0 = span[began].x, n = span[began].y;
             int last = 0;
             if (lane == 0) {
                 __threadfence();
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(NT, 1)
             }
             if (__shfl_sync(FULL, last, 0)) {
                 __syncwarp();
-                merge_parts<G>(a, pr, c0, n, h);
+                merge_parts<G>(a, row, c0, n, h);
             }
         }
     }
