@@ -220,9 +220,17 @@ __device__ __forceinline__ void advance(const Args &a, const Shared &s, Pos &p) 
     if (p.b < a.batch) p.nt = (s.ctx[p.b] + KT - 1) / KT;
 }
 
-// Merges pieces of one pair and head: lane i of `mask` holds piece i's address.
-// Every lane returns dims 4*lane .. +3 and the totals.  FAR: the pieces are
-// CTAs' parts (read from L2); else in this CTA's shared memory.
+// The largest of a warp's values (none NaN), by one integer reduction each way:
+// floats order as their bits with the sign bit, or all bits, flipped.
+__device__ __forceinline__ float warp_max(float x) {
+    const uint32_t b = __float_as_uint(x);
+    const uint32_t m = __reduce_max_sync(FULL, (b >> 31) ? ~b : b | 0x80000000u);
+    return __uint_as_float((m >> 31) ? m & 0x7fffffffu : ~m);
+}
+
+// Merges pieces of one pair and head: bit i of `mask` stands for the piece at
+// base + index(i) * kPiece.  Every lane returns dims 4*lane .. +3 and the totals.
+// FAR: the pieces are CTAs' parts (read from L2); else in shared memory.
 struct Merged {
     float m, mv, l;
     float4 o;
@@ -232,54 +240,47 @@ __device__ __forceinline__ float4 ld_piece(const float *p) {
     const float4 *v = reinterpret_cast<const float4 *>(p);
     return FAR ? __ldcg(v) : *v;
 }
-template <int G, bool FAR>
-__device__ __forceinline__ Merged merge_pieces(const float *piece, unsigned mask, int h) {
+template <int G, bool FAR, typename Index>
+__device__ __forceinline__ Merged merge_pieces(const float *base, Index index, unsigned mask, int h) {
     const int lane = threadIdx.x & 31;
     float4 ml = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-    if (mask >> lane & 1) ml = ld_piece<FAR>(piece + G * Q8_D + 4 * h);
-    const unsigned long long at = reinterpret_cast<unsigned long long>(piece + h * Q8_D);
+    if (mask >> lane & 1) ml = ld_piece<FAR>(base + (int64_t)index(lane) * kPiece<G> + G * Q8_D + 4 * h);
     constexpr int PF = FAR ? 8 : 4;  // pieces whose loads are in flight
-    float4 v[PF];
-    int from[PF];
-    auto load = [&](unsigned left) -> unsigned {
-#pragma unroll
-        for (int u = 0; u < PF; ++u) {
-            from[u] = left ? __ffs(left) - 1 : -1;
-            const float *src = reinterpret_cast<const float *>(__shfl_sync(FULL, at, max(from[u], 0)));
-            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (left) v[u] = ld_piece<FAR>(src + 4 * lane);
-            left &= left - 1;
-        }
-        return left;
-    };
-    unsigned left = load(mask);
+    const float *mine = base + h * Q8_D + 4 * lane;
     Merged r;
-    r.m = ml.x;
-    r.mv = ml.y;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        r.m = fmaxf(r.m, __shfl_xor_sync(FULL, r.m, d));
-        r.mv = fmaxf(r.mv, __shfl_xor_sync(FULL, r.mv, d));
-    }
-    // 2^(own - max): a piece without a finite score has l = 0 or NaN.
-    float l = ml.z * (ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - r.m));
-    const float f = ml.y == -INFINITY ? 1.f : fast_exp2(ml.y - r.mv);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) l += __shfl_xor_sync(FULL, l, d);
-    r.l = l;
     r.o = make_float4(0.f, 0.f, 0.f, 0.f);
-    while (true) {
+    float f = 0.f;
+    bool first = true;
+#pragma unroll 1
+    while (mask) {
+        float4 v[PF];
+        int from[PF];
 #pragma unroll
         for (int u = 0; u < PF; ++u) {
-            const float w = __shfl_sync(FULL, f, max(from[u], 0));
-            if (from[u] < 0) continue;
+            from[u] = mask ? __ffs(mask) - 1 : 32;
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mask) v[u] = ld_piece<FAR>(mine + (int64_t)index(from[u]) * kPiece<G>);
+            mask &= mask - 1;
+        }
+        if (first) {  // behind the first loads
+            first = false;
+            r.m = warp_max(ml.x);
+            r.mv = warp_max(ml.y);
+            // 2^(own - max): a piece without a finite score has l = 0 or NaN.
+            r.l = ml.z * (ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - r.m));
+            f = ml.y == -INFINITY ? 1.f : fast_exp2(ml.y - r.mv);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) r.l += __shfl_xor_sync(FULL, r.l, d);
+        }
+#pragma unroll
+        for (int u = 0; u < PF; ++u) {
+            const float w = __shfl_sync(FULL, f, from[u] & 31);
+            if (from[u] == 32) continue;
             r.o.x = fmaf(v[u].x, w, r.o.x);
             r.o.y = fmaf(v[u].y, w, r.o.y);
             r.o.z = fmaf(v[u].z, w, r.o.z);
             r.o.w = fmaf(v[u].w, w, r.o.w);
         }
-        if (!left) break;
-        left = load(left);
     }
     return r;
 }
@@ -295,12 +296,12 @@ __device__ __forceinline__ void write_out(const Args &a, const Merged &r, int64_
 // range) for head h, output row `row`.
 template <int G>
 __device__ void merge_parts(const Args &a, int64_t row, int c0, int n, int h) {
-    const int lane = threadIdx.x & 31;
     Merged r;
     for (int i = 0; i < n; i += 32) {
-        const int at = min(i + lane, n - 1), left = n - i;
-        const float *part = a.ws_part + (int64_t)(2 * (c0 + at) + (at == 0 ? 1 : 0)) * kPiece<G>;
-        const Merged q = merge_pieces<G, true>(part, left >= 32 ? FULL : (1u << left) - 1, h);
+        const int left = n - i;
+        const Merged q = merge_pieces<G, true>(
+            a.ws_part, [&](int j) { return 2 * (c0 + i + j) + (i + j == 0 ? 1 : 0); },
+            left >= 32 ? FULL : (1u << left) - 1, h);
         if (i == 0) {
             r = q;
             continue;
@@ -760,7 +761,6 @@ __global__ void __launch_bounds__(NT, 1)
     if (*abort) return;  // a wait ran out: the call's result is void
     {
         const int2 bg = lane < 2 * NW ? piece_pair[lane] : make_int2(-1, 0);
-        const float *piece = stash + lane * kPiece<G>;
         const unsigned valid = __ballot_sync(FULL, bg.x >= 0);
         const unsigned before = valid & ((1u << lane) - 1);
         const int from = before ? 31 - __clz(before) : 0;
@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(NT, 1)
             rest &= rest - 1;
             const unsigned mask = valid & ~((1u << i0) - 1) & (rest ? (1u << (__ffs(rest) - 1)) - 1 : FULL);
             const int b = __shfl_sync(FULL, bg.x, i0), g = __shfl_sync(FULL, bg.y, i0);
-            const Merged r = merge_pieces<G, false>(piece, mask, h);
+            const Merged r = merge_pieces<G, false>(stash, [](int j) { return j; }, mask, h);
             const uint32_t nt = cum[b + 1] - cum[b], x0 = (uint32_t)a.Hkv * cum[b] + (uint32_t)g * nt;
             const int64_t row = (int64_t)b * a.Hq + (int64_t)g * G + h;
             if (x0 >= c_begin && x0 + nt <= c_end) {
