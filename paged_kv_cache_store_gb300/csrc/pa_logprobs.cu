@@ -179,16 +179,23 @@ __device__ __forceinline__ void move_reference(Run &r, float to, float kk) {
     r.limit = to + LP_LAZY / kk;
 }
 
-// Sums of a pair (a lone logit: its partner is -inf).  The floor keeps 0 * y
-// finite for y = -inf.
-__device__ __forceinline__ void add_pair(Run &r, float x, float y, u64 negm, u64 kk2) {
+// Adds a pair's weights to s and weighted exponents to e (a lone logit: its
+// partner is -inf).  The floor keeps 0 * y finite for y = -inf.
+__device__ __forceinline__ void add_pair(u64 &s, u64 &e, float x, float y, u64 negm, u64 kk2) {
     float a, b;
     unpack2(mul2(add2(pack2(x, y), negm), kk2), a, b);
     a = max_nan(a, LP_FLOOR);
     b = max_nan(b, LP_FLOOR);
     const u64 ex = pack2(fast_exp2(a), fast_exp2(b));
-    r.s = add2(r.s, ex);
-    r.e = fma2(ex, pack2(a, b), r.e);
+    s = add2(s, ex);
+    e = fma2(ex, pack2(a, b), e);
+}
+
+// The reference, negated, as a pair; moved first if t exceeds its limit.
+__device__ __forceinline__ u64 reference(Run &r, float t, float kk) {
+    if (t > r.limit) move_reference(r, t, kk);
+    const float nm = r.m == -INFINITY ? 0.f : -r.m;
+    return pack2(nm, nm);
 }
 
 __device__ __forceinline__ void see(Run &r, float t, uint32_t vec) {
@@ -198,21 +205,34 @@ __device__ __forceinline__ void see(Run &r, float t, uint32_t vec) {
     }
 }
 
-// A vector's logits into the sums; returns the largest.
-template <bool FP32>
-__device__ __forceinline__ float take(Run &r, const Vec<FP32> &v, uint32_t vec, float kk, u64 kk2) {
-    const float t = v.top();
-    see(r, t, vec);
-    if (t > r.limit) move_reference(r, t, kk);
-    const float nm = r.m == -INFINITY ? 0.f : -r.m;
-    const u64 negm = pack2(nm, nm);
+// A batch of vectors (the first n of them) into the sums; returns the largest
+// logit.  The batch has sums of its own, so that the running ones take one
+// rounding a batch.
+template <bool FP32, int N>
+__device__ __forceinline__ float take(Run &r, const Vec<FP32> (&v)[N], int n, int vec0, float kk, u64 kk2) {
+    float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float p, q;
-        v.pair(j, p, q);
-        add_pair(r, p, q, negm, kk2);
-    }
-    return t;
+    for (int u = 0; u < N; ++u)
+        if (u < n) {
+            const float t = v[u].top();
+            see(r, t, (uint32_t)(vec0 + u * LP_THREADS));
+            top = fmaxf(top, t);
+        }
+    const u64 negm = reference(r, top, kk);
+    u64 s = pack2(0.f, 0.f), e = s;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+        if (u < n) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float p, q;
+                v[u].pair(j, p, q);
+                add_pair(s, e, p, q, negm, kk2);
+            }
+        }
+    r.s = add2(r.s, s);
+    r.e = add2(r.e, e);
+    return top;
 }
 
 // The largest 64-bit key of a warp, word by word.
@@ -297,11 +317,8 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
             const int v0 = i * BATCH + tid;
             Vec<FP32> next[UNROLL];
             if (i + 1 < batches) fetch(next, v0 + BATCH);
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int vec = v0 + u * LP_THREADS;
-                if (vec < nvec) top = fmaxf(top, take<FP32>(r, v[u], (uint32_t)vec, kk, kk2));
-            }
+            const int live = v0 < nvec ? (nvec - v0 + LP_THREADS - 1) / LP_THREADS : 0;
+            top = fmaxf(top, take<FP32>(r, v, live, v0, kk, kk2));
             if (--left == 0 || i + 1 == batches) {
                 if (a.top > 0) seg_top[seg][tid] = top;
                 top = -INFINITY;
@@ -318,9 +335,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
     if (tail < hi) {
         tail_logit = logit<FP32>(x, tail);
         see(r, tail_logit, (uint32_t)nvec);
-        if (tail_logit > r.limit) move_reference(r, tail_logit, kk);
-        const float nm = r.m == -INFINITY ? 0.f : -r.m;
-        add_pair(r, tail_logit, -INFINITY, pack2(nm, nm), kk2);
+        add_pair(r.s, r.e, tail_logit, -INFINITY, reference(r, tail_logit, kk), kk2);
     }
     // References become the largest logits themselves: ln of the final sum is
     // then small where one entry holds the row, and exact to fp32.
