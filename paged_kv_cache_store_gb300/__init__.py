@@ -395,9 +395,9 @@ def _q8_pool(k_cache, v_cache, k_scale, v_scale):
     shape = k_cache.shape
     if fmt is None or len(shape) != 4:
         raise TypeError("k_cache must be a [num_blocks, Hkv, B, D] tensor of float8_e4m3fn or int8")
-    _need(v_cache, dtype, "v_cache")
-    _need(k_scale, torch.uint8, "k_scale")
-    _need(v_scale, torch.uint8, "v_scale")
+    if v_cache.dtype is not dtype or k_scale.dtype is not torch.uint8 or v_scale.dtype is not torch.uint8:
+        raise TypeError(f"v_cache must be {dtype} and k_scale / v_scale {torch.uint8}, got {v_cache.dtype}, "
+                        f"{k_scale.dtype}, {v_scale.dtype}")
     if v_cache.shape != shape or not (k_scale.shape == v_scale.shape == shape[:3]):
         raise ValueError("k_cache / v_cache must be [num_blocks, Hkv, B, D] and k_scale / v_scale [num_blocks, Hkv, B]")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
@@ -460,17 +460,13 @@ def store_kvcache_q8(key, value, k_cache, v_cache, k_scale, v_scale, slot_mappin
     vs = _rows(value, "value", n, hkv, d)
     _slots(slot_mapping, n)
     ctx = _placed(stream, key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping)
-
-    def call():
-        _check(lib().pa_store_kvcache_q8(key.data_ptr(), ks, value.data_ptr(), vs, k_cache.data_ptr(),
-                                         v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                         slot_mapping.data_ptr(), n, hkv, d, B, nb, fmt, _raw_stream()),
-               "pa_store_kvcache_q8")
-
-    if ctx is None:
-        return call()
-    with ctx:
-        return call()
+    if ctx is not None:
+        with ctx:
+            return store_kvcache_q8(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping)
+    _check(lib().pa_store_kvcache_q8(key.data_ptr(), ks, value.data_ptr(), vs, k_cache.data_ptr(),
+                                     v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                     slot_mapping.data_ptr(), n, hkv, d, B, nb, fmt, _raw_stream()),
+           "pa_store_kvcache_q8")
 
 
 def load_kvcache_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k=None, out_v=None, stream=None):
@@ -481,20 +477,17 @@ def load_kvcache_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k=None
     _slots(slot_mapping)
     n = slot_mapping.shape[0]
     ctx = _placed(stream, k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k, out_v)
-
-    def call():
-        k = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device) if out_k is None else out_k
-        v = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device) if out_v is None else out_v
-        _check(lib().pa_load_kvcache_q8(k.data_ptr(), _rows(k, "out_k", n, hkv, d), v.data_ptr(),
-                                        _rows(v, "out_v", n, hkv, d), k_cache.data_ptr(), v_cache.data_ptr(),
-                                        k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(), n, hkv, d, B,
-                                        nb, fmt, _raw_stream()), "pa_load_kvcache_q8")
-        return k, v
-
-    if ctx is None:
-        return call()
-    with ctx:
-        return call()
+    if ctx is not None:
+        with ctx:
+            return load_kvcache_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k, out_v)
+    ks = hkv * d if out_k is None else _rows(out_k, "out_k", n, hkv, d)
+    vs = hkv * d if out_v is None else _rows(out_v, "out_v", n, hkv, d)
+    k = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device) if out_k is None else out_k
+    v = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device) if out_v is None else out_v
+    _check(lib().pa_load_kvcache_q8(k.data_ptr(), ks, v.data_ptr(), vs, k_cache.data_ptr(), v_cache.data_ptr(),
+                                    k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(), n, hkv, d, B, nb,
+                                    fmt, _raw_stream()), "pa_load_kvcache_q8")
+    return k, v
 
 
 def decode_q8_workspace(num_q_heads, num_kv_heads, head_dim=128, device="cuda"):
@@ -528,21 +521,18 @@ def decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
         raise ValueError("workspace must be contiguous")
     scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
     ctx = _placed(stream, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace, out)
-
-    def call():
-        ws = decode_q8_workspace(hq, hkv, d, q.device) if workspace is None else workspace
-        o = torch.empty(batch, hq, d, dtype=torch.bfloat16, device=q.device) if out is None else out
-        _check(lib().pa_decode_q8(o.data_ptr(), q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
-                                  k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
-                                  block_tables.shape[1], context_lens.data_ptr(), batch, hq, hkv, d, B, nb, fmt,
-                                  scale, ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream()),
-               "pa_decode_q8")
-        return o
-
-    if ctx is None:
-        return call()
-    with ctx:
-        return call()
+    if ctx is not None:
+        with ctx:
+            return decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, workspace, out)
+    if workspace is None:
+        workspace = decode_q8_workspace(hq, hkv, d, q.device)
+    if out is None:
+        out = torch.empty(batch, hq, d, dtype=torch.bfloat16, device=q.device)
+    _check(lib().pa_decode_q8(out.data_ptr(), q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
+                              k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+                              context_lens.data_ptr(), batch, hq, hkv, d, B, nb, fmt, scale, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _raw_stream()), "pa_decode_q8")
+    return out
 
 
 class Logprobs(NamedTuple):
@@ -582,28 +572,23 @@ def logprobs(logits, tokens, top_k=0, temperatures=None, out=None, stream=None):
             if tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"out.{name} must be contiguous {list(shape)}")
     ctx = _placed(stream, logits, tokens, temperatures, *(out or ()))
-
-    def call():
-        r = out
-        if r is None:
-            dev, k = logits.device, max(top_k, 0)
-            r = Logprobs(torch.empty(rows, dtype=torch.float32, device=dev),
-                         torch.empty(rows, dtype=torch.float32, device=dev),
-                         torch.empty(rows, k, dtype=torch.int32, device=dev) if k else None,
-                         torch.empty(rows, k, dtype=torch.float32, device=dev) if k else None)
-        # A lone row's stride does not matter; the library wants it well-formed.
-        stride = logits.stride(0) if rows > 1 else -(-vocab // 8) * 8
-        _check(lib().pa_logprobs(r[0].data_ptr(), r[1].data_ptr(), r[2].data_ptr() if top_k > 0 else None,
-                                 r[3].data_ptr() if top_k > 0 else None, logits.data_ptr(), stride,
-                                 1 if logits.dtype == torch.float32 else 0,
-                                 None if temperatures is None else temperatures.data_ptr(), tokens.data_ptr(), rows,
-                                 vocab, top_k, _raw_stream()), "pa_logprobs")
-        return r
-
-    if ctx is None:
-        return call()
-    with ctx:
-        return call()
+    if ctx is not None:
+        with ctx:
+            return logprobs(logits, tokens, top_k, temperatures, out)
+    if out is None:
+        dev, k = logits.device, max(top_k, 0)
+        out = Logprobs(torch.empty(rows, dtype=torch.float32, device=dev),
+                       torch.empty(rows, dtype=torch.float32, device=dev),
+                       torch.empty(rows, k, dtype=torch.int32, device=dev) if k else None,
+                       torch.empty(rows, k, dtype=torch.float32, device=dev) if k else None)
+    # A lone row's stride does not matter; the library wants it well-formed.
+    stride = logits.stride(0) if rows > 1 else -(-vocab // 8) * 8
+    _check(lib().pa_logprobs(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr() if top_k > 0 else None,
+                             out[3].data_ptr() if top_k > 0 else None, logits.data_ptr(), stride,
+                             1 if logits.dtype is torch.float32 else 0,
+                             None if temperatures is None else temperatures.data_ptr(), tokens.data_ptr(), rows, vocab,
+                             top_k, _raw_stream()), "pa_logprobs")
+    return out
 
 
 def set_checked(enabled: bool):
