@@ -6,14 +6,15 @@
 // of scattered blocks by TMA measured 7.1-7.3 TB/s this way and 4.7-4.8 TB/s
 // from 128-byte rows a token apart, [num_blocks, block_size, Hkv, 128].)
 //
-// Store: a half-warp takes up to H heads' rows of one (token, K or V): 16
-// lanes x 16 bytes of bf16 a row, the row's largest magnitude by four shuffles,
-// then 8 codes a lane.  Load: the same the other way.  Both are pure streams
-// (store: 256 bytes read and 129 written a row; load: 129 and 256) that would
-// be bound by instructions if each row found its own slot, block and offset
-// (three divisions; 2.8 TB/s): the unit's rows share them, and the next unit's
-// slot travels while this one's rows do.  H is 8 for calls that fill the GPU
-// with such units, else 2, which spreads short calls over more SMs.
+// Store: eight lanes take up to H heads' rows of one (token, K or V): 2 x 16
+// bytes of bf16 a lane and row (dims 8i.. and 64 + 8i..), the row's largest
+// magnitude by three shuffles, then 16 codes a lane.  Load: the same the other
+// way.  Both are pure streams (store: 256 bytes read and 129 written a row;
+// load: 129 and 256) that would be bound by instructions if each row found its
+// own slot, block and offset (three divisions; 2.8 TB/s): the unit's rows share
+// them, and the next unit's slot travels while this one's rows do.  H is 4 for
+// calls that fill the GPU with such units, else 1, which spreads short calls
+// over more SMs.
 #include <algorithm>
 
 #include "pa_q8.cuh"
@@ -22,6 +23,8 @@ namespace pa {
 namespace {
 
 constexpr int Q8_THREADS = 256;
+constexpr int LANES = 8;                        // of a unit
+constexpr int UNITS = Q8_THREADS / LANES;       // of a CTA
 
 struct Q8Rows {
     uint4 *key, *value;             // the bf16 rows (store: read, load: written)
@@ -35,8 +38,8 @@ struct Q8Rows {
 
 // Up to H heads' rows of a token's K or V.
 struct Unit {
-    uint4 *rows;             // this lane's 16 bytes of the first row
-    uint8_t *codes, *scale;  // its 8 codes, and the row's scale byte
+    uint4 *rows;             // this lane's first 16 bytes of the first row
+    uint8_t *codes, *scale;  // its first 8 codes, and the row's scale byte
     uint32_t n;              // rows
     bool live;               // a slot of the pool
 };
@@ -47,18 +50,18 @@ __device__ __forceinline__ uint32_t token_of(const Q8Rows &a, uint64_t u) {
     return u <= 0xffffffffull ? (uint32_t)u / per : (uint32_t)(u / per);
 }
 template <uint32_t H>
-__device__ __forceinline__ Unit unit_of(const Q8Rows &a, uint64_t u, uint32_t token, int32_t slot, int lane16) {
+__device__ __forceinline__ Unit unit_of(const Q8Rows &a, uint64_t u, uint32_t token, int32_t slot, int lane) {
     const uint32_t rest = (uint32_t)(u - (uint64_t)token * (2 * a.groups));
     const bool is_v = rest >= a.groups;
     const uint32_t head = (is_v ? rest - a.groups : rest) * H;
     Unit r;
     r.n = min(H, a.hkv - head);
-    r.rows = (is_v ? a.value + token * a.value16 : a.key + token * a.key16) + head * (Q8_D / 8) + lane16;
+    r.rows = (is_v ? a.value + token * a.value16 : a.key + token * a.key16) + head * (Q8_D / 8) + lane;
     r.live = slot >= 0 && slot < a.num_slots;
-    if (slot >= 0 && !r.live && rest == 0 && lane16 == 0) record_error(a.err, PA_DEV_BAD_SLOT, token);
+    if (slot >= 0 && !r.live && rest == 0 && lane == 0) record_error(a.err, PA_DEV_BAD_SLOT, token);
     const uint32_t at = r.live ? (uint32_t)slot : 0u, blk = at / a.block, off = at - blk * a.block;
     const int64_t row = ((int64_t)blk * a.hkv + head) * a.block + off;
-    r.codes = (is_v ? a.v_codes : a.k_codes) + row * Q8_D + 8 * lane16;
+    r.codes = (is_v ? a.v_codes : a.k_codes) + row * Q8_D + 8 * lane;
     r.scale = (is_v ? a.v_scales : a.k_scales) + row;
     return r;
 }
@@ -81,47 +84,52 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
 template <int FMT, uint32_t H>
 __global__ void __launch_bounds__(Q8_THREADS) store_kvcache_q8_kernel(const Q8Rows a) {
     pdl_wait_then_release();
-    const int lane16 = threadIdx.x & 15;
-    const unsigned half = 0xffffu << (threadIdx.x & 16);  // this half-warp's lanes
+    const int lane = threadIdx.x % LANES;
+    const unsigned group = 0xffu << (threadIdx.x & 24);  // this unit's lanes
     const uint64_t n = 2ull * a.num_tokens * a.groups;
-    const uint64_t step = (uint64_t)gridDim.x * (Q8_THREADS / 16);
-    uint64_t i = ((uint64_t)blockIdx.x * Q8_THREADS + threadIdx.x) >> 4;
+    const uint64_t step = (uint64_t)gridDim.x * UNITS;
+    uint64_t i = (uint64_t)blockIdx.x * UNITS + threadIdx.x / LANES;
     uint32_t token = i < n ? token_of(a, i) : 0;
     int32_t slot = i < n ? __ldg(a.slots + token) : -1;
     for (; i < n; i += step) {
-        const Unit u = unit_of<H>(a, i, token, slot, lane16);
-        uint4 v[H];
+        const Unit u = unit_of<H>(a, i, token, slot, lane);
+        uint4 v[H][2];
 #pragma unroll
-        for (uint32_t h = 0; h < H; ++h) {
-            v[h] = make_uint4(0, 0, 0, 0);
-            if (u.live && h < u.n) v[h] = ld_stream16(u.rows + h * (Q8_D / 8));
-        }
+        for (uint32_t h = 0; h < H; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                v[h][j] = make_uint4(0, 0, 0, 0);
+                if (u.live && h < u.n) v[h][j] = ld_stream16(u.rows + h * (Q8_D / 8) + j * LANES);
+            }
         if (i + step < n) {
             token = token_of(a, i + step);
             slot = __ldg(a.slots + token);
         }
-        if (!u.live) continue;  // padding (the half-warp as one)
+        if (!u.live) continue;  // padding (the unit's lanes as one)
 #pragma unroll
         for (uint32_t h = 0; h < H; ++h) {
-            const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+            if (h >= u.n) break;
+            const uint32_t w[8] = {v[h][0].x, v[h][0].y, v[h][0].z, v[h][0].w, v[h][1].x, v[h][1].y, v[h][1].z, v[h][1].w};
             uint32_t mx = w[0] & 0x7fff7fffu;
 #pragma unroll
-            for (int j = 1; j < 4; ++j) mx = max_nan_bf16x2(mx, w[j] & 0x7fff7fffu);
+            for (int j = 1; j < 8; ++j) mx = max_nan_bf16x2(mx, w[j] & 0x7fff7fffu);
 #pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) mx = max_nan_bf16x2(mx, __shfl_xor_sync(half, mx, o));
+            for (int o = LANES / 2; o >= 1; o >>= 1) mx = max_nan_bf16x2(mx, __shfl_xor_sync(group, mx, o));
             // Magnitudes order as their bits (a NaN above all).
             const uint32_t amax = max(mx & 0xffffu, mx >> 16);
             const bool finite = amax < 0x7f80u;
             const int e = q8_exponent<FMT>(amax);
             const float inv = __uint_as_float((uint32_t)(127 - (finite ? e : 0)) << 23);
-            uint2 c;
-            c.x = q8_encode4<FMT>(w[0], w[1], inv);
-            c.y = q8_encode4<FMT>(w[2], w[3], inv);
-            if (!finite) c = make_uint2(0, 0);
-            if (h < u.n) {
-                *reinterpret_cast<uint2 *>(u.codes + (int64_t)h * a.block * Q8_D) = c;
-                if (lane16 == 0) u.scale[(int64_t)h * a.block] = (uint8_t)(finite ? e + 127 : 255);
+            uint8_t *codes = u.codes + (int64_t)h * a.block * Q8_D;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint2 c;
+                c.x = q8_encode4<FMT>(w[4 * j], w[4 * j + 1], inv);
+                c.y = q8_encode4<FMT>(w[4 * j + 2], w[4 * j + 3], inv);
+                if (!finite) c = make_uint2(0, 0);
+                *reinterpret_cast<uint2 *>(codes + j * (Q8_D / 2)) = c;
             }
+            if (lane == 0) u.scale[(int64_t)h * a.block] = (uint8_t)(finite ? e + 127 : 255);
         }
     }
 }
@@ -129,22 +137,24 @@ __global__ void __launch_bounds__(Q8_THREADS) store_kvcache_q8_kernel(const Q8Ro
 template <int FMT, uint32_t H>
 __global__ void __launch_bounds__(Q8_THREADS) load_kvcache_q8_kernel(const Q8Rows a) {
     pdl_wait_then_release();
-    const int lane16 = threadIdx.x & 15;
+    const int lane = threadIdx.x % LANES;
     const uint64_t n = 2ull * a.num_tokens * a.groups;
-    const uint64_t step = (uint64_t)gridDim.x * (Q8_THREADS / 16);
-    uint64_t i = ((uint64_t)blockIdx.x * Q8_THREADS + threadIdx.x) >> 4;
+    const uint64_t step = (uint64_t)gridDim.x * UNITS;
+    uint64_t i = (uint64_t)blockIdx.x * UNITS + threadIdx.x / LANES;
     uint32_t token = i < n ? token_of(a, i) : 0;
     int32_t slot = i < n ? __ldg(a.slots + token) : -1;
     for (; i < n; i += step) {
-        const Unit u = unit_of<H>(a, i, token, slot, lane16);
-        uint2 c[H];
+        const Unit u = unit_of<H>(a, i, token, slot, lane);
+        uint2 c[H][2];
         uint32_t s[H];
 #pragma unroll
         for (uint32_t h = 0; h < H; ++h) {
-            c[h] = make_uint2(0, 0);  // a negative (or bad) slot reads as zeros
+            c[h][0] = c[h][1] = make_uint2(0, 0);  // a negative (or bad) slot reads as zeros
             s[h] = 127;
             if (u.live && h < u.n) {
-                c[h] = __ldg(reinterpret_cast<const uint2 *>(u.codes + (int64_t)h * a.block * Q8_D));
+                const uint2 *codes = reinterpret_cast<const uint2 *>(u.codes + (int64_t)h * a.block * Q8_D);
+                c[h][0] = __ldg(codes);
+                c[h][1] = __ldg(codes + LANES);
                 s[h] = __ldg(u.scale + (int64_t)h * a.block);
             }
         }
@@ -156,8 +166,11 @@ __global__ void __launch_bounds__(Q8_THREADS) load_kvcache_q8_kernel(const Q8Row
         for (uint32_t h = 0; h < H; ++h) {
             if (h >= u.n) break;
             const uint32_t sc = q8_scale_bf16x2(s[h]);
-            const uint2 x = q8_to_bf16<FMT>(c[h].x, sc), y = q8_to_bf16<FMT>(c[h].y, sc);
-            u.rows[h * (Q8_D / 8)] = make_uint4(x.x, x.y, y.x, y.y);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint2 x = q8_to_bf16<FMT>(c[h][j].x, sc), y = q8_to_bf16<FMT>(c[h][j].y, sc);
+                u.rows[h * (Q8_D / 8) + j * LANES] = make_uint4(x.x, x.y, y.x, y.y);
+            }
         }
     }
 }
@@ -165,12 +178,12 @@ __global__ void __launch_bounds__(Q8_THREADS) load_kvcache_q8_kernel(const Q8Row
 template <int FMT, uint32_t H>
 pa_status launch_rows(Q8Rows a, bool store, int sms, cudaStream_t stream) {
     a.groups = (a.hkv + H - 1) / H;
-    // A half-warp per unit and step; at most 8 (load: 16) CTAs of 16 half-warps
-    // per SM.  Sixteen shorten a long load, whose time is in its writes (262144
-    // tokens 250 us instead of 266), and not a store (16384 tokens 21.4, 20.7).
-    const int64_t units = 2LL * a.num_tokens * a.groups, per = Q8_THREADS / 16;
-    const int64_t most = (store ? 8LL : 16LL) * sms;
-    const dim3 grid((unsigned)std::min<int64_t>((units + per - 1) / per, most)), block(Q8_THREADS);
+    // Eight lanes per unit and step; at most 8 (load: 32) CTAs per SM.  A long
+    // load, whose time is in its writes, gains from many short CTAs (262144
+    // tokens: 265 us with 8, 245 with 16, 240 with 32), a store does not (16384
+    // tokens: 19.4 us with 8, 19.5 with 32).
+    const int64_t units = 2LL * a.num_tokens * a.groups, most = (store ? 8LL : 32LL) * sms;
+    const dim3 grid((unsigned)std::min<int64_t>((units + UNITS - 1) / UNITS, most)), block(Q8_THREADS);
     return store ? launch_pdl(store_kvcache_q8_kernel<FMT, H>, grid, block, 0, stream, "store_kvcache_q8_kernel", a)
                  : launch_pdl(load_kvcache_q8_kernel<FMT, H>, grid, block, 0, stream, "load_kvcache_q8_kernel", a);
 }
@@ -179,8 +192,11 @@ template <int FMT>
 pa_status launch_rows(const Q8Rows &a, bool store, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms <= 0) return fail(PA_ERR_CUDA, "no CUDA device");
-    const bool fills = 2LL * a.num_tokens * ((a.hkv + 7) / 8) >= 64LL * sms;
-    return fills ? launch_rows<FMT, 8>(a, store, sms, stream) : launch_rows<FMT, 2>(a, store, sms, stream);
+    // Four CTAs of units per SM and more: four rows a unit (2000 tokens of 8
+    // heads are just below: 4.0 us with one row or two); else one (64 tokens:
+    // 1.8 us, with two 1.9, with eight 3.2).
+    const bool fills = 2LL * a.num_tokens * ((a.hkv + 3) / 4) >= 4LL * UNITS * sms;
+    return fills ? launch_rows<FMT, 4>(a, store, sms, stream) : launch_rows<FMT, 1>(a, store, sms, stream);
 }
 
 pa_status rows_impl(const void *key, int64_t key_row_stride, const void *value, int64_t value_row_stride,
