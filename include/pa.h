@@ -426,7 +426,9 @@ PA_API pa_status pa_sample_gumbel(int32_t *out_tokens, const void *logits, int64
  *                          temperature is not gets NaN and ids -1
  *                          (PA_DEV_BAD_TEMPERATURE).
  *   tokens                 int32 [rows].
- *   top_k                  0..32, at most vocab.
+ *   top_k                  0..32, at most vocab; vocab at most 2^30.
+ * The same call gives the same bits again; the order of a row's sums (so the
+ * last bits) depends on rows and vocab.
  */
 PA_API pa_status pa_logprobs(float *logprobs, float *entropy, int32_t *top_ids, float *top_logprobs,
                              const void *logits, int64_t logits_row_stride, int32_t logits_is_fp32,

@@ -428,7 +428,8 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
     for (int w = 0; w < NW; ++w) nt_max = max(nt_max, wsum[NW + w]);
     const uint32_t least = max(kMinTilesPerCta, (nt_max + kMaxParts - 1) / kMaxParts);
-    const uint32_t ctas = total >= gridDim.x * (uint64_t)least ? gridDim.x : min(gridDim.x, (total + least - 1) / least), cta = blockIdx.x;
+    const uint32_t ctas = total >= gridDim.x * (uint64_t)least ? gridDim.x : (total + least - 1) / least;
+    const uint32_t cta = blockIdx.x;
     if (cta >= ctas) return;
     const Split by_cta((uint32_t)a.Hkv * cost[a.batch], ctas);
     const uint32_t cu = by_cta.start(cta), cu_end = by_cta.start(cta + 1);
@@ -590,7 +591,8 @@ __global__ void __launch_bounds__(NT, 1)
 
             for (int i = 0; i < take; ++i, ++n) {
                 const int stage = n % ST;
-                if (!mbar_wait(&bar[stage], (n / ST) & 1)) {
+                // (The lanes' own clocks may differ at the limit: they decide as one.)
+                if (!__all_sync(FULL, mbar_wait(&bar[stage], (n / ST) & 1))) {
                     if (lane == 0) record_error(a.err, PA_DEV_TIMEOUT, 500 + warp);
                     // Let the copies already issued land before shared memory goes away.
                     for (int j = n + 1; j < issued; ++j) (void)mbar_wait(&bar[j % ST], (j / ST) & 1);

@@ -555,6 +555,7 @@ extern "C" pa_status pa_logprobs(float *logprobs, float *entropy, int32_t *top_i
     if (rows < 0 || vocab < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
     if (rows == 0) return PA_OK;
     if (vocab == 0) return fail(PA_ERR_INVALID_ARG, "vocab must be positive");
+    if (vocab > 1 << 30) return fail(PA_ERR_UNSUPPORTED, "vocab %d (at most 2^30)", vocab);
     if (top_k < 0 || top_k > vocab) return fail(PA_ERR_INVALID_ARG, "top_k must be in [0, vocab]");
     if (top_k > LP_MAX_TOP) return fail(PA_ERR_UNSUPPORTED, "top_k %d (at most %d)", top_k, LP_MAX_TOP);
     if (!logprobs || !entropy || !logits || !tokens || (top_k > 0 && (!top_ids || !top_logprobs)))

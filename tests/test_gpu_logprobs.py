@@ -22,11 +22,9 @@ def place(x, dtype, pad=0):
     return t
 
 
-def check(x, tokens, top, temps=None, dtype=torch.bfloat16, pad=0, logits=None):
-    lg = place(x, dtype, pad) if logits is None else logits
-    r = pa.logprobs(lg, dev_i32(tokens), top, None if temps is None else torch.from_numpy(temps).cuda())
-    assert pa.get_device_error() == (0, 0)
-    want = define(lg.double().cpu().numpy(), tokens, top, temps)
+def compare(r, x, tokens, top, temps=None):
+    """Results r for rows of logits x (float64)."""
+    want = define(x, tokens, top, temps)
     for got, name, tol in ((r.logprobs, "logprobs", "tol_logprobs"), (r.entropy, "entropy", "tol_entropy"),
                            (r.top_logprobs, "top_logprobs", "tol_top")):
         if got is None:
@@ -39,7 +37,13 @@ def check(x, tokens, top, temps=None, dtype=torch.bfloat16, pad=0, logits=None):
         assert not np.any(off > 0), (name, float(off.max()))
     if top:
         assert np.array_equal(r.top_ids.cpu().numpy(), want["top_ids"])
-    return r
+
+
+def check(x, tokens, top, temps=None, dtype=torch.bfloat16, pad=0):
+    lg = place(x, dtype, pad)
+    r = pa.logprobs(lg, dev_i32(tokens), top, None if temps is None else torch.from_numpy(temps).cuda())
+    assert pa.get_device_error() == (0, 0)
+    compare(r, lg.double().cpu().numpy(), tokens, top, temps)
 
 
 def normal(seed, rows, vocab, std=2.0):
@@ -202,6 +206,16 @@ def test_after_the_sampler_in_a_captured_step():
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, other))
     assert pa.get_device_error() == (0, 0)
+
+
+def test_offsets_beyond_32_bits():
+    """The last rows of more than 2^31 logits."""
+    rows, vocab = 16000, 151936
+    big = torch.empty(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    big[-2:].copy_(torch.from_numpy(normal(2, 2, vocab)).cuda())
+    tok = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    r = pa.logprobs(big, tok, 3)
+    compare(pa.Logprobs(*(t[-2:] for t in r)), big[-2:].double().cpu().numpy(), [0, 0], 3)
 
 
 def test_refusals_of_the_binding():

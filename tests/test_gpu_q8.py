@@ -262,6 +262,65 @@ def test_decode_nan_rows_stay_in_their_head(fmt):
     assert np.array_equal(got, want)
 
 
+def test_decode_q_with_infinities_and_nans():
+    """A head's q with a NaN or an infinity makes that head's output NaN, no other's."""
+    inp = make_decode("q nan", 55, 3, 8, 2, [40, 333, 64])
+    pool = make_pool(inp, "e4m3")
+    bits = inp.q.copy()
+    bits[0, 1, 3], bits[1, 6, 127], bits[2, 0, 0] = 0x7F80, 0x7FC0, 0xFF80
+    out = pa.decode_q8(dev_bf16(bits), *dev_pool(*pool, "e4m3"), dev_i32(inp.block_tables), dev_i32(inp.context_lens),
+                       inp.scale)
+    clean = check_decode(inp, "e4m3", pool)
+    hit = torch.zeros(3, 8, dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[1, 6] = hit[2, 0] = True
+    assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], clean[~hit])
+
+
+def test_pool_beyond_32_bit_offsets():
+    """Blocks in the last part of pools of more than 2^32 bytes."""
+    nb, B, hkv = 17000, 256, 8
+    pool = [torch.empty(nb, hkv, B, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)] + \
+           [torch.empty(nb, hkv, B, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    assert pool[0].numel() > 1 << 32
+    bt = np.array([[nb - 1, 3], [nb - 700, -1]], np.int32)
+    ctx, n = np.array([300, 200], np.int32), 500
+    k, v, q = rows(1, 1, n, hkv), rows(1, 2, n, hkv), normal_bf16(1, 3, (2, 16, 128))
+    cu = dev_i32([0, 300, 500])
+    slots = pa.slot_mapping_prefill(dev_i32(bt), cu, cu, B, total_q=n)
+    pa.store_kvcache_q8(dev_bf16(k), dev_bf16(v), *pool, slots)
+    small = [np.zeros((4, hkv, B, 128), np.uint8) for _ in range(2)] + [np.zeros((4, hkv, B), np.uint8) for _ in range(2)]
+    where = np.concatenate([np.arange(300), 2 * B + np.arange(200)])  # the same rows in a small pool
+    q8.store(f64(k), small[0], small[2], where, "e4m3")
+    q8.store(f64(v), small[1], small[3], where, "e4m3")
+    lk, lv = pa.load_kvcache_q8(*pool, slots)
+    sk, sv = pa.load_kvcache_q8(*dev_pool(*small, "e4m3"), dev_i32(where))
+    assert torch.equal(lk, sk) and torch.equal(lv, sv)
+    args = dev_bf16(q), dev_i32(ctx)
+    out = pa.decode_q8(args[0], *pool, dev_i32(bt), args[1])
+    want = pa.decode_q8(args[0], *dev_pool(*small, "e4m3"), dev_i32([[0, 1], [2, -1]]), args[1])
+    assert torch.equal(out, want) and torch.isfinite(out).all()
+    assert pa.get_device_error() == (0, 0)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with its own workspace."""
+    a = make_decode("a", 92, 6, 16, 8, [3000, 40, 700, 1, 2048, 999])
+    b = make_decode("b", 93, 3, 16, 8, [5000, 6000, 31])
+    jobs = []
+    for inp, fmt in ((a, "e4m3"), (b, "int8")):
+        args = [dev_bf16(inp.q), *dev_pool(*make_pool(inp, fmt), fmt), dev_i32(inp.block_tables),
+                dev_i32(inp.context_lens), inp.scale]
+        jobs.append((args, pa.decode_q8(*args), pa.decode_q8_workspace(16, 8), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for j, (args, _, ws, s) in enumerate(jobs):
+            got[j].append(pa.decode_q8(*args, workspace=ws, stream=s))
+    torch.cuda.synchronize()
+    for j, (_, want, _, _) in enumerate(jobs):
+        assert all(torch.equal(g, want) for g in got[j])
+
+
 def test_decode_strided_q_is_the_same():
     inp = make_decode("strided", 61, 4, 8, 2, [100, 40, 700, 64])
     pool = make_pool(inp, "int8")

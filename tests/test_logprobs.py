@@ -58,6 +58,7 @@ def test_argument_checks(L):
     assert call(k=-1) == pa.PA_ERR_INVALID_ARG
     assert call(k=33) == pa.PA_ERR_UNSUPPORTED
     assert call(vocab=4, k=5) == pa.PA_ERR_INVALID_ARG
+    assert call(vocab=(1 << 30) + 8, ls=1 << 31) == pa.PA_ERR_UNSUPPORTED
     assert call(fp32=2) == pa.PA_ERR_INVALID_ARG
     assert call(ls=999) == pa.PA_ERR_INVALID_ARG
     assert call(ls=1004) == pa.PA_ERR_INVALID_ARG          # bf16 rows stay 16-byte aligned
