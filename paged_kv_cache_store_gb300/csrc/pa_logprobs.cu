@@ -35,11 +35,8 @@
 namespace pa {
 namespace {
 
-constexpr int LP_THREADS = 256;
-constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_MAX_CLUSTER = 8;
 constexpr int LP_MAX_TOP = 32;
-constexpr int LP_CAP = 1024;      // collected entries of a chunk
 constexpr int LP_SEGS = 8;        // parts of a thread's vectors with a maximum of their own
 constexpr float LP_LAZY = 32.f;   // log2 headroom before the reference moves
 constexpr float LP_FLOOR = -200.f;  // 2^-200 is 0: keeps 0 * y finite for y = -inf
@@ -201,7 +198,7 @@ __device__ __forceinline__ u64 reference(Run &r, float t, float kk) {
 // A batch of vectors (the first n of them) into the sums; returns the largest
 // logit.  The batch has sums of its own, so that the running ones take one
 // rounding a batch.
-template <bool FP32, int N>
+template <int THREADS, bool FP32, int N>
 __device__ __forceinline__ float take(Run &r, const Vec<FP32> (&v)[N], int n, int vec0, float kk, u64 kk2) {
     float top = -INFINITY;
 #pragma unroll
@@ -210,7 +207,7 @@ __device__ __forceinline__ float take(Run &r, const Vec<FP32> (&v)[N], int n, in
             const float t = v[u].top();
             if (t > r.top) {
                 r.top = t;
-                r.top_vec = (uint32_t)(vec0 + u * LP_THREADS);
+                r.top_vec = (uint32_t)(vec0 + u * THREADS);
             }
             top = fmaxf(top, t);
         }
@@ -253,23 +250,25 @@ __device__ __forceinline__ Stat warp_join(Stat a, float kk) {
     return Stat{m, a.s, a.e};
 }
 
-template <bool FP32>
-__global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a) {
+template <bool FP32, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const LpArgs a) {
+    constexpr int WARPS = THREADS / 32;
+    constexpr int CAP = 4 * THREADS;  // collected entries of a chunk
     pdl_wait_then_release();
     // Distributed shared memory is written only once every CTA of the cluster runs.
     if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    __shared__ u64 buf[LP_CAP];
-    __shared__ float seg_top[LP_SEGS][LP_THREADS];
-    __shared__ u64 group[LP_WARPS][32];
-    __shared__ Stat stats[LP_WARPS];
-    __shared__ uint16_t items[LP_SEGS * LP_THREADS];  // segment, thread
+    __shared__ u64 buf[CAP];
+    __shared__ float seg_top[LP_SEGS][THREADS];
+    __shared__ u64 group[WARPS][32];
+    __shared__ Stat stats[WARPS];
+    __shared__ uint16_t items[LP_SEGS * THREADS];  // segment, thread
     __shared__ int count, nitems;
     __shared__ u64 threshold;
     __shared__ u64 lists[LP_MAX_CLUSTER][LP_MAX_TOP];  // in the cluster's first CTA
     __shared__ Stat cstats[LP_MAX_CLUSTER];            // likewise
     __shared__ u64 mine[LP_MAX_TOP];
     constexpr int UNROLL = FP32 ? 2 : 4;  // vectors of a thread in flight (64 bytes)
-    constexpr int BATCH = UNROLL * LP_THREADS;
+    constexpr int BATCH = UNROLL * THREADS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.cluster;
     const int64_t row = blockIdx.x / (unsigned)S;
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         threshold = 0;
     }
     // The given token's logit, ahead of its use.
-    const bool answers = rank == 0 && tid == LP_THREADS - 1;
+    const bool answers = rank == 0 && tid == THREADS - 1;
     const int32_t tok = answers ? __ldg(a.tokens + row) : -1;
     const float tok_logit = tok >= 0 && tok < a.vocab ? logit<FP32>(x, tok) : 0.f;
 
@@ -301,7 +300,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
     const u64 kk2 = pack2(kk, kk);
     auto fetch = [&](Vec<FP32>(&v)[UNROLL], int i) {  // batch i; a repeat past the end is ignored later
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) v[u].load(x, lo + 8 * min(i * BATCH + tid + u * LP_THREADS, nvec - 1));
+        for (int u = 0; u < UNROLL; ++u) v[u].load(x, lo + 8 * min(i * BATCH + tid + u * THREADS, nvec - 1));
     };
     // Batches of a segment; segment s holds batches [s * per, (s + 1) * per).
     const int batches = (nvec + BATCH - 1) / BATCH, per = (batches + LP_SEGS - 1) / LP_SEGS;
@@ -315,9 +314,9 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
             Vec<FP32> next[UNROLL];
             if (i + 1 < batches) fetch(next, i + 1);
             if ((i + 1) * BATCH <= nvec) {  // (without a test per vector: 201 us instead of 216 for 4096 rows)
-                top = fmaxf(top, take<FP32>(r, v, UNROLL, v0, kk, kk2));
+                top = fmaxf(top, take<THREADS, FP32>(r, v, UNROLL, v0, kk, kk2));
             } else if (v0 < nvec) {
-                top = fmaxf(top, take<FP32>(r, v, (nvec - v0 + LP_THREADS - 1) / LP_THREADS, v0, kk, kk2));
+                top = fmaxf(top, take<THREADS, FP32>(r, v, (nvec - v0 + THREADS - 1) / THREADS, v0, kk, kk2));
             }
             if (--left == 0 || i + 1 == batches) {
                 if (a.top > 0) seg_top[seg][tid] = top;
@@ -359,15 +358,16 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         __syncthreads();
         u64 g0 = group[0][lane], g1 = group[1][lane];  // even and odd warps' lanes
 #pragma unroll
-        for (int w = 2; w < LP_WARPS; w += 2) {
+        for (int w = 2; w < WARPS; w += 2) {
             g0 = max(g0, group[w][lane]);
             g1 = max(g1, group[w + 1][lane]);
         }
-        // Each warp ranks eight of the 64 groups; keys are distinct but for 0 (an
+        // Each warp ranks its share of the 64 groups; keys are distinct but for 0 (an
         // empty group), which the threshold is if fewer than k groups hold any.
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const u64 k = __shfl_sync(FULL, j < 4 ? g0 : g1, warp * 4 + (j & 3));
+        constexpr int SHARE = 32 / WARPS;
+#pragma unroll 8
+        for (int j = 0; j < 2 * SHARE; ++j) {
+            const u64 k = __shfl_sync(FULL, j < SHARE ? g0 : g1, warp * SHARE + j % SHARE);
             const int above = __popc(__ballot_sync(FULL, g0 > k)) + __popc(__ballot_sync(FULL, g1 > k));
             if (above == a.top - 1 && lane == 0) threshold = k;
         }
@@ -376,29 +376,29 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         auto collect = [&](float t, uint32_t vec, int i) {
             if (key_of(t, vec) >= thr) {
                 const int at = atomicAdd(&count, 1);
-                if (at < LP_CAP) buf[at] = key_of(t, (uint32_t)i);
+                if (at < CAP) buf[at] = key_of(t, (uint32_t)i);
             }
         };
         if (own != 0 && own >= thr) {
             const float thr_top = thr >> 32 ? from_ordered((uint32_t)(thr >> 32)) : -INFINITY;
             for (int seg = 0; seg * per < batches; ++seg)
-                if (seg_top[seg][tid] >= thr_top) items[atomicAdd(&nitems, 1)] = (uint16_t)(seg * LP_THREADS + tid);
+                if (seg_top[seg][tid] >= thr_top) items[atomicAdd(&nitems, 1)] = (uint16_t)(seg * THREADS + tid);
             if (tail < hi) collect(tail_logit, (uint32_t)nvec, tail);
         }
         __syncthreads();
         // An item's vectors: segment's batches, UNROLL of the thread's in each.
         const int vecs = per * UNROLL, work = nitems * vecs;
-        for (int w0 = tid; w0 < work; w0 += 2 * LP_THREADS) {
+        for (int w0 = tid; w0 < work; w0 += 2 * THREADS) {
             Vec<FP32> v[2];
             int at[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int w = w0 + u * LP_THREADS;
+                const int w = w0 + u * THREADS;
                 at[u] = nvec;
                 if (w < work) {
                     const int item = w / vecs, j = w - item * vecs;
-                    at[u] = (items[item] / LP_THREADS * per + j / UNROLL) * BATCH + j % UNROLL * LP_THREADS +
-                            items[item] % LP_THREADS;
+                    at[u] = (items[item] / THREADS * per + j / UNROLL) * BATCH + j % UNROLL * THREADS +
+                            items[item] % THREADS;
                 }
                 if (at[u] < nvec) v[u].load(x, lo + 8 * at[u]);
             }
@@ -415,15 +415,15 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (hit >> j & 1) {
-                        if (to < LP_CAP) buf[to] = key_of(t[j], (uint32_t)(lo + 8 * at[u] + j));
+                        if (to < CAP) buf[to] = key_of(t[j], (uint32_t)(lo + 8 * at[u] + j));
                         ++to;
                     }
             }
         }
         __syncthreads();
         const int n = count;
-        if (n >= want && n <= LP_CAP) {
-            for (int i = tid; i < n; i += LP_THREADS) {
+        if (n >= want && n <= CAP) {
+            for (int i = tid; i < n; i += THREADS) {
                 const u64 k = buf[i];
                 int above = 0;
                 int j = 0;
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
             u64 last = ~0ull;
             for (int i = 0; i < want; ++i) {
                 u64 best = 0;
-                for (int e = lo + tid; e < hi; e += LP_THREADS) {
+                for (int e = lo + tid; e < hi; e += THREADS) {
                     const u64 k = key_of(logit<FP32>(x, e), (uint32_t)e);
                     if (k < last && k > best) best = k;
                 }
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
                 __syncthreads();
                 best = group[0][0];
 #pragma unroll
-                for (int w = 1; w < LP_WARPS; ++w) best = max(best, group[0][w]);
+                for (int w = 1; w < WARPS; ++w) best = max(best, group[0][w]);
                 if (tid == 0) mine[i] = best;
                 last = best;
             }
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
     }
     __syncthreads();
     // ---- the CTA's statistics (each warp joins them), to the cluster's first CTA
-    Stat all = warp_join(lane < LP_WARPS ? stats[lane] : Stat{-INFINITY, 0.f, 0.f}, kk);
+    Stat all = warp_join(lane < WARPS ? stats[lane] : Stat{-INFINITY, 0.f, 0.f}, kk);
     if (S > 1) {
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         if (tid < a.top) {
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
         a.logprobs[row] = lp;
         a.entropy[row] = bad_t ? NAN : all.s == 0.f ? 0.f : lsum - 0.6931471805599453f * (all.e / all.s);
     }
-    for (int i = tid; i < S * a.top; i += LP_THREADS) {
+    for (int i = tid; i < S * a.top; i += THREADS) {
         const int c = i / a.top, at = i - c * a.top;
         const u64 k = S > 1 ? lists[c][at] : mine[at];
         if (k == 0) continue;
@@ -519,19 +519,35 @@ __global__ void __launch_bounds__(LP_THREADS, 4) logprobs_kernel(const LpArgs a)
     }
 }
 
-// CTAs per row: the smallest power of two that gives ~4 CTAs per SM over the
-// rows, at most 8 (a portable cluster) and at least 2048 logits per CTA.
+// CTAs per row: the largest power of two with which the rows' CTAs run at once
+// (four of 256 threads per SM), at most 8 (a portable cluster) and at least 2048
+// logits per CTA.  One step more costs a second wave and a cluster's barriers:
+// 256 rows of 151936 28 us with four CTAs a row, 22.5 with two; 512 rows of 8000
+// 13.7 with two, 7.7 with one.
 int lp_ctas_per_row(int rows, int vocab, int sms) {
     int S = 1;
-    while (S < LP_MAX_CLUSTER && (int64_t)rows * S < 4LL * sms && vocab / (2 * S) >= 2048) S *= 2;
+    while (S < LP_MAX_CLUSTER && (int64_t)rows * 2 * S <= 4LL * sms && vocab / (2 * S) >= 2048) S *= 2;
     return S;
 }
 
-template <bool FP32>
+// Threads per CTA.  A CTA streams its chunk, then goes through the selection's
+// phases, some 5 us whatever the chunk; with CTAs of 128 threads twice as many
+// rows are on their way.  That pays where rows wait for a CTA (4096 rows of 500
+// logits 22.6 us instead of 35.3, of 32000 60.6 instead of 68.8; of 50257 no
+// difference; of 151936 205 instead of 204, with 32 alternatives 257 instead of
+// 228) and for short chunks that fill the GPU once (512 rows of 8000 7.1 instead
+// of 7.7, of 32000 20.0 instead of 17.2 in fp32), not for few rows (40 of 4000
+// 5.2 instead of 5.0).  With 64 threads nothing was faster than with 128.
+int lp_threads(int64_t ctas, int chunk, int sms) {
+    const int most = ctas > 4LL * sms ? 40960 : ctas > 2LL * sms ? 8192 : 0;
+    return chunk <= most ? 128 : 256;
+}
+
+template <bool FP32, int THREADS>
 pa_status launch_logprobs(const LpArgs &a, int32_t rows, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.cluster * (unsigned)rows);
-    cfg.blockDim = dim3(LP_THREADS);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -542,7 +558,7 @@ pa_status launch_logprobs(const LpArgs &a, int32_t rows, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, logprobs_kernel<FP32>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, logprobs_kernel<FP32, THREADS>, a);
     if (e != cudaSuccess) return cuda_fail(e, "logprobs_kernel");
     return check_launch("logprobs_kernel");
 }
@@ -584,5 +600,7 @@ extern "C" pa_status pa_logprobs(float *logprobs, float *entropy, int32_t *top_i
     a.cluster = lp_ctas_per_row(rows, vocab, sms);
     a.err = device_error_ptr();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return logits_is_fp32 ? launch_logprobs<true>(a, rows, s) : launch_logprobs<false>(a, rows, s);
+    if (lp_threads((int64_t)rows * a.cluster, (vocab + a.cluster - 1) / a.cluster, sms) == 128)
+        return logits_is_fp32 ? launch_logprobs<true, 128>(a, rows, s) : launch_logprobs<false, 128>(a, rows, s);
+    return logits_is_fp32 ? launch_logprobs<true, 256>(a, rows, s) : launch_logprobs<false, 256>(a, rows, s);
 }

@@ -65,11 +65,13 @@ def test_vocabulary_sizes(vocab, dtype):
           temps=rng.uniform(0.3, 2.0, 4).astype(F32))
 
 
-@pytest.mark.parametrize("rows", [1, 2, 40, 75, 151, 700])
-def test_row_counts(rows):
-    """Every cluster size, and more rows than CTAs that run at once."""
+@pytest.mark.parametrize("vocab", [20011, 3001])
+@pytest.mark.parametrize("rows", [1, 2, 40, 75, 151, 320, 700])
+def test_row_counts(rows, vocab):
+    """Every cluster size and both CTA sizes, and more rows than CTAs that run at once."""
     rng = np.random.default_rng(rows)
-    check(normal(rows, rows, 20011), rng.integers(0, 20011, rows), 5)
+    for dtype in (torch.bfloat16, torch.float32):
+        check(normal(rows, rows, vocab), rng.integers(0, vocab, rows), 20, dtype=dtype)
 
 
 def test_qwen3_vocabulary_at_the_sampling_temperatures():
@@ -132,19 +134,21 @@ def test_nan_and_infinite_logits():
 
 def test_large_entries_packed_together():
     """Orders and layouts in which one thread, warp or CTA owns every large entry."""
-    vocab = 60000
-    up = np.linspace(-30, 30, vocab, dtype=F32)
-    stride = up.copy()
-    stride[0::2048] = 100 + np.arange(len(stride[0::2048]), dtype=F32)   # one thread's first logits
-    block = up.copy()
-    block[1000:1400] = 50 + np.arange(400, dtype=F32)
-    every = normal(1, 1, vocab)[0]
-    for k in range(8):
-        every[k::2048] = 40 + 0.01 * np.arange(len(every[k::2048]), dtype=F32)  # one thread's every logit
-    x = np.stack([up, up[::-1], stride, block, every])
-    for rows in (x, np.repeat(x, 130, axis=0)):
-        for top in (5, 32):
-            check(rows, np.arange(len(rows)) % vocab, top, dtype=torch.float32)
+    for vocab in (60000, 30000):
+        up = np.linspace(-30, 30, vocab, dtype=F32)
+        block = up.copy()
+        block[1000:1400] = 50 + np.arange(400, dtype=F32)
+        x = [up, up[::-1], block]
+        for step in (1024, 2048):  # a vector for each of 128 or 256 threads
+            stride, every = up.copy(), normal(1, 1, vocab)[0]
+            stride[0::step] = 100 + np.arange(len(stride[0::step]), dtype=F32)   # one thread's first logits
+            for k in range(8):  # one thread's every logit
+                every[k::step] = 40 + 0.01 * np.arange(len(every[k::step]), dtype=F32)
+            x += [stride, every]
+        x = np.stack(x)
+        for rows in (x, np.repeat(x, 90, axis=0)):
+            for top in (5, 32):
+                check(rows, np.arange(len(rows)) % vocab, top, dtype=torch.float32)
 
 
 def test_overflowing_collection():
