@@ -510,6 +510,28 @@ PA_API pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, co
                               int32_t format, float softmax_scale, void *workspace, size_t workspace_bytes,
                               pa_stream_t stream);
 
+/*
+ * pa_decode_store_q8 -- pa_decode_q8 that first stores the step's new token, as
+ * pa_decode_store does for the bf16 pool: for every sequence with ctx =
+ * context_lens[b] > 0 the rows new_k[b], new_v[b] ([Hkv, 128] bf16, row strides
+ * in elements, multiples of 8; 16-byte aligned) are quantised into the slot of
+ * position ctx-1 -- the same bytes pa_store_kvcache_q8 writes -- and attended to
+ * like every other key, with the same outputs as that call followed by
+ * pa_decode_q8, in one launch.  A block id outside [0, num_blocks) at that
+ * position: the row is not stored and reads as zeros.  A context length out of
+ * range (PA_DEV_BAD_CONTEXT): the row is not stored.  The slots of different
+ * sequences must be distinct.  Other arguments and the workspace as
+ * pa_decode_q8.
+ */
+PA_API pa_status pa_decode_store_q8(void *out, const void *q, int64_t q_row_stride, const void *new_k,
+                                    int64_t new_k_row_stride, const void *new_v, int64_t new_v_row_stride,
+                                    void *k_cache, void *v_cache, void *k_scale, void *v_scale,
+                                    const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *context_lens, int32_t batch, int32_t num_q_heads,
+                                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                    int32_t num_blocks, int32_t format, float softmax_scale, void *workspace,
+                                    size_t workspace_bytes, pa_stream_t stream);
+
 /* --------------------------------------------------------------------------
  * Host block manager: the pool's allocator and prefix cache, whose block
  * tables the kernels above consume.  Host code only (no GPU, no CUDA calls).

@@ -67,6 +67,8 @@ SIGNATURES = {
     "pa_decode_q8_workspace_size": (_sz, [_i32, _i32, _i32]),
     "pa_decode_q8": (C.c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
                                _i32, _i32, _f32, _vp, _sz, _vp]),
+    "pa_decode_store_q8": (C.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32,
+                                     _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _sz, _vp]),
     "pa_set_checked": (C.c_int, [_i32]),
     # host block manager
     "pa_bm_create": (C.c_int, [_i32, _i32, C.POINTER(_vp)]),
@@ -498,10 +500,12 @@ def decode_q8_workspace(num_q_heads, num_kv_heads, head_dim=128, device="cuda"):
 
 
 def decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, softmax_scale=None, workspace=None,
-              out=None, stream=None):
+              out=None, stream=None, new_k=None, new_v=None):
     """Paged decode attention over the 8-bit pool.  q [batch, Hq, 128] bf16
     (rows may be strided); block_tables int32 [batch, max_blocks];
-    context_lens int32 [batch].  Returns out [batch, Hq, 128] bf16."""
+    context_lens int32 [batch].  Returns out [batch, Hq, 128] bf16.  With
+    new_k / new_v ([batch, Hkv, 128] bf16, rows may be strided) the kernel first
+    stores them at position context_lens-1 (pa_decode_store_q8)."""
     (nb, hkv, B, d), fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
     _need(block_tables, torch.int32, "block_tables")
     _need(context_lens, torch.int32, "context_lens")
@@ -519,15 +523,30 @@ def decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
             raise ValueError("out must be contiguous and of q's shape")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    stores = new_k is not None or new_v is not None
+    if stores:
+        if new_k is None or new_v is None:
+            raise ValueError("the fused store needs new_k and new_v")
+        nks, nvs = _rows(new_k, "new_k", batch, hkv, d), _rows(new_v, "new_v", batch, hkv, d)
     scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
-    ctx = _placed(stream, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace, out)
+    ctx = _placed(stream, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace, out, new_k,
+                  new_v)
     if ctx is not None:
         with ctx:
-            return decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, workspace, out)
+            return decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, workspace, out,
+                             None, new_k, new_v)
     if workspace is None:
         workspace = decode_q8_workspace(hq, hkv, d, q.device)
     if out is None:
         out = torch.empty(batch, hq, d, dtype=torch.bfloat16, device=q.device)
+    if stores:
+        _check(lib().pa_decode_store_q8(out.data_ptr(), q.data_ptr(), qs, new_k.data_ptr(), nks, new_v.data_ptr(), nvs,
+                                        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), batch,
+                                        hq, hkv, d, B, nb, fmt, scale, workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), _raw_stream()),
+               "pa_decode_store_q8")
+        return out
     _check(lib().pa_decode_q8(out.data_ptr(), q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
                               k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
                               context_lens.data_ptr(), batch, hq, hkv, d, B, nb, fmt, scale, workspace.data_ptr(),

@@ -41,6 +41,10 @@
 //    CTA that arrives last merges them.  Pieces are combined in list order,
 //    so the result does not depend on timing.  A pair is cut between at most
 //    kMaxParts CTAs (or so), since its parts are read by one CTA.
+//  * Fused store: the warp that has a pair's last tile loads the new token's K
+//    and V row of that kv head when the segment begins, quantises them (four
+//    values a lane), and puts codes and scale bytes into the landed tile and
+//    into the pool.  Nothing else in the launch reads that slot.
 //  * All waits are bounded; a timeout records PA_DEV_TIMEOUT and ends the warp.
 #include <math.h>
 
@@ -114,6 +118,10 @@ struct Args {
     int32_t max_blocks, batch, Hq, Hkv, block_size, box_rows, num_blocks;
     float scale_log2;
     int32_t ctx_limit;
+    // Fused store: the new token's rows (null: none) and the pool they go to.
+    const uint2 *new_k, *new_v;
+    int64_t new_k_stride, new_v_stride;  // in 8-byte units
+    uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
     float *ws_part;
     int *ws_cnt;
     DevError *err;
@@ -162,6 +170,22 @@ template <int FMT>
 __device__ __forceinline__ void v_to_f16(uint32_t w, uint32_t &d0, uint32_t &d1) {
     if (FMT == PA_Q8_INT8) q8_int8_to_f16<0x4240, 0x4341>(w, d0, d1);
     else q8_to_f16<FMT>(__byte_perm(w, 0, 0x3120), d0, d1);
+}
+
+// Quantises the row whose values 4*lane .. +3 the warp's lanes hold (bf16): the
+// lane's four codes, and the row's scale byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t quantise_row(uint2 w, uint32_t &scale) {
+    // Magnitudes order as their bits, infinities and NaN above all.
+    uint32_t mx = max(max(w.x & 0x7fffu, (w.x >> 16) & 0x7fffu), max(w.y & 0x7fffu, (w.y >> 16) & 0x7fffu));
+    mx = __reduce_max_sync(FULL, mx);
+    if (mx >= 0x7f80u) {
+        scale = 255;
+        return 0;
+    }
+    const int e = q8_exponent<FMT>(mx);
+    scale = (uint32_t)(e + 127);
+    return q8_encode4<FMT>(w.x, w.y, __uint_as_float((uint32_t)(127 - e) << 23));
 }
 
 // A position of the flat list.
@@ -584,6 +608,16 @@ __global__ void __launch_bounds__(NT, 1)
                 advance(a, sh, pn);
                 load_q(pn);
             }
+            // The new token is the last key of the pair's last tile (none where the
+            // context length was out of range and is taken as the table's).
+            const bool stores = a.new_k && p.t + take == p.nt && __ldg(a.ctx_lens + p.b) == ctx;
+            uint2 nk = make_uint2(0, 0), nv = nk;
+            int new_blk = -1;
+            if (stores) {
+                nk = __ldg(a.new_k + p.b * a.new_k_stride + p.g * (Q8_D / 4) + lane);
+                nv = __ldg(a.new_v + p.b * a.new_v_stride + p.g * (Q8_D / 4) + lane);
+                new_blk = __ldg(a.block_tables + (int64_t)p.b * a.max_blocks + (int)((uint32_t)(ctx - 1) / (uint32_t)a.block_size));
+            }
             float o[8][4];
 #pragma unroll
             for (int c = 0; c < 8; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
@@ -601,6 +635,27 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 const uint32_t ks = smem_addr(ring + stage * STAGE_BYTES), vs = ks + TILE_BYTES;
                 const int nvalid = min(KT, ctx - (p.t + i) * KT);
+                if (stores && i + 1 == take && new_blk >= 0 && new_blk < a.num_blocks) {
+                    // (An invalid block reads as zeros, as without the fusion.)
+                    const int key = nvalid - 1;  // of the tile
+                    uint32_t ke, ve;
+                    const uint32_t kc = quantise_row<FMT>(nk, ke), vc = quantise_row<FMT>(nv, ve);
+                    const uint32_t at = (uint32_t)key * Q8_D + (uint32_t)(((lane >> 2) ^ (key & 7)) << 4) + (uint32_t)(lane & 3) * 4;
+                    *reinterpret_cast<uint32_t *>(ring + stage * STAGE_BYTES + at) = kc;
+                    *reinterpret_cast<uint32_t *>(ring + stage * STAGE_BYTES + TILE_BYTES + at) = vc;
+                    const int64_t row = ((int64_t)new_blk * a.Hkv + p.g) * a.block_size +
+                                        (int)((uint32_t)(ctx - 1) % (uint32_t)a.block_size);
+                    *reinterpret_cast<uint32_t *>(a.k_codes + row * Q8_D + 4 * lane) = kc;
+                    *reinterpret_cast<uint32_t *>(a.v_codes + row * Q8_D + 4 * lane) = vc;
+                    if (lane == key) {
+                        k_byte[0] = ke;
+                        v_byte[0] = ve;
+                        a.k_scales[row] = (uint8_t)ke;
+                        a.v_scales[row] = (uint8_t)ve;
+                    }
+                    fence_proxy_async_smem();  // a later copy overwrites these bytes
+                    __syncwarp();
+                }
                 // Lane j holds key j's scale, and the exponent of its value's.
                 const float k_sc = q8_scale(k_byte[0]);
                 const float v_ex = v_byte[0] == 255 ? NAN : (float)((int)v_byte[0] - 127);
@@ -841,23 +896,12 @@ bool supported_group(int num_q_heads, int num_kv_heads) {
     return G == 1 || G == 2 || G == 4 || G == 8;
 }
 
-}  // namespace
-}  // namespace pa
-
-extern "C" {
-
-size_t pa_decode_q8_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
-    if (head_dim != pa::Q8_D || !pa::supported_group(num_q_heads, num_kv_heads)) return 0;
-    return pa::ws_layout(num_q_heads / num_kv_heads).total;
-}
-
-pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const void *k_cache, const void *v_cache,
-                       const void *k_scale, const void *v_scale, const int32_t *block_tables,
-                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch, int32_t num_q_heads,
-                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
-                       int32_t format, float softmax_scale, void *workspace, size_t workspace_bytes,
-                       pa_stream_t stream) {
-    using namespace pa;
+pa_status decode_q8_impl(void *out, const void *q, int64_t q_row_stride, const void *new_k, int64_t new_k_row_stride,
+                         const void *new_v, int64_t new_v_row_stride, void *k_cache, void *v_cache, void *k_scale,
+                         void *v_scale, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                         const int32_t *context_lens, int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t format,
+                         float softmax_scale, void *workspace, size_t workspace_bytes, pa_stream_t stream) {
     if (batch < 0) return fail(PA_ERR_INVALID_ARG, "batch < 0");
     if (batch == 0) return PA_OK;
     if (batch > kMaxBatch) return fail(PA_ERR_UNSUPPORTED, "batch %d > %d", batch, kMaxBatch);
@@ -916,6 +960,14 @@ pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const voi
     A.scale_log2 = softmax_scale * 1.4426950408889634f;
     A.ctx_limit = max_blocks_per_seq * block_size;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    A.new_k = static_cast<const uint2 *>(new_k);
+    A.new_v = static_cast<const uint2 *>(new_v);
+    A.new_k_stride = new_k_row_stride / 4;
+    A.new_v_stride = new_v_row_stride / 4;
+    A.k_codes = static_cast<uint8_t *>(k_cache);
+    A.v_codes = static_cast<uint8_t *>(v_cache);
+    A.k_scales = static_cast<uint8_t *>(k_scale);
+    A.v_scales = static_cast<uint8_t *>(v_scale);
     A.ws_part = reinterpret_cast<float *>(ws);
     A.ws_cnt = reinterpret_cast<int *>(ws + W.cnt_off);
     A.err = device_error_ptr();
@@ -925,6 +977,50 @@ pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const voi
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return format == PA_Q8_E4M3 ? launch_g<PA_Q8_E4M3>(G, A, tk, tv, grid, s)
                                 : launch_g<PA_Q8_INT8>(G, A, tk, tv, grid, s);
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+size_t pa_decode_q8_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+    if (head_dim != pa::Q8_D || !pa::supported_group(num_q_heads, num_kv_heads)) return 0;
+    return pa::ws_layout(num_q_heads / num_kv_heads).total;
+}
+
+pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const void *k_cache, const void *v_cache,
+                       const void *k_scale, const void *v_scale, const int32_t *block_tables,
+                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch, int32_t num_q_heads,
+                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                       int32_t format, float softmax_scale, void *workspace, size_t workspace_bytes,
+                       pa_stream_t stream) {
+    return pa::decode_q8_impl(out, q, q_row_stride, nullptr, 0, nullptr, 0, const_cast<void *>(k_cache),
+                              const_cast<void *>(v_cache), const_cast<void *>(k_scale), const_cast<void *>(v_scale),
+                              block_tables, max_blocks_per_seq, context_lens, batch, num_q_heads, num_kv_heads,
+                              head_dim, block_size, num_blocks, format, softmax_scale, workspace, workspace_bytes,
+                              stream);
+}
+
+pa_status pa_decode_store_q8(void *out, const void *q, int64_t q_row_stride, const void *new_k,
+                             int64_t new_k_row_stride, const void *new_v, int64_t new_v_row_stride, void *k_cache,
+                             void *v_cache, void *k_scale, void *v_scale, const int32_t *block_tables,
+                             int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t batch,
+                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                             int32_t num_blocks, int32_t format, float softmax_scale, void *workspace,
+                             size_t workspace_bytes, pa_stream_t stream) {
+    using namespace pa;
+    if (batch > 0) {
+        if (!new_k || !new_v) return fail(PA_ERR_INVALID_ARG, "null new_k/new_v");
+        if (!aligned16(new_k) || !aligned16(new_v)) return fail(PA_ERR_INVALID_ARG, "new_k/new_v must be 16-byte aligned");
+        const int64_t row = (int64_t)num_kv_heads * Q8_D;
+        if (new_k_row_stride < row || new_v_row_stride < row || new_k_row_stride % 8 || new_v_row_stride % 8)
+            return fail(PA_ERR_INVALID_ARG, "new_k/new_v row strides must be >= num_kv_heads*head_dim and multiples of 8");
+    }
+    return decode_q8_impl(out, q, q_row_stride, new_k, new_k_row_stride, new_v, new_v_row_stride, k_cache, v_cache,
+                          k_scale, v_scale, block_tables, max_blocks_per_seq, context_lens, batch, num_q_heads,
+                          num_kv_heads, head_dim, block_size, num_blocks, format, softmax_scale, workspace,
+                          workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -371,6 +371,57 @@ def test_decode_shared_blocks_and_repeats():
 
 
 # ---------------------------------------------------------------------------
+# The store fused into the decode
+# ---------------------------------------------------------------------------
+
+def same_bytes(a, b):
+    return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("hq,hkv,B,ctx", [(16, 8, 256, EDGE_CTX), (64, 8, 16, EDGE_CTX), (3, 3, 48, EDGE_CTX),
+                                          (8, 2, 32, [0, 1, 0, 32, 33, 5000, 64, 0]), (8, 1, 512, [9000])])
+def test_decode_store_is_store_then_decode(hq, hkv, B, ctx, fmt):
+    """Outputs, codes and scales bit by bit, rows inside a wider tensor; slots
+    that hold stale bytes (NaN codes and scales among them) before the call."""
+    inp = make_decode("fused", 7, len(ctx), hq, hkv, [max(c, 1) for c in ctx], block_size=B)
+    inp.context_lens[:] = ctx
+    host = make_pool(inp, fmt)
+    nk, nv = rows(3, 1, len(ctx), hkv, 5), rows(3, 2, len(ctx), hkv, 5)
+    nk[0, 0, 3] = 0x7F80 if ctx[0] > 1 else nk[0, 0, 3]
+    wide = dev_bf16(np.concatenate([nk, nv], axis=1))
+    dk, dv = wide[:, :hkv], wide[:, hkv:]
+    bt, c, q = dev_i32(inp.block_tables), dev_i32(inp.context_lens), dev_bf16(inp.q)
+    apart, fused = dev_pool(*host, fmt), dev_pool(*host, fmt)
+    pa.store_kvcache_q8(dk, dv, *apart, pa.slot_mapping_decode(bt, c, B))
+    want = pa.decode_q8(q, *apart, bt, c, inp.scale)
+    ws = pa.decode_q8_workspace(hq, hkv)
+    for _ in range(2):  # the second call stores the same rows again
+        got = pa.decode_q8(q, *fused, bt, c, inp.scale, workspace=ws, new_k=dk, new_v=dv)
+        assert torch.equal(torch.nan_to_num(got, nan=77.0), torch.nan_to_num(want, nan=77.0))
+        assert same_bytes(fused, apart)
+    assert pa.get_device_error() == (0, 0)
+
+
+def test_decode_store_with_an_invalid_block():
+    inp = make_decode("bad slot", 9, 2, 8, 2, [100, 300])
+    pool = dev_pool(*make_pool(inp, "e4m3"), "e4m3")
+    before = [t.clone() for t in pool]
+    bt = inp.block_tables.copy()
+    bt[0, 0], bt[1, 1] = -1, inp.num_blocks
+    new = dev_bf16(rows(1, 1, 2, 2))
+    out = pa.decode_q8(dev_bf16(inp.q), *pool, dev_i32(bt), dev_i32(inp.context_lens), inp.scale, new_k=new, new_v=new)
+    assert same_bytes(pool, before) and torch.isfinite(out).all() and not out[0].any()
+    pa.get_device_error()
+    pa.decode_q8(dev_bf16(inp.q), *pool, dev_i32(inp.block_tables), dev_i32([5000, -1]), inp.scale, new_k=new, new_v=new)
+    assert pa.get_device_error()[0] == pa.PA_DEV_BAD_CONTEXT and same_bytes(pool, before)
+    with pytest.raises(ValueError):
+        pa.decode_q8(dev_bf16(inp.q), *pool, dev_i32(bt), dev_i32(inp.context_lens), new_k=new)
+    with pytest.raises(ValueError):
+        pa.decode_q8(dev_bf16(inp.q), *pool, dev_i32(bt), dev_i32(inp.context_lens), new_k=new, new_v=new[:1])
+
+
+# ---------------------------------------------------------------------------
 # Together
 # ---------------------------------------------------------------------------
 

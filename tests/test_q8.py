@@ -144,6 +144,23 @@ def test_decode_argument_checks(L):
     assert L.pa_decode_q8_workspace_size(64, 8, 128) <= 32 << 20
 
 
+def test_decode_store_argument_checks(L):
+    def call(**kw):
+        a = dict(out=P, q=P, qs=2048, nk=P, nks=1024, nv=P, nvs=1024, kc=P, vc=P, sk=P, sv=P, bt=P, mb=16, ctx=P,
+                 batch=4, hq=16, hkv=8, d=128, B=256, nb=64, fmt=1, scale=0.088, ws=P, wsb=1 << 30, stream=None)
+        a.update(kw)
+        return L.pa_decode_store_q8(*a.values())
+
+    assert call(batch=0) == pa.PA_OK
+    assert call(nk=None) == pa.PA_ERR_INVALID_ARG
+    assert call(nv=None) == pa.PA_ERR_INVALID_ARG
+    assert call(nk=C.c_void_p(264)) == pa.PA_ERR_INVALID_ARG
+    assert call(nks=1016) == pa.PA_ERR_INVALID_ARG
+    assert call(nvs=1028) == pa.PA_ERR_INVALID_ARG
+    assert call(hq=24) == pa.PA_ERR_UNSUPPORTED                # pa_decode_q8's own checks follow
+    assert call(ws=None) == pa.PA_ERR_WORKSPACE
+
+
 def test_binding_refuses_host_tensors():
     pool = [torch.zeros(2, 2, 16, 128, dtype=torch.int8) for _ in range(2)] + \
            [torch.zeros(2, 2, 16, dtype=torch.uint8) for _ in range(2)]
