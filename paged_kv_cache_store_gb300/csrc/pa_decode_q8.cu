@@ -188,6 +188,14 @@ __device__ __forceinline__ uint32_t quantise_row(uint2 w, uint32_t &scale) {
     return q8_encode4<FMT>(w.x, w.y, __uint_as_float((uint32_t)(127 - e) << 23));
 }
 
+// Adds to a counter: releases what the warp wrote before (ordered by its
+// barrier), acquires what the earlier adders released.
+__device__ __forceinline__ int add_acq_rel(int *p, int v) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
 // A position of the flat list.
 struct Pos {
     int b, g, t, nt;
@@ -536,15 +544,18 @@ __global__ void __launch_bounds__(NT, 1)
             if (++ix < x_end) {
                 advance(a, sh, ip);
                 off += KT;
+                bool other = false;  // another block
                 while (off >= a.block_size) {
                     off -= a.block_size;
                     ++lb;
+                    other = true;
                 }
                 if (ip.t == 0) {  // another pair
                     lb = sub16 < a.block_size ? 0 : 1;
                     off = sub16 - lb * a.block_size;
+                    other = true;
                 }
-                blk = fetch();
+                if (other) blk = fetch();
             }
         };
         int issued = 0;
@@ -847,13 +858,9 @@ __global__ void __launch_bounds__(NT, 1)
             const int c0 = span[began].x, n = span[began].y;
             int last = 0;
             if (lane == 0) {
-                __threadfence();
                 int *cnt = a.ws_cnt + c0 * 8 + h;
-                last = atomicAdd(cnt, 1) == n - 1;
-                if (last) {
-                    __threadfence();
-                    *cnt = 0;  // ready for the next call
-                }
+                last = add_acq_rel(cnt, 1) == n - 1;
+                if (last) *cnt = 0;  // ready for the next call
             }
             if (__shfl_sync(FULL, last, 0)) {
                 __syncwarp();

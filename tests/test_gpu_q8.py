@@ -226,6 +226,20 @@ def test_decode_many_short_sequences():
     assert torch.all(out[torch.from_numpy(ctx == 0).cuda()] == 0)
 
 
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (1, 1)])
+def test_decode_largest_batch(hq, hkv):
+    ctx = np.random.default_rng(5).integers(1, 40, size=2048)
+    ctx[::7] = 1
+    check_decode(make_decode("2048", 33, 2048, hq, hkv, ctx, block_size=16), "e4m3")
+
+
+def test_decode_no_context_at_all():
+    inp = make_decode("zero", 34, 5, 8, 2, [1] * 5)
+    inp.context_lens[:] = 0
+    inp.block_tables[:] = -1
+    assert not check_decode(inp, "int8").any()
+
+
 def test_decode_q_of_extreme_sizes():
     inp = make_decode("q", 41, 3, 8, 2, [50, 300, 17])
     q = f64(inp.q)
