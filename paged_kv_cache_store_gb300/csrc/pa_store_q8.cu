@@ -12,9 +12,9 @@
 // way.  Both are pure streams (store: 256 bytes read and 129 written a row;
 // load: 129 and 256) that would be bound by instructions if each row found its
 // own slot, block and offset (three divisions; 2.8 TB/s): the unit's rows share
-// them, and the next unit's slot travels while this one's rows do.  H is 4 for
-// calls that fill the GPU with such units, else 1, which spreads short calls
-// over more SMs.
+// them, and the next unit's slot travels while this one's rows do.  H is 2 in the
+// store (six CTAs an SM; 16384 tokens 19.0 us, with H = 4 and four CTAs 19.5) and
+// 4 in the load (16384 tokens 14.9 us, with 2 15.8), or less in small calls.
 #include <algorithm>
 
 #include "pa_q8.cuh"
@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
 }
 
 template <int FMT, uint32_t H>
-__global__ void __launch_bounds__(Q8_THREADS) store_kvcache_q8_kernel(const Q8Rows a) {
+__global__ void __launch_bounds__(Q8_THREADS, 6) store_kvcache_q8_kernel(const Q8Rows a) {
     pdl_wait_then_release();
     const int lane = threadIdx.x % LANES;
     const unsigned group = 0xffu << (threadIdx.x & 24);  // this unit's lanes
@@ -175,28 +175,44 @@ __global__ void __launch_bounds__(Q8_THREADS) load_kvcache_q8_kernel(const Q8Row
     }
 }
 
-template <int FMT, uint32_t H>
-pa_status launch_rows(Q8Rows a, bool store, int sms, cudaStream_t stream) {
+// Units of H rows where a token has that many and each SM gets a CTA of them;
+// smaller calls take units of one row, which more SMs share.  With 8 heads, units
+// of one row or of H: 64 tokens stored in 1.8 or 2.2 us, 1000 in 3.0 or 2.5,
+// 16384 in 20.9 or 19.0; 100 loaded in 1.8 or 2.3 (four), 1000 in 2.6 or 2.3 (two),
+// 2000 in 3.5, 3.6 (two) or 3.1, 16384 in 17.0, 15.8 or 14.9.  Fewer heads, 65536
+// tokens loaded: one head in 8.9 or 11.6 (four), two in 17.3, 15.9 or 17.3.
+template <uint32_t H>
+bool units_of(const Q8Rows &a, int sms) {
+    return a.hkv >= H && 2LL * a.num_tokens * ((a.hkv + H - 1) / H) >= (int64_t)UNITS * sms;
+}
+// Eight lanes per unit and step, at most `most` CTAs per SM.  A long load, whose
+// time is in its writes, gains from many short CTAs (262144 tokens: 265 us with
+// 8, 245 with 16, 239 with 32, 237 with 64); a store of 65536 tokens takes 80 us
+// with 8, 70.7 with 16 and 70.1 with 64, one of 16384 20.6, 19.0 and 19.6.
+template <uint32_t H>
+dim3 rows_grid(Q8Rows &a, int64_t most, int sms) {
     a.groups = (a.hkv + H - 1) / H;
-    // Eight lanes per unit and step; at most 8 (load: 32) CTAs per SM.  A long
-    // load, whose time is in its writes, gains from many short CTAs (262144
-    // tokens: 265 us with 8, 245 with 16, 240 with 32), a store does not (16384
-    // tokens: 19.4 us with 8, 19.5 with 32).
-    const int64_t units = 2LL * a.num_tokens * a.groups, most = (store ? 8LL : 32LL) * sms;
-    const dim3 grid((unsigned)std::min<int64_t>((units + UNITS - 1) / UNITS, most)), block(Q8_THREADS);
-    return store ? launch_pdl(store_kvcache_q8_kernel<FMT, H>, grid, block, 0, stream, "store_kvcache_q8_kernel", a)
-                 : launch_pdl(load_kvcache_q8_kernel<FMT, H>, grid, block, 0, stream, "load_kvcache_q8_kernel", a);
+    const int64_t units = 2LL * a.num_tokens * a.groups;
+    return dim3((unsigned)std::min<int64_t>((units + UNITS - 1) / UNITS, most * sms));
+}
+template <int FMT, uint32_t H>
+pa_status launch_store(Q8Rows a, int sms, cudaStream_t stream) {
+    const dim3 grid = rows_grid<H>(a, 16, sms);
+    return launch_pdl(store_kvcache_q8_kernel<FMT, H>, grid, dim3(Q8_THREADS), 0, stream, "store_kvcache_q8_kernel", a);
+}
+template <int FMT, uint32_t H>
+pa_status launch_load(Q8Rows a, int sms, cudaStream_t stream) {
+    const dim3 grid = rows_grid<H>(a, 64, sms);
+    return launch_pdl(load_kvcache_q8_kernel<FMT, H>, grid, dim3(Q8_THREADS), 0, stream, "load_kvcache_q8_kernel", a);
 }
 
 template <int FMT>
 pa_status launch_rows(const Q8Rows &a, bool store, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms <= 0) return fail(PA_ERR_CUDA, "no CUDA device");
-    // Four CTAs of units per SM and more: four rows a unit (2000 tokens of 8
-    // heads are just below: 4.0 us with one row or two); else one (64 tokens:
-    // 1.8 us, with two 1.9, with eight 3.2).
-    const bool fills = 2LL * a.num_tokens * ((a.hkv + 3) / 4) >= 4LL * UNITS * sms;
-    return fills ? launch_rows<FMT, 4>(a, store, sms, stream) : launch_rows<FMT, 1>(a, store, sms, stream);
+    if (store) return units_of<2>(a, sms) ? launch_store<FMT, 2>(a, sms, stream) : launch_store<FMT, 1>(a, sms, stream);
+    if (units_of<4>(a, sms)) return launch_load<FMT, 4>(a, sms, stream);
+    return units_of<2>(a, sms) ? launch_load<FMT, 2>(a, sms, stream) : launch_load<FMT, 1>(a, sms, stream);
 }
 
 pa_status rows_impl(const void *key, int64_t key_row_stride, const void *value, int64_t value_row_stride,

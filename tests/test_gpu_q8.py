@@ -136,6 +136,26 @@ def test_load_bit_exact(hkv, nb, B, fmt):
     assert torch.all(wide[:, hkv] == 7.0)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("hkv", [1, 2, 3, 4, 5, 7, 8])
+def test_long_calls_of_every_head_count(hkv, fmt):
+    """Calls long enough for every number of rows that a unit may take, and
+    head counts that such a number does not divide."""
+    n, nb, B = 6000, 130, 48
+    rng = np.random.default_rng(hkv)
+    slots = rng.permutation(nb * B)[:n].astype(np.int32)
+    slots[rng.random(n) < 0.1] = -1
+    key, value = rows(hkv, 1, n, hkv), rows(hkv, 2, n, hkv, 20)
+    check_store(key, value, slots, nb, B, fmt)
+    kc, vc, ks, vs = stale_pool(3, nb, hkv, B)
+    q8.store(f64(key), kc, ks, slots, fmt)
+    q8.store(f64(value), vc, vs, slots, fmt)
+    got = pa.load_kvcache_q8(*dev_pool(kc, vc, ks, vs, fmt), dev_i32(slots))
+    for t, x in zip(got, (key, value)):
+        want = np.where((slots < 0)[:, None, None], 0.0, q8.values(*q8.quantise(f64(x), fmt), fmt))
+        assert np.array_equal(f64(t.view(torch.int16).cpu().numpy().view(np.uint16)), want)
+
+
 def test_out_of_range_slots_are_recorded():
     kc, vc, ks, vs = stale_pool(2, 2, 2, 16)
     pool = dev_pool(kc, vc, ks, vs, "int8")
