@@ -17,13 +17,15 @@
 //    logits) that first held it, and the largest of each eighth of its
 //    vectors.  The threads form 64 groups, by lane and the warp's parity; the
 //    k-th largest of the groups' maxima, with its vector as the tie-break, is
-//    a threshold that at least k entries of the CTA's chunk reach.  The eighths whose maximum reaches it are listed and
-//    re-read by all threads, which collect the entries that do: for logits in
-//    random order 5 of them at k = 5, 24 at 20 and 44 at 32.  (Re-reading a thread's whole share cost 42 % more DRAM traffic: a
-//    row has left L2 by then.  Re-reading by the owners alone cost 13 us a
-//    row: a warp's lanes had different eighths to wait for.)  The collected
-//    keys (logit, then index) are ranked by counting.  A chunk with more than CAP such entries, or with NaNs that
-//    hid some, is selected by k passes of a plain maximum instead.
+//    a threshold that at least k entries of the CTA's chunk reach.  The
+//    eighths whose maximum reaches it are listed and re-read by all threads,
+//    which collect the entries that do: for logits in random order 5 of them
+//    at k = 5, 24 at 20 and 44 at 32.  (Re-reading a thread's whole share cost
+//    42 % more DRAM traffic: a row has left L2 by then.  Re-reading by the
+//    owners alone cost 13 us a row: a warp's lanes had different eighths to
+//    wait for.)  The collected keys (logit, then index) are ranked by
+//    counting.  A chunk with more than CAP such entries, or with NaNs that hid
+//    some, is selected by k passes of a plain maximum instead.
 //    The CTAs' lists meet in the cluster's first CTA, where an entry's rank is
 //    its place in its own list plus the entries above it in the others'.
 #include <math.h>
