@@ -496,8 +496,11 @@ PA_API pa_status pa_load_kvcache_q8(void *key, int64_t key_row_stride, void *val
  * sequence's outputs of that kv head NaN.
  *   workspace   device scratch of >= pa_decode_q8_workspace_size(...) bytes,
  *               16-byte aligned, ZERO-FILLED before its first use; contract as
- *               for pa_decode (every call leaves it ready for the next; not
- *               shared by calls that may run at the same time).
+ *               for pa_decode (every call leaves it ready for the next; zero it
+ *               again after PA_DEV_TIMEOUT; not shared by calls that may run at
+ *               the same time).  It serves pa_decode_q8 and
+ *               pa_decode_store_q8 calls of any shape for which it is large
+ *               enough, in turn, and no other entry point.
  * Other arguments and limits as pa_decode, and batch * num_kv_heads *
  * max_blocks_per_seq * block_size < 2^35.
  */

@@ -493,8 +493,9 @@ def load_kvcache_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, out_k=None
 
 
 def decode_q8_workspace(num_q_heads, num_kv_heads, head_dim=128, device="cuda"):
-    """Zero-filled workspace for decode_q8 (it depends only on the GQA group);
-    the calls leave it ready for the next one on the same stream."""
+    """Zero-filled workspace for decode_q8 (its size depends only on the GQA
+    group; one of a larger group serves the smaller ones too); the calls leave
+    it ready for the next one on the same stream."""
     n = int(lib().pa_decode_q8_workspace_size(num_q_heads, num_kv_heads, head_dim))
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
 

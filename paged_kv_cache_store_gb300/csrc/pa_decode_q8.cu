@@ -95,18 +95,15 @@ constexpr size_t smem_bytes(int batch, int G) {
 constexpr size_t kMaxSmem = 232448;
 static_assert(smem_bytes(kMaxBatch, 8) <= kMaxSmem, "shared memory budget");
 
-// Workspace: the CTAs' parts [kMaxGrid][2] (of the pair that began in an earlier
-// range, of the one that begins in this range and ends in a later one), then
-// the arrival counters [kMaxGrid][8] (of the latter pair's heads).
-struct WsLayout {
-    size_t cnt_off, total;
-};
-WsLayout ws_layout(int G) {
-    WsLayout w;
-    w.cnt_off = (size_t)2 * kMaxGrid * G * (Q8_D + 4) * 4;
-    w.total = w.cnt_off + (size_t)kMaxGrid * 8 * 4;
-    return w;
-}
+// Workspace: the arrival counters [kMaxGrid][8] (of the heads of the pair that
+// begins in a CTA's range and ends in a later one), then the CTAs' parts
+// [kMaxGrid][2] (of the pair that began in an earlier range, of the one that
+// begins in this range).  The counters, which a call finds and leaves zeroed,
+// come first: their place does not depend on the group, so that calls of other
+// groups, whose parts end elsewhere, never write over them.
+constexpr size_t kWsParts = (size_t)kMaxGrid * 8 * 4;  // bytes before the parts
+static_assert(kWsParts % 256 == 0, "the parts are read 16 bytes at a time");
+size_t ws_bytes(int G) { return kWsParts + (size_t)2 * kMaxGrid * G * (Q8_D + 4) * 4; }
 
 struct Args {
     __nv_bfloat16 *out;
@@ -935,9 +932,9 @@ pa_status decode_q8_impl(void *out, const void *q, int64_t q_row_stride, const v
         return fail(PA_ERR_INVALID_ARG, "out/q/cache/scale pointers must be 16-byte aligned");
     if (!(softmax_scale > 0.f) || !isfinite(softmax_scale))
         return fail(PA_ERR_INVALID_ARG, "softmax_scale must be positive and finite");
-    const WsLayout W = ws_layout(G);
-    if (!workspace || workspace_bytes < W.total)
-        return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", W.total,
+    const size_t need = ws_bytes(G);
+    if (!workspace || workspace_bytes < need)
+        return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                     workspace ? workspace_bytes : (size_t)0);
     if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
 
@@ -975,8 +972,8 @@ pa_status decode_q8_impl(void *out, const void *q, int64_t q_row_stride, const v
     A.v_codes = static_cast<uint8_t *>(v_cache);
     A.k_scales = static_cast<uint8_t *>(k_scale);
     A.v_scales = static_cast<uint8_t *>(v_scale);
-    A.ws_part = reinterpret_cast<float *>(ws);
-    A.ws_cnt = reinterpret_cast<int *>(ws + W.cnt_off);
+    A.ws_cnt = reinterpret_cast<int *>(ws);
+    A.ws_part = reinterpret_cast<float *>(ws + kWsParts);
     A.err = device_error_ptr();
     A.checked = checked_mode() ? 1 : 0;
     const int grid = std::min(sm_count(), kMaxGrid);
@@ -993,7 +990,7 @@ extern "C" {
 
 size_t pa_decode_q8_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
     if (head_dim != pa::Q8_D || !pa::supported_group(num_q_heads, num_kv_heads)) return 0;
-    return pa::ws_layout(num_q_heads / num_kv_heads).total;
+    return pa::ws_bytes(num_q_heads / num_kv_heads);
 }
 
 pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, const void *k_cache, const void *v_cache,

@@ -1,0 +1,44 @@
+"""GPU tests of the 8-bit pool at its edges: workspaces that serve several
+shapes, rows at both ends of bf16's range, scores whose factors leave fp32's
+range, sizes beyond 32 bits."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_store_gb300 as pa
+from oracle import q8
+from paged_kv_cache_store_gb300.workloads import f32_to_bf16_bits, make_decode, normal_bf16
+from gpu_util import dev_bf16, dev_i32, host_f64
+from test_gpu_q8 import FMTS, check_decode, check_store, dev_pool, f64, make_pool, rows, same_bytes
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(x):
+    with np.errstate(over="ignore"):
+        return f32_to_bf16_bits(np.asarray(x).astype(np.float32))
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_one_workspace_serves_every_gqa_group(fused):
+    """A workspace sized for the largest group, used by calls of every group in
+    turn: what one call leaves in it is nothing to the next."""
+    ws = pa.decode_q8_workspace(64, 8)
+    for hq, ctx in [(64, [4000, 77, 1300]), (16, [5000, 5000]), (8, [3000, 1, 900, 6000]), (32, [7000, 255]),
+                    (64, [2500, 9]), (16, [1, 4000, 17])]:
+        inp = make_decode(f"ws {hq}", 20 + hq, len(ctx), hq, 8, ctx)
+        kc, vc, ks, vs = make_pool(inp, "int8")
+        pool = dev_pool(kc, vc, ks, vs, "int8")
+        kw = {}
+        if fused:
+            nk, nv = rows(hq, 1, len(ctx), 8), rows(hq, 2, len(ctx), 8)
+            kw = dict(new_k=dev_bf16(nk), new_v=dev_bf16(nv))
+            at = [int(inp.block_tables[b][(c - 1) // 256]) * 256 + (c - 1) % 256 for b, c in enumerate(ctx)]
+            q8.store(f64(nk), kc, ks, at, "int8")
+            q8.store(f64(nv), vc, vs, at, "int8")
+        out = torch.full((len(ctx), hq, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+        pa.decode_q8(dev_bf16(inp.q), *pool, dev_i32(inp.block_tables), dev_i32(inp.context_lens), inp.scale,
+                     workspace=ws, out=out, **kw)
+        assert pa.get_device_error() == (0, 0)
+        want, tol = q8.decode(f64(inp.q), kc, ks, vc, vs, "int8", inp.block_tables, inp.context_lens, inp.scale)
+        assert np.all(np.abs(host_f64(out) - want) <= tol), (hq, ctx)
