@@ -451,11 +451,12 @@ PA_API pa_status pa_logprobs(float *logprobs, float *entropy, int32_t *top_ids, 
  * scale 255 marks a row that held a NaN or an infinity: it reads as NaN.  The
  * scale is the smallest power of two (at least 2^-126) with
  * max|x| <= 448 * 2^e (PA_Q8_E4M3) or 127 * 2^e (PA_Q8_INT8), and a code is
- * x * 2^-e rounded once, to nearest, ties to even.  The result is a function
- * of the row alone: it depends on no other token, so appending a token never
- * touches older ones.  An error of a value is at most 2^-4 of it (E4M3, above
- * 2^-15 of the row's largest magnitude) or 1/126 of the row's largest
- * magnitude (INT8).
+ * x * 2^-e rounded once, to nearest, ties to even, to a code whose value is
+ * below 2^128 (bf16's last numbers would round up to it: finite rows read back
+ * as finite numbers).  The result is a function of the row alone: it depends on
+ * no other token, so appending a token never touches older ones.  An error of a
+ * value is at most 2^-4 of it (E4M3, above 2^-15 of the row's largest
+ * magnitude) or 1/126 of the row's largest magnitude (INT8).
  * Pointers 16-byte aligned; num_blocks * block_size * num_kv_heads < 2^31.
  * ------------------------------------------------------------------------ */
 

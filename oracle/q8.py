@@ -27,7 +27,9 @@ def code_values(codes: np.ndarray, fmt: str) -> np.ndarray:
 
 
 def quantise(x: np.ndarray, fmt: str):
-    """Codes and scale bytes of rows x [..., 128] (float64 values of bf16)."""
+    """Codes and scale bytes of rows x [..., 128] (float64 values of bf16).  A
+    code is the nearest whose value is below 2^128, the first number that bf16
+    does not hold."""
     x = np.asarray(x, np.float64)
     finite = np.all(np.isfinite(x), axis=-1)
     y = np.where(finite[..., None], x, 0.0)
@@ -36,6 +38,10 @@ def quantise(x: np.ndarray, fmt: str):
     for k in range(-126, 128):  # the smallest power of two that fits (at least 2^-126)
         e = np.where((a > LIMIT[fmt] * 2.0 ** (k - 1)) & (k > e), float(k), e)
     y = y * np.exp2(-e)[..., None]
+    held = _E4M3[:127] if fmt == "e4m3" else np.arange(128.0)
+    for k in np.unique(e):
+        top = held[held * 2.0 ** k < 2.0 ** 128].max()
+        y[e == k] = np.clip(y[e == k], -top, top)
     if fmt == "int8":
         codes = np.rint(y).astype(np.int8).view(np.uint8)
     else:

@@ -180,6 +180,7 @@ __device__ __forceinline__ uint32_t quantise_row(uint2 w, uint32_t &scale) {
         scale = 255;
         return 0;
     }
+    if (mx > kQ8Top<FMT>) w = make_uint2(q8_below_2_128<FMT>(w.x), q8_below_2_128<FMT>(w.y));
     const int e = q8_exponent<FMT>(mx);
     scale = (uint32_t)(e + 127);
     return q8_encode4<FMT>(w.x, w.y, __uint_as_float((uint32_t)(127 - e) << 23));

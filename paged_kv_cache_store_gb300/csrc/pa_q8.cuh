@@ -2,7 +2,9 @@
 //
 // A row (the 128 values of one token and kv head) is held as 128 one-byte
 // codes and one scale byte s: value = code * 2^(s - 127).  s is 255 for a row
-// that held a NaN or an infinity (every value reads back as NaN).
+// that held a NaN or an infinity (every value reads back as NaN).  Finite rows
+// have finite values: a code whose value would be 2^128, which bf16 does not
+// hold, is the one below.
 //
 // The scale is a power of two, so x * 2^-e is exact and a code is ONE rounding
 // of the bf16 value (to nearest, ties to even); a code has at most 7
@@ -27,6 +29,20 @@ __device__ __forceinline__ int q8_exponent(uint32_t amax_bits) {
     const int p = (int)(amax_bits >> 7) - 127, m = (int)(amax_bits & 0x7f);
     const int e = FMT == PA_Q8_E4M3 ? p - 8 + (m > 0x60 ? 1 : 0) : p - 6 + (m > 0x7e ? 1 : 0);
     return max(e, -126);
+}
+
+// Rows with a larger magnitude than this (bf16 bits) may hold numbers that round
+// up to 2^128, as code 256 of scale 2^120 (E4M3) or 64 of 2^122 (INT8); the
+// scales below end before 2^128, at 448 * 2^119 and 127 * 2^121.
+template <int FMT>
+constexpr uint32_t kQ8Top = FMT == PA_Q8_E4M3 ? 0x7f60u : 0x7f7eu;
+// Such a row's pair of bf16, drawn in to the largest numbers that round to the
+// codes below, 240 (from 247) and 63 (from 63.25).
+template <int FMT>
+__device__ __forceinline__ uint32_t q8_below_2_128(uint32_t w) {
+    constexpr uint32_t most = FMT == PA_Q8_E4M3 ? 0x7f777f77u : 0x7f7d7f7du;
+    asm("min.bf16x2 %0, %0, %1;\n\tmax.bf16x2 %0, %0, %2;" : "+r"(w) : "r"(most), "r"(most | 0x80008000u));
+    return w;
 }
 
 // 2^(s - 127) in fp32; NaN for 255.

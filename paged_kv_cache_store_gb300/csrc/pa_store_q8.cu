@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(Q8_THREADS, 6) store_kvcache_q8_kernel(const Q
 #pragma unroll
         for (uint32_t h = 0; h < H; ++h) {
             if (h >= u.n) break;
-            const uint32_t w[8] = {v[h][0].x, v[h][0].y, v[h][0].z, v[h][0].w, v[h][1].x, v[h][1].y, v[h][1].z, v[h][1].w};
+            uint32_t w[8] = {v[h][0].x, v[h][0].y, v[h][0].z, v[h][0].w, v[h][1].x, v[h][1].y, v[h][1].z, v[h][1].w};
             uint32_t mx = w[0] & 0x7fff7fffu;
 #pragma unroll
             for (int j = 1; j < 8; ++j) mx = max_nan_bf16x2(mx, w[j] & 0x7fff7fffu);
@@ -118,6 +118,10 @@ __global__ void __launch_bounds__(Q8_THREADS, 6) store_kvcache_q8_kernel(const Q
             // Magnitudes order as their bits (a NaN above all).
             const uint32_t amax = max(mx & 0xffffu, mx >> 16);
             const bool finite = amax < 0x7f80u;
+            if (amax > kQ8Top<FMT>) {  // rare
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = q8_below_2_128<FMT>(w[j]);
+            }
             const int e = q8_exponent<FMT>(amax);
             const float inv = __uint_as_float((uint32_t)(127 - (finite ? e : 0)) << 23);
             uint8_t *codes = u.codes + (int64_t)h * a.block * Q8_D;

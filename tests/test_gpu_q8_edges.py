@@ -42,3 +42,52 @@ def test_one_workspace_serves_every_gqa_group(fused):
         assert pa.get_device_error() == (0, 0)
         want, tol = q8.decode(f64(inp.q), kc, ks, vc, vs, "int8", inp.block_tables, inp.context_lens, inp.scale)
         assert np.all(np.abs(host_f64(out) - want) <= tol), (hq, ctx)
+
+
+def top_rows():
+    """Rows whose largest magnitudes are bf16's last values (0x7f7f is the
+    largest), at and around what a code would round up to 2^128."""
+    x = f64(normal_bf16(21, 1, (48, 2, 128))) * 2.0 ** 122
+    key = bits(x)
+    for i in range(40):
+        key[i, :, 7 + i] = 0x7F7F - i
+        key[i, :, 99 - i] = 0xFF7F - i // 2
+    key[40] = 0x7F7F
+    key[41] = 0xFF7E
+    key[42, :, ::2] = 0x7F60
+    return key
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_finite_rows_read_back_finite(fmt):
+    """The largest bf16 numbers too: codes as the definition has them, values
+    finite and within the documented error."""
+    key = top_rows()
+    n, hkv = key.shape[:2]
+    slots = np.arange(n, dtype=np.int32)
+    check_store(key, key[::-1].copy(), slots, 3, 16, fmt)
+    pool = pa.kvcache_q8(3, 16, hkv, dtype=FMTS[fmt])
+    pa.store_kvcache_q8(dev_bf16(key), dev_bf16(key), *pool, dev_i32(slots))
+    x = f64(key)
+    for t in pa.load_kvcache_q8(*pool, dev_i32(slots)):
+        got = host_f64(t)
+        assert np.isfinite(got).all()
+        a = np.abs(x).max(-1, keepdims=True)
+        if fmt == "e4m3":
+            big = np.abs(x) >= 2.0 ** -13 * a
+            assert np.all(np.abs(got - x)[big] <= 2.0 ** -4 * np.abs(x)[big])
+        else:
+            assert np.all(np.abs(got - x) <= a / 85)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_fused_store_of_rows_at_the_top(fmt):
+    key = top_rows()
+    n, hkv = key.shape[:2]
+    inp = make_decode("top", 22, n, 4, hkv, [1 + i % 5 for i in range(n)], block_size=16)
+    host = make_pool(inp, fmt)
+    apart, fused = dev_pool(*host, fmt), dev_pool(*host, fmt)
+    bt, c, new = dev_i32(inp.block_tables), dev_i32(inp.context_lens), dev_bf16(key)
+    pa.store_kvcache_q8(new, new, *apart, pa.slot_mapping_decode(bt, c, 16))
+    pa.decode_q8(dev_bf16(inp.q), *fused, bt, c, inp.scale, new_k=new, new_v=new)
+    assert same_bytes(fused, apart)
