@@ -84,7 +84,9 @@ def decode(q, kc, ks, vc, vs, fmt, block_tables, context_lens, scale):
     largest weight at 2^7 or more, so 2^-32 max_p(p * scale_p) * sum_p |code_p|.
     The scores are fp32 (|x| < 64 in base 2, sums of 128 products), and so are
     the exponentials and the weights' sum: each under 2^-14 of a weight, so
-    3 * 2^-14 sum_p p|v|."""
+    3 * 2^-14 sum_p p|v|.
+    Outputs below bf16's normal range are rounded to multiples of 2^-133 (from
+    fp32 numbers that are multiples of 2^-149): under 2^-133."""
     batch, hq, d = q.shape
     hkv, B = kc.shape[1:3]
     G = hq // hkv
@@ -106,5 +108,5 @@ def decode(q, kc, ks, vc, vs, fmt, block_tables, context_lens, scale):
             sv = np.exp2(vs[blk, g, off].astype(np.float64) - 127)
             codes = np.abs(code_values(vc[blk, g, off], fmt)).sum(0)
             tol[b, h] = (2.0 ** -8 * np.abs(out[b, h]) + (2.0 ** -11 + 3 * 2.0 ** -14) * (p @ np.abs(v))
-                         + 2.0 ** -32 * (p * sv).max(-1, keepdims=True) * codes)
+                         + 2.0 ** -32 * (p * sv).max(-1, keepdims=True) * codes + 2.0 ** -133)
     return out, tol

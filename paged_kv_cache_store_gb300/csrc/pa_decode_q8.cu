@@ -315,11 +315,24 @@ __device__ __forceinline__ Merged merge_pieces(const float *base, Index index, u
     return r;
 }
 
+// 2^(mv - m) / l, by which a pair's sum of weighted codes becomes its output, in
+// two factors: value rows near either end of bf16's range have exponents beyond
+// fp32's (mv - m down to -142 and up to 128).  The second is 1, 2^64 or 2^-64, so
+// that the others lose nothing.
+struct OutScale {
+    float f, far;
+    __device__ float operator()(float o) const { return o * f * far; }
+};
+__device__ __forceinline__ OutScale out_scale(float m, float mv, float l) {
+    const float e = mv - m, shift = e < -64.f ? -64.f : e > 64.f ? 64.f : 0.f;
+    return {fast_exp2(e - shift) / l, shift < 0.f ? 0x1p-64f : shift > 0.f ? 0x1p64f : 1.f};
+}
+
 __device__ __forceinline__ void write_out(const Args &a, const Merged &r, int64_t row) {
-    const float f = fast_exp2(r.mv - r.m) / r.l;
+    const OutScale f = out_scale(r.m, r.mv, r.l);
     __nv_bfloat162 *od = reinterpret_cast<__nv_bfloat162 *>(a.out + row * Q8_D + 4 * (threadIdx.x & 31));
-    od[0] = __floats2bfloat162_rn(r.o.x * f, r.o.y * f);
-    od[1] = __floats2bfloat162_rn(r.o.z * f, r.o.w * f);
+    od[0] = __floats2bfloat162_rn(f(r.o.x), f(r.o.y));
+    od[1] = __floats2bfloat162_rn(f(r.o.z), f(r.o.w));
 }
 
 // Merges the parts of a pair that n CTAs from c0 on share (it begins in c0's
@@ -791,12 +804,12 @@ __global__ void __launch_bounds__(NT, 1)
                 l1 += __shfl_xor_sync(FULL, l1, d);
             }
             if (p.t == 0 && take == p.nt) {
-                const float f0 = fast_exp2(mv0 - m0) / l0, f1 = fast_exp2(mv1 - m1) / l1;
+                const OutScale f0 = out_scale(m0, mv0, l0), f1 = out_scale(m1, mv1, l1);
                 __nv_bfloat16 *dst = a.out + ((int64_t)p.b * a.Hq + (int64_t)p.g * G + 2 * t4) * Q8_D + 2 * g4;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    if (h0) *reinterpret_cast<__nv_bfloat162 *>(dst + 16 * c) = __floats2bfloat162_rn(o[c][0] * f0, o[c][2] * f0);
-                    if (h1) *reinterpret_cast<__nv_bfloat162 *>(dst + Q8_D + 16 * c) = __floats2bfloat162_rn(o[c][1] * f1, o[c][3] * f1);
+                    if (h0) *reinterpret_cast<__nv_bfloat162 *>(dst + 16 * c) = __floats2bfloat162_rn(f0(o[c][0]), f0(o[c][2]));
+                    if (h1) *reinterpret_cast<__nv_bfloat162 *>(dst + Q8_D + 16 * c) = __floats2bfloat162_rn(f1(o[c][1]), f1(o[c][3]));
                 }
             } else {
                 // A piece of the pair: only a range's first and last segments can be.

@@ -91,3 +91,26 @@ def test_fused_store_of_rows_at_the_top(fmt):
     pa.store_kvcache_q8(new, new, *apart, pa.slot_mapping_decode(bt, c, 16))
     pa.decode_q8(dev_bf16(inp.q), *fused, bt, c, inp.scale, new_k=new, new_v=new)
     assert same_bytes(fused, apart)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("power", [-122, -119, -115, -110, -70, 70, 110, 122])
+def test_decode_of_small_and_large_values(power, fmt):
+    """Value rows near both ends of bf16's range: the outputs are of their size."""
+    ctx = [1, 3, 40, 700, 5000]
+    inp = make_decode("values", 23, len(ctx), 8, 2, ctx)
+    inp.v_cache[:] = bits(f64(inp.v_cache) * 2.0 ** power)
+    out = check_decode(inp, fmt)
+    assert (out.abs().amax(-1) > 0).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_decode_of_every_scale_byte(fmt):
+    """Value rows under the smallest and the largest scale bytes, 0 and 254 too
+    (which the store does not write), with codes that keep the values in range."""
+    inp = make_decode("bytes", 24, 4, 8, 2, [17, 64, 300, 1])
+    kc, vc, ks, vs = make_pool(inp, fmt)
+    one = np.random.default_rng(3).choice(np.array([0x38, 0xB8, 0x30, 0] if fmt == "e4m3" else [1, 255, 0, 1],
+                                                   np.uint8), size=vc.shape)
+    for byte in (0, 1, 2, 7, 252, 253, 254):
+        check_decode(inp, fmt, (kc, one if byte > 200 else vc, ks, np.full_like(vs, byte)))
