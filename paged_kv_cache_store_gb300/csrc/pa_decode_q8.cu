@@ -315,6 +315,16 @@ __device__ __forceinline__ Merged merge_pieces(const float *base, Index index, u
     return r;
 }
 
+// The factor of a key's and of a head's scale, at most the largest fp32 number
+// (NaN kept).  The two are multiplied first: either alone may take a product of
+// codes out of fp32's range although the score is an ordinary number.  Without
+// the limit a product of 0 would become NaN where both are huge.
+__device__ __forceinline__ float score_scale(float k, float q) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(k * q), "f"(3.402823466e38f));
+    return r;
+}
+
 // 2^(mv - m) / l, by which a pair's sum of weighted codes becomes its output, in
 // two factors: value rows near either end of bf16's range have exponents beyond
 // fp32's (mv - m down to -142 and up to 128).  The second is 1, 2^64 or 2^-64, so
@@ -707,10 +717,10 @@ __global__ void __launch_bounds__(NT, 1)
                     const int key0 = u * 16 + g4, key1 = key0 + 8;
                     const float k0 = __shfl_sync(FULL, k_sc, key0), k1 = __shfl_sync(FULL, k_sc, key1);
                     const float v0 = __shfl_sync(FULL, v_ex, key0), v1 = __shfl_sync(FULL, v_ex, key1);
-                    xx[u][0] = s[u][0] * k0 * qs0;
-                    xx[u][1] = s[u][1] * k0 * qs1;
-                    xx[u][2] = s[u][2] * k1 * qs0;
-                    xx[u][3] = s[u][3] * k1 * qs1;
+                    xx[u][0] = s[u][0] * score_scale(k0, qs0);
+                    xx[u][1] = s[u][1] * score_scale(k0, qs1);
+                    xx[u][2] = s[u][2] * score_scale(k1, qs0);
+                    xx[u][3] = s[u][3] * score_scale(k1, qs1);
                     yy[u][0] = xx[u][0] + v0;
                     yy[u][1] = xx[u][1] + v0;
                     yy[u][2] = xx[u][2] + v1;

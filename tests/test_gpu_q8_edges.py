@@ -114,3 +114,24 @@ def test_decode_of_every_scale_byte(fmt):
                                                    np.uint8), size=vc.shape)
     for byte in (0, 1, 2, 7, 252, 253, 254):
         check_decode(inp, fmt, (kc, one if byte > 200 else vc, ks, np.full_like(vs, byte)))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("k_power,q_power,scale_power", [(124, -110, -18), (125, -120, -9), (-115, 120, -9), (-122, 118, 0)])
+def test_decode_scores_of_huge_and_tiny_factors(k_power, q_power, scale_power, fmt):
+    """Ordinary scores that are products of a huge and a tiny factor."""
+    inp = make_decode("factors", 25, 4, 8, 2, [33, 700, 2, 128])
+    inp.k_cache[:] = bits(f64(inp.k_cache) * 2.0 ** k_power)
+    q = bits(f64(inp.q) * 2.0 ** q_power)
+    check_decode(inp, fmt, q=q, scale=2.0 ** scale_power)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_decode_of_huge_keys_that_are_orthogonal_to_huge_queries(fmt):
+    inp = make_decode("orthogonal", 26, 3, 8, 2, [33, 700, 2])
+    k, q = f64(inp.k_cache) * 2.0 ** 122, f64(inp.q) * 2.0 ** 120
+    k[..., 64:] = 0.0
+    q[..., :64] = 0.0
+    inp.k_cache[:] = bits(k)
+    out = check_decode(inp, fmt, q=bits(q), scale=1.0)
+    assert torch.isfinite(out).all()
