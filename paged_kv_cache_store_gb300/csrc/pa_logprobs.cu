@@ -330,14 +330,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             for (int u = 0; u < UNROLL; ++u) v[u] = next[u];
         }
     }
-    // The ragged end of the row: one logit per thread.
+    // The ragged end of the row: one logit per thread, each a vector of its own
+    // number (after the others, in order), so that equal ones have distinct keys.
     const int tail = lo + 8 * nvec + tid;
     float tail_logit = 0.f;
     if (tail < hi) {
         tail_logit = logit<FP32>(x, tail);
         if (tail_logit > r.top || r.top_vec == 0xffffffffu) {
             r.top = tail_logit != tail_logit ? -INFINITY : tail_logit;
-            r.top_vec = (uint32_t)nvec;
+            r.top_vec = (uint32_t)(nvec + tid);
         }
         add_pair(r.s, r.e, tail_logit, -INFINITY, reference(r, tail_logit, kk), kk2);
     }
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             const float thr_top = thr >> 32 ? from_ordered((uint32_t)(thr >> 32)) : -INFINITY;
             for (int seg = 0; seg * per < batches; ++seg)
                 if (seg_top[seg][tid] >= thr_top) items[atomicAdd(&nitems, 1)] = (uint16_t)(seg * THREADS + tid);
-            if (tail < hi) collect(tail_logit, (uint32_t)nvec, tail);
+            if (tail < hi) collect(tail_logit, (uint32_t)(nvec + tid), tail);
         }
         __syncthreads();
         // An item's vectors: segment's batches, UNROLL of the thread's in each.
