@@ -422,9 +422,10 @@ PA_API pa_status pa_sample_gumbel(int32_t *out_tokens, const void *logits, int64
  *   logits                 [rows, vocab] bf16 (logits_is_fp32 = 0) or fp32 (1);
  *                          row stride in elements, >= vocab and a multiple of 8
  *                          (bf16) or 4 (fp32); 16-byte aligned.
- *   temperatures           fp32 [rows], each > 1e-10, or NULL (1).  A row whose
- *                          temperature is not gets NaN and ids -1
- *                          (PA_DEV_BAD_TEMPERATURE).
+ *   temperatures           fp32 [rows], each > 1e-10, or NULL (1).  Infinite
+ *                          ones give equal probabilities to all logits but
+ *                          -inf.  A row whose temperature is not > 1e-10 gets
+ *                          NaN and ids -1 (PA_DEV_BAD_TEMPERATURE).
  *   tokens                 int32 [rows].
  *   top_k                  0..32, at most vocab; vocab at most 2^30.
  * The same call gives the same bits again; the order of a row's sums (so the

@@ -25,7 +25,8 @@ def logprobs(logits, tokens, top, temperatures=None):
     out["top_ids"] = np.zeros((rows, top), np.int64)
     out["top_logprobs"], out["tol_top"] = np.zeros((rows, top)), np.zeros((rows, top))
     for r in range(rows):
-        z, tok = x[r] / t[r], int(tokens[r])
+        z, tok = x[r].copy(), int(tokens[r])
+        z[z > -np.inf] /= t[r]  # -inf stays, under T = inf too
         # NaN last, then -inf; the sort is stable, so equal logits keep index order.
         order = np.argsort(-np.where(np.isnan(x[r]), -np.inf, x[r]), kind="stable")
         order = np.concatenate([order[~np.isnan(x[r][order])], order[np.isnan(x[r][order])]])[:top]

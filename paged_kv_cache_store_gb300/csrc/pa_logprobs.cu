@@ -277,7 +277,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     const int rank = (int)(blockIdx.x % (unsigned)S);
     const float T = a.temperatures ? __ldg(a.temperatures + row) : 1.f;
     const bool bad_t = !(T > 1e-10f);
-    const float kk = bad_t ? 1.f : 1.4426950408889634f / T;
+    // (At least the smallest fp32 number: under T = inf, -inf stays -inf and every
+    // finite difference has weight 1.)
+    const float kk = bad_t ? 1.f : fmaxf(1.4426950408889634f / T, 0x1p-149f);
     const char *x = static_cast<const char *>(a.logits) + row * a.stride * (FP32 ? 4 : 2);
     // This CTA's chunk of the row, a multiple of 8 logits except at the end.
     const int chunk = (int)((((int64_t)a.vocab + S - 1) / S + 7) & ~7ll);
@@ -482,7 +484,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     // ---- the row's answers
     const float lsum = logf(all.s);
     auto logprob = [&](float t) -> float {
-        if (all.s == 0.f) return -INFINITY;  // a row without a finite logit
+        // A row without a finite logit; a logit of probability 0 (also where T is inf).
+        if (all.s == 0.f || (t == -INFINITY && all.s == all.s)) return -INFINITY;
         return (t - all.m) / T - lsum;
     };
     if (answers) {

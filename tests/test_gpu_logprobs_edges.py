@@ -54,3 +54,16 @@ def test_ties_in_the_ragged_end_take_no_longer():
         assert (out.top_ids == want).all()
         t = device_us(lambda: pa.logprobs(tied, tok, top, out=out))
         assert t <= 2 * device_us(lambda: pa.logprobs(apart, tok, top, out=out)), (top, t)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", [3, 8, 1001, 40000, 40007])
+def test_infinite_and_huge_temperatures(vocab, dtype):
+    """T = inf: uniform over what is not -inf, in whole and in ragged rows."""
+    x = normal(vocab, 5, vocab)
+    x[1, 1:] = -np.inf
+    x[2, ::2] = -np.inf
+    x[3, ::2] = float(torch.finfo(torch.bfloat16).min)
+    x[4, 0] = -np.inf
+    for t in (np.inf, 3e38, 1e20):
+        check(x, [0, 1, 2, 0, vocab - 1], min(5, vocab), np.full(5, t, np.float32), dtype=dtype)
