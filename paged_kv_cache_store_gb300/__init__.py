@@ -440,10 +440,17 @@ def _rows(t, name, n, heads, d):
     return s0 if shape[0] > 1 else heads * d
 
 
+def _fits(n, name):
+    """Sizes are int32 in the library, and ctypes would cut longer ones down."""
+    if not -(1 << 31) <= n < 1 << 31:
+        raise ValueError(f"{name} {n} does not fit 32 bits")
+
+
 def _slots(slot_mapping, n=None):
     _need(slot_mapping, torch.int32, "slot_mapping")
     if slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or (n is not None and slot_mapping.shape[0] != n):
         raise ValueError("slot_mapping must be contiguous with one entry per token")
+    _fits(slot_mapping.shape[0], "number of tokens")
 
 
 def _raw_stream():
@@ -516,6 +523,8 @@ def decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
     qs = _rows(q, "q", batch, hq, d)
     if block_tables.dim() != 2 or block_tables.shape[0] != batch or context_lens.shape != (batch,):
         raise ValueError("block_tables must be [batch, max_blocks] and context_lens [batch]")
+    _fits(batch, "batch")
+    _fits(block_tables.shape[1], "width of block_tables")
     if not (block_tables.is_contiguous() and context_lens.is_contiguous()):
         raise ValueError("block_tables and context_lens must be contiguous")
     if out is not None:
@@ -575,6 +584,8 @@ def logprobs(logits, tokens, top_k=0, temperatures=None, out=None, stream=None):
         raise ValueError("logits must be [rows, vocab] and tokens [rows]")
     rows, vocab = logits.shape
     top_k = int(top_k)
+    for n, name in ((rows, "number of rows"), (vocab, "vocabulary"), (top_k, "top_k")):
+        _fits(n, name)
     if not tokens.is_contiguous() or (vocab > 1 and logits.stride(1) != 1):
         raise ValueError("rows must be contiguous")
     if temperatures is not None:
@@ -596,15 +607,15 @@ def logprobs(logits, tokens, top_k=0, temperatures=None, out=None, stream=None):
         with ctx:
             return logprobs(logits, tokens, top_k, temperatures, out)
     if out is None:
-        dev, k = logits.device, max(top_k, 0)
+        dev, k = logits.device, min(max(top_k, 0), vocab)
         out = Logprobs(torch.empty(rows, dtype=torch.float32, device=dev),
                        torch.empty(rows, dtype=torch.float32, device=dev),
                        torch.empty(rows, k, dtype=torch.int32, device=dev) if k else None,
                        torch.empty(rows, k, dtype=torch.float32, device=dev) if k else None)
     # A lone row's stride does not matter; the library wants it well-formed.
     stride = logits.stride(0) if rows > 1 else -(-vocab // 8) * 8
-    _check(lib().pa_logprobs(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr() if top_k > 0 else None,
-                             out[3].data_ptr() if top_k > 0 else None, logits.data_ptr(), stride,
+    tops = (None, None) if out[2] is None or out[3] is None else (out[2].data_ptr(), out[3].data_ptr())
+    _check(lib().pa_logprobs(out[0].data_ptr(), out[1].data_ptr(), *tops, logits.data_ptr(), stride,
                              1 if logits.dtype is torch.float32 else 0,
                              None if temperatures is None else temperatures.data_ptr(), tokens.data_ptr(), rows, vocab,
                              top_k, _raw_stream()), "pa_logprobs")

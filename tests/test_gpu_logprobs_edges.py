@@ -67,3 +67,16 @@ def test_infinite_and_huge_temperatures(vocab, dtype):
     x[4, 0] = -np.inf
     for t in (np.inf, 3e38, 1e20):
         check(x, [0, 1, 2, 0, vocab - 1], min(5, vocab), np.full(5, t, np.float32), dtype=dtype)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    tok = dev_i32([0])
+    lg = torch.zeros(1, (1 << 32) + 8, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: pa.logprobs(lg, tok), lambda: pa.logprobs(lg[:, :64], tok, 1 << 32),
+                 lambda: pa.logprobs(lg[:, :64], tok, -(1 << 32))):
+        with pytest.raises((ValueError, pa.PagedAttentionError)):
+            call()
+    many = torch.zeros((1 << 32) + 1, dtype=torch.int32, device="cuda")
+    wide = lg.view(-1)[:8].expand((1 << 32) + 1, 8)
+    with pytest.raises(ValueError):
+        pa.logprobs(wide, many)

@@ -135,3 +135,11 @@ def test_decode_of_huge_keys_that_are_orthogonal_to_huge_queries(fmt):
     inp.k_cache[:] = bits(k)
     out = check_decode(inp, fmt, q=bits(q), scale=1.0)
     assert torch.isfinite(out).all()
+
+
+def test_a_table_wider_than_32_bits_is_refused():
+    pool = pa.kvcache_q8(2, 16, 1)
+    q, ctx = torch.zeros(1, 1, 128, dtype=torch.bfloat16, device="cuda"), dev_i32([3])
+    bt = torch.zeros(1, (1 << 32) + 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        pa.decode_q8(q, *pool, bt, ctx)
