@@ -492,9 +492,10 @@ PA_API pa_status pa_load_kvcache_q8(void *key, int64_t key_row_stride, void *val
 /*
  * pa_decode_q8 -- pa_decode over an 8-bit pool (one query token per sequence;
  * store its own key first).  Same definition, with K and V the values the
- * pool stands for; q and out bf16.  The scores use q and the codes exactly
- * (fp32 accumulation); the softmax weights, each times its value row's scale,
- * are rounded to fp16.  A key or value row that reads as NaN makes its
+ * pool stands for; q and out bf16.  The scores use the codes exactly and q to
+ * within 2^-39 of its head's largest element (elements from 2^-31 of it on are
+ * exact), with fp32 accumulation; the softmax weights, each times its value
+ * row's scale, are rounded to fp16.  A key or value row that reads as NaN makes its
  * sequence's outputs of that kv head NaN.
  *   workspace   device scratch of >= pa_decode_q8_workspace_size(...) bytes,
  *               16-byte aligned, ZERO-FILLED before its first use; contract as

@@ -27,8 +27,9 @@
 //    permute and packed subtract for INT8).  One ldmatrix register holds four
 //    dims of a key, or two dims of two keys (.trans); the order in which the
 //    MMA wants them is met by permuting the dims of q and of the output.
-//  * q is brought to fp16 by a power of two per head (exact but for elements
-//    below 2^-14 of the head's largest, off by at most 2^-25 of that).
+//  * q is brought to fp16 by a power of two per head that takes its largest
+//    element to the top of fp16's range: exact but for elements below 2^-31 of
+//    that, which are off by at most 2^-39 of it (fp32 sums lose 2^-24).
 //  * V's scale is folded into the exponent of its weight:
 //    P'_p = 2^(x_p + vs_p - 127 - mv) with a running reference mv of its own,
 //    so the fp16 weights are relative to the largest weighted row, which is
@@ -620,8 +621,9 @@ __global__ void __launch_bounds__(NT, 1)
                              max(qw[c].y & 0x7fffu, (qw[c].y >> 16) & 0x7fffu)));
                 mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
                 mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
-                // 2^-e brings the largest magnitude to [1, 2) ([2, 4) at the top of the range).
-                const int e = min(max((int)(mx >> 7), 1), 253) - 127;
+                // 2^-e brings the largest magnitude to [2^14, 2^15).  A head below 2^-95 goes less
+                // far, to multiples of 2^-24 (bf16's are of 2^-133), which fp16 holds exactly.
+                const int e = min(max((int)(mx >> 7), 32), 254) - 127 - 14;
                 const float f = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {

@@ -143,3 +143,31 @@ def test_a_table_wider_than_32_bits_is_refused():
     bt = torch.zeros(1, (1 << 32) + 1, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         pa.decode_q8(q, *pool, bt, ctx)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("spread", [12, 16, 18, 20, 24])
+def test_decode_q_spread_within_a_head(spread, fmt):
+    """A head whose largest element meets only zeros, so that its scores are
+    those of elements 2^spread smaller."""
+    inp = make_decode("spread", 27, 4, 8, 2, [33, 700, 2, 128])
+    k, q = f64(inp.k_cache), f64(inp.q) * 2.0 ** -spread
+    k[..., 5] = 0.0
+    q[..., 5] = 1.5
+    inp.k_cache[:] = bits(k)
+    check_decode(inp, fmt, q=bits(q), scale=2.0 ** (spread - 4))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_decode_q_at_both_ends_of_the_range(fmt):
+    """Heads whose largest element is bf16's largest, near its smallest, or 0."""
+    inp = make_decode("ends", 29, 4, 8, 2, [33, 700, 2, 128])
+    base = f64(inp.q)
+    for power, scale in ((125, 2.0 ** -125), (-93, 2.0 ** 93), (-96, 2.0 ** 96), (-112, 2.0 ** 112),
+                         (-124, 2.0 ** 124)):
+        q = base * 2.0 ** power * 0.25
+        q[1, 3] = 0.0
+        if power > 0:
+            q[0, 0, 9] = 3.3895313892515355e38
+            q[2, 5, 7] = -3.3895313892515355e38
+        check_decode(inp, fmt, q=bits(q), scale=scale / 8)
