@@ -221,7 +221,11 @@ PA_API pa_status pa_decode(void *out, const void *q, int64_t q_row_stride, const
  * mapping nor a separate store launch.  Afterwards the caches hold exactly what
  * pa_slot_mapping_decode + pa_store_kvcache would have written.  Other
  * arguments, the workspace contract and the outputs are those of pa_decode;
- * new_k / new_v 16-byte aligned.
+ * new_k / new_v 16-byte aligned.  The stored slots must be distinct, and none
+ * may lie in the context of another row of the batch (rows that are one
+ * sequence at lengths n and n+1, say): within the launch nothing orders one
+ * row's store before another row's reads.  Use pa_store_kvcache and then
+ * pa_decode there.
  */
 PA_API pa_status pa_decode_store(void *out, const void *q, int64_t q_row_stride, const void *new_k,
                                  int64_t new_k_row_stride, const void *new_v, int64_t new_v_row_stride,
@@ -525,9 +529,12 @@ PA_API pa_status pa_decode_q8(void *out, const void *q, int64_t q_row_stride, co
  * like every other key, with the same outputs as that call followed by
  * pa_decode_q8, in one launch.  A block id outside [0, num_blocks) at that
  * position: the row is not stored and reads as zeros.  A context length out of
- * range (PA_DEV_BAD_CONTEXT): the row is not stored.  The slots of different
- * sequences must be distinct.  Other arguments and the workspace as
- * pa_decode_q8.
+ * range (PA_DEV_BAD_CONTEXT): the row is not stored.  The stored slots must be
+ * distinct, and none may lie in the context of another row of the batch: within
+ * the launch nothing orders one row's store before another row's reads (rows
+ * that are one sequence at lengths n and n+1, as when draft tokens are scored
+ * together, need pa_store_kvcache_q8 and then pa_decode_q8).  Other arguments
+ * and the workspace as pa_decode_q8.
  */
 PA_API pa_status pa_decode_store_q8(void *out, const void *q, int64_t q_row_stride, const void *new_k,
                                     int64_t new_k_row_stride, const void *new_v, int64_t new_v_row_stride,

@@ -226,7 +226,8 @@ def decode(q, k_cache, v_cache, block_tables, context_lens, softmax_scale=None, 
     caches [num_blocks, B, Hkv, D]; block_tables int32 [batch, max_blocks];
     context_lens int32 [batch].  Returns out [batch, Hq, D] bf16.  With
     new_k / new_v ([batch, Hkv, D] bf16, rows may be strided) the kernel first
-    stores them at position context_lens-1 (pa_decode_store).  With
+    stores them at position context_lens-1 (pa_decode_store); no other row's
+    context may hold a position that is stored (store_kvcache first there).  With
     shared_prefix, sequences that share leading blocks read them once
     (pa_decode_shared_prefix; its workspace is larger)."""
     _need(q, torch.bfloat16, "q")
@@ -513,7 +514,8 @@ def decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
     (rows may be strided); block_tables int32 [batch, max_blocks];
     context_lens int32 [batch].  Returns out [batch, Hq, 128] bf16.  With
     new_k / new_v ([batch, Hkv, 128] bf16, rows may be strided) the kernel first
-    stores them at position context_lens-1 (pa_decode_store_q8)."""
+    stores them at position context_lens-1 (pa_decode_store_q8); no other row's
+    context may hold a position that is stored (store_kvcache_q8 first there)."""
     (nb, hkv, B, d), fmt = _q8_pool(k_cache, v_cache, k_scale, v_scale)
     _need(block_tables, torch.int32, "block_tables")
     _need(context_lens, torch.int32, "context_lens")

@@ -171,3 +171,27 @@ def test_decode_q_at_both_ends_of_the_range(fmt):
             q[0, 0, 9] = 3.3895313892515355e38
             q[2, 5, 7] = -3.3895313892515355e38
         check_decode(inp, fmt, q=bits(q), scale=scale / 8)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_several_tokens_of_one_sequence_in_a_batch(fmt):
+    """Draft tokens of one sequence scored as rows of a batch, over one table at
+    lengths n, n + 1, n + 2: stored by a call of their own (the fused store's
+    slots may not lie in another row's context)."""
+    for n in (30, 31, 254, 1500):
+        inp = make_decode("draft", 28, 3, 8, 2, [n + 3] * 3)
+        bt = np.repeat(inp.block_tables[:1], 3, axis=0)
+        ctx = np.array([n + 1, n + 2, n + 3], np.int32)
+        one = make_decode("draft", 28, 3, 8, 2, [n + 3] * 3)
+        one.block_tables, one.context_lens = bt, ctx
+        kc, vc, ks, vs = make_pool(one, fmt)
+        pool = dev_pool(kc, vc, ks, vs, fmt)
+        nk, nv = rows(n, 1, 3, 2), rows(n, 2, 3, 2)
+        slots = pa.slot_mapping_decode(dev_i32(bt), dev_i32(ctx), 256)
+        pa.store_kvcache_q8(dev_bf16(nk), dev_bf16(nv), *pool, slots)
+        at = slots.cpu().numpy()
+        q8.store(f64(nk), kc, ks, at, fmt)
+        q8.store(f64(nv), vc, vs, at, fmt)
+        out = pa.decode_q8(dev_bf16(inp.q), *pool, dev_i32(bt), dev_i32(ctx), inp.scale)
+        want, tol = q8.decode(f64(inp.q), kc, ks, vc, vs, fmt, bt, ctx, inp.scale)
+        assert np.all(np.abs(host_f64(out) - want) <= tol)
