@@ -460,8 +460,11 @@ PA_API pa_status pa_logprobs(float *logprobs, float *entropy, int32_t *top_ids, 
  * below 2^128 (bf16's last numbers would round up to it: finite rows read back
  * as finite numbers).  The result is a function of the row alone: it depends on
  * no other token, so appending a token never touches older ones.  An error of a
- * value is at most 2^-4 of it (E4M3, above 2^-15 of the row's largest
- * magnitude) or 1/126 of the row's largest magnitude (INT8).
+ * value is at most
+ *   E4M3  the larger of 2^-4 of it and 2^-10 * 2^e (2^-4 of it from 2^-13 of the
+ *         row's largest magnitude on, and anywhere in rows under 448 * 2^-126),
+ *   INT8  1/126 of the row's largest magnitude (1/85 where that is the largest
+ *         bf16 number; 2^-127 for rows under 127 * 2^-126).
  * Pointers 16-byte aligned; num_blocks * block_size * num_kv_heads < 2^31.
  * ------------------------------------------------------------------------ */
 
