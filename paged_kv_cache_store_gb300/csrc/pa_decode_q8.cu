@@ -66,7 +66,15 @@ constexpr int TILE_BYTES = KT * Q8_D;                 // K or V codes of a tile
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;
 constexpr int kMaxBatch = 2048;
 constexpr int kMaxGrid = 160;     // CTAs of the persistent grid (min(SMs, this))
-constexpr uint32_t kMaxParts = 32;     // CTAs that share a pair, about
+// CTAs that share a pair, about.  More stream a lone pair in less time and merge
+// more parts at its end; 16, 32, 64 or 152 of them: one sequence of 32768 keys
+// under one kv head 17.5, 13.7, 14.1 or 20.8 us, of 4096 keys 8.8, 9.5, 11.9 or
+// 11.8, one of 32768 among 255 short ones (one kv head) 24.0, 18.5, 18.4 or 16.6,
+// under eight kv heads 35.5 to 35.7; full batches and long contexts do not differ.
+constexpr uint32_t kMaxParts = 32;
+// Tiles of a CTA, at least (its range then holds the beginning of one): with 2, 4
+// or 8, four sequences of 600 keys at most 7.6, 7.6 or 7.9 us, eight of 300 9.5,
+// 9.5 or 10.1, four of 100 5.4, 5.3 or 5.9.
 constexpr uint32_t kMinTilesPerCta = 2;
 constexpr float kLazyRescale = 8.f;  // log2 headroom before a running reference must move
 constexpr float kWeightTop = 7.f;    // log2 of the largest fp16 weight when its reference moves

@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             const int v0 = i * BATCH + tid;
             Vec<FP32> next[UNROLL];
             if (i + 1 < batches) fetch(next, i + 1);
-            if ((i + 1) * BATCH <= nvec) {  // (without a test per vector: 201 us instead of 216 for 4096 rows)
+            if ((i + 1) * BATCH <= nvec) {  // (without a test per vector: 204 us instead of 216 for 4096 rows)
                 top = fmaxf(top, take<THREADS, FP32>(r, v, UNROLL, v0, kk, kk2));
             } else if (v0 < nvec) {
                 top = fmaxf(top, take<THREADS, FP32>(r, v, (nvec - v0 + THREADS - 1) / THREADS, v0, kk, kk2));

@@ -73,9 +73,10 @@ __device__ __forceinline__ uint32_t q8_encode4(uint32_t lo, uint32_t hi, float i
     return r;
 }
 
-// Two pairs of INT8 codes of a word as f16x2, exactly: the byte (offset by 128)
-// is put under the exponent of 1024 and 1152 is subtracted, one permute and one
-// packed subtract per pair.  A selector names its pair's bytes (0x4140: 0 and 1).
+// Two pairs of INT8 codes of a word as f16x2, exactly, by the well-known way of
+// making floats of small integers: the byte (offset by 128) is put under the
+// exponent of 1024 and 1152 is subtracted, one permute and one packed subtract
+// per pair.  A selector names its pair's bytes (0x4140: 0 and 1).
 template <uint32_t LO, uint32_t HI>
 __device__ __forceinline__ void q8_int8_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
     const uint32_t u = w ^ 0x80808080u;

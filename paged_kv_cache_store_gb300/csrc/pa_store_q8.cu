@@ -13,8 +13,8 @@
 // load: 129 and 256) that would be bound by instructions if each row found its
 // own slot, block and offset (three divisions; 2.8 TB/s): the unit's rows share
 // them, and the next unit's slot travels while this one's rows do.  H is 2 in the
-// store (six CTAs an SM; 16384 tokens 19.0 us, with H = 4 and four CTAs 19.5) and
-// 4 in the load (16384 tokens 14.9 us, with 2 15.8), or less in small calls.
+// store (six CTAs an SM; 16384 tokens 19.1 us, with H = 4 and four CTAs 19.5) and
+// 4 in the load (16384 tokens 14.7 us, with 2 15.8), or less in small calls.
 #include <algorithm>
 
 #include "pa_q8.cuh"
@@ -192,7 +192,7 @@ bool units_of(const Q8Rows &a, int sms) {
 // Eight lanes per unit and step, at most `most` CTAs per SM.  A long load, whose
 // time is in its writes, gains from many short CTAs (262144 tokens: 265 us with
 // 8, 245 with 16, 239 with 32, 237 with 64); a store of 65536 tokens takes 80 us
-// with 8, 70.7 with 16 and 70.1 with 64, one of 16384 20.6, 19.0 and 19.6.
+// with 8, 71 with 16 and 70 with 64, one of 16384 20.6, 19.1 and 19.6.
 template <uint32_t H>
 dim3 rows_grid(Q8Rows &a, int64_t most, int sms) {
     a.groups = (a.hkv + H - 1) / H;
