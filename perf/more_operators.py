@@ -153,9 +153,9 @@ def work(case):
         return {"bytes": 4 * int(keys.sum()) * case["hkv"] * D + 4 * int(n.sum()) * case["hq"] * D,
                 "flops": 4 * D * case["hq"] * int((n * keys).sum())}
     if op == "verify":
-        # The rows of the nodes that are reached (about two thirds of a draft's tokens are kept), one row of
-        # draws, and a row of draft probabilities where one is subtracted.
-        reach = min(case["nodes"], 3 if case["shape"] == "chain" else 4)
+        # The rows of the nodes that are reached (about four with drawn drafts, two with chosen candidates, as
+        # these inputs are), one row of draws, and a row of draft probabilities where one is subtracted.
+        reach = min(case["nodes"], 4 if case["probs"] else 2)
         size = 4 if case["dtype"] == "fp32" else 2
         a_seq = case["vocab"] * (reach * size + 4 + (4 if case["probs"] else 0))
         return {"bytes": case["batch"] * a_seq, "flops": case["batch"] * case["vocab"] * 4 * (reach + 1)}
