@@ -89,7 +89,20 @@ enum {
                                   (no work done); where = bytes of padding needed */
     PA_DEV_BAD_TEMPERATURE = 7, /* sampler, log probabilities: temperature not > 1e-10;
                                   where = row */
-    PA_DEV_BAD_TOKEN = 8       /* log probabilities: token >= vocab; where = row */
+    PA_DEV_BAD_TOKEN = 8,      /* log probabilities: token >= vocab; where = row.
+                                  verification: drafted token outside [0, vocab);
+                                  where = sequence*num_nodes + node */
+    PA_DEV_BAD_TREE = 9        /* drafts: a node's parent is not an earlier node, or a kept
+                                  path does not ascend; where = sequence*num_nodes + node
+                                  (place in the path) */
+};
+
+/* Scaling of rotary frequencies for long contexts (pa_rope_frequencies). */
+enum {
+    PA_ROPE_PLAIN = 0,
+    PA_ROPE_LINEAR = 1,        /* positions divided by a factor */
+    PA_ROPE_NTK = 2,           /* a larger base */
+    PA_ROPE_YARN = 3           /* long wavelengths divided, short ones kept, a ramp between */
 };
 
 /* Code formats of an 8-bit KV pool (pa_store_kvcache_q8 and what reads it). */
@@ -547,6 +560,183 @@ PA_API pa_status pa_decode_store_q8(void *out, const void *q, int64_t q_row_stri
                                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                     int32_t num_blocks, int32_t format, float softmax_scale, void *workspace,
                                     size_t workspace_bytes, pa_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Speculative decoding over the pool.  (An addition of this library: the source
+ * pages decode one token per sequence and step.)
+ *
+ * A step scores a small tree of drafted tokens per sequence in one pass of the
+ * model: node 0 is the token that the drafts continue (the last one of the
+ * sequence, whose K/V is not in the cache yet), node i > 0 a drafted token that
+ * continues node parents[i] < i; a chain has parents[i] = i - 1.  At most 64
+ * nodes.  The nodes' K/V rows take the positions that follow the context, in
+ * the order of the nodes: context_lens[b] counts all keys, the n nodes of the
+ * step the last of them (n = draft_lens[b], or num_drafts for every row with
+ * context_lens[b] > 0 where draft_lens is NULL).  In the order of a step:
+ *   pa_tree_metadata       masks, rotary positions and slots of the nodes
+ *   pa_rope_store_kvcache  rotation of q and k, store of k and v   (per layer)
+ *   pa_decode_tree         attention                               (per layer)
+ *   pa_verify_drafts       which drafts the target keeps, and the next token
+ *   pa_compact_kvcache     the kept nodes' rows moved next to the context
+ * Nodes i >= n of a row are padding: no slot, zero outputs.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * pa_rope_frequencies -- rotary frequencies (host code; freqs and gain are host
+ * pointers).  freqs[i], i < rotary_dim/2, are turns per position as fractions of
+ * 2^64, so that position * freqs[i] modulo 2^64 is the exact turn whatever the
+ * position: f_i = theta^(-2i/R) radians per position, and with `factor` s:
+ *   PA_ROPE_LINEAR  f_i / s
+ *   PA_ROPE_NTK     theta * s^(R/(R-2)) in place of theta
+ *   PA_ROPE_YARN    f_i (1 - r_i) + f_i / s * r_i, r_i = clamp((i - lo)/(hi - lo), 0, 1)
+ *                   with lo, hi = floor, ceil of R ln(original_context / (2 pi beta))
+ *                   / (2 ln theta) at beta_fast and beta_slow (usually 32 and 1),
+ *                   clamped to [0, R-1]; *gain = 0.1 ln s + 1 (else 1)
+ * rotary_dim: a multiple of 16 up to 128; theta > 1, factor >= 1.
+ */
+PA_API pa_status pa_rope_frequencies(uint64_t *freqs, float *gain, int32_t rotary_dim, double theta, int32_t scaling,
+                                     double factor, double original_context, double beta_fast, double beta_slow);
+
+/*
+ * pa_rope -- per-head norm and rotation of q and k.  For each head x of 128 at
+ * positions[t]: with a norm weight (q_norm / k_norm, bf16 [128], NULL: none)
+ *   x <- x / sqrt(mean(x^2) + eps) * weight,
+ * then the pairs (x[i], x[i + R/2]), or (x[2i], x[2i+1]) when interleaved, i < R/2,
+ * R = rotary_dim, are rotated by positions[t] * f_i and multiplied by gain; the
+ * values from R on are not rotated.  fp32 throughout, one rounding to bf16.
+ *   out_q, out_k    bf16; token t's Hq*128 (Hkv*128) values at out + t*stride.
+ *                   out_q may be q itself with its stride, out_k may be key.
+ *   q, key          bf16, row strides in elements: >= a token's values, multiples
+ *                   of 8 (fused-QKV views are allowed).
+ *   positions       int32 [num_tokens].
+ *   freqs           device copy of pa_rope_frequencies' [rotary_dim/2].
+ * Pointers 16-byte aligned (freqs: 8).  num_tokens == 0 is a no-op.
+ */
+PA_API pa_status pa_rope(void *out_q, int64_t out_q_row_stride, void *out_k, int64_t out_k_row_stride, const void *q,
+                         int64_t q_row_stride, const void *key, int64_t key_row_stride, const int32_t *positions,
+                         const uint64_t *freqs, int32_t rotary_dim, int32_t interleaved, float gain,
+                         const void *q_norm, const void *k_norm, float eps, int32_t num_tokens, int32_t num_q_heads,
+                         int32_t num_kv_heads, int32_t head_dim, pa_stream_t stream);
+
+/*
+ * pa_rope_store_kvcache -- pa_rope, with the rotated keys and the values written
+ * into the pool as pa_store_kvcache writes them: same slots, padding (negative
+ * slots: neither K nor V is written, q is rotated all the same), bad slots
+ * (PA_DEV_BAD_SLOT) and layout.  One launch; the caches hold exactly what pa_rope
+ * and then pa_store_kvcache would have written.
+ */
+PA_API pa_status pa_rope_store_kvcache(void *out_q, int64_t out_q_row_stride, const void *q, int64_t q_row_stride,
+                                       const void *key, int64_t key_row_stride, const void *value,
+                                       int64_t value_row_stride, const int32_t *positions, const uint64_t *freqs,
+                                       int32_t rotary_dim, int32_t interleaved, float gain, const void *q_norm,
+                                       const void *k_norm, float eps, void *k_cache, void *v_cache,
+                                       const int32_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                                       int32_t num_kv_heads, int32_t head_dim, int64_t num_slots, pa_stream_t stream);
+
+/*
+ * pa_tree_metadata -- what a step's kernels need of its trees.  For node i < n of
+ * sequence b (outputs [batch, num_drafts]):
+ *   tree_mask     bit j set where j is i or an ancestor of i
+ *   positions     context_lens[b] - n + depth of i (the root's depth is 0)
+ *   slot_mapping  slot of position context_lens[b] - n + i (-1 where the table
+ *                 holds none); padding: mask 0, position 0, slot -1
+ * parents int32 [batch, num_drafts] (entry 0 of a row is not read), NULL: chains.
+ * A parent that is not an earlier node ends the walk up (PA_DEV_BAD_TREE); lengths
+ * that do not fit make the row padding (PA_DEV_BAD_CONTEXT).
+ */
+PA_API pa_status pa_tree_metadata(int64_t *tree_mask, int32_t *positions, int32_t *slot_mapping,
+                                  const int32_t *parents, const int32_t *context_lens, const int32_t *draft_lens,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                                  int32_t num_drafts, int32_t block_size, pa_stream_t stream);
+
+/*
+ * pa_decode_tree -- pa_decode for num_drafts query tokens per sequence, each with
+ * its own set of the drafts' keys.  With n and ctx = context_lens[b] as above,
+ * query i < n sees the keys at positions p < ctx - n, and that of draft j < n (at
+ * position ctx - n + j) where bit j of tree_mask[b][i] is set; tree_mask NULL: the
+ * drafts j <= i.  Any pattern is allowed; a query that sees nothing has output
+ * zero.  num_drafts == 1 with bit 0 set is pa_decode.  What a mask hides does not
+ * matter, NaN and infinities included.  The weights are rounded to bf16, and
+ * normalised by the sum of the rounded ones.
+ *   out           bf16 [batch, num_drafts, Hq, 128] contiguous; zeros for i >= n.
+ *   q             bf16; the Hq*128 values of (b, i) at q + (b*num_drafts + i)*q_row_stride.
+ *   tree_mask     int64 [batch, num_drafts].
+ *   draft_lens    int32 [batch] or NULL.  Lengths that do not fit (ctx < n among
+ *                 them) are recorded as PA_DEV_BAD_CONTEXT and give zeros.
+ *   workspace     >= pa_decode_tree_workspace_size(...) bytes, 16-byte aligned,
+ *                 ZERO-FILLED before its first use; contract as for pa_decode.  It
+ *                 serves calls of any shape for which it is large enough, in turn,
+ *                 and no other entry point.
+ * num_drafts <= 64, batch <= 2048; other arguments and limits as pa_decode, and
+ * batch * num_kv_heads * max_blocks_per_seq * block_size / 64 (twice that above 256
+ * query heads times drafts per kv head) < 2^31.
+ */
+PA_API size_t pa_decode_tree_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                            int32_t num_drafts);
+PA_API pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const void *k_cache,
+                                const void *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                const int32_t *context_lens, const int32_t *draft_lens, const int64_t *tree_mask,
+                                int32_t batch, int32_t num_drafts, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t block_size, int32_t num_blocks, float softmax_scale,
+                                void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_verify_drafts -- which drafted tokens the target model keeps, and the token
+ * after them: speculative sampling from given random numbers.  Per sequence,
+ * from node v = 0: p = softmax(float(logits[b][v]) / T_b), w = p, s = 1, and for
+ * v's children in order, child c with token x:
+ *   with draft_probs (q = draft_probs[b][v], the distribution that each of v's
+ *   children was drawn from on its own):
+ *     kept if uniforms[b][c] * q(x) * s < w(x), else w <- max(w - s q, 0), s <- sum w
+ *   without (children are chosen candidates):
+ *     kept if uniforms[b][c] * s < w(x), else s <- s - w(x), w(x) <- 0.
+ * A kept child becomes v.  Where no child is kept, the sequence's next token is
+ * argmax_i w_i / max(exp_noise[b][i], 1e-10), the lowest index among equals (with p
+ * for w where nothing is left of w): tokens are distributed as the target's own.
+ *   out_tokens   int32 [batch, num_nodes]: the kept tokens, then the next; -1 after.
+ *   out_nodes    int32 [batch, num_nodes]: 0 and the kept nodes; -1 after.
+ *   out_counts   int32 [batch]: entries of either.
+ *   logits       bf16 or fp32, row (b*num_nodes + v); stride as pa_sample_gumbel.
+ *   tokens       int32 [batch, num_nodes] (entry 0 of a row is not used).  One outside
+ *                [0, vocab) is no child (PA_DEV_BAD_TOKEN).
+ *   parents      int32 [batch, num_nodes] or NULL (chains).  A node whose parent is
+ *                not an earlier node is no child (PA_DEV_BAD_TREE).
+ *   uniforms     fp32 [batch, num_nodes] in [0, 1); exp_noise fp32 [batch, vocab], row
+ *                stride a multiple of 4: the caller's random numbers.
+ *   temperatures fp32 [batch], each > 1e-10; else count 0 (PA_DEV_BAD_TEMPERATURE).
+ *   draft_probs  fp32, row (b*probs_rows + v), row stride a multiple of 4, or NULL;
+ *                probs_rows >= num_nodes - 1 (the last node has no children).
+ *   draft_lens   int32 [batch], nodes of each sequence (0: padding, count 0), or NULL.
+ * NaN logits count as -inf, +inf as the largest number.  num_nodes <= 64, batch <=
+ * 65535, vocab <= 2^30; logits, exp_noise and draft_probs 16-byte aligned.  A small
+ * temperature (1e-6) gives greedy verification.
+ */
+PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *out_nodes, int32_t *out_counts, const void *logits,
+                                  int64_t logits_row_stride, int32_t logits_is_fp32, const int32_t *tokens,
+                                  const int32_t *parents, const float *uniforms, const float *exp_noise,
+                                  int64_t noise_row_stride, const float *temperatures, const float *draft_probs,
+                                  int64_t probs_row_stride, int32_t probs_rows, const int32_t *draft_lens,
+                                  int32_t batch, int32_t num_nodes, int32_t vocab, pa_stream_t stream);
+
+/*
+ * pa_compact_kvcache -- after a verification: for j < counts[b] the K and V rows
+ * of position base + nodes[b][j] are copied to position base + j, base =
+ * context_lens[b] - n (n as above), in every layer, as if read before any is
+ * written.  nodes / counts are pa_verify_drafts' out_nodes / out_counts: nodes[b][0]
+ * = 0, ascending, below n; the first one that is not ends its row's moves
+ * (PA_DEV_BAD_TREE).  The context is then base + counts[b] keys long.  Rows of other
+ * positions stay as they are.  A block id outside [0, num_blocks): that row is not
+ * moved (PA_DEV_BAD_BLOCK).
+ *   k_cache, v_cache  the first layer's pools; the next layer's follow
+ *                     k_layer_stride / v_layer_stride elements on (multiples of 8).
+ * Bit-exact.  num_nodes <= 64.
+ */
+PA_API pa_status pa_compact_kvcache(void *k_cache, int64_t k_layer_stride, void *v_cache, int64_t v_layer_stride,
+                                    const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *context_lens, const int32_t *draft_lens, const int32_t *nodes,
+                                    const int32_t *counts, int32_t batch, int32_t num_nodes, int32_t num_layers,
+                                    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                    pa_stream_t stream);
 
 /* --------------------------------------------------------------------------
  * Host block manager: the pool's allocator and prefix cache, whose block

@@ -13,6 +13,9 @@ Entry points (same names as the C ABI without the ``pa_`` prefix):
   sample_gumbel, set_checked, get_device_error;
   kvcache_q8, store_kvcache_q8, load_kvcache_q8, decode_q8_workspace,
   decode_q8 (the 8-bit pool); logprobs;
+  rope_frequencies, rope, rope_store_kvcache, tree_metadata,
+  decode_tree_workspace, decode_tree, verify_drafts, compact_kvcache
+  (speculative decoding);
   block_manager.BlockManager wraps the host block manager (pa_bm_*).
 """
 from __future__ import annotations
@@ -29,8 +32,9 @@ LIB_PATH = os.path.join(_PKG, "libpa.so")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA, PA_ERR_DEVICE_CHECK = range(6)
 (PA_DEV_TIMEOUT, PA_DEV_BAD_SLOT, PA_DEV_BAD_CONTEXT, PA_DEV_BAD_BLOCK, PA_DEV_BAD_SEQLENS, PA_DEV_SMEM_ALIGN,
- PA_DEV_BAD_TEMPERATURE, PA_DEV_BAD_TOKEN) = range(1, 9)
+ PA_DEV_BAD_TEMPERATURE, PA_DEV_BAD_TOKEN, PA_DEV_BAD_TREE) = range(1, 10)
 PA_Q8_E4M3, PA_Q8_INT8 = range(2)
+PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_YARN = range(4)
 
 # Every symbol include/pa.h declares, with its ctypes signature.
 _i32, _i64, _sz, _f32, _vp = C.c_int32, C.c_int64, C.c_size_t, C.c_float, C.c_void_p
@@ -69,6 +73,20 @@ SIGNATURES = {
                                _i32, _i32, _f32, _vp, _sz, _vp]),
     "pa_decode_store_q8": (C.c_int, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32,
                                      _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _sz, _vp]),
+    "pa_rope_frequencies": (C.c_int, [_vp, C.POINTER(C.c_float), _i32, C.c_double, _i32, C.c_double, C.c_double,
+                                      C.c_double, C.c_double]),
+    "pa_rope": (C.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _f32, _i32,
+                          _i32, _i32, _i32, _vp]),
+    "pa_rope_store_kvcache": (C.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _f32, _vp,
+                                        _vp, _f32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i64, _vp]),
+    "pa_tree_metadata": (C.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp]),
+    "pa_decode_tree_workspace_size": (_sz, [_i32, _i32, _i32, _i32]),
+    "pa_decode_tree": (C.c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                 _i32, _f32, _vp, _sz, _vp]),
+    "pa_verify_drafts": (C.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _i32, _vp,
+                                   _i32, _i32, _i32, _vp]),
+    "pa_compact_kvcache": (C.c_int, [_vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                     _i32, _i32, _vp]),
     "pa_set_checked": (C.c_int, [_i32]),
     # host block manager
     "pa_bm_create": (C.c_int, [_i32, _i32, C.POINTER(_vp)]),
@@ -622,6 +640,346 @@ def logprobs(logits, tokens, top_k=0, temperatures=None, out=None, stream=None):
                              None if temperatures is None else temperatures.data_ptr(), tokens.data_ptr(), rows, vocab,
                              top_k, _raw_stream()), "pa_logprobs")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Speculative decoding: trees of drafted tokens, node 0 the token that they
+# continue, node i > 0 under parents[i] < i; at most 64 nodes a sequence.
+# ---------------------------------------------------------------------------
+class Rope(NamedTuple):
+    """Rotary frequencies as rope_frequencies makes them."""
+    freqs: torch.Tensor  # int64 [rotary_dim / 2] on the GPU: turns per position, fractions of 2^64
+    gain: float          # multiplies what is rotated (1 but for yarn)
+    interleaved: bool    # pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2)
+
+
+_ROPE_SCALINGS = {"linear": PA_ROPE_LINEAR, "ntk": PA_ROPE_NTK, "yarn": PA_ROPE_YARN}
+
+
+def rope_frequencies(rotary_dim=128, theta=10000.0, scaling=None, interleaved=False, device="cuda"):
+    """Rotary frequencies for rope / rope_store_kvcache, made once per model.
+    scaling: None, ("linear", factor), ("ntk", factor) or ("yarn", factor,
+    original_context[, beta_fast, beta_slow])."""
+    kind, args = PA_ROPE_PLAIN, ()
+    if scaling is not None:
+        if not isinstance(scaling, (tuple, list)) or not scaling or scaling[0] not in _ROPE_SCALINGS:
+            raise ValueError(f"scaling must be None or a tuple that starts with one of {sorted(_ROPE_SCALINGS)}")
+        kind, args = _ROPE_SCALINGS[scaling[0]], tuple(float(x) for x in scaling[1:])
+        if len(args) not in ((2, 4) if kind == PA_ROPE_YARN else (1,)):
+            raise ValueError("scaling must be (kind, factor), for yarn (kind, factor, original_context"
+                             "[, beta_fast, beta_slow])")
+    factor, original, fast, slow = args + (1.0, 0.0, 32.0, 1.0)[len(args):]
+    rotary_dim = int(rotary_dim)
+    _fits(rotary_dim, "rotary_dim")
+    freqs, gain = (C.c_uint64 * max(64, 1))(), C.c_float()
+    _check(lib().pa_rope_frequencies(freqs, C.byref(gain), rotary_dim, float(theta), kind, factor, original, fast,
+                                     slow), "pa_rope_frequencies")
+    host = torch.tensor([f - (1 << 64) if f >> 63 else f for f in freqs[:rotary_dim // 2]], dtype=torch.int64)
+    return Rope(host.to(device), gain.value, bool(interleaved))
+
+
+def _rope_args(q, k, positions, frequencies, q_norm, k_norm, out_q):
+    """Checks what rope and rope_store_kvcache share; returns (tokens, q heads, kv heads, D, strides)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("q and k must be [N, heads, 128]")
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    for x, name in ((n, "number of tokens"), (hq, "number of q heads"), (hkv, "number of kv heads")):
+        _fits(x, name)
+    qs, ks = _rows(q, "q", n, hq, d), _rows(k, "k", n, hkv, d)
+    _need(positions, torch.int32, "positions")
+    if positions.shape != (n,) or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous [N]")
+    _need(frequencies.freqs, torch.int64, "frequencies.freqs")
+    if frequencies.freqs.dim() != 1 or not frequencies.freqs.is_contiguous():
+        raise ValueError("frequencies.freqs must be contiguous [rotary_dim / 2]")
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _need(w, torch.bfloat16, name)
+            if w.shape != (d,) or not w.is_contiguous():
+                raise ValueError(f"{name} must be contiguous [{d}]")
+    oqs = hq * d if out_q is None else _rows(out_q, "out_q", n, hq, d)
+    return n, hq, hkv, d, qs, ks, oqs
+
+
+def rope(q, k, positions, frequencies, q_norm=None, k_norm=None, eps=1e-6, out_q=None, out_k=None, stream=None):
+    """Per-head norm (weights q_norm / k_norm, bf16 [128] or None) and rotation of
+    q [N, Hq, 128] and k [N, Hkv, 128] (bf16, rows may be strided) at positions
+    (int32 [N]), frequencies from rope_frequencies.  Returns (out_q, out_k); out_q may be q itself, out_k may be k."""
+    n, hq, hkv, d, qs, ks, oqs = _rope_args(q, k, positions, frequencies, q_norm, k_norm, out_q)
+    oks = hkv * d if out_k is None else _rows(out_k, "out_k", n, hkv, d)
+    ctx = _placed(stream, q, k, positions, frequencies.freqs, q_norm, k_norm, out_q, out_k)
+    if ctx is not None:
+        with ctx:
+            return rope(q, k, positions, frequencies, q_norm, k_norm, eps, out_q, out_k)
+    if out_q is None:
+        out_q = torch.empty(n, hq, d, dtype=torch.bfloat16, device=q.device)
+    if out_k is None:
+        out_k = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=q.device)
+    _check(lib().pa_rope(out_q.data_ptr(), oqs, out_k.data_ptr(), oks, q.data_ptr(), qs, k.data_ptr(), ks,
+                         positions.data_ptr(), frequencies.freqs.data_ptr(), 2 * frequencies.freqs.shape[0],
+                         1 if frequencies.interleaved else 0, frequencies.gain,
+                         None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                         float(eps), n, hq, hkv, d, _raw_stream()), "pa_rope")
+    return out_q, out_k
+
+
+def _bf16_caches(k_cache, v_cache, dims=(4,)):
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, torch.bfloat16, name)
+    if k_cache.dim() not in dims or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be of one shape, [num_blocks, B, Hkv, 128]")
+    for t in (k_cache, v_cache):
+        if not (t if t.dim() == 4 else t[0] if t.shape[0] else t).is_contiguous():
+            raise ValueError("caches must be contiguous")
+    for x, name in zip(k_cache.shape, ("number of layers", "number of blocks", "block size", "number of kv heads")[
+            5 - k_cache.dim():]):
+        _fits(x, name)
+
+
+def rope_store_kvcache(q, key, value, positions, frequencies, k_cache, v_cache, slot_mapping, q_norm=None,
+                       k_norm=None, eps=1e-6, out_q=None, stream=None):
+    """rope of q [N, Hq, 128] and key [N, Hkv, 128], the rotated keys and value
+    [N, Hkv, 128] written into the pool [num_blocks, B, Hkv, 128] at slot_mapping
+    (int32 [N], negatives skipped).  Returns the rotated q (out_q may be q itself)."""
+    n, hq, hkv, d, qs, ks, oqs = _rope_args(q, key, positions, frequencies, q_norm, k_norm, out_q)
+    vs = _rows(value, "value", n, hkv, d)
+    _bf16_caches(k_cache, v_cache)
+    nb, B, ch, cd = k_cache.shape
+    if (ch, cd) != (hkv, d):
+        raise ValueError(f"caches must be [num_blocks, B, {hkv}, {d}]")
+    _slots(slot_mapping, n)
+    ctx = _placed(stream, q, key, value, positions, frequencies.freqs, k_cache, v_cache, slot_mapping, q_norm, k_norm,
+                  out_q)
+    if ctx is not None:
+        with ctx:
+            return rope_store_kvcache(q, key, value, positions, frequencies, k_cache, v_cache, slot_mapping, q_norm,
+                                      k_norm, eps, out_q)
+    if out_q is None:
+        out_q = torch.empty(n, hq, d, dtype=torch.bfloat16, device=q.device)
+    _check(lib().pa_rope_store_kvcache(
+        out_q.data_ptr(), oqs, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, positions.data_ptr(),
+        frequencies.freqs.data_ptr(), 2 * frequencies.freqs.shape[0], 1 if frequencies.interleaved else 0,
+        frequencies.gain, None if q_norm is None else q_norm.data_ptr(),
+        None if k_norm is None else k_norm.data_ptr(), float(eps),
+        k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, hq, hkv, d, nb * B, _raw_stream()),
+        "pa_rope_store_kvcache")
+    return out_q
+
+
+def _int_rows(t, name, shape, dtype=torch.int32):
+    """Checks a contiguous tensor that may be None."""
+    if t is None:
+        return None
+    _need(t, dtype, name)
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _tables(block_tables, context_lens, batch):
+    _need(block_tables, torch.int32, "block_tables")
+    _need(context_lens, torch.int32, "context_lens")
+    if block_tables.dim() != 2 or block_tables.shape[0] != batch or context_lens.shape != (batch,):
+        raise ValueError("block_tables must be [batch, max_blocks] and context_lens [batch]")
+    if not (block_tables.is_contiguous() and context_lens.is_contiguous()):
+        raise ValueError("block_tables and context_lens must be contiguous")
+    _fits(batch, "batch")
+    _fits(block_tables.shape[1], "width of block_tables")
+
+
+class TreeMetadata(NamedTuple):
+    """What tree_metadata returns, node by node."""
+    tree_mask: torch.Tensor     # int64 [batch, num_drafts]
+    positions: torch.Tensor     # int32 [batch * num_drafts]
+    slot_mapping: torch.Tensor  # int32 [batch * num_drafts]
+
+
+def tree_metadata(parents, context_lens, block_tables, block_size, draft_lens=None, num_drafts=None, stream=None):
+    """Masks, rotary positions and slots of a step's trees.  parents int32
+    [batch, num_drafts], or None with num_drafts given (chains); context_lens
+    int32 [batch] counts all keys, the step's nodes the last of them; draft_lens
+    int32 [batch] or None (num_drafts everywhere)."""
+    batch = context_lens.shape[0] if isinstance(context_lens, torch.Tensor) and context_lens.dim() == 1 else -1
+    _tables(block_tables, context_lens, batch)
+    if parents is None:
+        if num_drafts is None:
+            raise ValueError("num_drafts is needed without parents")
+        t = int(num_drafts)
+    else:
+        if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+            raise ValueError("parents must be [batch, num_drafts]")
+        t = parents.shape[1]
+        if num_drafts is not None and num_drafts != t:
+            raise ValueError("num_drafts is not the width of parents")
+    _fits(t, "num_drafts")
+    _fits(int(block_size), "block size")
+    par, lens = _int_rows(parents, "parents", (batch, t)), _int_rows(draft_lens, "draft_lens", (batch,))
+    ctx = _placed(stream, context_lens, block_tables, parents, draft_lens)
+    if ctx is not None:
+        with ctx:
+            return tree_metadata(parents, context_lens, block_tables, block_size, draft_lens, t)
+    dev, size = context_lens.device, max(t, 0)
+    out = TreeMetadata(torch.empty(batch, size, dtype=torch.int64, device=dev),
+                       torch.empty(batch * size, dtype=torch.int32, device=dev),
+                       torch.empty(batch * size, dtype=torch.int32, device=dev))
+    _check(lib().pa_tree_metadata(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), par,
+                                  context_lens.data_ptr(), lens, block_tables.data_ptr(), block_tables.shape[1], batch,
+                                  t, int(block_size), _raw_stream()), "pa_tree_metadata")
+    return out
+
+
+def decode_tree_workspace(num_q_heads, num_kv_heads, head_dim=128, num_drafts=64, device="cuda"):
+    """Zero-filled workspace for decode_tree (its size depends on the query heads
+    per kv head and on num_drafts; a larger one serves smaller calls too); the
+    calls leave it ready for the next one on the same stream."""
+    n = int(lib().pa_decode_tree_workspace_size(num_q_heads, num_kv_heads, head_dim, num_drafts))
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def decode_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask=None, softmax_scale=None, draft_lens=None,
+                workspace=None, out=None, stream=None):
+    """Paged attention of the drafted tokens of each sequence.  q [batch,
+    num_drafts, Hq, 128] bf16 (tokens may be strided evenly); caches [num_blocks,
+    B, Hkv, 128]; context_lens int32 [batch] counts all keys, the drafts the last
+    of them (stored before the call); tree_mask int64 [batch, num_drafts]: bit j
+    where the draft sees draft j (None: chains); draft_lens int32 [batch] or None.
+    Returns out, of q's shape; zeros for padding."""
+    _bf16_caches(k_cache, v_cache)
+    nb, B, hkv, d = k_cache.shape
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError(f"q must be [batch, num_drafts, Hq, {d}]")
+    batch, t, hq, _ = q.shape
+    _need(q, torch.bfloat16, "q")
+    s0, s1, s2, s3 = q.stride()
+    if q.shape[3] != d or (d > 1 and s3 != 1) or (hq > 1 and s2 != d) or (batch > 1 and t > 1 and s0 != t * s1):
+        raise ValueError(f"q must be [batch, num_drafts, Hq, {d}], each token contiguous and all evenly spaced")
+    qs = s1 if t > 1 else s0 if batch > 1 else hq * d
+    _tables(block_tables, context_lens, batch)
+    _fits(t, "num_drafts")
+    mask = _int_rows(tree_mask, "tree_mask", (batch, t), torch.int64)
+    lens = _int_rows(draft_lens, "draft_lens", (batch,))
+    if out is not None:
+        _need(out, torch.bfloat16, "out")
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous and of q's shape")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
+    ctx = _placed(stream, q, k_cache, v_cache, block_tables, context_lens, tree_mask, draft_lens, workspace, out)
+    if ctx is not None:
+        with ctx:
+            return decode_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask, scale, draft_lens, workspace,
+                               out)
+    if workspace is None:
+        workspace = decode_tree_workspace(hq, hkv, d, t, q.device)
+    if out is None:
+        out = torch.empty(batch, t, hq, d, dtype=torch.bfloat16, device=q.device)
+    _check(lib().pa_decode_tree(out.data_ptr(), q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
+                                block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), lens, mask,
+                                batch, t, hq, hkv, d, B, nb, scale, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _raw_stream()), "pa_decode_tree")
+    return out
+
+
+class Verified(NamedTuple):
+    """What verify_drafts returns; -1 after a row's `counts` entries."""
+    tokens: torch.Tensor  # int32 [batch, num_nodes]: the kept tokens, then the next one
+    nodes: torch.Tensor   # int32 [batch, num_nodes]: 0 and the kept nodes
+    counts: torch.Tensor  # int32 [batch]
+
+
+def _flat_rows(t, name):
+    """Elements between the rows of a [batch, rows, vocab] tensor, evenly spaced."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions")
+    b, r, v = t.shape
+    if (v > 1 and t.stride(2) != 1) or (b > 1 and r > 1 and t.stride(0) != r * t.stride(1)):
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
+    return t.stride(1) if r > 1 else t.stride(0) if b > 1 else -(-v // 8) * 8
+
+
+def verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, draft_probs=None, draft_lens=None,
+                  out=None, stream=None):
+    """Speculative sampling: which drafted tokens the target keeps, and the next
+    token.  logits [batch, num_nodes, vocab] bf16 or fp32 (rows may be strided
+    evenly), the target's at every node; tokens / parents int32 [batch,
+    num_nodes] (parents None: chains); uniforms fp32 [batch, num_nodes] in [0, 1);
+    exp_noise fp32 [batch, vocab] of Exp(1) draws; temperatures fp32 [batch];
+    draft_probs fp32 [batch, at least num_nodes - 1, vocab], the distributions
+    that the nodes' children were drawn from, or None (chosen candidates);
+    draft_lens int32 [batch], nodes of each tree, or None.  `out`, a Verified of
+    contiguous tensors, is filled and returned."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("logits must be a bfloat16 or float32 tensor")
+    ls = _flat_rows(logits, "logits")
+    batch, n, vocab = logits.shape
+    for x, name in ((batch, "batch"), (n, "number of nodes"), (vocab, "vocabulary")):
+        _fits(x, name)
+    ptr = [_int_rows(t, name, shape, dtype) for t, name, shape, dtype in (
+        (tokens, "tokens", (batch, n), torch.int32), (parents, "parents", (batch, n), torch.int32),
+        (uniforms, "uniforms", (batch, n), torch.float32), (temperatures, "temperatures", (batch,), torch.float32),
+        (draft_lens, "draft_lens", (batch,), torch.int32))]
+    _need(exp_noise, torch.float32, "exp_noise")
+    if tuple(exp_noise.shape) != (batch, vocab) or (vocab > 1 and exp_noise.stride(1) != 1):
+        raise ValueError("exp_noise must be [batch, vocab] with contiguous rows")
+    es = exp_noise.stride(0) if batch > 1 else -(-vocab // 4) * 4
+    ps, pr = 0, 0
+    if draft_probs is not None:
+        _need(draft_probs, torch.float32, "draft_probs")
+        ps = _flat_rows(draft_probs, "draft_probs")
+        if draft_probs.shape[0] != batch or draft_probs.shape[2] != vocab or draft_probs.shape[1] < n - 1:
+            raise ValueError("draft_probs must be [batch, at least num_nodes - 1, vocab]")
+        pr = draft_probs.shape[1]
+        _fits(pr, "rows of draft_probs")
+    if out is not None:
+        for t, shape, name in ((out[0], (batch, n), "tokens"), (out[1], (batch, n), "nodes"),
+                               (out[2], (batch,), "counts")):
+            if _int_rows(t, f"out.{name}", shape) is None:
+                raise TypeError(f"out.{name} must be a CUDA tensor")
+    ctx = _placed(stream, logits, tokens, parents, uniforms, exp_noise, temperatures, draft_probs, draft_lens,
+                  *(out or ()))
+    if ctx is not None:
+        with ctx:
+            return verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, draft_probs, draft_lens,
+                                 out)
+    if out is None:
+        out = Verified(torch.empty(batch, n, dtype=torch.int32, device=logits.device),
+                       torch.empty(batch, n, dtype=torch.int32, device=logits.device),
+                       torch.empty(batch, dtype=torch.int32, device=logits.device))
+    _check(lib().pa_verify_drafts(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), logits.data_ptr(), ls,
+                                  1 if logits.dtype is torch.float32 else 0, ptr[0], ptr[1], ptr[2],
+                                  exp_noise.data_ptr(), es, ptr[3],
+                                  None if draft_probs is None else draft_probs.data_ptr(), ps, pr, ptr[4], batch, n,
+                                  vocab, _raw_stream()), "pa_verify_drafts")
+    return out
+
+
+def compact_kvcache(k_cache, v_cache, block_tables, context_lens, nodes, counts, draft_lens=None, stream=None):
+    """Move the kept nodes' K and V rows next to the context: position base +
+    nodes[b, j] to base + j for j < counts[b], base = context_lens[b] minus the
+    tree's size (draft_lens, or nodes' width).  Caches [num_blocks, B, Hkv, 128], or
+    [layers, num_blocks, B, Hkv, 128] for all layers in one call (each layer
+    contiguous); nodes int32 [batch, num_nodes] and counts int32 [batch] as
+    verify_drafts returns them."""
+    _bf16_caches(k_cache, v_cache, (4, 5))
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    nb, B, hkv, d = k_cache.shape[-4:]
+    strides = [t.stride(0) if t.dim() == 5 and layers > 1 else 0 for t in (k_cache, v_cache)]
+    if not isinstance(nodes, torch.Tensor) or nodes.dim() != 2:
+        raise ValueError("nodes must be [batch, num_nodes]")
+    batch, n = nodes.shape
+    _tables(block_tables, context_lens, batch)
+    _fits(n, "number of nodes")
+    ptr = [_int_rows(t, name, shape) for t, name, shape in (
+        (draft_lens, "draft_lens", (batch,)), (nodes, "nodes", (batch, n)), (counts, "counts", (batch,)))]
+    ctx = _placed(stream, k_cache, v_cache, block_tables, context_lens, nodes, counts, draft_lens)
+    if ctx is not None:
+        with ctx:
+            return compact_kvcache(k_cache, v_cache, block_tables, context_lens, nodes, counts, draft_lens)
+    _check(lib().pa_compact_kvcache(k_cache.data_ptr(), strides[0], v_cache.data_ptr(), strides[1],
+                                    block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), *ptr,
+                                    batch, n, layers, hkv, d, B, nb, _raw_stream()), "pa_compact_kvcache")
 
 
 def set_checked(enabled: bool):

@@ -1,0 +1,673 @@
+// pa_draft.cu -- what surrounds the attention of a tree of drafted tokens: its
+// masks, positions and slots, the verification of the drafts, and the move of
+// the kept rows next to the context.
+//
+// Verification, per sequence: node 0 is the token that the drafts continue, node
+// i > 0 a drafted token under parent[i] < i.  At a node v with target
+// probabilities p = softmax(logits_v / T), w = p and s = 1, for its children in
+// order, child c with token x and given number u:
+//   kept if u q(x) s < w(x),  else w <- max(w - s q, 0), s <- sum w,
+// q = draft_probs_v, the distribution that the children were drawn from, each on
+// its own.  (u < ratio of the normalised w / s to q, without a division.)  Unrolled,
+// w = max(p - S q, 0) with S the sum of the s so far: a scalar carries the whole
+// state, and w is never written.  Without draft_probs the children are chosen
+// candidates, q is 1 at the child's token: w(x) <- 0.  The walk goes on from a
+// kept child; where none is kept, the last token is argmax w / max(E, 1e-10), E the
+// given exponential numbers: a draw from w / s.
+//
+// How: a thread-block cluster per sequence walks its tree, so only the rows of
+// the nodes that are reached are read.  A node costs one pass over its logits
+// (maximum and sum), one more per rejected child that has a sibling after it, and
+// the last node one pass for the draw (its logits from L2).
+#include <float.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "pa_internal.cuh"
+
+namespace pa {
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int kMaxNodes = 64;
+
+// ---------------------------------------------------------------------------
+// Masks, positions and slots
+// ---------------------------------------------------------------------------
+struct MetaArgs {
+    unsigned long long *mask;
+    int32_t *positions, *slots;
+    const int32_t *parents, *ctx, *lens, *bt;
+    int32_t max_blocks, batch, nodes, block_size;
+    DevError *err;
+};
+
+// Tree size of sequence b: draft_lens, or all nodes of a row with a context; 0
+// (recorded) where the lengths do not fit.
+__device__ __forceinline__ int tree_size(int ctx, const int32_t *lens, int b, int nodes, int64_t limit, bool &bad) {
+    const int n = lens ? __ldg(lens + b) : (ctx > 0 ? nodes : 0);
+    bad = ctx < 0 || ctx > limit || n < 0 || n > nodes || n > ctx;
+    return bad ? 0 : n;
+}
+
+// A thread per node walks up to the root.
+__global__ void __launch_bounds__(128) tree_metadata_kernel(const __grid_constant__ MetaArgs a) {
+    pdl_wait_then_release();
+    const int64_t t = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (t >= (int64_t)a.batch * a.nodes) return;
+    const int b = (int)(t / a.nodes), i = (int)(t - (int64_t)b * a.nodes);
+    const int ctx = __ldg(a.ctx + b);
+    bool bad;
+    const int n = tree_size(ctx, a.lens, b, a.nodes, (int64_t)a.max_blocks * a.block_size, bad);
+    if (bad && i == 0) record_error(a.err, PA_DEV_BAD_CONTEXT, b);
+    if (i >= n) {
+        a.mask[t] = 0;
+        a.positions[t] = 0;
+        a.slots[t] = -1;
+        return;
+    }
+    unsigned long long m = 1ull << i;
+    int v = i, depth = 0;
+    while (v > 0) {
+        const int p = a.parents ? __ldg(a.parents + (int64_t)b * a.nodes + v) : v - 1;
+        if (p < 0 || p >= v) {
+            if (v == i) record_error(a.err, PA_DEV_BAD_TREE, t);
+            break;
+        }
+        m |= 1ull << p;
+        ++depth;
+        v = p;
+    }
+    a.mask[t] = m;
+    a.positions[t] = ctx - n + depth;
+    const int p = ctx - n + i, blk = __ldg(a.bt + (int64_t)b * a.max_blocks + p / a.block_size);
+    a.slots[t] = blk < 0 ? -1 : blk * a.block_size + p % a.block_size;
+}
+
+// ---------------------------------------------------------------------------
+// Moving the kept rows
+// ---------------------------------------------------------------------------
+constexpr int MOVE_THREADS = 256;
+
+struct MoveArgs {
+    uint4 *k, *v;
+    int64_t k_layer, v_layer;  // 16-byte units between layers
+    const int32_t *bt, *ctx, *lens, *nodes, *counts;
+    int32_t max_blocks, batch, width, layers, row16, block_size, num_blocks;
+    DevError *err;
+};
+
+// A CTA takes a sequence and a share of its (layer, K or V, 16-byte column)
+// items.  nodes[j] >= j along a path, so a row is never written before it is read
+// as long as a column's rows are moved in order; up to eight loads are in flight.
+__global__ void __launch_bounds__(MOVE_THREADS) compact_kernel(const __grid_constant__ MoveArgs a) {
+    pdl_wait_then_release();
+    __shared__ int64_t src[kMaxNodes], dst[kMaxNodes];
+    __shared__ int moves;
+    const int b = blockIdx.x, lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        const int ctx = __ldg(a.ctx + b);
+        bool bad;
+        const int n = tree_size(ctx, a.lens, b, a.width, (int64_t)a.max_blocks * a.block_size, bad);
+        if (bad && lane == 0 && blockIdx.y == 0) record_error(a.err, PA_DEV_BAD_CONTEXT, b);
+        const int count = min(max(__ldg(a.counts + b), 0), n), base = ctx - n;
+        const int32_t *bt = a.bt + (int64_t)b * a.max_blocks;
+        int total = 0;
+        bool stop = false;
+        for (int j0 = 0; j0 < count; j0 += 32) {
+            const int j = j0 + lane;
+            int node = j;
+            bool wrong = false;
+            if (j < count) {
+                node = __ldg(a.nodes + (int64_t)b * a.width + j);
+                const int prev = j ? __ldg(a.nodes + (int64_t)b * a.width + j - 1) : -1;
+                wrong = node <= prev || node >= n || (j == 0 && node != 0);
+            }
+            const unsigned w = __ballot_sync(FULL, wrong);
+            if (w && lane == 0 && blockIdx.y == 0)
+                record_error(a.err, PA_DEV_BAD_TREE, (long long)b * a.width + j0 + __ffs(w) - 1);
+            const bool before = !stop && (w == 0 || j < j0 + __ffs(w) - 1);  // the path up to its first bad node
+            stop = stop || w != 0;
+            bool go = before && j < count && node != j;
+            int64_t s = 0, d = 0;
+            if (go) {
+                const int ps = base + node, pd = base + j;
+                const int bs = __ldg(bt + ps / a.block_size), bd = __ldg(bt + pd / a.block_size);
+                if (bs < 0 || bs >= a.num_blocks || bd < 0 || bd >= a.num_blocks) {
+                    if (blockIdx.y == 0) record_error(a.err, PA_DEV_BAD_BLOCK,
+                                                      (long long)b * a.max_blocks +
+                                                          (bs < 0 || bs >= a.num_blocks ? ps : pd) / a.block_size);
+                    go = false;
+                } else {
+                    s = ((int64_t)bs * a.block_size + ps % a.block_size) * a.row16;
+                    d = ((int64_t)bd * a.block_size + pd % a.block_size) * a.row16;
+                }
+            }
+            const unsigned g = __ballot_sync(FULL, go);
+            if (go) {
+                const int at = total + __popc(g & ((1u << lane) - 1));
+                src[at] = s;
+                dst[at] = d;
+            }
+            total += __popc(g);
+        }
+        if (lane == 0) moves = total;
+    }
+    __syncthreads();
+    const int nm = moves;
+    if (nm == 0) return;
+    const int64_t items = 2LL * a.layers * a.row16;
+    for (int64_t i = (int64_t)blockIdx.y * MOVE_THREADS + threadIdx.x; i < items; i += (int64_t)gridDim.y * MOVE_THREADS) {
+        const int64_t line = i / a.row16;  // layer, K or V
+        const int col = (int)(i - line * a.row16);
+        uint4 *c = ((line & 1) ? a.v + (line >> 1) * a.v_layer : a.k + (line >> 1) * a.k_layer) + col;
+        for (int j0 = 0; j0 < nm; j0 += 8) {
+            uint4 x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (j0 + e < nm) x[e] = c[src[j0 + e]];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (j0 + e < nm) c[dst[j0 + e]] = x[e];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Verification
+// ---------------------------------------------------------------------------
+constexpr int VT = 256;           // threads of a CTA
+constexpr int VW = VT / 32;
+constexpr int V_MAX_CLUSTER = 8;
+constexpr float E_MIN = 1e-10f;   // the sampler's clamp of the exponential numbers
+
+struct VerifyArgs {
+    int32_t *out_tokens, *out_nodes, *out_counts;
+    const void *logits;
+    int64_t logits_stride;       // elements between rows
+    const int32_t *tokens, *parents;
+    const float *u, *noise;
+    int64_t noise_stride;
+    const float *temperatures;
+    const float *probs;
+    int64_t probs_stride;
+    int32_t probs_rows;          // rows of draft_probs per sequence
+    const int32_t *lens;
+    int32_t batch, nodes, vocab, cluster;
+    DevError *err;
+};
+
+struct __align__(8) Best {
+    float key;
+    int idx;
+};
+__device__ __forceinline__ bool better(Best a, Best b) { return a.key > b.key || (a.key == b.key && a.idx < b.idx); }
+
+__device__ __forceinline__ uint4 ld16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// A logit as it counts: NaN as -inf, +inf as the largest number.
+__device__ __forceinline__ float tame(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
+
+template <bool FP32>
+__device__ __forceinline__ float logit_at(const VerifyArgs &a, int64_t row, int i) {
+    if (FP32) return tame(__ldg(static_cast<const float *>(a.logits) + row * a.logits_stride + i));
+    const uint16_t h = __ldg(static_cast<const uint16_t *>(a.logits) + row * a.logits_stride + i);
+    return tame(__uint_as_float((uint32_t)h << 16));
+}
+
+// Eight logits from index i on (a multiple of 8).
+template <bool FP32>
+struct Raw {
+    uint4 w[FP32 ? 2 : 1];
+    __device__ __forceinline__ void load(const VerifyArgs &a, int64_t row, int i) {
+        if (FP32) {
+            const float *p = static_cast<const float *>(a.logits) + row * a.logits_stride + i;
+            w[0] = ld16(p);
+            w[FP32 ? 1 : 0] = ld16(p + 4);
+        } else {
+            w[0] = ld16(static_cast<const uint16_t *>(a.logits) + row * a.logits_stride + i);
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint4 v = w[0];
+        if (FP32) {
+            const uint4 t = w[FP32 ? 1 : 0];
+            x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z);
+            x[3] = __uint_as_float(v.w); x[4] = __uint_as_float(t.x); x[5] = __uint_as_float(t.y);
+            x[6] = __uint_as_float(t.z); x[7] = __uint_as_float(t.w);
+        } else {
+            x[0] = bf16lo(v.x); x[1] = bf16hi(v.x); x[2] = bf16lo(v.y); x[3] = bf16hi(v.y);
+            x[4] = bf16lo(v.z); x[5] = bf16hi(v.z); x[6] = bf16lo(v.w); x[7] = bf16hi(v.w);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = tame(x[e]);
+    }
+};
+
+struct VerifyShared {
+    int32_t parent[kMaxNodes], token[kMaxNodes];
+    float u[kMaxNodes], x[kMaxNodes], q[kMaxNodes], p[kMaxNodes];  // of the children of the current node: logit, q, p
+    int32_t gone[kMaxNodes];                                       // tokens of the rejected candidates
+    float2 warp[VW];
+    float2 all[2][V_MAX_CLUSTER];  // the CTAs' values, written by each into all
+};
+
+// Reductions over the cluster.  Each CTA's value goes to every CTA of the
+// cluster; two buffers in turn, so one barrier each: a buffer is written again
+// only after the barrier that follows its last reading.
+template <typename F>
+__device__ __forceinline__ float2 cluster_reduce(VerifyShared &s, float2 v, int S, int &turn, F combine) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        float2 t;
+        t.x = __shfl_xor_sync(FULL, v.x, o);
+        t.y = __shfl_xor_sync(FULL, v.y, o);
+        v = combine(v, t);
+    }
+    if (lane == 0) s.warp[warp] = v;
+    __syncthreads();
+    v = s.warp[0];
+#pragma unroll
+    for (int w = 1; w < VW; ++w) v = combine(v, s.warp[w]);
+    if (S == 1) {
+        __syncthreads();
+        return v;
+    }
+    if ((int)threadIdx.x < S) {
+        uint32_t rank, dst;
+        asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(dst)
+                     : "r"(smem_addr(&s.all[turn][rank])), "r"((uint32_t)threadIdx.x));
+        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(__float_as_uint(v.x)),
+                     "r"(__float_as_uint(v.y))
+                     : "memory");
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    v = s.all[turn][0];
+    for (int c = 1; c < S; ++c) v = combine(v, s.all[turn][c]);
+    turn ^= 1;
+    return v;
+}
+
+template <bool FP32, bool PROBS>
+__global__ void __launch_bounds__(VT) verify_kernel(const __grid_constant__ VerifyArgs a) {
+    pdl_wait_then_release();
+    __shared__ VerifyShared s;
+    // The cluster's CTAs have started before any of them writes into another
+    // (waited for ahead of the first reduction).
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    const int b = blockIdx.y, S = a.cluster, rank = blockIdx.x, tid = threadIdx.x;
+    const bool lead = rank == 0 && tid == 0;
+    const float T = __ldg(a.temperatures + b);
+    int n = a.lens ? __ldg(a.lens + b) : a.nodes;
+    const bool bad_t = !(T > 1e-10f), bad_n = n < 0 || n > a.nodes;
+    if (lead && bad_t) record_error(a.err, PA_DEV_BAD_TEMPERATURE, b);
+    if (lead && bad_n) record_error(a.err, PA_DEV_BAD_CONTEXT, b);
+    if (bad_n || bad_t) n = 0;
+    if (rank == 0)
+        for (int i = tid; i < a.nodes; i += VT) {
+            a.out_tokens[(int64_t)b * a.nodes + i] = -1;
+            a.out_nodes[(int64_t)b * a.nodes + i] = -1;
+        }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (n == 0) {  // a padded row: uniform over the cluster
+        if (lead) a.out_counts[b] = 0;
+        return;
+    }
+    for (int i = tid; i < n; i += VT) {
+        const int p = a.parents ? __ldg(a.parents + (int64_t)b * a.nodes + i) : i - 1;
+        const int x = __ldg(a.tokens + (int64_t)b * a.nodes + i);
+        const bool bad_p = i > 0 && (p < 0 || p >= i), bad_x = i > 0 && (x < 0 || x >= a.vocab);
+        if (rank == 0 && bad_p) record_error(a.err, PA_DEV_BAD_TREE, (long long)b * a.nodes + i);
+        if (rank == 0 && bad_x) record_error(a.err, PA_DEV_BAD_TOKEN, (long long)b * a.nodes + i);
+        s.parent[i] = i == 0 || bad_p || bad_x ? -1 : p;  // nobody's child: never kept, never subtracted
+        s.token[i] = x;
+        s.u[i] = __ldg(a.u + (int64_t)b * a.nodes + i);
+    }
+    // log2(e) / T, the float and what it leaves.
+    const double kd = fmax(1.4426950408889634 / (double)T, 1e-37);
+    const float k = (float)kd, k_lo = (float)(kd - (double)k);
+    // This CTA's chunk of a row: whole groups of 8 logits, then the ragged end.
+    const int chunk = ((a.vocab + S - 1) / S + 7) & ~7;
+    const int lo = min(a.vocab, rank * chunk), hi = min(a.vocab, lo + chunk);
+    const int nvec = (hi - lo) / 8, tail = lo + 8 * nvec;
+    const float *er = a.noise + (int64_t)b * a.noise_stride;
+    int turn = 0, cur = 0, count = 1, gone = 0;
+    float m = 0.f, inv_l = 0.f, sub = 0.f;  // of the current node: maximum, 1 / sum, S
+    __syncthreads();
+    while (true) {
+        // ---- maximum and sum of the current node's row
+        const int64_t row = (int64_t)b * a.nodes + cur;
+        const float *qr = PROBS ? a.probs + ((int64_t)b * a.probs_rows + cur) * a.probs_stride : nullptr;
+        if (tid < n && s.parent[tid] == cur) {  // (n <= 64: the children's own entries, meanwhile)
+            s.x[tid] = logit_at<FP32>(a, row, s.token[tid]);
+            s.q[tid] = PROBS ? __ldg(qr + s.token[tid]) : 1.f;
+        }
+        float tm = -INFINITY, ts = 0.f;
+        auto add = [&](float top, const float *x, int num) {
+            if (top > tm) {
+                ts *= tm == -INFINITY ? 0.f : fast_exp2((tm - top) * k);
+                tm = top;
+            }
+            if (tm == -INFINITY) return;
+            for (int e = 0; e < num; ++e) {
+                const float d = x[e] - tm;
+                ts += fast_exp2(fmaf(d, k, d * k_lo));
+            }
+        };
+        for (int v0 = tid; v0 < nvec; v0 += 4 * VT) {
+            Raw<FP32> w[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (v0 + h * VT < nvec) w[h].load(a, row, lo + 8 * (v0 + h * VT));
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                if (v0 + h * VT >= nvec) break;
+                float x[8];
+                w[h].get(x);
+                const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+                if (top > tm) {
+                    ts *= tm == -INFINITY ? 0.f : fast_exp2((tm - top) * k);
+                    tm = top;
+                }
+                if (tm == -INFINITY) continue;
+                float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float d = x[e] - tm;
+                    y[e & 3] += fast_exp2(fmaf(d, k, d * k_lo));
+                }
+                ts += (y[0] + y[1]) + (y[2] + y[3]);
+            }
+        }
+        for (int i = tail + tid; i < hi; i += VT) {
+            const float x = logit_at<FP32>(a, row, i);
+            add(x, &x, 1);
+        }
+        const float2 st = cluster_reduce(s, make_float2(tm, ts), S, turn, [&](float2 p, float2 q) {
+            const float mm = fmaxf(p.x, q.x);
+            if (mm == -INFINITY) return make_float2(mm, 0.f);
+            return make_float2(mm, (p.x == -INFINITY ? 0.f : p.y * fast_exp2((p.x - mm) * k)) +
+                                       (q.x == -INFINITY ? 0.f : q.y * fast_exp2((q.x - mm) * k)));
+        });
+        m = st.x == -INFINITY ? 0.f : st.x;
+        inv_l = st.y > 0.f ? 1.f / st.y : 0.f;  // a row of -inf alone: every probability 0
+        // p of the children, with the exponent in 64 bits.
+        if (tid < n && s.parent[tid] == cur) {
+            const double y = fmax((double)(s.x[tid] - m) * kd, -1000.0);
+            const double whole = rint(y);
+            s.p[tid] = ldexpf(exp2f((float)(y - whole)), (int)whole) * inv_l;
+        }
+        __syncthreads();
+        // ---- its children in order
+        float left = 1.f;  // s
+        sub = 0.f;
+        gone = 0;
+        int next = -1;
+        for (int c = cur + 1; c < n; ++c) {
+            if (s.parent[c] != cur) continue;
+            const float p = s.p[c], q = s.q[c];
+            float w;
+            if (PROBS) {
+                w = fmaxf(fmaf(-sub, q, p), 0.f);
+            } else {
+                w = p;
+                for (int g = 0; g < gone; ++g)
+                    if (s.gone[g] == s.token[c]) w = 0.f;  // a candidate given twice
+            }
+            if (s.u[c] * q * left < w) {
+                next = c;
+                break;
+            }
+            if (!PROBS) {
+                left = fmaxf(left - w, 0.f);
+                __syncthreads();  // the list has been read
+                if (tid == 0) s.gone[gone] = s.token[c];
+                ++gone;
+                __syncthreads();
+                continue;
+            }
+            sub += left;
+            bool more = false;
+            for (int d = c + 1; d < n; ++d) more = more || s.parent[d] == cur;
+            if (!more) break;
+            // s <- sum of max(p - S q, 0)
+            float acc = 0.f;
+            for (int v = tid; v < nvec; v += VT) {
+                Raw<FP32> w8;
+                const int i = lo + 8 * v;
+                w8.load(a, row, i);
+                const uint4 q0 = ld16(qr + i), q1 = ld16(qr + i + 4);
+                float x[8];
+                w8.get(x);
+                const float qq[8] = {__uint_as_float(q0.x), __uint_as_float(q0.y), __uint_as_float(q0.z),
+                                     __uint_as_float(q0.w), __uint_as_float(q1.x), __uint_as_float(q1.y),
+                                     __uint_as_float(q1.z), __uint_as_float(q1.w)};
+                float part = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float d = x[e] - m;
+                    part += fmaxf(fmaf(-sub, qq[e], fast_exp2(fmaf(d, k, d * k_lo)) * inv_l), 0.f);
+                }
+                acc += part;
+            }
+            for (int i = tail + tid; i < hi; i += VT) {
+                const float d = logit_at<FP32>(a, row, i) - m;
+                acc += fmaxf(fmaf(-sub, __ldg(qr + i), fast_exp2(fmaf(d, k, d * k_lo)) * inv_l), 0.f);
+            }
+            left = cluster_reduce(s, make_float2(acc, 0.f), S, turn,
+                                  [](float2 p, float2 q) { return make_float2(p.x + q.x, 0.f); }).x;
+        }
+        if (next < 0) break;
+        if (lead) {
+            a.out_tokens[(int64_t)b * a.nodes + count - 1] = s.token[next];
+            a.out_nodes[(int64_t)b * a.nodes + count] = next;
+        }
+        ++count;
+        cur = next;
+        __syncthreads();  // the children's entries are written again
+    }
+    // ---- the last token: argmax w / E, of p / E where nothing is left of w
+    const int64_t row = (int64_t)b * a.nodes + cur;
+    const float *qr = PROBS && sub > 0.f ? a.probs + ((int64_t)b * a.probs_rows + cur) * a.probs_stride : nullptr;
+    Best best;
+    for (int all = 0;; ++all) {
+        if (all) {
+            sub = 0.f;
+            qr = nullptr;
+            gone = 0;
+        }
+        best = {0.f, 0x7fffffff};
+        auto offer = [&](float w, float e, int i) {
+            const Best t = {__fdividef(w, fmaxf(e, E_MIN)), i};
+            if (!(t.key > 0.f) || !better(t, best)) return;
+            if (!PROBS)
+                for (int g = 0; g < gone; ++g)
+                    if (s.gone[g] == i) return;
+            best = t;
+        };
+        for (int v = tid; v < nvec; v += VT) {
+            Raw<FP32> w8;
+            const int i = lo + 8 * v;
+            w8.load(a, row, i);
+            const uint4 e0 = ld16(er + i), e1 = ld16(er + i + 4);
+            uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
+            if (PROBS && qr) {
+                q0 = ld16(qr + i);
+                q1 = ld16(qr + i + 4);
+            }
+            float x[8];
+            w8.get(x);
+            const float ee[8] = {__uint_as_float(e0.x), __uint_as_float(e0.y), __uint_as_float(e0.z),
+                                 __uint_as_float(e0.w), __uint_as_float(e1.x), __uint_as_float(e1.y),
+                                 __uint_as_float(e1.z), __uint_as_float(e1.w)};
+            const float qq[8] = {__uint_as_float(q0.x), __uint_as_float(q0.y), __uint_as_float(q0.z),
+                                 __uint_as_float(q0.w), __uint_as_float(q1.x), __uint_as_float(q1.y),
+                                 __uint_as_float(q1.z), __uint_as_float(q1.w)};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = x[e] - m;
+                float w = fast_exp2(fmaf(d, k, d * k_lo)) * inv_l;
+                if (PROBS) w = fmaf(-sub, qq[e], w);
+                offer(w, ee[e], i + e);
+            }
+        }
+        for (int i = tail + tid; i < hi; i += VT) {
+            const float d = logit_at<FP32>(a, row, i) - m;
+            float w = fast_exp2(fmaf(d, k, d * k_lo)) * inv_l;
+            if (PROBS && qr) w = fmaf(-sub, __ldg(qr + i), w);
+            offer(w, __ldg(er + i), i);
+        }
+        const float2 r = cluster_reduce(s, make_float2(best.key, __int_as_float(best.idx)), S, turn, [](float2 p, float2 q) {
+            const Best x = {p.x, __float_as_int(p.y)}, y = {q.x, __float_as_int(q.y)};
+            return better(y, x) ? q : p;
+        });
+        best = {r.x, __float_as_int(r.y)};
+        if (best.key > 0.f || all || (sub == 0.f && gone == 0)) break;  // uniform over the cluster
+    }
+    if (lead) {
+        a.out_tokens[(int64_t)b * a.nodes + count - 1] = best.idx == 0x7fffffff ? 0 : best.idx;
+        a.out_nodes[(int64_t)b * a.nodes] = 0;
+        a.out_counts[b] = count;
+    }
+}
+
+// CTAs per sequence: the smallest power of two that gives four CTAs per SM over
+// the batch, at most 8 (a portable cluster) and 2048 logits a CTA at least.
+int ctas_per_seq(int batch, int vocab, int sms) {
+    int S = 1;
+    while (S < V_MAX_CLUSTER && (int64_t)batch * S < 4LL * sms && vocab / (2 * S) >= 2048) S *= 2;
+    return S;
+}
+
+template <bool FP32, bool PROBS>
+pa_status launch_verify(VerifyArgs &a, cudaStream_t stream) {
+    a.cluster = ctas_per_seq(a.batch, a.vocab, sm_count());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.cluster, (unsigned)a.batch);
+    cfg.blockDim = dim3(VT);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<FP32, PROBS>, a);
+    if (e != cudaSuccess) return cuda_fail(e, "verify_kernel");
+    return check_launch("verify_kernel");
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+pa_status pa_tree_metadata(int64_t *tree_mask, int32_t *positions, int32_t *slot_mapping, const int32_t *parents,
+                           const int32_t *context_lens, const int32_t *draft_lens, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, int32_t batch, int32_t num_drafts, int32_t block_size,
+                           pa_stream_t stream) {
+    using namespace pa;
+    if (batch < 0) return fail(PA_ERR_INVALID_ARG, "batch < 0");
+    if (num_drafts <= 0) return fail(PA_ERR_INVALID_ARG, "num_drafts must be positive");
+    if (num_drafts > kMaxNodes) return fail(PA_ERR_UNSUPPORTED, "%d drafts (at most %d)", num_drafts, kMaxNodes);
+    if (batch == 0) return PA_OK;
+    if (!tree_mask || !positions || !slot_mapping || !context_lens || !block_tables)
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    if (block_size <= 0 || max_blocks_per_seq <= 0)
+        return fail(PA_ERR_INVALID_ARG, "block_size and max_blocks_per_seq must be positive");
+    if (reinterpret_cast<uintptr_t>(tree_mask) & 7u) return fail(PA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
+    MetaArgs a = {reinterpret_cast<unsigned long long *>(tree_mask), positions, slot_mapping, parents, context_lens,
+                  draft_lens, block_tables, max_blocks_per_seq, batch, num_drafts, block_size, device_error_ptr()};
+    const int64_t grid = ((int64_t)batch * num_drafts + 127) / 128;
+    return launch_pdl(tree_metadata_kernel, dim3((unsigned)grid), dim3(128), 0, reinterpret_cast<cudaStream_t>(stream),
+                      "tree_metadata_kernel", a);
+}
+
+pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *out_nodes, int32_t *out_counts, const void *logits,
+                           int64_t logits_row_stride, int32_t logits_is_fp32, const int32_t *tokens,
+                           const int32_t *parents, const float *uniforms, const float *exp_noise,
+                           int64_t noise_row_stride, const float *temperatures, const float *draft_probs,
+                           int64_t probs_row_stride, int32_t probs_rows, const int32_t *draft_lens, int32_t batch,
+                           int32_t num_nodes, int32_t vocab, pa_stream_t stream) {
+    using namespace pa;
+    if (batch < 0 || vocab < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
+    if (num_nodes <= 0) return fail(PA_ERR_INVALID_ARG, "num_nodes must be positive");
+    if (num_nodes > kMaxNodes) return fail(PA_ERR_UNSUPPORTED, "%d nodes (at most %d)", num_nodes, kMaxNodes);
+    if (batch == 0) return PA_OK;
+    if (vocab == 0) return fail(PA_ERR_INVALID_ARG, "vocab must be positive");
+    if (vocab > (1 << 30)) return fail(PA_ERR_UNSUPPORTED, "vocab %d (at most 2^30)", vocab);
+    if (batch > 65535) return fail(PA_ERR_UNSUPPORTED, "batch %d (at most 65535 sequences per call)", batch);
+    if (!out_tokens || !out_nodes || !out_counts || !logits || !tokens || !uniforms || !exp_noise || !temperatures)
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    if (logits_is_fp32 != 0 && logits_is_fp32 != 1) return fail(PA_ERR_INVALID_ARG, "logits_is_fp32 must be 0 or 1");
+    const int align = logits_is_fp32 ? 4 : 8;
+    if (logits_row_stride < vocab || logits_row_stride % align)
+        return fail(PA_ERR_INVALID_ARG, "logits_row_stride must be >= vocab and a multiple of %d", align);
+    if (noise_row_stride < vocab || noise_row_stride % 4)
+        return fail(PA_ERR_INVALID_ARG, "noise_row_stride must be >= vocab and a multiple of 4");
+    if (draft_probs) {
+        if (probs_row_stride < vocab || probs_row_stride % 4)
+            return fail(PA_ERR_INVALID_ARG, "probs_row_stride must be >= vocab and a multiple of 4");
+        if (probs_rows < num_nodes - 1)
+            return fail(PA_ERR_INVALID_ARG, "draft_probs has %d rows a sequence, at least num_nodes - 1 are needed", probs_rows);
+    }
+    if (!aligned16(logits) || !aligned16(exp_noise) || !aligned16(draft_probs))
+        return fail(PA_ERR_INVALID_ARG, "logits, exp_noise and draft_probs must be 16-byte aligned");
+    if (sm_count() <= 0) return fail(PA_ERR_CUDA, "no CUDA device");
+    VerifyArgs a = {out_tokens, out_nodes, out_counts, logits, logits_row_stride, tokens, parents, uniforms, exp_noise,
+                    noise_row_stride, temperatures, draft_probs, probs_row_stride, probs_rows, draft_lens, batch,
+                    num_nodes, vocab, 1, device_error_ptr()};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (logits_is_fp32) return draft_probs ? launch_verify<true, true>(a, s) : launch_verify<true, false>(a, s);
+    return draft_probs ? launch_verify<false, true>(a, s) : launch_verify<false, false>(a, s);
+}
+
+pa_status pa_compact_kvcache(void *k_cache, int64_t k_layer_stride, void *v_cache, int64_t v_layer_stride,
+                             const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+                             const int32_t *draft_lens, const int32_t *nodes, const int32_t *counts, int32_t batch,
+                             int32_t num_nodes, int32_t num_layers, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int32_t num_blocks, pa_stream_t stream) {
+    using namespace pa;
+    if (batch < 0 || num_layers < 0) return fail(PA_ERR_INVALID_ARG, "negative size");
+    if (num_nodes <= 0) return fail(PA_ERR_INVALID_ARG, "num_nodes must be positive");
+    if (num_nodes > kMaxNodes) return fail(PA_ERR_UNSUPPORTED, "%d nodes (at most %d)", num_nodes, kMaxNodes);
+    if (batch == 0 || num_layers == 0) return PA_OK;
+    if (!k_cache || !v_cache || !block_tables || !context_lens || !nodes || !counts)
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    if (num_kv_heads <= 0 || head_dim <= 0) return fail(PA_ERR_INVALID_ARG, "bad head shape");
+    if (head_dim != 128) return fail(PA_ERR_UNSUPPORTED, "head_dim %d (only 128)", head_dim);
+    if (num_kv_heads > (1 << 20)) return fail(PA_ERR_UNSUPPORTED, "too many heads");
+    if (block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
+        return fail(PA_ERR_INVALID_ARG, "block_size, max_blocks_per_seq and num_blocks must be positive");
+    if (num_layers > 1 && (k_layer_stride % 8 || v_layer_stride % 8 || k_layer_stride <= 0 || v_layer_stride <= 0))
+        return fail(PA_ERR_INVALID_ARG, "layer strides must be positive multiples of 8 elements");
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(PA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+    const int sms = sm_count();
+    if (sms <= 0) return fail(PA_ERR_CUDA, "no CUDA device");
+    MoveArgs a = {static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), k_layer_stride / 8, v_layer_stride / 8,
+                  block_tables, context_lens, draft_lens, nodes, counts, max_blocks_per_seq, batch, num_nodes, num_layers,
+                  num_kv_heads * 16, block_size, num_blocks, device_error_ptr()};
+    // One item a thread while the CTAs fit the GPU together (eight per SM), more after that.
+    const int64_t items = 2LL * num_layers * a.row16;
+    const int64_t y = std::max<int64_t>(1, std::min<int64_t>((items + MOVE_THREADS - 1) / MOVE_THREADS,
+                                                             std::min<int64_t>(65535, 8LL * sms / batch)));
+    return launch_pdl(compact_kernel, dim3((unsigned)batch, (unsigned)y), dim3(MOVE_THREADS), 0,
+                      reinterpret_cast<cudaStream_t>(stream), "compact_kernel", a);
+}
+
+}  // extern "C"
