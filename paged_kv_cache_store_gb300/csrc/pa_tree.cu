@@ -55,25 +55,26 @@ constexpr int kMinTiles = 2;             // a CTA's share at least
 constexpr float kLazy = 8.f;             // log2 headroom before the running maximum must move
 constexpr unsigned FULL = 0xffffffffu;
 
-template <int NT>
-struct Cfg {
-    static constexpr int ST = NT == 1 ? 5 : 4;  // ring stages
-    static constexpr int THREADS = 128 + 128 * NT;
-    static constexpr int OFF_K = NT * QTILE;
-    static constexpr int OFF_V = OFF_K + ST * KV_BYTES;
-    static constexpr int OFF_BAR = OFF_V + ST * KV_BYTES;
-    // Barriers: rings, then per row tile and buffer.
-    static constexpr int KFULL = 0, KEMPTY = ST, VFULL = 2 * ST, VEMPTY = 3 * ST, SFULL = 4 * ST, PFULL = SFULL + 2 * NT,
-                         PDONE = PFULL + 2 * NT, OEMPTY = PDONE + 2 * NT, QFULL = OEMPTY + NT, QEMPTY = QFULL + 1,
-                         DRAIN = QEMPTY + 1, NBAR = DRAIN + 2;
-    static constexpr int OFF_MISC = OFF_BAR + (NBAR * 8 + 15) / 16 * 16;  // TMEM address, abort flag, marks, scan scratch
-    static constexpr int OFF_ARR = OFF_MISC + 128;       // ctx, n, cum [batch + 1]
-    static constexpr uint32_t COLS = NT == 1 ? 256 : 512;
-    static constexpr uint32_t COL_O = NT * 128;          // S(h, b) at h * 128 + b * 64, O(h) at COL_O + h * 128
+// PAIR: an item has up to two row tiles, which share its K/V tiles.  Otherwise it
+// has one, and consecutive items alternate between the two row-tile sets (Q,
+// scores, O and softmax warps), so that one item's start and end run beside the
+// other's tiles.
+constexpr int ST = 4;                            // ring stages
+constexpr int THREADS = 384;
+constexpr int OFF_K = 2 * QTILE;
+constexpr int OFF_V = OFF_K + ST * KV_BYTES;
+constexpr int OFF_BAR = OFF_V + ST * KV_BYTES;
+enum {  // barriers: rings, then per row tile [2] (and score buffer [2])
+    KFULL = 0, KEMPTY = KFULL + ST, VFULL = KEMPTY + ST, VEMPTY = VFULL + ST, SFULL = VEMPTY + ST, PFULL = SFULL + 4,
+    PDONE = PFULL + 4, OEMPTY = PDONE + 4, QFULL = OEMPTY + 2, QEMPTY = QFULL + 2, WROTE = QEMPTY + 2, TOLD = WROTE + 2,
+    DRAIN = TOLD + 2, NBAR = DRAIN + 2
 };
-__host__ __device__ constexpr size_t tree_smem(int off_arr, int batch) { return off_arr + 12 * (size_t)(batch + 1) + 1024; }
-static_assert(tree_smem(Cfg<1>::OFF_ARR, kMaxBatch) <= 232448 && tree_smem(Cfg<2>::OFF_ARR, kMaxBatch) <= 232448,
-              "shared memory");
+constexpr int OFF_MISC = OFF_BAR + (NBAR * 8 + 15) / 16 * 16;  // TMEM address, abort, marks [4], last [2], scan scratch [12]
+constexpr int OFF_JOBS = OFF_MISC + 128;                       // Job [2][2]
+constexpr int OFF_ARR = OFF_JOBS + 4 * 28;                        // ctx, n, cum [batch + 1]
+constexpr uint32_t TMEM_COLS = 512, COL_O = 256;               // S(h, b) at h * 128 + b * 64, O(h) at COL_O + h * 128
+constexpr size_t tree_smem(int batch) { return OFF_ARR + 12 * (size_t)(batch + 1) + 1024; }
+static_assert(tree_smem(kMaxBatch) <= 232448, "shared memory");
 
 // Floats of a part: o [rows][D], (m, l) [rows], a multiple of 16 bytes.
 __host__ __device__ constexpr size_t slot_of(int rows) { return ((size_t)rows * (D + 2) + 3) / 4 * 4; }
@@ -87,7 +88,7 @@ struct TreeArgs {
     const unsigned long long *mask;  // null: a chain
     int32_t max_blocks, batch, drafts, Hq, Hkv, G, block_size, num_blocks, box_rows, checked;
     float scale_log2;
-    int *count;    // [grid][8] arrivals
+    int *count;    // [grid][2] arrivals: of the row tiles of the item that begins in a range and ends in a later one
     float *parts;  // [grid][2] of slot_of(part_rows)
     int32_t part_rows;
     DevError *err;
@@ -112,6 +113,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);
 }
+// Two fp32 at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ void st_shared_u4(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
@@ -126,7 +146,7 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
     return w;
 }
 
-// Where a CTA's range stands: an item and the tiles of it that are the CTA's.
+// A part of an item that is a CTA's.
 struct Seg {
     int b, g, blk;       // sequence, kv head, row block
     int t0, t1, nt;      // tiles [t0, t1) of nt
@@ -134,15 +154,16 @@ struct Seg {
     uint32_t first;      // the item's first unit
 };
 
-template <int NT>
+// Walks the segments of a CTA's range of units; every role of the CTA makes the
+// same walk.
+template <bool PAIR>
 struct Walker {
+    static constexpr int BLOCK = PAIR ? 2 * ROWS : ROWS;  // rows of an item
     const int *ctx_s, *n_s;
     const uint32_t *cum;
     int G;
     uint32_t x, x1;
     int b;
-    __device__ __forceinline__ int rows_of(int bb) const { return n_s[bb] * G; }
-    __device__ __forceinline__ int tiles_of(int bb) const { return (ctx_s[bb] + TILE - 1) / TILE; }
     __device__ __forceinline__ void start(uint32_t x0, uint32_t xe, int batch) {
         x = x0;
         x1 = xe;
@@ -157,8 +178,8 @@ struct Walker {
     __device__ __forceinline__ bool next(Seg &s) {
         while (x < x1) {
             while (cum[b + 1] <= x) ++b;
-            const int nt = tiles_of(b), u = nt + kItemCost;
-            const int blocks = (rows_of(b) + ROWS * NT - 1) / (ROWS * NT);
+            const int nt = (ctx_s[b] + TILE - 1) / TILE, u = nt + kItemCost, rows = n_s[b] * G;
+            const int blocks = (rows + BLOCK - 1) / BLOCK;
             const uint32_t local = x - cum[b], it = local / (uint32_t)u;
             const int t0 = (int)(local - it * (uint32_t)u);
             const uint32_t first = cum[b] + it * (uint32_t)u;
@@ -166,12 +187,12 @@ struct Walker {
             x = end;
             if (t0 >= nt) continue;
             s.b = b;
-            s.g = (int)it / blocks;
-            s.blk = (int)it % blocks;
+            s.g = PAIR ? (int)it / blocks : (int)it;
+            s.blk = PAIR ? (int)it % blocks : 0;
             s.t0 = t0;
             s.t1 = min((int)(end - first), nt);
             s.nt = nt;
-            s.rows = min(rows_of(b) - s.blk * ROWS * NT, ROWS * NT);
+            s.rows = min(rows - s.blk * BLOCK, BLOCK);
             s.first = first;
             return true;
         }
@@ -179,57 +200,131 @@ struct Walker {
     }
 };
 
-template <int NT>
-__global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
+// Parts to combine: rows [row0, row0 + live) of an item, from CTAs c0 on.
+struct Job {
+    int b, g, blk, row0, live, c0, nparts;
+};
+
+// Combines the parts of an item's rows of one row tile and writes them
+// out: four rows per warp and four parts at a time, 16 row loads in flight.  A
+// part's m of -inf has seen nothing; NaN in l or o goes on.
+template <typename OutRow>
+__device__ __forceinline__ void merge_rows(const TreeArgs &a, const Job &job, int w, int lane, OutRow out_row) {
+    constexpr int RM = 4, PM = 4, PL = 32 / RM;  // rows, parts at a time, lanes of a row
+    const size_t slot_floats = slot_of(a.part_rows);
+    const int c0 = job.c0, nparts = job.nparts, tr0 = job.row0, live = job.live;
+    const int r = lane & (RM - 1), ps = lane / RM;
+    auto slot = [&](int p) -> const float * { return a.parts + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats; };
+    for (int r0 = RM * w; r0 < live; r0 += 4 * RM) {
+        const int nr = min(RM, live - r0);
+        auto ml_of = [&](int p) -> float2 {  // of row r0 + r in part p
+            return p < nparts && r < nr
+                       ? __ldcg(reinterpret_cast<const float2 *>(slot(p) + (size_t)a.part_rows * D) + tr0 + r0 + r)
+                       : make_float2(-INFINITY, 0.f);
+        };
+        float m = -INFINITY, l = 0.f;
+        for (int p = ps; p < nparts; p += PL) {
+            const float2 ml = ml_of(p);
+            const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+            l = l * fast_exp2(m - ref) + ml.y * fast_exp2(ml.x - ref);
+            m = mn;
+        }
+#pragma unroll
+        for (int o = RM; o < 32; o <<= 1) {
+            const float m2 = __shfl_xor_sync(FULL, m, o), l2 = __shfl_xor_sync(FULL, l, o);
+            const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn;
+            l = l * fast_exp2(m - ref) + l2 * fast_exp2(m2 - ref);
+            m = mn;
+        }
+        const float ref = m == -INFINITY ? 0.f : m, inv = l == 0.f ? 0.f : 1.f / l;
+        float4 acc[RM];
+#pragma unroll
+        for (int e = 0; e < RM; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float wgt = 0.f;
+#pragma unroll 1
+        for (int p0 = 0; p0 < nparts; p0 += PM) {
+            float4 v[PM][RM];
+#pragma unroll
+            for (int pp = 0; pp < PM; ++pp)
+#pragma unroll
+                for (int e = 0; e < RM; ++e)
+                    if (e < nr && p0 + pp < nparts)
+                        v[pp][e] =
+                            __ldcg(reinterpret_cast<const float4 *>(slot(p0 + pp) + (size_t)(tr0 + r0 + e) * D) + lane);
+            if (p0 % PL == 0) wgt = fast_exp2(ml_of(p0 + ps).x - ref);  // of row r in part p0 + ps
+#pragma unroll
+            for (int pp = 0; pp < PM; ++pp)
+#pragma unroll
+                for (int e = 0; e < RM; ++e) {
+                    const float f = __shfl_sync(FULL, wgt, ((p0 + pp) % PL) * RM + e);
+                    if (e < nr && p0 + pp < nparts) {
+                        acc[e].x = fmaf(v[pp][e].x, f, acc[e].x);
+                        acc[e].y = fmaf(v[pp][e].y, f, acc[e].y);
+                        acc[e].z = fmaf(v[pp][e].z, f, acc[e].z);
+                        acc[e].w = fmaf(v[pp][e].w, f, acc[e].w);
+                    }
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < RM; ++e) {
+            const float f = __shfl_sync(FULL, inv, e);
+            if (e < nr)
+                reinterpret_cast<uint2 *>(out_row(tr0 + r0 + e))[lane] =
+                    make_uint2(pack_bf16(acc[e].x * f, acc[e].y * f), pack_bf16(acc[e].z * f, acc[e].w * f));
+        }
+    }
+}
+
+template <bool PAIR>
+__global__ void __launch_bounds__(THREADS, 1)
     decode_tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const __grid_constant__ TreeArgs a) {
-    using C = Cfg<NT>;
-    constexpr int ST = C::ST;
+    constexpr int BLOCK = Walker<PAIR>::BLOCK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
-    volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
-    uint32_t *wsum = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC + 16);
-    int *ctx_s = reinterpret_cast<int *>(smem + C::OFF_ARR);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + OFF_MISC + 4);
+    uint32_t *wsum = reinterpret_cast<uint32_t *>(smem + OFF_MISC + 48);
+    int *ctx_s = reinterpret_cast<int *>(smem + OFF_ARR);
     int *n_s = ctx_s + (a.batch + 1);
     uint32_t *cum = reinterpret_cast<uint32_t *>(n_s + (a.batch + 1));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int NWARPS = C::THREADS / 32;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NBAR; ++i) {
-            const bool per_warp = (i >= C::PFULL && i < C::PFULL + 2 * NT) || (i >= C::OEMPTY && i < C::OEMPTY + NT);
-            mbar_init(&bar[i], per_warp ? 4u : 1u);  // the four softmax warps of a row tile arrive one each
+        for (int i = 0; i < NBAR; ++i) {
+            // The four softmax warps of a row tile arrive one each.
+            const bool per_warp = (i >= PFULL && i < PFULL + 4) || (i >= OEMPTY && i < OEMPTY + 2) ||
+                                  (i >= WROTE && i < WROTE + 2);
+            mbar_init(&bar[i], per_warp ? 4u : 1u);
         }
-        abort[0] = abort[1] = abort[2] = 0;  // and the two marks behind it
+        for (int i = 0; i < 7; ++i) abort[i] = 0;  // and the marks behind it
         fence_mbar_init();
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, C::COLS);
+        tmem_alloc(tmem_slot, TMEM_COLS);
         tmem_relinquish();
     }
     pdl_wait_then_release();
     // Lengths, and the running sum of the sequences' units (tiles, and kItemCost
     // more per item).
     uint32_t carry = 0;
-    for (int base = 0; base < a.batch; base += C::THREADS) {
+    for (int base = 0; base < a.batch; base += THREADS) {
         const int b = base + threadIdx.x;
         uint32_t u = 0;
         if (b < a.batch) {
             int ctx = __ldg(a.ctx + b);
-            int n = a.lens ? __ldg(a.lens + b) : min(a.drafts, max(ctx, 0));
-            if (ctx < 0 || ctx > (int64_t)a.max_blocks * a.block_size || n < 0 || n > a.drafts || n > ctx ||
-                (!a.lens && ctx > 0 && ctx < a.drafts)) {
+            int n = a.lens ? __ldg(a.lens + b) : ctx > 0 ? a.drafts : 0;
+            if (ctx < 0 || ctx > (int64_t)a.max_blocks * a.block_size || n < 0 || n > a.drafts || n > ctx) {
                 if (blockIdx.x == 0) record_error(a.err, PA_DEV_BAD_CONTEXT, b);
                 n = 0;
             }
             if (n == 0) ctx = 0;
             ctx_s[b] = ctx;
             n_s[b] = n;
-            const int blocks = (n * a.G + ROWS * NT - 1) / (ROWS * NT);
+            const int blocks = (n * a.G + BLOCK - 1) / BLOCK;
             u = n ? (uint32_t)((ctx + TILE - 1) / TILE + kItemCost) * (uint32_t)(a.Hkv * blocks) : 0u;
         }
         uint32_t inc = u;
@@ -241,7 +336,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
         if (lane == 31) wsum[warp] = inc;
         __syncthreads();
         uint32_t before = carry, all = carry;
-        for (int w = 0; w < NWARPS; ++w) {
+        for (int w = 0; w < THREADS / 32; ++w) {
             if (w < warp) before += wsum[w];
             all += wsum[w];
         }
@@ -256,16 +351,12 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
     const uint32_t tmem = *tmem_slot;
     const uint32_t P = carry;  // units in all
     const uint32_t nC = min((uint32_t)gridDim.x, max(1u, P / kMinTiles));
-    Walker<NT> walk{ctx_s, n_s, cum, a.G};
-    const bool works = blockIdx.x < nC && P > 0;
-    if (works) {
+    Walker<PAIR> walk{ctx_s, n_s, cum, a.G, 0u, 0u, 0};
+    if (blockIdx.x < nC && P > 0)
         walk.start((uint32_t)((uint64_t)blockIdx.x * P / nC), (uint32_t)((uint64_t)(blockIdx.x + 1) * P / nC), a.batch);
-    } else {
-        walk.x = walk.x1 = 0;
-        walk.b = 0;
-    }
-    // The CTA whose range holds unit x.
-    auto owner = [&](uint32_t x) -> int { return (int)(((uint64_t)(x + 1) * nC - 1) / P); };
+    // Row tiles of segment number k.
+    auto h_begin = [](int k) -> int { return PAIR ? 0 : k & 1; };
+    auto h_end = [](int k, const Seg &s) -> int { return PAIR ? (s.rows + ROWS - 1) / ROWS : (k & 1) + 1; };
     Seg s;
     bool ok = true;
 
@@ -273,21 +364,29 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
         // ---------------------------------------------------------------- K and V tiles
         uint32_t gg = 0;
         const int R = a.box_rows;
-        while (ok && walk.next(s)) {
-            const int32_t *bt = a.bt + (int64_t)s.b * a.max_blocks;
+        // Block ids base + lane of a segment, the next one's fetched while this one is loaded.
+        auto first_block = [&](const Seg &t) -> int { return t.t0 * TILE / a.block_size; };
+        auto ids = [&](const Seg &t, int base) -> int {
+            return __ldg(a.bt + (int64_t)t.b * a.max_blocks + min(base + lane, (ctx_s[t.b] - 1) / a.block_size));
+        };
+        Seg nx;
+        bool have = walk.next(nx);
+        int nid = have ? ids(nx, first_block(nx)) : 0;
+        while (ok && have) {
+            s = nx;
+            int id = nid, base = first_block(s);
+            have = walk.next(nx);
+            if (have) nid = ids(nx, first_block(nx));
             const int key_end = ctx_s[s.b];
-            const int last = (key_end - 1) / a.block_size;  // the sequence's last block
-            int base = s.t0 * TILE / a.block_size;
-            int id = __ldg(bt + min(base + lane, last));    // block ids base + lane
             for (int j = s.t0; ok && j < s.t1; ++j, ++gg) {
                 const int st = gg % ST;
                 const int nsub = (min(TILE, key_end - j * TILE) + R - 1) / R;
                 if (lane == 0) {
-                    ok = wait_or_abort(&bar[C::KEMPTY + st], ((gg / ST) & 1u) ^ 1u, abort, a.err, 700) &&
-                         wait_or_abort(&bar[C::VEMPTY + st], ((gg / ST) & 1u) ^ 1u, abort, a.err, 701);
+                    ok = wait_or_abort(&bar[KEMPTY + st], ((gg / ST) & 1u) ^ 1u, abort, a.err, 700) &&
+                         wait_or_abort(&bar[VEMPTY + st], ((gg / ST) & 1u) ^ 1u, abort, a.err, 701);
                     if (ok) {
-                        mbar_arrive_expect_tx(&bar[C::KFULL + st], (uint32_t)(nsub * R * D * 2));
-                        mbar_arrive_expect_tx(&bar[C::VFULL + st], (uint32_t)(nsub * R * D * 2));
+                        mbar_arrive_expect_tx(&bar[KFULL + st], (uint32_t)(nsub * R * D * 2));
+                        mbar_arrive_expect_tx(&bar[VFULL + st], (uint32_t)(nsub * R * D * 2));
                     }
                 }
                 ok = __shfl_sync(FULL, ok ? 1 : 0, 0) != 0;
@@ -295,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
                     const int key = j * TILE + sub * R, lb = key / a.block_size;
                     if (lb >= base + 32) {
                         base = lb;
-                        id = __ldg(bt + min(base + lane, last));
+                        id = ids(s, base);
                     }
                     const int blk = __shfl_sync(FULL, id, lb - base);
                     if (lane == 0) {
@@ -304,17 +403,12 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
                             record_error(a.err, PA_DEV_BAD_BLOCK, (long long)s.b * a.max_blocks + lb);
                         // A box outside the pool is filled with zeros.
                         const int row = bad ? -2 * R : blk * a.block_size + key % a.block_size;
-                        uint8_t *k = smem + C::OFF_K + st * KV_BYTES + sub * R * 128;
-                        uint8_t *v = smem + C::OFF_V + st * KV_BYTES + sub * R * 128;
-                        if (R == TILE) {
-                            tma_load_4d_plain(k, &tmk, 0, row, 0, s.g, &bar[C::KFULL + st]);
-                            tma_load_4d_plain(v, &tmv, 0, row, 0, s.g, &bar[C::VFULL + st]);
-                        } else {
-                            tma_load_4d_plain(k, &tmk, 0, row, 0, s.g, &bar[C::KFULL + st]);
-                            tma_load_4d_plain(k + KV_HALF, &tmk, 0, row, 1, s.g, &bar[C::KFULL + st]);
-                            tma_load_4d_plain(v, &tmv, 0, row, 0, s.g, &bar[C::VFULL + st]);
-                            tma_load_4d_plain(v + KV_HALF, &tmv, 0, row, 1, s.g, &bar[C::VFULL + st]);
-                        }
+                        uint8_t *k = smem + OFF_K + st * KV_BYTES + sub * R * 128;
+                        uint8_t *v = smem + OFF_V + st * KV_BYTES + sub * R * 128;
+                        tma_load_4d_plain(k, &tmk, 0, row, 0, s.g, &bar[KFULL + st]);
+                        if (R != TILE) tma_load_4d_plain(k + KV_HALF, &tmk, 0, row, 1, s.g, &bar[KFULL + st]);
+                        tma_load_4d_plain(v, &tmv, 0, row, 0, s.g, &bar[VFULL + st]);
+                        if (R != TILE) tma_load_4d_plain(v + KV_HALF, &tmv, 0, row, 1, s.g, &bar[VFULL + st]);
                     }
                 }
                 if (!ok) break;
@@ -322,29 +416,31 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
         }
         if (lane == 0 && !ok) {  // issued copies land before the shared memory is given back
             for (uint32_t x = gg >= (uint32_t)ST ? gg - ST : 0; x < gg; ++x) {
-                (void)mbar_wait(&bar[C::KFULL + x % ST], (x / ST) & 1u);
-                (void)mbar_wait(&bar[C::VFULL + x % ST], (x / ST) & 1u);
+                (void)mbar_wait(&bar[KFULL + x % ST], (x / ST) & 1u);
+                (void)mbar_wait(&bar[VFULL + x % ST], (x / ST) & 1u);
             }
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- S = Q K^T
         if (lane == 0) {
-            uint32_t gg = 0, ui = 0, th[NT] = {};  // tiles in all, items, tiles of each row tile
+            uint32_t gg = 0, th[2] = {0, 0}, uq[2] = {0, 0};  // tiles, and per row tile: tiles, segments
             bool issued = false;
-            while (ok && walk.next(s)) {
-                if (!(ok = wait_or_abort(&bar[C::QFULL], ui & 1u, abort, a.err, 702))) break;
-                const int nh = NT == 1 ? 1 : (s.rows + ROWS - 1) / ROWS;
+            for (int k = 0; ok && walk.next(s); ++k) {
+                const int h0 = h_begin(k), h1 = h_end(k, s);
                 for (int j = s.t0; ok && j < s.t1; ++j, ++gg) {
                     const int st = gg % ST;
-                    if (!(ok = wait_or_abort(&bar[C::KFULL + st], (gg / ST) & 1u, abort, a.err, 703))) break;
-                    const uint64_t kdesc = smem_desc_sw128(smem_addr(smem + C::OFF_K + st * KV_BYTES), 16, SBO);
+                    if (!(ok = wait_or_abort(&bar[KFULL + st], (gg / ST) & 1u, abort, a.err, 703))) break;
+                    const uint64_t kdesc = smem_desc_sw128(smem_addr(smem + OFF_K + st * KV_BYTES), 16, SBO);
 #pragma unroll
-                    for (int h = 0; h < NT; ++h) {
-                        if (h >= nh) break;
+                    for (int h = 0; h < 2; ++h) {
+                        if (h < h0 || h >= h1) continue;
                         const int b = th[h] & 1;
+                        if (j == s.t0) {
+                            if (!(ok = wait_or_abort(&bar[QFULL + h], uq[h] & 1u, abort, a.err, 702))) break;
+                            ++uq[h];
+                        }
                         // The buffer is free once the P.V of two tiles ago has read it.
-                        if (!(ok = wait_or_abort(&bar[C::PDONE + 2 * h + b], ((th[h] >> 1) & 1u) ^ 1u, abort, a.err,
-                                                 704)))
+                        if (!(ok = wait_or_abort(&bar[PDONE + 2 * h + b], ((th[h] >> 1) & 1u) ^ 1u, abort, a.err, 704)))
                             break;
                         tc_fence_after();
                         const uint64_t qdesc = smem_desc_sw128(smem_addr(smem + h * QTILE), 16, SBO);
@@ -354,147 +450,176 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
                                         qdesc + (uint64_t)(((kk >> 2) * QHALF + (kk & 3) * 32) >> 4),
                                         kdesc + (uint64_t)(((kk >> 2) * KV_HALF + (kk & 3) * 32) >> 4), IDESC_S,
                                         kk > 0 ? 1u : 0u);
-                        mma_commit(&bar[C::SFULL + 2 * h + b]);
+                        mma_commit(&bar[SFULL + 2 * h + b]);
+                        if (j == s.t1 - 1) mma_commit(&bar[QEMPTY + h]);  // the segment's products have read Q
                         issued = true;
                         ++th[h];
                     }
                     if (!ok) break;
-                    mma_commit(&bar[C::KEMPTY + st]);
+                    mma_commit(&bar[KEMPTY + st]);
                 }
-                if (ok) mma_commit(&bar[C::QEMPTY]);  // every product of the item has read Q
-                ++ui;
             }
             if (issued && *abort) {
-                mma_commit(&bar[C::DRAIN]);
-                (void)mbar_wait(&bar[C::DRAIN], 0);
+                mma_commit(&bar[DRAIN]);
+                (void)mbar_wait(&bar[DRAIN], 0);
             }
         }
     } else if (warp == 2) {
         // ---------------------------------------------------------------- O += P V
         if (lane == 0) {
-            uint32_t gg = 0, th[NT] = {}, uh[NT] = {};
+            uint32_t gg = 0, th[2] = {0, 0}, uh[2] = {0, 0};
             bool issued = false;
-            while (ok && walk.next(s)) {
-                const int nh = NT == 1 ? 1 : (s.rows + ROWS - 1) / ROWS;
+            for (int k = 0; ok && walk.next(s); ++k) {
+                const int h0 = h_begin(k), h1 = h_end(k, s);
                 for (int j = s.t0; ok && j < s.t1; ++j, ++gg) {
                     const int st = gg % ST;
-                    if (!(ok = wait_or_abort(&bar[C::VFULL + st], (gg / ST) & 1u, abort, a.err, 705))) break;
+                    if (!(ok = wait_or_abort(&bar[VFULL + st], (gg / ST) & 1u, abort, a.err, 705))) break;
                     const int steps = (min(TILE, ctx_s[s.b] - j * TILE) + 15) / 16;  // keys past the last: P is 0
-                    const uint64_t vdesc = smem_desc_sw128(smem_addr(smem + C::OFF_V + st * KV_BYTES), KV_HALF, SBO);
+                    const uint64_t vdesc = smem_desc_sw128(smem_addr(smem + OFF_V + st * KV_BYTES), KV_HALF, SBO);
 #pragma unroll
-                    for (int h = 0; h < NT; ++h) {
-                        if (h >= nh) break;
+                    for (int h = 0; h < 2; ++h) {
+                        if (h < h0 || h >= h1) continue;
                         const int b = th[h] & 1;
-                        if (j == s.t0) {  // O is free once the last item's was read
-                            if (!(ok = wait_or_abort(&bar[C::OEMPTY + h], (uh[h] & 1u) ^ 1u, abort, a.err, 706))) break;
+                        if (j == s.t0) {  // O is free once the row tile's last segment was read
+                            if (!(ok = wait_or_abort(&bar[OEMPTY + h], (uh[h] & 1u) ^ 1u, abort, a.err, 706))) break;
                             ++uh[h];
                         }
-                        if (!(ok = wait_or_abort(&bar[C::PFULL + 2 * h + b], (th[h] >> 1) & 1u, abort, a.err, 707)))
-                            break;
+                        if (!(ok = wait_or_abort(&bar[PFULL + 2 * h + b], (th[h] >> 1) & 1u, abort, a.err, 707))) break;
                         tc_fence_after();
                         for (int kk = 0; kk < steps; ++kk)  // 16 keys a step = 8 TMEM columns of P
-                            mma_bf16_ts(tmem + C::COL_O + h * 128, tmem + h * 128 + b * TILE + kk * 8,
+                            mma_bf16_ts(tmem + COL_O + h * 128, tmem + h * 128 + b * TILE + kk * 8,
                                         vdesc + (uint64_t)((kk * 16 * 128) >> 4), IDESC_PV,
                                         (j > s.t0 || kk > 0) ? 1u : 0u);
-                        mma_commit(&bar[C::PDONE + 2 * h + b]);
+                        mma_commit(&bar[PDONE + 2 * h + b]);
                         issued = true;
                         ++th[h];
                     }
                     if (!ok) break;
-                    mma_commit(&bar[C::VEMPTY + st]);
+                    mma_commit(&bar[VEMPTY + st]);
                 }
             }
             if (issued && *abort) {
-                mma_commit(&bar[C::DRAIN + 1]);
-                (void)mbar_wait(&bar[C::DRAIN + 1], 0);
+                mma_commit(&bar[DRAIN + 1]);
+                (void)mbar_wait(&bar[DRAIN + 1], 0);
             }
         }
     } else if (warp == 3) {
         // ---------------------------------------------------------------- Q rows
-        uint32_t ui = 0;
-        while (ok && walk.next(s)) {
-            ok = __all_sync(FULL, wait_or_abort(&bar[C::QEMPTY], (ui & 1u) ^ 1u, abort, a.err, 708));
-            if (!ok) break;
+        uint32_t uq[2] = {0, 0};
+        for (int k = 0; ok && walk.next(s); ++k) {
             const __nv_bfloat16 *q = a.q + (int64_t)s.b * a.drafts * a.q_stride + (int64_t)s.g * a.G * D;
-            const uint32_t qs = smem_addr(smem);
             const int c = lane & 15;  // two rows a step, 16 lanes each; 8 steps in flight
-            for (int r0 = 0; r0 < s.rows; r0 += 16) {
-                uint4 v[8];
+#pragma unroll 1
+            for (int h = h_begin(k); ok && h < h_end(k, s); ++h) {
+                const uint32_t u = h ? uq[1]++ : uq[0]++;
+                ok = __all_sync(FULL, wait_or_abort(&bar[QEMPTY + h], (u & 1u) ^ 1u, abort, a.err, 708));
+                if (!ok) break;
+                const uint32_t qs = smem_addr(smem) + h * QTILE;
+                const int row0 = PAIR ? h * ROWS : 0, live = min(s.rows - row0, ROWS), rr0 = s.blk * BLOCK + row0;
+                for (int r0 = 0; r0 < live; r0 += 16) {
+                    uint4 v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int r = r0 + 2 * e + (lane >> 4), rr = s.blk * ROWS * NT + r;
-                    if (r < s.rows)
-                        v[e] = __ldg(reinterpret_cast<const uint4 *>(q + (int64_t)(rr / a.G) * a.q_stride + (rr % a.G) * D) + c);
-                }
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = r0 + 2 * e + (lane >> 4), rr = rr0 + r;
+                        if (r < live)
+                            v[e] = __ldg(
+                                reinterpret_cast<const uint4 *>(q + (int64_t)(rr / a.G) * a.q_stride + (rr % a.G) * D) + c);
+                    }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int r = r0 + 2 * e + (lane >> 4);
-                    if (r < s.rows)
-                        st_shared_u4(qs + (uint32_t)((r >> 7) * QTILE + (c >> 3) * QHALF + (r & 127) * 128 +
-                                                     (((c & 7) ^ (r & 7)) << 4)),
-                                     v[e]);
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = r0 + 2 * e + (lane >> 4);
+                        if (r < live)
+                            st_shared_u4(qs + (uint32_t)((c >> 3) * QHALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)), v[e]);
+                    }
                 }
+                fence_proxy_async_smem();  // the MMA reads Q through the async proxy
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[QFULL + h]);
             }
-            fence_proxy_async_smem();  // the MMA reads Q through the async proxy
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[C::QFULL]);
-            ++ui;
         }
     } else {
         // ---------------------------------------------------------------- softmax, output
-        const int h = NT == 1 ? 0 : (warp - 4) >> 2;  // row tile
+        const int h = (warp - 4) >> 2;  // row tile
         const int quarter = warp & 3;
         const int wrow = quarter * 32, row = wrow + lane;  // row of the tile == TMEM lane
-        const uint32_t t_lane = tmem + ((uint32_t)wrow << 16);
-        const uint32_t t_o = t_lane + C::COL_O + h * 128;
+        const uint32_t t_s = tmem + ((uint32_t)wrow << 16) + h * 128, t_o = tmem + ((uint32_t)wrow << 16) + COL_O + h * 128;
         const float sl = a.scale_log2;
-        auto wwait = [&](uint64_t *bb, uint32_t parity, int where) -> bool {
-            return __all_sync(FULL, wait_or_abort(bb, parity, abort, a.err, where));
+        auto wwait = [&](int i, uint32_t parity, int where) -> bool {
+            return __all_sync(FULL, wait_or_abort(&bar[i], parity, abort, a.err, where));
         };
         {
-            // Rows past a sequence's drafts: zeros.
-            const int sw = (warp - 4) + 4 * NT * blockIdx.x, nsw = 4 * NT * gridDim.x;
-            const int per = a.Hq * (D / 8) ;  // 16-byte chunks of a token
-            for (int t = sw; t < a.batch * a.drafts; t += nsw) {
+            // Tokens past a sequence's drafts: zeros.
+            const int per = a.Hq * (D / 8);  // 16-byte chunks of a token
+            for (int t = warp - 4 + 8 * blockIdx.x; t < a.batch * a.drafts; t += 8 * gridDim.x) {
                 const int b = t / a.drafts;
                 if (t - b * a.drafts < n_s[b]) continue;
                 uint4 *dst = reinterpret_cast<uint4 *>(a.out) + (int64_t)t * per;
                 for (int c = lane; c < per; c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        // odd[seg & 1] == seg + 1: a draft's V in segment number seg held something
-        // not finite.  (No warp is more than one segment ahead of another: a
-        // segment's last product needs the P of all of them.)
-        volatile int *odd = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
-        uint32_t gg = 0, th = 0;  // tiles in all (V ring), tiles of this row tile
-        for (int seg = 0; ok && walk.next(s); ++seg) {
-            const int live = min(max(s.rows - h * ROWS, 0), ROWS);  // live rows of this row tile
-            if (live == 0) {
-                gg += s.t1 - s.t0;
-                continue;
+        // A mark of segment number k (k + 1 in its place): a draft's V held
+        // something not finite.  Two places in turn: no warp is more than one
+        // segment of its own ahead of another, as a segment's last product needs the
+        // P of all of them.
+        volatile int *marks = abort + 1;
+        volatile int *last = abort + 5;  // jobs of each row tile
+        Job *jobs = reinterpret_cast<Job *>(smem + OFF_JOBS);
+        // The next segment that this row tile has rows in: its number, its first
+        // tile's number, and (asked for ahead) this row's mask.
+        int k_next = 0;
+        uint32_t g_next = 0;
+        struct Own {
+            Seg s;
+            int k;
+            uint32_t g;
+            unsigned long long m;
+        };
+        auto fetch = [&](Own &o) -> bool {
+            while (walk.next(o.s)) {
+                const int k = k_next++;
+                const uint32_t g = g_next;
+                g_next += o.s.t1 - o.s.t0;
+                if (h < h_begin(k) || h >= h_end(k, o.s)) continue;
+                o.k = k;
+                o.g = g;
+                o.m = 0;
+                const int row0 = PAIR ? h * ROWS : 0;
+                if (row0 + row < o.s.rows) {
+                    const int di = (o.s.blk * BLOCK + row0 + row) / a.G;
+                    o.m = a.mask ? __ldg(a.mask + (int64_t)o.s.b * a.drafts + di) : di >= 63 ? ~0ull : (2ull << di) - 1;
+                }
+                return true;
             }
+            return false;
+        };
+        Own nx;
+        bool have = fetch(nx);
+        uint32_t th = 0, ns = 0;  // tiles of this row tile, parts written
+        while (ok && have) {
+            s = nx.s;
+            const int k = nx.k;
+            uint32_t gg = nx.g;
+            unsigned long long m64 = nx.m;
+            have = fetch(nx);
+            const int row0 = PAIR ? h * ROWS : 0;
+            const int live = min(s.rows - row0, ROWS);  // live rows of this row tile
             const int ctx = ctx_s[s.b], n = n_s[s.b], first = ctx - n;
-            const int grow = s.blk * ROWS * NT + h * ROWS + row;  // row of the (sequence, kv head)
-            const int di = grow / a.G;                            // its draft
             const bool mine = row < live, wlive = wrow < live;
-            unsigned long long m64 = 0;
-            if (mine) {
-                m64 = a.mask ? __ldg(a.mask + (int64_t)s.b * a.drafts + di) : di >= 63 ? ~0ull : (2ull << di) - 1;
-                if (n < 64) m64 &= (1ull << n) - 1;
-            }
+            if (n < 64) m64 &= (1ull << n) - 1;
+            volatile int *mark = marks + (PAIR ? k & 1 : 2 * h + ((k >> 1) & 1));
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = s.t0; ok && j < s.t1; ++j, ++gg, ++th) {
                 const int b = th & 1, kb = j * TILE;
-                const uint32_t cs = t_lane + h * 128 + b * TILE;
+                const uint32_t cs = t_s + b * TILE;
                 if (kb + TILE > first) {
                     // A tile with drafts: V's rows past the last key that the
                     // product reads become zeros, and drafts' values that are not
                     // finite too.  Each row tile of the item does it before its
                     // product; what the first has mended, the second leaves.
                     const int st = gg % ST;
-                    if (!(ok = wwait(&bar[C::VFULL + st], (gg / ST) & 1u, 709))) break;
+                    if (!(ok = wwait(VFULL + st, (gg / ST) & 1u, 709))) break;
                     const int kend = min(TILE, ctx - kb), kpad = (kend + 15) & ~15, k0 = max(0, first - kb);
-                    const uint32_t vb = smem_addr(smem + C::OFF_V + st * KV_BYTES);
+                    const uint32_t vb = smem_addr(smem + OFF_V + st * KV_BYTES);
                     for (int i = threadIdx.x & 127; i < (kpad - k0) * 16; i += 128) {
                         const int r = k0 + (i >> 4), c = i & 15;
                         const uint32_t at = vb + (uint32_t)((c >> 3) * KV_HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -503,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
                             if (w.x | w.y | w.z | w.w) st_shared_u4(at, make_uint4(0u, 0u, 0u, 0u));
                         } else if (not_finite2(w.x) || not_finite2(w.y) || not_finite2(w.z) || not_finite2(w.w)) {
                             // Seen by every warp at the segment's end: its P follows this.
-                            odd[seg & 1] = seg + 1;
+                            *mark = k + 1;
                             __threadfence_block();
                             st_shared_u4(at, make_uint4(finite_only(w.x), finite_only(w.y), finite_only(w.z),
                                                         finite_only(w.w)));
@@ -511,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                if (!(ok = wwait(&bar[C::SFULL + 2 * h + b], (th >> 1) & 1u, 710))) break;
+                if (!(ok = wwait(SFULL + 2 * h + b, (th >> 1) & 1u, 710))) break;
                 tc_fence_after();
                 if (wlive) {
                     uint32_t r[TILE];
@@ -521,27 +646,26 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
                     if (kb + TILE > first) {
                         const int d = first - kb;  // keys of the tile before the drafts
                         unsigned long long vis;
-                        if (d >= TILE) vis = ~0ull;
-                        else if (d > 0) vis = ((1ull << d) - 1) | (m64 << d);
+                        if (d > 0) vis = ((1ull << d) - 1) | (m64 << d);
                         else vis = -d < 64 ? m64 >> -d : 0ull;
                         const uint32_t vlo = (uint32_t)vis, vhi = (uint32_t)(vis >> 32);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            if (!((vlo >> k) & 1u)) r[k] = __float_as_uint(-INFINITY);
-                            if (!((vhi >> k) & 1u)) r[k + 32] = __float_as_uint(-INFINITY);
+                        for (int e = 0; e < 32; ++e) {
+                            if (!((vlo >> e) & 1u)) r[e] = __float_as_uint(-INFINITY);
+                            if (!((vhi >> e) & 1u)) r[e + 32] = __float_as_uint(-INFINITY);
                         }
                     }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k2 = 0; k2 < TILE / 2; ++k2)
-                        m4[k2 & 3] = max3(m4[k2 & 3], __uint_as_float(r[2 * k2]), __uint_as_float(r[2 * k2 + 1]));
+                    for (int e = 0; e < TILE / 2; ++e)
+                        m4[e & 3] = max3(m4[e & 3], __uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
                     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     const bool grow_m = mine && (mx - m_run) * sl > kLazy;  // rows that are not live stay put
                     const float m_new = grow_m ? mx : m_run;
                     const float alpha = grow_m ? fast_exp2((m_run - m_new) * sl) : 1.f;
                     if (j > s.t0 && __any_sync(FULL, grow_m)) {
                         // O holds the products up to the previous tile before it is rescaled.
-                        if (!(ok = wwait(&bar[C::PDONE + 2 * h + ((th - 1) & 1)], ((th - 1) >> 1) & 1u, 711))) break;
+                        if (!(ok = wwait(PDONE + 2 * h + ((th - 1) & 1), ((th - 1) >> 1) & 1u, 711))) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
@@ -556,146 +680,137 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
                     l_run *= alpha;
                     m_run = m_new;
                     const float neg_m = m_run == -INFINITY ? 0.f : -m_run * sl;
-                    float rs[4] = {0.f, 0.f, 0.f, 0.f};
+                    float2 rs[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+                    const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(neg_m, neg_m);
                     uint32_t pk[TILE / 2];
 #pragma unroll
-                    for (int k2 = 0; k2 < TILE / 2; ++k2) {
-                        const float p0 = fast_exp2(fmaf(__uint_as_float(r[2 * k2]), sl, neg_m));
-                        const float p1 = fast_exp2(fmaf(__uint_as_float(r[2 * k2 + 1]), sl, neg_m));
-                        pk[k2] = pack_bf16(p0, p1);
-                        rs[k2 & 3] += bf16lo(pk[k2]) + bf16hi(pk[k2]);
+                    for (int e = 0; e < TILE / 2; ++e) {
+                        const float2 x = fma2(make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), sl2, nm2);
+                        pk[e] = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
+                        rs[e & 3] = add2(rs[e & 3], make_float2(bf16lo(pk[e]), bf16hi(pk[e])));
                     }
                     tmem_st32(cs, pk);  // P over the first 32 columns of the buffer
                     tmem_st_wait();
-                    l_run += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+                    l_run += ((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y));
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[C::PFULL + 2 * h + b]);
+                if (lane == 0) mbar_arrive(&bar[PFULL + 2 * h + b]);
             }
             if (!ok) break;
             // ---- the segment's rows
-            if (!(ok = wwait(&bar[C::PDONE + 2 * h + ((th - 1) & 1)], ((th - 1) >> 1) & 1u, 712))) break;
+            if (!(ok = wwait(PDONE + 2 * h + ((th - 1) & 1), ((th - 1) >> 1) & 1u, 712))) break;
             tc_fence_after();
-            uint32_t o[D];
+            const bool whole = s.t0 == 0 && s.t1 == s.nt;
+            // A part: slot 1 of the item's first CTA, slot 0 of the others.
+            int c0 = 0, nparts = 1;
+            float *slot = nullptr;
+            if (!whole) {  // the CTA whose range holds unit x: ((x + 1) nC - 1) / P
+                c0 = (int)(((uint64_t)(s.first + 1) * nC - 1) / P);
+                nparts = (int)(((uint64_t)(s.first + s.nt) * nC - 1) / P) - c0 + 1;
+                slot = a.parts + (size_t)(2 * blockIdx.x + (blockIdx.x == c0 ? 1 : 0)) * slot_of(a.part_rows);
+            }
             if (wlive) {
+                const float inv = !whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;  // a row that sees nothing: zeros
+                const bool odd = *mark == k + 1;
+                const int gr = s.blk * BLOCK + row0 + row;  // row of the (sequence, kv head)
+                __nv_bfloat16 *dst = a.out + (((int64_t)s.b * a.drafts + gr / a.G) * a.Hq + s.g * a.G + gr % a.G) * D;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(t_o + c * 32, o);
+                    tmem_ld_wait();
+                    if (odd) {
+                        // What was taken out of V: added to the rows that see it.
+                        const int lo = max(0, s.t0 * TILE - first), hi = min(n, s.t1 * TILE - first);
+                        for (int j = lo; j < hi; ++j) {
+                            const int p = first + j, blk = __ldg(a.bt + (int64_t)s.b * a.max_blocks + p / a.block_size);
+                            if (blk < 0 || blk >= a.num_blocks) continue;
+                            const uint16_t *v = reinterpret_cast<const uint16_t *>(
+                                a.v_cache + (((int64_t)blk * a.block_size + p % a.block_size) * a.Hkv + s.g) * D + c * 32);
+                            const float x = __uint_as_float((uint32_t)__ldg(v + lane) << 16);  // 32 values across the warp
+                            if (!__any_sync(FULL, !isfinite(x))) continue;
+                            const bool sees = mine && ((m64 >> j) & 1);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(t_o + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * c]));
-                tmem_ld_wait();
+                            for (int e = 0; e < 32; ++e) {
+                                const float y = __shfl_sync(FULL, x, e);
+                                if (sees && !isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+                            }
+                        }
+                    }
+                    if (mine && whole) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t *v = &o[8 * e];
+                            reinterpret_cast<uint4 *>(dst)[4 * c + e] =
+                                make_uint4(pack_bf16(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv),
+                                           pack_bf16(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv),
+                                           pack_bf16(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv),
+                                           pack_bf16(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv));
+                        }
+                    } else if (mine) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            reinterpret_cast<uint4 *>(slot + (size_t)(row0 + row) * D)[8 * c + e] =
+                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[C::OEMPTY + h]);
-            if (!wlive) continue;
-            if (odd[seg & 1] == seg + 1) {
-                // What was taken out of V: added to the rows that see it.
-                const int lo = max(0, s.t0 * TILE - first), hi = min(n, s.t1 * TILE - first);  // drafts of the segment
-                for (int j = lo; j < hi; ++j) {
-                    const int p = first + j, blk = __ldg(a.bt + (int64_t)s.b * a.max_blocks + p / a.block_size);
-                    if (blk < 0 || blk >= a.num_blocks) continue;
-                    const uint2 *v = reinterpret_cast<const uint2 *>(
-                        a.v_cache + (((int64_t)blk * a.block_size + p % a.block_size) * a.Hkv + s.g) * D);
-                    const uint2 w = __ldg(v + lane);  // the row across the warp
-                    if (!__any_sync(FULL, not_finite2(w.x) || not_finite2(w.y))) continue;
-                    const bool sees = mine && ((m64 >> j) & 1);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const uint32_t w0 = __shfl_sync(FULL, w.x, c), w1 = __shfl_sync(FULL, w.y, c);
-                        const float x[4] = {bf16lo(w0), bf16hi(w0), bf16lo(w1), bf16hi(w1)};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (sees && !isfinite(x[e])) o[4 * c + e] = __float_as_uint(__uint_as_float(o[4 * c + e]) + x[e]);
-                    }
-                }
-            }
-            const bool whole = s.t0 == 0 && s.t1 == s.nt;
-            auto out_row = [&](int gr) -> __nv_bfloat16 * {
-                return a.out + (((int64_t)s.b * a.drafts + gr / a.G) * a.Hq + s.g * a.G + gr % a.G) * D;
-            };
-            if (whole) {
-                if (mine) {
-                    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // a row that sees nothing: zeros
-                    uint4 *dst = reinterpret_cast<uint4 *>(out_row(grow));
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const uint32_t *v = &o[8 * c];
-                        dst[c] = make_uint4(pack_bf16(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv),
-                                            pack_bf16(__uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv),
-                                            pack_bf16(__uint_as_float(v[4]) * inv, __uint_as_float(v[5]) * inv),
-                                            pack_bf16(__uint_as_float(v[6]) * inv, __uint_as_float(v[7]) * inv));
-                    }
-                }
-                continue;
-            }
-            // A part: slot 1 of the item's first CTA, slot 0 of the others.
-            const int c0 = owner(s.first), nparts = owner(s.first + (uint32_t)s.nt - 1) - c0 + 1;
-            const size_t slot_floats = slot_of(a.part_rows);
-            const int trow = h * ROWS + row;
-            {
-                float *slot = a.parts + (size_t)(2 * blockIdx.x + (blockIdx.x == c0 ? 1 : 0)) * slot_floats;
-                if (mine) {
-                    float4 *dst = reinterpret_cast<float4 *>(slot + (size_t)trow * D);
-#pragma unroll
-                    for (int c = 0; c < D / 4; ++c)
-                        dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                             __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
-                    reinterpret_cast<float2 *>(slot + (size_t)a.part_rows * D)[trow] = make_float2(m_run * sl, l_run);
-                }
-            }
+            if (lane == 0) mbar_arrive(&bar[OEMPTY + h]);
+            if (whole) continue;
+            if (mine) reinterpret_cast<float2 *>(slot + (size_t)a.part_rows * D)[row0 + row] = make_float2(m_run * sl, l_run);
+            // The row tile's four warps have written: the part is counted; where it
+            // is the item's last, they combine the parts.
             __threadfence();
             __syncwarp();
-            int arrived = 0;
-            int *cnt = a.count + c0 * 8 + h * 4 + quarter;
-            if (lane == 0) arrived = atomicAdd(cnt, 1);
-            arrived = __shfl_sync(FULL, arrived, 0);
-            if (arrived != nparts - 1) continue;
-            __threadfence();
-            if (lane == 0) *cnt = 0;  // as it was found
-            for (int rr = 0; rr < min(32, live - wrow); ++rr) {
-                const int tr = h * ROWS + wrow + rr;
-                float m = -INFINITY, l = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int p = 0; p < nparts; ++p) {
-                    const float *slot = a.parts + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats;
-                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot + (size_t)a.part_rows * D) + tr);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot + (size_t)tr * D) + lane);
-                    const float mn = fmaxf(m, ml.x);
-                    if (mn == -INFINITY) {  // nothing seen so far; NaN goes on
-                        acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
-                        l += ml.y;
-                        continue;
+            if (lane == 0) mbar_arrive(&bar[WROTE + h]);
+            if (quarter == 0) {
+                if (!(ok = wwait(WROTE + h, ns & 1u, 713))) break;
+                if (lane == 0) {
+                    int *cnt = a.count + 2 * c0 + h * (PAIR ? 1 : 0);
+                    __threadfence();
+                    if (atomicAdd(cnt, 1) == nparts - 1) {
+                        __threadfence();
+                        *cnt = 0;  // as it was found
+                        jobs[2 * h + last[h]] = {s.b, s.g, s.blk, row0, live, c0, nparts};
+                        last[h] = last[h] + 1;
                     }
-                    const float f0 = fast_exp2(m - mn), f1 = fast_exp2(ml.x - mn);
-                    acc.x = acc.x * f0 + v.x * f1;
-                    acc.y = acc.y * f0 + v.y * f1;
-                    acc.z = acc.z * f0 + v.z * f1;
-                    acc.w = acc.w * f0 + v.w * f1;
-                    l = l * f0 + ml.y * f1;
-                    m = mn;
+                    mbar_arrive(&bar[TOLD + h]);
                 }
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint2 w = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-                reinterpret_cast<uint2 *>(out_row(s.blk * ROWS * NT + tr))[lane] = w;
             }
+            if (!(ok = wwait(TOLD + h, ns & 1u, 714))) break;
+            ++ns;
+        }
+        // The items whose last part was this CTA's (a CTA has two parts at most):
+        // here, where nothing of the loop above is alive in registers.
+        for (int i = 0; ok && i < last[h]; ++i) {
+            const Job job = jobs[2 * h + i];
+            __threadfence();
+            merge_rows(a, job, quarter, lane, [&](int tr) -> __nv_bfloat16 * {
+                const int gr = job.blk * BLOCK + tr;
+                return a.out + (((int64_t)job.b * a.drafts + gr / a.G) * a.Hq + job.g * a.G + gr % a.G) * D;
+            });
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, C::COLS);
+    if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-// Counters, then the parts.  A row block of an item has at most min(drafts * G,
-// 128 * NT) rows.
+// Counters (at the same place for every shape), then the parts.
 struct Layout {
-    int nt, part_rows;
+    bool pair;
+    int part_rows;  // rows of an item at most
     size_t parts, bytes;
 };
 Layout layout_of(int drafts, int G) {
     Layout l;
-    l.nt = drafts * G > ROWS ? 2 : 1;
-    l.part_rows = std::min(drafts * G, ROWS * l.nt);
-    l.parts = (size_t)kMaxGrid * 8 * sizeof(int);
+    l.pair = drafts * G > ROWS;
+    l.part_rows = std::min(drafts * G, 2 * ROWS);
+    l.parts = (size_t)kMaxGrid * 2 * sizeof(int);
     l.bytes = l.parts + (size_t)kMaxGrid * 2 * slot_of(l.part_rows) * sizeof(float);
     return l;
 }
@@ -703,20 +818,20 @@ Layout layout_of(int drafts, int G) {
 // Per (device, variant): the shared-memory attribute has been set.
 std::atomic<int> g_attr_done[64][2];
 
-template <int NT>
+template <bool PAIR>
 pa_status launch_tree(const CUtensorMap &tmk, const CUtensorMap &tmv, const TreeArgs &a, int grid, cudaStream_t stream) {
-    const size_t smem = tree_smem(Cfg<NT>::OFF_ARR, a.batch);
+    const size_t smem = tree_smem(a.batch);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     if (dev < 0 || dev >= 64) return fail(PA_ERR_UNSUPPORTED, "device %d", dev);
-    if (!g_attr_done[dev][NT - 1].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(decode_tree_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)tree_smem(Cfg<NT>::OFF_ARR, kMaxBatch));
+    if (!g_attr_done[dev][PAIR].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(decode_tree_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)tree_smem(kMaxBatch));
         if (e != cudaSuccess) return cuda_fail(e, "decode_tree_kernel shared memory");
-        g_attr_done[dev][NT - 1].store(1, std::memory_order_release);
+        g_attr_done[dev][PAIR].store(1, std::memory_order_release);
     }
-    return launch_pdl(decode_tree_kernel<NT>, dim3((unsigned)grid), dim3(Cfg<NT>::THREADS), smem, stream,
+    return launch_pdl(decode_tree_kernel<PAIR>, dim3((unsigned)grid), dim3(THREADS), smem, stream,
                       "decode_tree_kernel", tmk, tmv, a);
 }
 
@@ -769,7 +884,7 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     const Layout l = layout_of(num_drafts, G);
     const int64_t keys = (int64_t)max_blocks_per_seq * block_size;
     if (keys > 0x7fffffffLL - 4096) return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size must fit 31 bits");
-    const int64_t blocks = (num_drafts * G + ROWS * l.nt - 1) / (ROWS * l.nt);
+    const int64_t blocks = (num_drafts * G + 2 * ROWS - 1) / (2 * ROWS);
     const int64_t a_seq = (int64_t)num_kv_heads * blocks * ((keys + TILE - 1) / TILE + kItemCost);
     if (num_kv_heads > (1 << 16) || a_seq > 0x7fffffffLL / batch)
         return fail(PA_ERR_UNSUPPORTED, "too many tiles (batch * num_kv_heads * max_blocks_per_seq * block_size)");
@@ -812,7 +927,7 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     if (st != PA_OK) return st;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid), a_seq * batch / kMinTiles));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    return l.nt == 1 ? launch_tree<1>(tmk, tmv, a, (int)grid, cs) : launch_tree<2>(tmk, tmv, a, (int)grid, cs);
+    return l.pair ? launch_tree<true>(tmk, tmv, a, (int)grid, cs) : launch_tree<false>(tmk, tmv, a, (int)grid, cs);
 }
 
 }  // extern "C"
