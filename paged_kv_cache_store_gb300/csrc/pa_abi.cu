@@ -133,6 +133,24 @@ pa_status encode_kv_tensor_map_halves(CUtensorMap *map, const void *base, int64_
     return encode_halves_map(map, base, num_slots, (int64_t)num_kv_heads * 256, num_kv_heads, box_rows, 2);
 }
 
+pa_status encode_token_heads_map(CUtensorMap *map, const void *base, int64_t num_tokens, int64_t token_stride_bytes,
+                                 int32_t num_heads, int32_t box_heads, int32_t box_tokens) {
+    pa_status st = get_encoder();
+    if (st != PA_OK) return st;
+    // Dims innermost first: 64 elements of a head's half, head, token, half.
+    const cuuint64_t dims[4] = {64u, (cuuint64_t)num_heads, (cuuint64_t)num_tokens, 2u};
+    const cuuint64_t strides[3] = {256u, (cuuint64_t)token_stride_bytes, 128u};
+    const cuuint32_t box[4] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens, 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
+                          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %lld tokens x %d heads", (int)r,
+                    (long long)num_tokens, num_heads);
+    return PA_OK;
+}
+
 pa_status encode_row_map_u8(CUtensorMap *map, const void *base, int64_t num_rows, int32_t box_rows) {
     pa_status st = get_encoder();
     if (st != PA_OK) return st;

@@ -227,6 +227,11 @@ pa_status encode_halves_map(CUtensorMap *map, const void *base, int64_t num_rows
 pa_status encode_tensor_map_3d(CUtensorMap *map, const void *base, int64_t dim0, int64_t dim1, int64_t dim2,
                                int64_t stride1_bytes, int64_t stride2_bytes, int32_t box0, int32_t box2,
                                bool swizzle128);
+// A view of [tokens][heads][128] bf16 (token stride in bytes, a multiple of 16)
+// as [half][token][head][64], box {64, box_heads, box_tokens, 1}: a box lands as
+// rows of 128 bytes, the heads of a token one after the other.
+pa_status encode_token_heads_map(CUtensorMap *map, const void *base, int64_t num_tokens, int64_t token_stride_bytes,
+                                 int32_t num_heads, int32_t box_heads, int32_t box_tokens);
 // 2-D map over an 8-bit pool's [num_rows][128] one-byte rows with box
 // {128, box_rows} and 128-byte swizzle.
 pa_status encode_row_map_u8(CUtensorMap *map, const void *base, int64_t num_rows, int32_t box_rows);

@@ -10,10 +10,10 @@
 // a matrix product for the 5th-generation tensor cores.  An item is one
 // (sequence, kv head, block of 128 * NT rows); its 64-key tiles, laid end to end
 // over all items, are cut into one range of equal cost per CTA.  Roles of a CTA:
-//   warp 0     K and V tiles by TMA into rings of ST stages, block ids 32 at a time
+//   warp 0     Q rows and K tiles by TMA, block ids 32 at a time
 //   warp 1     S = Q K^T (M = 128, N = 64, K = 128) into one of two TMEM buffers
 //   warp 2     O += P V (P from TMEM, V as an MN-major operand)
-//   warp 3     Q rows of the next item into shared memory
+//   warp 3     V tiles by TMA
 //   warps 4..  one thread per row: online softmax in base 2, P over S as bf16
 // Of the 128 rows of an MMA only the live ones are loaded and read back; the
 // others hold whatever the memory held, which cannot reach a live row.
@@ -42,8 +42,6 @@ constexpr int TILE = 64;                 // keys per tile
 constexpr int ROWS = 128;                // rows of one MMA
 constexpr int KV_BYTES = TILE * D * 2;   // a K or V tile: 16 KiB, [2 halves][64 rows][128 B]
 constexpr int KV_HALF = KV_BYTES / 2;
-constexpr int QTILE = ROWS * D * 2;      // 32 KiB, [2 halves][128 rows][128 B]
-constexpr int QHALF = QTILE / 2;
 constexpr uint32_t SBO = 1024;           // 8 rows x 128 B between core-matrix groups
 constexpr uint32_t IDESC_S = idesc_bf16_f32(ROWS, TILE, false, false);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(ROWS, D, false, true);
@@ -59,34 +57,32 @@ constexpr unsigned FULL = 0xffffffffu;
 // has one, and consecutive items alternate between the two row-tile sets (Q,
 // scores, O and softmax warps), so that one item's start and end run beside the
 // other's tiles.
-constexpr int ST = 4;                            // ring stages
 constexpr int THREADS = 384;
-constexpr int OFF_K = 2 * QTILE;
-constexpr int OFF_V = OFF_K + ST * KV_BYTES;
-constexpr int OFF_BAR = OFF_V + ST * KV_BYTES;
+constexpr int KMAX = 6, VMAX = 8;                // ring stages at most
 enum {  // barriers: rings, then per row tile [2] (and score buffer [2])
-    KFULL = 0, KEMPTY = KFULL + ST, VFULL = KEMPTY + ST, VEMPTY = VFULL + ST, SFULL = VEMPTY + ST, PFULL = SFULL + 4,
-    PDONE = PFULL + 4, OEMPTY = PDONE + 4, QFULL = OEMPTY + 2, QEMPTY = QFULL + 2, WROTE = QEMPTY + 2, TOLD = WROTE + 2,
-    DRAIN = TOLD + 2, NBAR = DRAIN + 2
+    KFULL = 0, KEMPTY = KFULL + KMAX, VFULL = KEMPTY + KMAX, VEMPTY = VFULL + VMAX, SFULL = VEMPTY + VMAX,
+    PFULL = SFULL + 4, PDONE = PFULL + 4, OEMPTY = PDONE + 4, QFULL = OEMPTY + 2, QEMPTY = QFULL + 2,
+    WROTE = QEMPTY + 2, TOLD = WROTE + 2, DRAIN = TOLD + 2, NBAR = DRAIN + 2
 };
-constexpr int OFF_MISC = OFF_BAR + (NBAR * 8 + 15) / 16 * 16;  // TMEM address, abort, marks [4], last [2], scan scratch [12]
-constexpr int OFF_JOBS = OFF_MISC + 128;                       // Job [2][2]
-constexpr int OFF_ARR = OFF_JOBS + 4 * 28;                        // ctx, n, cum [batch + 1]
+// Shared memory: Q [2], the rings, then from off_bar on the barriers, a few words
+// (TMEM address, abort, marks [4], jobs [2], scan scratch [12]), the jobs [2][2],
+// and per sequence the running sum of units, the length (int) and the drafts (byte).
+constexpr int MISC = (NBAR * 8 + 15) / 16 * 16, JOBS = MISC + 128, ARRAYS = JOBS + 4 * 28;
 constexpr uint32_t TMEM_COLS = 512, COL_O = 256;               // S(h, b) at h * 128 + b * 64, O(h) at COL_O + h * 128
-constexpr size_t tree_smem(int batch) { return OFF_ARR + 12 * (size_t)(batch + 1) + 1024; }
-static_assert(tree_smem(kMaxBatch) <= 232448, "shared memory");
+constexpr int kMaxSmem = 232448;
+constexpr int fixed_smem(int batch) { return 1024 + ARRAYS + 9 * (batch + 1); }
 
 // Floats of a part: o [rows][D], (m, l) [rows], a multiple of 16 bytes.
 __host__ __device__ constexpr size_t slot_of(int rows) { return ((size_t)rows * (D + 2) + 3) / 4 * 4; }
 
 struct TreeArgs {
     __nv_bfloat16 *out;
-    const __nv_bfloat16 *q;
     const __nv_bfloat16 *v_cache;
-    int64_t q_stride;  // elements between tokens
     const int32_t *bt, *ctx, *lens;
     const unsigned long long *mask;  // null: a chain
-    int32_t max_blocks, batch, drafts, Hq, Hkv, G, block_size, num_blocks, box_rows, checked;
+    int32_t max_blocks, batch, drafts, Hq, Hkv, G, block_size, num_blocks, box_rows, q_box, checked;
+    int32_t q_rows;          // rows that a Q tile has room for (a multiple of 8): the MMA reads on past them
+    int32_t k_stages, v_stages;
     float scale_log2;
     int *count;    // [grid][2] arrivals: of the row tiles of the item that begins in a range and ends in a later one
     float *parts;  // [grid][2] of slot_of(part_rows)
@@ -159,7 +155,8 @@ struct Seg {
 template <bool PAIR>
 struct Walker {
     static constexpr int BLOCK = PAIR ? 2 * ROWS : ROWS;  // rows of an item
-    const int *ctx_s, *n_s;
+    const int *ctx_s;
+    const uint8_t *n_s;
     const uint32_t *cum;
     int G;
     uint32_t x, x1;
@@ -277,18 +274,21 @@ __device__ __forceinline__ void merge_rows(const TreeArgs &a, const Job &job, in
 
 template <bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
-    decode_tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                       const __grid_constant__ TreeArgs a) {
+    decode_tree_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ TreeArgs a) {
     constexpr int BLOCK = Walker<PAIR>::BLOCK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_MISC);
-    volatile int *abort = reinterpret_cast<volatile int *>(smem + OFF_MISC + 4);
-    uint32_t *wsum = reinterpret_cast<uint32_t *>(smem + OFF_MISC + 48);
-    int *ctx_s = reinterpret_cast<int *>(smem + OFF_ARR);
-    int *n_s = ctx_s + (a.batch + 1);
-    uint32_t *cum = reinterpret_cast<uint32_t *>(n_s + (a.batch + 1));
+    const int qhalf = a.q_rows * 128, qtile = 2 * qhalf;
+    uint8_t *k_ring = smem + 2 * qtile, *v_ring = k_ring + a.k_stages * KV_BYTES;
+    uint8_t *ctl = v_ring + a.v_stages * KV_BYTES;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(ctl);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctl + MISC);
+    volatile int *abort = reinterpret_cast<volatile int *>(ctl + MISC + 4);
+    uint32_t *wsum = reinterpret_cast<uint32_t *>(ctl + MISC + 48);
+    uint32_t *cum = reinterpret_cast<uint32_t *>(ctl + ARRAYS);
+    int *ctx_s = reinterpret_cast<int *>(cum + (a.batch + 1));
+    uint8_t *n_s = reinterpret_cast<uint8_t *>(ctx_s + (a.batch + 1));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < 7; ++i) abort[i] = 0;  // and the marks behind it
         fence_mbar_init();
+        prefetch_tensormap(&tmq);
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (n == 0) ctx = 0;
             ctx_s[b] = ctx;
-            n_s[b] = n;
+            n_s[b] = (uint8_t)n;
             const int blocks = (n * a.G + BLOCK - 1) / BLOCK;
             u = n ? (uint32_t)((ctx + TILE - 1) / TILE + kItemCost) * (uint32_t)(a.Hkv * blocks) : 0u;
         }
@@ -360,10 +361,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     Seg s;
     bool ok = true;
 
-    if (warp == 0) {
-        // ---------------------------------------------------------------- K and V tiles
-        uint32_t gg = 0;
+    // A ring's place: stage, and the parity of its current round.
+    struct Ring {
+        int n, st = 0;
+        uint32_t par = 0;
+        __device__ __forceinline__ Ring(int stages) : n(stages) {}
+        __device__ __forceinline__ void next() {
+            if (++st == n) {
+                st = 0;
+                par ^= 1u;
+            }
+        }
+    };
+
+    if (warp == 0 || warp == 3) {
+        // ---------------------------------------------------------------- Q and K tiles; V tiles
+        const bool is_k = warp == 0;
+        const CUtensorMap *tm = is_k ? &tmk : &tmv;
+        const int full = is_k ? KFULL : VFULL, empty = is_k ? KEMPTY : VEMPTY;
+        uint8_t *base_tile = is_k ? k_ring : v_ring;
+        Ring ring(is_k ? a.k_stages : a.v_stages);
         const int R = a.box_rows;
+        uint32_t issued = 0, uq[2] = {0, 0};  // tiles, Q tiles
         // Block ids base + lane of a segment, the next one's fetched while this one is loaded.
         auto first_block = [&](const Seg &t) -> int { return t.t0 * TILE / a.block_size; };
         auto ids = [&](const Seg &t, int base) -> int {
@@ -372,25 +391,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         Seg nx;
         bool have = walk.next(nx);
         int nid = have ? ids(nx, first_block(nx)) : 0;
-        while (ok && have) {
+        for (int k = 0; ok && have; ++k) {
             s = nx;
             int id = nid, base = first_block(s);
             have = walk.next(nx);
             if (have) nid = ids(nx, first_block(nx));
             const int key_end = ctx_s[s.b];
-            for (int j = s.t0; ok && j < s.t1; ++j, ++gg) {
-                const int st = gg % ST;
+            if (is_k && lane == 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h < h_begin(k) || h >= h_end(k, s)) continue;
+                    if (!(ok = wait_or_abort(&bar[QEMPTY + h], (uq[h] & 1u) ^ 1u, abort, a.err, 708))) break;
+                    // Whole boxes, whatever the sequence's drafts: the rows past them are not live.
+                    const int token = s.b * a.drafts + (s.blk * BLOCK + (PAIR ? h * ROWS : 0)) / a.G;
+                    mbar_arrive_expect_tx(&bar[QFULL + h], (uint32_t)(2 * a.q_box * a.G * 128));
+                    tma_load_4d_plain(smem + h * qtile, &tmq, 0, s.g * a.G, token, 0, &bar[QFULL + h]);
+                    tma_load_4d_plain(smem + h * qtile + qhalf, &tmq, 0, s.g * a.G, token, 1, &bar[QFULL + h]);
+                    ++uq[h];
+                }
+            }
+            for (int j = s.t0; j < s.t1; ++j) {
                 const int nsub = (min(TILE, key_end - j * TILE) + R - 1) / R;
                 if (lane == 0) {
-                    ok = wait_or_abort(&bar[KEMPTY + st], ((gg / ST) & 1u) ^ 1u, abort, a.err, 700) &&
-                         wait_or_abort(&bar[VEMPTY + st], ((gg / ST) & 1u) ^ 1u, abort, a.err, 701);
-                    if (ok) {
-                        mbar_arrive_expect_tx(&bar[KFULL + st], (uint32_t)(nsub * R * D * 2));
-                        mbar_arrive_expect_tx(&bar[VFULL + st], (uint32_t)(nsub * R * D * 2));
-                    }
+                    ok = ok && wait_or_abort(&bar[empty + ring.st], ring.par ^ 1u, abort, a.err, is_k ? 700 : 701);
+                    if (ok) mbar_arrive_expect_tx(&bar[full + ring.st], (uint32_t)(nsub * R * D * 2));
                 }
                 ok = __shfl_sync(FULL, ok ? 1 : 0, 0) != 0;
-                for (int sub = 0; ok && sub < nsub; ++sub) {
+                if (!ok) break;
+                for (int sub = 0; sub < nsub; ++sub) {
                     const int key = j * TILE + sub * R, lb = key / a.block_size;
                     if (lb >= base + 32) {
                         base = lb;
@@ -399,38 +427,36 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int blk = __shfl_sync(FULL, id, lb - base);
                     if (lane == 0) {
                         const bool bad = blk < 0 || blk >= a.num_blocks;
-                        if (bad && a.checked)
+                        if (bad && is_k && a.checked)
                             record_error(a.err, PA_DEV_BAD_BLOCK, (long long)s.b * a.max_blocks + lb);
                         // A box outside the pool is filled with zeros.
                         const int row = bad ? -2 * R : blk * a.block_size + key % a.block_size;
-                        uint8_t *k = smem + OFF_K + st * KV_BYTES + sub * R * 128;
-                        uint8_t *v = smem + OFF_V + st * KV_BYTES + sub * R * 128;
-                        tma_load_4d_plain(k, &tmk, 0, row, 0, s.g, &bar[KFULL + st]);
-                        if (R != TILE) tma_load_4d_plain(k + KV_HALF, &tmk, 0, row, 1, s.g, &bar[KFULL + st]);
-                        tma_load_4d_plain(v, &tmv, 0, row, 0, s.g, &bar[VFULL + st]);
-                        if (R != TILE) tma_load_4d_plain(v + KV_HALF, &tmv, 0, row, 1, s.g, &bar[VFULL + st]);
+                        uint8_t *dst = base_tile + ring.st * KV_BYTES + sub * R * 128;
+                        tma_load_4d_plain(dst, tm, 0, row, 0, s.g, &bar[full + ring.st]);
+                        if (R != TILE) tma_load_4d_plain(dst + KV_HALF, tm, 0, row, 1, s.g, &bar[full + ring.st]);
                     }
                 }
-                if (!ok) break;
+                ring.next();
+                ++issued;
             }
         }
-        if (lane == 0 && !ok) {  // issued copies land before the shared memory is given back
-            for (uint32_t x = gg >= (uint32_t)ST ? gg - ST : 0; x < gg; ++x) {
-                (void)mbar_wait(&bar[KFULL + x % ST], (x / ST) & 1u);
-                (void)mbar_wait(&bar[VFULL + x % ST], (x / ST) & 1u);
-            }
+        if (lane == 0 && *abort) {  // issued copies land before the shared memory is given back
+            for (uint32_t x = issued >= (uint32_t)ring.n ? issued - ring.n : 0; x < issued; ++x)
+                (void)mbar_wait(&bar[full + x % ring.n], (x / ring.n) & 1u);
+            for (int h = 0; h < 2; ++h)
+                if (uq[h] > 0) (void)mbar_wait(&bar[QFULL + h], (uq[h] - 1) & 1u);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- S = Q K^T
         if (lane == 0) {
-            uint32_t gg = 0, th[2] = {0, 0}, uq[2] = {0, 0};  // tiles, and per row tile: tiles, segments
+            Ring ring(a.k_stages);
+            uint32_t th[2] = {0, 0}, uq[2] = {0, 0};  // of each row tile: tiles, segments
             bool issued = false;
             for (int k = 0; ok && walk.next(s); ++k) {
                 const int h0 = h_begin(k), h1 = h_end(k, s);
-                for (int j = s.t0; ok && j < s.t1; ++j, ++gg) {
-                    const int st = gg % ST;
-                    if (!(ok = wait_or_abort(&bar[KFULL + st], (gg / ST) & 1u, abort, a.err, 703))) break;
-                    const uint64_t kdesc = smem_desc_sw128(smem_addr(smem + OFF_K + st * KV_BYTES), 16, SBO);
+                for (int j = s.t0; ok && j < s.t1; ++j) {
+                    if (!(ok = wait_or_abort(&bar[KFULL + ring.st], ring.par, abort, a.err, 703))) break;
+                    const uint64_t kdesc = smem_desc_sw128(smem_addr(k_ring + ring.st * KV_BYTES), 16, SBO);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (h < h0 || h >= h1) continue;
@@ -443,11 +469,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (!(ok = wait_or_abort(&bar[PDONE + 2 * h + b], ((th[h] >> 1) & 1u) ^ 1u, abort, a.err, 704)))
                             break;
                         tc_fence_after();
-                        const uint64_t qdesc = smem_desc_sw128(smem_addr(smem + h * QTILE), 16, SBO);
+                        const uint64_t qdesc = smem_desc_sw128(smem_addr(smem + h * qtile), 16, SBO);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             mma_bf16_ss(tmem + h * 128 + b * TILE,
-                                        qdesc + (uint64_t)(((kk >> 2) * QHALF + (kk & 3) * 32) >> 4),
+                                        qdesc + (uint64_t)(((kk >> 2) * qhalf + (kk & 3) * 32) >> 4),
                                         kdesc + (uint64_t)(((kk >> 2) * KV_HALF + (kk & 3) * 32) >> 4), IDESC_S,
                                         kk > 0 ? 1u : 0u);
                         mma_commit(&bar[SFULL + 2 * h + b]);
@@ -456,7 +482,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ++th[h];
                     }
                     if (!ok) break;
-                    mma_commit(&bar[KEMPTY + st]);
+                    mma_commit(&bar[KEMPTY + ring.st]);
+                    ring.next();
                 }
             }
             if (issued && *abort) {
@@ -467,15 +494,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 2) {
         // ---------------------------------------------------------------- O += P V
         if (lane == 0) {
-            uint32_t gg = 0, th[2] = {0, 0}, uh[2] = {0, 0};
+            Ring ring(a.v_stages);
+            uint32_t th[2] = {0, 0}, uh[2] = {0, 0};
             bool issued = false;
             for (int k = 0; ok && walk.next(s); ++k) {
                 const int h0 = h_begin(k), h1 = h_end(k, s);
-                for (int j = s.t0; ok && j < s.t1; ++j, ++gg) {
-                    const int st = gg % ST;
-                    if (!(ok = wait_or_abort(&bar[VFULL + st], (gg / ST) & 1u, abort, a.err, 705))) break;
+                for (int j = s.t0; ok && j < s.t1; ++j) {
+                    if (!(ok = wait_or_abort(&bar[VFULL + ring.st], ring.par, abort, a.err, 705))) break;
                     const int steps = (min(TILE, ctx_s[s.b] - j * TILE) + 15) / 16;  // keys past the last: P is 0
-                    const uint64_t vdesc = smem_desc_sw128(smem_addr(smem + OFF_V + st * KV_BYTES), KV_HALF, SBO);
+                    const uint64_t vdesc = smem_desc_sw128(smem_addr(v_ring + ring.st * KV_BYTES), KV_HALF, SBO);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (h < h0 || h >= h1) continue;
@@ -495,46 +522,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ++th[h];
                     }
                     if (!ok) break;
-                    mma_commit(&bar[VEMPTY + st]);
+                    mma_commit(&bar[VEMPTY + ring.st]);
+                    ring.next();
                 }
             }
             if (issued && *abort) {
                 mma_commit(&bar[DRAIN + 1]);
                 (void)mbar_wait(&bar[DRAIN + 1], 0);
-            }
-        }
-    } else if (warp == 3) {
-        // ---------------------------------------------------------------- Q rows
-        uint32_t uq[2] = {0, 0};
-        for (int k = 0; ok && walk.next(s); ++k) {
-            const __nv_bfloat16 *q = a.q + (int64_t)s.b * a.drafts * a.q_stride + (int64_t)s.g * a.G * D;
-            const int c = lane & 15;  // two rows a step, 16 lanes each; 8 steps in flight
-#pragma unroll 1
-            for (int h = h_begin(k); ok && h < h_end(k, s); ++h) {
-                const uint32_t u = h ? uq[1]++ : uq[0]++;
-                ok = __all_sync(FULL, wait_or_abort(&bar[QEMPTY + h], (u & 1u) ^ 1u, abort, a.err, 708));
-                if (!ok) break;
-                const uint32_t qs = smem_addr(smem) + h * QTILE;
-                const int row0 = PAIR ? h * ROWS : 0, live = min(s.rows - row0, ROWS), rr0 = s.blk * BLOCK + row0;
-                for (int r0 = 0; r0 < live; r0 += 16) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = r0 + 2 * e + (lane >> 4), rr = rr0 + r;
-                        if (r < live)
-                            v[e] = __ldg(
-                                reinterpret_cast<const uint4 *>(q + (int64_t)(rr / a.G) * a.q_stride + (rr % a.G) * D) + c);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int r = r0 + 2 * e + (lane >> 4);
-                        if (r < live)
-                            st_shared_u4(qs + (uint32_t)((c >> 3) * QHALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)), v[e]);
-                    }
-                }
-                fence_proxy_async_smem();  // the MMA reads Q through the async proxy
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[QFULL + h]);
             }
         }
     } else {
@@ -563,7 +557,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // P of all of them.
         volatile int *marks = abort + 1;
         volatile int *last = abort + 5;  // jobs of each row tile
-        Job *jobs = reinterpret_cast<Job *>(smem + OFF_JOBS);
+        Job *jobs = reinterpret_cast<Job *>(ctl + JOBS);
         // The next segment that this row tile has rows in: its number, its first
         // tile's number, and (asked for ahead) this row's mask.
         int k_next = 0;
@@ -616,10 +610,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     // product reads become zeros, and drafts' values that are not
                     // finite too.  Each row tile of the item does it before its
                     // product; what the first has mended, the second leaves.
-                    const int st = gg % ST;
-                    if (!(ok = wwait(VFULL + st, (gg / ST) & 1u, 709))) break;
+                    const uint32_t round = gg / (uint32_t)a.v_stages, st = gg - round * (uint32_t)a.v_stages;
+                    if (!(ok = wwait(VFULL + st, round & 1u, 709))) break;
                     const int kend = min(TILE, ctx - kb), kpad = (kend + 15) & ~15, k0 = max(0, first - kb);
-                    const uint32_t vb = smem_addr(smem + OFF_V + st * KV_BYTES);
+                    const uint32_t vb = smem_addr(v_ring + st * KV_BYTES);
                     for (int i = threadIdx.x & 127; i < (kpad - k0) * 16; i += 128) {
                         const int r = k0 + (i >> 4), c = i & 15;
                         const uint32_t at = vb + (uint32_t)((c >> 3) * KV_HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
@@ -819,20 +813,20 @@ Layout layout_of(int drafts, int G) {
 std::atomic<int> g_attr_done[64][2];
 
 template <bool PAIR>
-pa_status launch_tree(const CUtensorMap &tmk, const CUtensorMap &tmv, const TreeArgs &a, int grid, cudaStream_t stream) {
-    const size_t smem = tree_smem(a.batch);
+pa_status launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const TreeArgs &a, int grid, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     if (dev < 0 || dev >= 64) return fail(PA_ERR_UNSUPPORTED, "device %d", dev);
     if (!g_attr_done[dev][PAIR].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(decode_tree_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)tree_smem(kMaxBatch));
+                                 kMaxSmem);
         if (e != cudaSuccess) return cuda_fail(e, "decode_tree_kernel shared memory");
         g_attr_done[dev][PAIR].store(1, std::memory_order_release);
     }
-    return launch_pdl(decode_tree_kernel<PAIR>, dim3((unsigned)grid), dim3(THREADS), smem, stream,
-                      "decode_tree_kernel", tmk, tmv, a);
+    return launch_pdl(decode_tree_kernel<PAIR>, dim3((unsigned)grid), dim3(THREADS),
+                      (size_t)4 * a.q_rows * 128 + (a.k_stages + a.v_stages) * KV_BYTES + fixed_smem(a.batch), stream,
+                      "decode_tree_kernel", tmq, tmk, tmv, a);
 }
 
 }  // namespace
@@ -895,9 +889,7 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     if (sms <= 0) return fail(PA_ERR_CUDA, "no CUDA device");
     TreeArgs a = {};
     a.out = static_cast<__nv_bfloat16 *>(out);
-    a.q = static_cast<const __nv_bfloat16 *>(q);
     a.v_cache = static_cast<const __nv_bfloat16 *>(v_cache);
-    a.q_stride = q_row_stride;
     a.bt = block_tables;
     a.ctx = context_lens;
     a.lens = draft_lens;
@@ -919,15 +911,24 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     a.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + l.parts);
     a.part_rows = l.part_rows;
     a.err = device_error_ptr();
-    CUtensorMap tmk, tmv;
+    a.q_box = std::min(num_drafts, ROWS / G);
+    // Few rows leave room for more K and V in flight.  A V tile is held until its
+    // P.V is done, a K tile only until its scores are: V gets the larger share.
+    a.q_rows = std::min(ROWS, (a.q_box * G + 7) / 8 * 8);
+    const int tiles = std::min(KMAX + VMAX, (kMaxSmem - fixed_smem(batch) - 4 * a.q_rows * 128) / KV_BYTES);
+    a.k_stages = std::min(KMAX, tiles * 3 / 7);
+    a.v_stages = std::min(VMAX, tiles - a.k_stages);
+    CUtensorMap tmq, tmk, tmv;
+    pa_status st = encode_token_heads_map(&tmq, q, (int64_t)batch * num_drafts, q_row_stride * 2, num_q_heads, G, a.q_box);
+    if (st != PA_OK) return st;
     const int64_t slots = (int64_t)num_blocks * block_size;
-    pa_status st = encode_halves_map(&tmk, k_cache, slots, (int64_t)num_kv_heads * D * 2, num_kv_heads, r, r == TILE ? 2 : 1);
+    st = encode_halves_map(&tmk, k_cache, slots, (int64_t)num_kv_heads * D * 2, num_kv_heads, r, r == TILE ? 2 : 1);
     if (st != PA_OK) return st;
     st = encode_halves_map(&tmv, v_cache, slots, (int64_t)num_kv_heads * D * 2, num_kv_heads, r, r == TILE ? 2 : 1);
     if (st != PA_OK) return st;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid), a_seq * batch / kMinTiles));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    return l.pair ? launch_tree<true>(tmk, tmv, a, (int)grid, cs) : launch_tree<false>(tmk, tmv, a, (int)grid, cs);
+    return l.pair ? launch_tree<true>(tmq, tmk, tmv, a, (int)grid, cs) : launch_tree<false>(tmq, tmk, tmv, a, (int)grid, cs);
 }
 
 }  // extern "C"
