@@ -657,7 +657,8 @@ PA_API pa_status pa_tree_metadata(int64_t *tree_mask, int32_t *positions, int32_
  * drafts j <= i.  Any pattern is allowed; a query that sees nothing has output
  * zero.  num_drafts == 1 with bit 0 set is pa_decode.  What a mask hides does not
  * matter, NaN and infinities included.  The weights are rounded to bf16, and
- * normalised by the sum of the rounded ones.
+ * normalised by the sum of the rounded ones.  The same call gives the same bits
+ * again; a row's last bits depend on the batch, by which the keys are cut.
  *   out           bf16 [batch, num_drafts, Hq, 128] contiguous; zeros for i >= n.
  *   q             bf16; the Hq*128 values of (b, i) at q + (b*num_drafts + i)*q_row_stride.
  *   tree_mask     int64 [batch, num_drafts].

@@ -83,6 +83,7 @@ struct TreeArgs {
     int32_t max_blocks, batch, drafts, Hq, Hkv, G, block_size, num_blocks, box_rows, q_box, checked;
     int32_t q_rows;          // rows that a Q tile has room for (a multiple of 8): the MMA reads on past them
     int32_t k_stages, v_stages;
+    int32_t lanes;           // ranges side by side, each over Hkv / lanes of the heads
     float scale_log2;
     int *count;    // [grid][2] arrivals: of the row tiles of the item that begins in a range and ends in a later one
     float *parts;  // [grid][2] of slot_of(part_rows)
@@ -158,7 +159,7 @@ struct Walker {
     const int *ctx_s;
     const uint8_t *n_s;
     const uint32_t *cum;
-    int G;
+    int G, g0;  // the lane's first head
     uint32_t x, x1;
     int b;
     __device__ __forceinline__ void start(uint32_t x0, uint32_t xe, int batch) {
@@ -184,7 +185,7 @@ struct Walker {
             x = end;
             if (t0 >= nt) continue;
             s.b = b;
-            s.g = PAIR ? (int)it / blocks : (int)it;
+            s.g = g0 + (PAIR ? (int)it / blocks : (int)it);
             s.blk = PAIR ? (int)it % blocks : 0;
             s.t0 = t0;
             s.t1 = min((int)(end - first), nt);
@@ -211,7 +212,7 @@ __device__ __forceinline__ void merge_rows(const TreeArgs &a, const Job &job, in
     const size_t slot_floats = slot_of(a.part_rows);
     const int c0 = job.c0, nparts = job.nparts, tr0 = job.row0, live = job.live;
     const int r = lane & (RM - 1), ps = lane / RM;
-    auto slot = [&](int p) -> const float * { return a.parts + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats; };
+    auto slot = [&](int p) -> const float * { return a.parts + (size_t)(2 * (c0 + p * a.lanes) + (p == 0 ? 1 : 0)) * slot_floats; };
     for (int r0 = RM * w; r0 < live; r0 += 4 * RM) {
         const int nr = min(RM, live - r0);
         auto ml_of = [&](int p) -> float2 {  // of row r0 + r in part p
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             ctx_s[b] = ctx;
             n_s[b] = (uint8_t)n;
             const int blocks = (n * a.G + BLOCK - 1) / BLOCK;
-            u = n ? (uint32_t)((ctx + TILE - 1) / TILE + kItemCost) * (uint32_t)(a.Hkv * blocks) : 0u;
+            u = n ? (uint32_t)((ctx + TILE - 1) / TILE + kItemCost) * (uint32_t)(a.Hkv / a.lanes * blocks) : 0u;
         }
         uint32_t inc = u;
 #pragma unroll
@@ -350,11 +351,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t P = carry;  // units in all
-    const uint32_t nC = min((uint32_t)gridDim.x, max(1u, P / kMinTiles));
-    Walker<PAIR> walk{ctx_s, n_s, cum, a.G, 0u, 0u, 0};
-    if (blockIdx.x < nC && P > 0)
-        walk.start((uint32_t)((uint64_t)blockIdx.x * P / nC), (uint32_t)((uint64_t)(blockIdx.x + 1) * P / nC), a.batch);
+    // The lane's units, its ranges, and this CTA's.
+    const uint32_t P = carry, W = min(gridDim.x / (uint32_t)a.lanes, max(1u, P / kMinTiles));
+    const uint32_t range = blockIdx.x / (uint32_t)a.lanes, side = blockIdx.x - range * (uint32_t)a.lanes;
+    Walker<PAIR> walk{ctx_s, n_s, cum, a.G, (int)side * (a.Hkv / a.lanes), 0u, 0u, 0};
+    if (range < W && P > 0)
+        walk.start((uint32_t)((uint64_t)range * P / W), (uint32_t)((uint64_t)(range + 1) * P / W), a.batch);
     // Row tiles of segment number k.
     auto h_begin = [](int k) -> int { return PAIR ? 0 : k & 1; };
     auto h_end = [](int k, const Seg &s) -> int { return PAIR ? (s.rows + ROWS - 1) / ROWS : (k & 1) + 1; };
@@ -699,9 +701,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             // A part: slot 1 of the item's first CTA, slot 0 of the others.
             int c0 = 0, nparts = 1;
             float *slot = nullptr;
-            if (!whole) {  // the CTA whose range holds unit x: ((x + 1) nC - 1) / P
-                c0 = (int)(((uint64_t)(s.first + 1) * nC - 1) / P);
-                nparts = (int)(((uint64_t)(s.first + s.nt) * nC - 1) / P) - c0 + 1;
+            if (!whole) {  // the range that holds unit x: ((x + 1) W - 1) / P
+                const int r0 = (int)(((uint64_t)(s.first + 1) * W - 1) / P);
+                nparts = (int)(((uint64_t)(s.first + s.nt) * W - 1) / P) - r0 + 1;
+                c0 = r0 * a.lanes + (int)side;
                 slot = a.parts + (size_t)(2 * blockIdx.x + (blockIdx.x == c0 ? 1 : 0)) * slot_of(a.part_rows);
             }
             if (wlive) {
@@ -927,6 +930,12 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     st = encode_halves_map(&tmv, v_cache, slots, (int64_t)num_kv_heads * D * 2, num_kv_heads, r, r == TILE ? 2 : 1);
     if (st != PA_OK) return st;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid), a_seq * batch / kMinTiles));
+    // Side by side, the CTAs of a range walk the same keys of different heads at
+    // the same time, so that the pool's rows (all heads of a token) are read whole.
+    // As many lanes as leave at most a tenth of the CTAs without work.
+    a.lanes = 1;
+    for (int n = 2; n <= num_kv_heads && n <= grid; ++n)
+        if (num_kv_heads % n == 0 && grid / n * n * 10 >= grid * 9) a.lanes = n;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     return l.pair ? launch_tree<true>(tmq, tmk, tmv, a, (int)grid, cs) : launch_tree<false>(tmq, tmk, tmv, a, (int)grid, cs);
 }

@@ -312,12 +312,15 @@ def test_one_workspace_for_calls_of_many_shapes():
 
 def test_lengths_that_do_not_fit_are_recorded():
     t = Tree(33, [100, 200, 300], 4, 4, 2, 64)
+    want, tol = OD.decode_tree(f64(t.q), f64(t.kc), f64(t.vc), t.bt, t.ctx, t.sees, t.scale)
     for ctx in (3, -1, t.bt.shape[1] * 64 + 1):
         c = t.ctx.copy()
         c[1] = ctx
         out = t.run(context_lens=dev_i32(c))
         assert pa.get_device_error() == (pa.PA_DEV_BAD_CONTEXT, 1)
-        assert not out[1].any() and torch.equal(out[::2], t.run()[::2])
+        assert not out[1].any()
+        # The others' keys are cut elsewhere without it: within the bound, not bit by bit.
+        near(host_f64(out)[::2], want[::2], tol[::2])
     out = t.run(draft_lens=dev_i32([4, 5, 4]))
     assert pa.get_device_error() == (pa.PA_DEV_BAD_CONTEXT, 1) and not out[1].any()
 
