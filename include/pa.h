@@ -664,7 +664,7 @@ PA_API pa_status pa_tree_metadata(int64_t *tree_mask, int32_t *positions, int32_
  *   tree_mask     int64 [batch, num_drafts].
  *   draft_lens    int32 [batch] or NULL.  Lengths that do not fit (ctx < n among
  *                 them) are recorded as PA_DEV_BAD_CONTEXT and give zeros.
- *   workspace     >= pa_decode_tree_workspace_size(...) bytes, 16-byte aligned,
+ *   workspace     >= pa_decode_tree_workspace_size(...) bytes, 32-byte aligned,
  *                 ZERO-FILLED before its first use; contract as for pa_decode.  It
  *                 serves calls of any shape for which it is large enough, in turn,
  *                 and no other entry point.

@@ -48,7 +48,6 @@ constexpr uint32_t IDESC_PV = idesc_bf16_f32(ROWS, D, false, true);
 constexpr int kMaxBatch = 2048;
 constexpr int kMaxDrafts = 64;
 constexpr int kMaxGrid = 256;
-constexpr int kItemCost = 1;             // an item costs this many tiles on top of its own
 constexpr int kMinTiles = 2;             // a CTA's share at least
 constexpr float kLazy = 8.f;             // log2 headroom before the running maximum must move
 constexpr unsigned FULL = 0xffffffffu;
@@ -62,18 +61,18 @@ constexpr int KMAX = 6, VMAX = 8;                // ring stages at most
 enum {  // barriers: rings, then per row tile [2] (and score buffer [2])
     KFULL = 0, KEMPTY = KFULL + KMAX, VFULL = KEMPTY + KMAX, VEMPTY = VFULL + VMAX, SFULL = VEMPTY + VMAX,
     PFULL = SFULL + 4, PDONE = PFULL + 4, OEMPTY = PDONE + 4, QFULL = OEMPTY + 2, QEMPTY = QFULL + 2,
-    WROTE = QEMPTY + 2, TOLD = WROTE + 2, DRAIN = TOLD + 2, NBAR = DRAIN + 2
+    WROTE = QEMPTY + 2, TOLD = WROTE + 2, DRAIN = TOLD + 2, ENDED = DRAIN + 2, WROTE2, TOLD2, NBAR
 };
 // Shared memory: Q [2], the rings, then from off_bar on the barriers, a few words
 // (TMEM address, abort, marks [4], jobs [2], scan scratch [12]), the jobs [2][2],
-// and per sequence the running sum of units, the length (int) and the drafts (byte).
-constexpr int MISC = (NBAR * 8 + 15) / 16 * 16, JOBS = MISC + 128, ARRAYS = JOBS + 4 * 28;
+// and per sequence the running sum of tiles, the length (int) and the drafts (byte).
+constexpr int MISC = (NBAR * 8 + 15) / 16 * 16, JOBS = MISC + 128, ARRAYS = JOBS + 4 * 32;
 constexpr uint32_t TMEM_COLS = 512, COL_O = 256;               // S(h, b) at h * 128 + b * 64, O(h) at COL_O + h * 128
 constexpr int kMaxSmem = 232448;
 constexpr int fixed_smem(int batch) { return 1024 + ARRAYS + 9 * (batch + 1); }
 
-// Floats of a part: o [rows][D], (m, l) [rows], a multiple of 16 bytes.
-__host__ __device__ constexpr size_t slot_of(int rows) { return ((size_t)rows * (D + 2) + 3) / 4 * 4; }
+// Floats of a part: o [rows][D], (m, l) [rows], a multiple of 32 bytes.
+__host__ __device__ constexpr size_t slot_of(int rows) { return ((size_t)rows * (D + 2) + 7) / 8 * 8; }
 
 struct TreeArgs {
     __nv_bfloat16 *out;
@@ -85,7 +84,10 @@ struct TreeArgs {
     int32_t k_stages, v_stages;
     int32_t lanes;           // ranges side by side, each over Hkv / lanes of the heads
     float scale_log2;
-    int *count;    // [grid][2] arrivals: of the row tiles of the item that begins in a range and ends in a later one
+    // Arrivals [3][kMaxGrid][2 row tiles]: of the first kFan parts of the item that
+    // begins in a CTA's range and ends in a later one; of the kFan parts that begin
+    // with this CTA's; of such groups of the item that begins here.
+    int *count;
     float *parts;  // [grid][2] of slot_of(part_rows)
     int32_t part_rows;
     DevError *err;
@@ -148,10 +150,10 @@ struct Seg {
     int b, g, blk;       // sequence, kv head, row block
     int t0, t1, nt;      // tiles [t0, t1) of nt
     int rows;            // live rows of the item
-    uint32_t first;      // the item's first unit
+    uint32_t first;      // the item's first tile among the lane's
 };
 
-// Walks the segments of a CTA's range of units; every role of the CTA makes the
+// Walks the segments of a CTA's range of tiles; every role of the CTA makes the
 // same walk.
 template <bool PAIR>
 struct Walker {
@@ -172,23 +174,20 @@ struct Walker {
         }
         b = lo;
     }
-    // The next item that has tiles in the range.
+    // The next item in the range.
     __device__ __forceinline__ bool next(Seg &s) {
-        while (x < x1) {
+        if (x < x1) {
             while (cum[b + 1] <= x) ++b;
-            const int nt = (ctx_s[b] + TILE - 1) / TILE, u = nt + kItemCost, rows = n_s[b] * G;
+            const int nt = (ctx_s[b] + TILE - 1) / TILE, rows = n_s[b] * G;
             const int blocks = (rows + BLOCK - 1) / BLOCK;
-            const uint32_t local = x - cum[b], it = local / (uint32_t)u;
-            const int t0 = (int)(local - it * (uint32_t)u);
-            const uint32_t first = cum[b] + it * (uint32_t)u;
-            const uint32_t end = min(first + (uint32_t)u, x1);
-            x = end;
-            if (t0 >= nt) continue;
+            const uint32_t local = x - cum[b], it = local / (uint32_t)nt;
+            const uint32_t first = cum[b] + it * (uint32_t)nt;
             s.b = b;
             s.g = g0 + (PAIR ? (int)it / blocks : (int)it);
             s.blk = PAIR ? (int)it % blocks : 0;
-            s.t0 = t0;
-            s.t1 = min((int)(end - first), nt);
+            s.t0 = (int)(x - first);
+            x = min(first + (uint32_t)nt, x1);
+            s.t1 = (int)(x - first);
             s.nt = nt;
             s.rows = min(rows - s.blk * BLOCK, BLOCK);
             s.first = first;
@@ -198,31 +197,54 @@ struct Walker {
     }
 };
 
-// Parts to combine: rows [row0, row0 + live) of an item, from CTAs c0 on.
+// Parts [p0, p1) of an item to combine, in steps of `step`: rows [row0, row0 +
+// live) of the item.  Part p is that of CTA c0 + p * lanes.
 struct Job {
-    int b, g, blk, row0, live, c0, nparts;
+    int b, g, blk, row0, live, c0, nparts, p0;
 };
+constexpr int kFan = 8;  // parts combined at a time
 
-// Combines the parts of an item's rows of one row tile and writes them
-// out: four rows per warp and four parts at a time, 16 row loads in flight.  A
-// part's m of -inf has seen nothing; NaN in l or o goes on.
-template <typename OutRow>
-__device__ __forceinline__ void merge_rows(const TreeArgs &a, const Job &job, int w, int lane, OutRow out_row) {
+// Combines parts p0, p0 + step, ... < p1 of a job's rows.  `final`: writes the rows out;
+// otherwise leaves the combined part in p0's place.  Eight warps, w of them; four rows
+// per warp and four parts at a time, 16 row loads in flight.  A part's m of -inf has seen nothing; NaN
+// in l or o goes on.
+// A call of its own, with scalars alone: inlined, or with the arguments' address
+// taken, it costs the softmax loop its registers (64 drafts 311 -> 350 us).
+struct Merge {
+    float *first, *rest;  // the first part; part i > 0 at rest + i * apart
+    size_t apart;
+    int part_rows, tr0, live, n;
+    // The output row of row r of the (sequence, kv head): out + (r / G) * token + r % G * D.
+    __nv_bfloat16 *out;
+    int64_t token;
+    int gr0, G;
+};
+__device__ __noinline__ void merge_rows(Merge g, bool final, int w, int lane) {
     constexpr int RM = 4, PM = 4, PL = 32 / RM;  // rows, parts at a time, lanes of a row
-    const size_t slot_floats = slot_of(a.part_rows);
-    const int c0 = job.c0, nparts = job.nparts, tr0 = job.row0, live = job.live;
-    const int r = lane & (RM - 1), ps = lane / RM;
-    auto slot = [&](int p) -> const float * { return a.parts + (size_t)(2 * (c0 + p * a.lanes) + (p == 0 ? 1 : 0)) * slot_floats; };
-    for (int r0 = RM * w; r0 < live; r0 += 4 * RM) {
-        const int nr = min(RM, live - r0);
-        auto ml_of = [&](int p) -> float2 {  // of row r0 + r in part p
-            return p < nparts && r < nr
-                       ? __ldcg(reinterpret_cast<const float2 *>(slot(p) + (size_t)a.part_rows * D) + tr0 + r0 + r)
+    const int n = g.n, r = lane & (RM - 1), ps = lane / RM;
+    auto slot = [&](int i) -> float * { return i == 0 ? g.first : g.rest + (size_t)i * g.apart; };
+    for (int r0 = RM * w; r0 < g.live; r0 += 8 * RM) {
+        const int nr = min(RM, g.live - r0);
+        float4 v[PM][RM];
+        auto load = [&](int i0) {  // rows r0 .. of parts i0 ..
+#pragma unroll
+            for (int pp = 0; pp < PM; ++pp)
+#pragma unroll
+                for (int e = 0; e < RM; ++e)
+                    if (e < nr && i0 + pp < n)
+                        v[pp][e] =
+                            __ldcg(reinterpret_cast<const float4 *>(slot(i0 + pp) + (size_t)(g.tr0 + r0 + e) * D) + lane);
+        };
+        auto ml_of = [&](int i) -> float2 {  // of row r0 + r in the i-th part
+            return i < n && r < nr
+                       ? __ldcg(reinterpret_cast<const float2 *>(slot(i) + (size_t)g.part_rows * D) + g.tr0 + r0 + r)
                        : make_float2(-INFINITY, 0.f);
         };
-        float m = -INFINITY, l = 0.f;
-        for (int p = ps; p < nparts; p += PL) {
-            const float2 ml = ml_of(p);
+        const float2 ml0 = ml_of(ps);
+        load(0);
+        float m = ml0.x, l = ml0.y;
+        for (int i = ps + PL; i < n; i += PL) {
+            const float2 ml = ml_of(i);
             const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn;
             l = l * fast_exp2(m - ref) + ml.y * fast_exp2(ml.x - ref);
             m = mn;
@@ -238,24 +260,19 @@ __device__ __forceinline__ void merge_rows(const TreeArgs &a, const Job &job, in
         float4 acc[RM];
 #pragma unroll
         for (int e = 0; e < RM; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        float wgt = 0.f;
+        float wgt = fast_exp2(ml0.x - ref);  // of row r in the part ps (of the eight under way)
 #pragma unroll 1
-        for (int p0 = 0; p0 < nparts; p0 += PM) {
-            float4 v[PM][RM];
-#pragma unroll
-            for (int pp = 0; pp < PM; ++pp)
-#pragma unroll
-                for (int e = 0; e < RM; ++e)
-                    if (e < nr && p0 + pp < nparts)
-                        v[pp][e] =
-                            __ldcg(reinterpret_cast<const float4 *>(slot(p0 + pp) + (size_t)(tr0 + r0 + e) * D) + lane);
-            if (p0 % PL == 0) wgt = fast_exp2(ml_of(p0 + ps).x - ref);  // of row r in part p0 + ps
+        for (int i0 = 0; i0 < n; i0 += PM) {
+            if (i0 > 0) {
+                load(i0);
+                if (i0 % PL == 0) wgt = fast_exp2(ml_of(i0 + ps).x - ref);
+            }
 #pragma unroll
             for (int pp = 0; pp < PM; ++pp)
 #pragma unroll
                 for (int e = 0; e < RM; ++e) {
-                    const float f = __shfl_sync(FULL, wgt, ((p0 + pp) % PL) * RM + e);
-                    if (e < nr && p0 + pp < nparts) {
+                    const float f = __shfl_sync(FULL, wgt, ((i0 + pp) % PL) * RM + e);
+                    if (e < nr && i0 + pp < n) {
                         acc[e].x = fmaf(v[pp][e].x, f, acc[e].x);
                         acc[e].y = fmaf(v[pp][e].y, f, acc[e].y);
                         acc[e].z = fmaf(v[pp][e].z, f, acc[e].z);
@@ -263,12 +280,19 @@ __device__ __forceinline__ void merge_rows(const TreeArgs &a, const Job &job, in
                     }
                 }
         }
+        if (!final && ps == 0 && r < nr)  // (every lane has read the rows' m and l)
+            reinterpret_cast<float2 *>(g.first + (size_t)g.part_rows * D)[g.tr0 + r0 + r] = make_float2(m, l);
 #pragma unroll
         for (int e = 0; e < RM; ++e) {
             const float f = __shfl_sync(FULL, inv, e);
-            if (e < nr)
-                reinterpret_cast<uint2 *>(out_row(tr0 + r0 + e))[lane] =
+            if (e >= nr) continue;
+            if (final) {
+                const int gr = g.gr0 + r0 + e;
+                reinterpret_cast<uint2 *>(g.out + (gr / g.G) * g.token + (gr % g.G) * D)[lane] =
                     make_uint2(pack_bf16(acc[e].x * f, acc[e].y * f), pack_bf16(acc[e].z * f, acc[e].w * f));
+            } else {
+                reinterpret_cast<float4 *>(g.first + (size_t)(g.tr0 + r0 + e) * D)[lane] = acc[e];
+            }
         }
     }
 }
@@ -297,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // The four softmax warps of a row tile arrive one each.
             const bool per_warp = (i >= PFULL && i < PFULL + 4) || (i >= OEMPTY && i < OEMPTY + 2) ||
                                   (i >= WROTE && i < WROTE + 2);
-            mbar_init(&bar[i], per_warp ? 4u : 1u);
+            mbar_init(&bar[i], i == ENDED || i == WROTE2 ? 8u : per_warp ? 4u : 1u);
         }
         for (int i = 0; i < 7; ++i) abort[i] = 0;  // and the marks behind it
         fence_mbar_init();
@@ -310,8 +334,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_relinquish();
     }
     pdl_wait_then_release();
-    // Lengths, and the running sum of the sequences' units (tiles, and kItemCost
-    // more per item).
+    // Lengths, and the running sum of the sequences' tiles.
     uint32_t carry = 0;
     for (int base = 0; base < a.batch; base += THREADS) {
         const int b = base + threadIdx.x;
@@ -327,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             ctx_s[b] = ctx;
             n_s[b] = (uint8_t)n;
             const int blocks = (n * a.G + BLOCK - 1) / BLOCK;
-            u = n ? (uint32_t)((ctx + TILE - 1) / TILE + kItemCost) * (uint32_t)(a.Hkv / a.lanes * blocks) : 0u;
+            u = (uint32_t)((ctx + TILE - 1) / TILE) * (uint32_t)(a.Hkv / a.lanes * blocks);
         }
         uint32_t inc = u;
 #pragma unroll
@@ -351,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // The lane's units, its ranges, and this CTA's.
+    // The lane's tiles, its ranges, and this CTA's.
     const uint32_t P = carry, W = min(gridDim.x / (uint32_t)a.lanes, max(1u, P / kMinTiles));
     const uint32_t range = blockIdx.x / (uint32_t)a.lanes, side = blockIdx.x - range * (uint32_t)a.lanes;
     Walker<PAIR> walk{ctx_s, n_s, cum, a.G, (int)side * (a.Hkv / a.lanes), 0u, 0u, 0};
@@ -588,9 +611,33 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             return false;
         };
+        // The row tile's four warps have written: one of them counts it.  The one that
+        // brings the counter to `all` leaves it at zero, as it was found, and calls
+        // `then` before the others go on.
+        uint32_t ns = 0;
+        auto arrive = [&](int *cnt, int all, auto then) -> bool {
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[WROTE + h]);
+            if (quarter == 0) {
+                if (!wwait(WROTE + h, ns & 1u, 713)) return false;
+                if (lane == 0) {
+                    __threadfence();
+                    if (atomicAdd(cnt, 1) == all - 1) {
+                        __threadfence();
+                        *cnt = 0;
+                        then();
+                    }
+                    mbar_arrive(&bar[TOLD + h]);
+                }
+            }
+            if (!wwait(TOLD + h, ns & 1u, 714)) return false;
+            ++ns;
+            return true;
+        };
         Own nx;
         bool have = fetch(nx);
-        uint32_t th = 0, ns = 0;  // tiles of this row tile, parts written
+        uint32_t th = 0;  // tiles of this row tile
         while (ok && have) {
             s = nx.s;
             const int k = nx.k;
@@ -701,7 +748,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // A part: slot 1 of the item's first CTA, slot 0 of the others.
             int c0 = 0, nparts = 1;
             float *slot = nullptr;
-            if (!whole) {  // the range that holds unit x: ((x + 1) W - 1) / P
+            if (!whole) {  // the range that holds tile x: ((x + 1) W - 1) / P
                 const int r0 = (int)(((uint64_t)(s.first + 1) * W - 1) / P);
                 nparts = (int)(((uint64_t)(s.first + s.nt) * W - 1) / P) - r0 + 1;
                 c0 = r0 * a.lanes + (int)side;
@@ -747,9 +794,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     } else if (mine) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            reinterpret_cast<uint4 *>(slot + (size_t)(row0 + row) * D)[8 * c + e] =
-                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 4; ++e)  // 32 bytes a store: whole sectors
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                             slot + (size_t)(row0 + row) * D + 32 * c + 8 * e),
+                                         "r"(o[8 * e]), "r"(o[8 * e + 1]), "r"(o[8 * e + 2]), "r"(o[8 * e + 3]),
+                                         "r"(o[8 * e + 4]), "r"(o[8 * e + 5]), "r"(o[8 * e + 6]), "r"(o[8 * e + 7])
+                                         : "memory");
                     }
                 }
             }
@@ -758,37 +808,66 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive(&bar[OEMPTY + h]);
             if (whole) continue;
             if (mine) reinterpret_cast<float2 *>(slot + (size_t)a.part_rows * D)[row0 + row] = make_float2(m_run * sl, l_run);
-            // The row tile's four warps have written: the part is counted; where it
-            // is the item's last, they combine the parts.
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[WROTE + h]);
-            if (quarter == 0) {
-                if (!(ok = wwait(WROTE + h, ns & 1u, 713))) break;
-                if (lane == 0) {
-                    int *cnt = a.count + 2 * c0 + h * (PAIR ? 1 : 0);
-                    __threadfence();
-                    if (atomicAdd(cnt, 1) == nparts - 1) {
-                        __threadfence();
-                        *cnt = 0;  // as it was found
-                        jobs[2 * h + last[h]] = {s.b, s.g, s.blk, row0, live, c0, nparts};
-                        last[h] = last[h] + 1;
-                    }
-                    mbar_arrive(&bar[TOLD + h]);
-                }
-            }
-            if (!(ok = wwait(TOLD + h, ns & 1u, 714))) break;
-            ++ns;
+            // The part is counted among the kFan that are combined together; where it
+            // is the last of them, the CTA combines them after its walk.
+            const int p = (int)range - c0 / a.lanes, p0 = p / kFan * kFan;
+            int *cnt = a.count + 2 * ((c0 + p0 * a.lanes) + (p0 > 0 ? kMaxGrid : 0)) + (PAIR ? h : 0);
+            if (!(ok = arrive(cnt, min(kFan, nparts - p0), [&]() {
+                      jobs[2 * h + last[h]] = {s.b, s.g, s.blk, row0, live, c0, nparts, p0};
+                      last[h] = last[h] + 1;
+                  })))
+                break;
         }
-        // The items whose last part was this CTA's (a CTA has two parts at most):
-        // here, where nothing of the loop above is alive in registers.
-        for (int i = 0; ok && i < last[h]; ++i) {
-            const Job job = jobs[2 * h + i];
-            __threadfence();
-            merge_rows(a, job, quarter, lane, [&](int tr) -> __nv_bfloat16 * {
-                const int gr = job.blk * BLOCK + tr;
-                return a.out + (((int64_t)job.b * a.drafts + gr / a.G) * a.Hq + job.g * a.G + gr % a.G) * D;
-            });
+        // The parts whose last was this CTA's (it has two parts at most): here, where
+        // nothing of the loop above is alive in registers, and by both row tiles' warps.
+        if (lane == 0) mbar_arrive(&bar[ENDED]);
+        ok = ok && wwait(ENDED, 0u, 715);
+        const int njobs0 = ok ? last[0] : 0, njobs = ok ? njobs0 + last[1] : 0;
+        uint32_t nw = 0;  // combined parts counted
+        for (int i = 0; ok && i < njobs; ++i) {
+            const Job &job = jobs[i < njobs0 ? i : 2 + i - njobs0];
+            const int jh = PAIR && i >= njobs0 ? 1 : 0;
+            const bool one = job.nparts <= kFan;
+            // More parts than that: they are combined by several CTAs, and the
+            // combined ones by the last of these.
+            for (bool final = one;; final = true) {
+                __threadfence();
+                const int p0 = final ? 0 : job.p0;
+                const int step = final && !one ? kFan : 1, p1 = final ? job.nparts : min(p0 + kFan, job.nparts);
+                const size_t slot_floats = slot_of(a.part_rows);
+                Merge g;
+                g.rest = a.parts + (size_t)(2 * (job.c0 + p0 * a.lanes)) * slot_floats;
+                g.first = g.rest + (p0 == 0 ? slot_floats : 0);
+                g.apart = (size_t)(2 * step * a.lanes) * slot_floats;
+                g.part_rows = a.part_rows;
+                g.tr0 = job.row0;
+                g.live = job.live;
+                g.n = (p1 - p0 + step - 1) / step;
+                g.token = (int64_t)a.Hq * D;
+                g.out = a.out + (int64_t)job.b * a.drafts * g.token + job.g * a.G * D;
+                g.gr0 = job.blk * BLOCK + job.row0;
+                g.G = a.G;
+                merge_rows(g, final, warp - 4, lane);
+                if (final) break;
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[WROTE2]);
+                if (warp == 4) {
+                    if (!(ok = wwait(WROTE2, nw & 1u, 716))) break;
+                    if (lane == 0) {
+                        int *cnt = a.count + 2 * (job.c0 + 2 * kMaxGrid) + jh;
+                        __threadfence();
+                        const bool is_last = atomicAdd(cnt, 1) == (job.nparts + kFan - 1) / kFan - 1;
+                        __threadfence();
+                        if (is_last) *cnt = 0;
+                        marks[0] = is_last;  // (of the walk, and free now)
+                        mbar_arrive(&bar[TOLD2]);
+                    }
+                }
+                if (!(ok = wwait(TOLD2, nw & 1u, 717))) break;
+                ++nw;
+                if (!marks[0]) break;
+            }
         }
     }
     tc_fence_before();
@@ -807,7 +886,7 @@ Layout layout_of(int drafts, int G) {
     Layout l;
     l.pair = drafts * G > ROWS;
     l.part_rows = std::min(drafts * G, 2 * ROWS);
-    l.parts = (size_t)kMaxGrid * 2 * sizeof(int);
+    l.parts = (size_t)3 * kMaxGrid * 2 * sizeof(int);
     l.bytes = l.parts + (size_t)kMaxGrid * 2 * slot_of(l.part_rows) * sizeof(float);
     return l;
 }
@@ -882,12 +961,12 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     const int64_t keys = (int64_t)max_blocks_per_seq * block_size;
     if (keys > 0x7fffffffLL - 4096) return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size must fit 31 bits");
     const int64_t blocks = (num_drafts * G + 2 * ROWS - 1) / (2 * ROWS);
-    const int64_t a_seq = (int64_t)num_kv_heads * blocks * ((keys + TILE - 1) / TILE + kItemCost);
+    const int64_t a_seq = (int64_t)num_kv_heads * blocks * ((keys + TILE - 1) / TILE);
     if (num_kv_heads > (1 << 16) || a_seq > 0x7fffffffLL / batch)
         return fail(PA_ERR_UNSUPPORTED, "too many tiles (batch * num_kv_heads * max_blocks_per_seq * block_size)");
     if (!workspace || workspace_bytes < l.bytes)
         return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : (size_t)0, l.bytes);
-    if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(workspace) & 31u) return fail(PA_ERR_INVALID_ARG, "workspace must be 32-byte aligned");
     const int sms = sm_count();
     if (sms <= 0) return fail(PA_ERR_CUDA, "no CUDA device");
     TreeArgs a = {};

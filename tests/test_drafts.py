@@ -223,7 +223,7 @@ def test_decode_tree_argument_checks(L):
     for kw in (dict(batch=-1), dict(t=0), dict(out=None), dict(q=None), dict(k=None), dict(v=None), dict(bt=None),
                dict(ctx=None), dict(hq=12), dict(hkv=0), dict(qs=2040), dict(qs=2052), dict(scale=0.0),
                dict(scale=float("inf")), dict(scale=float("nan")), dict(mb=0), dict(B=0), dict(nb=0), dict(q=ODD),
-               dict(k=ODD), dict(out=ODD), dict(ws=ODD), dict(mask=C.c_void_p(260))):
+               dict(k=ODD), dict(out=ODD), dict(ws=ODD), dict(ws=C.c_void_p(272)), dict(mask=C.c_void_p(260))):
         assert call(**kw) == pa.PA_ERR_INVALID_ARG, kw
     for kw in (dict(hq=24), dict(hq=128), dict(d=64), dict(B=24), dict(t=65), dict(batch=2049), dict(nb=1 << 24),
                dict(batch=2048, mb=1 << 20, nb=1024, B=1024)):
