@@ -11,7 +11,8 @@
 // (sequence, kv head, block of 128 * NT rows); its 64-key tiles, laid end to end
 // over all items, are cut into one range of equal cost per CTA.  Roles of a CTA:
 //   warp 0     Q rows and K tiles by TMA, block ids 32 at a time
-//   warp 1     S = Q K^T (M = 128, N = 64, K = 128) into one of two TMEM buffers
+//   warp 1     S = Q K^T (M = 128, N = 64, K = 128) into one of a row tile's two TMEM
+//              buffers
 //   warp 2     O += P V (P from TMEM, V as an MN-major operand)
 //   warp 3     V tiles by TMA
 //   warps 4..  one thread per row: online softmax in base 2, P over S as bf16
@@ -61,10 +62,11 @@ constexpr int KMAX = 6, VMAX = 8;                // ring stages at most
 enum {  // barriers: rings, then per row tile [2] (and score buffer [2])
     KFULL = 0, KEMPTY = KFULL + KMAX, VFULL = KEMPTY + KMAX, VEMPTY = VFULL + VMAX, SFULL = VEMPTY + VMAX,
     PFULL = SFULL + 4, PDONE = PFULL + 4, OEMPTY = PDONE + 4, QFULL = OEMPTY + 2, QEMPTY = QFULL + 2,
-    WROTE = QEMPTY + 2, TOLD = WROTE + 2, DRAIN = TOLD + 2, ENDED = DRAIN + 2, WROTE2, TOLD2, NBAR
+    ENDED = QEMPTY + 2, WROTE, TOLD, DRAIN, NBAR = DRAIN + 2
 };
 // Shared memory: Q [2], the rings, then from off_bar on the barriers, a few words
-// (TMEM address, abort, marks [4], jobs [2], scan scratch [12]), the jobs [2][2],
+// (TMEM address, abort, marks [4], parts held [2], two words of the parts' count, scan
+// scratch [12]), the parts [2][2],
 // and per sequence the running sum of tiles, the length (int) and the drafts (byte).
 constexpr int MISC = (NBAR * 8 + 15) / 16 * 16, JOBS = MISC + 128, ARRAYS = JOBS + 4 * 32;
 constexpr uint32_t TMEM_COLS = 512, COL_O = 256;               // S(h, b) at h * 128 + b * 64, O(h) at COL_O + h * 128
@@ -82,6 +84,7 @@ struct TreeArgs {
     int32_t max_blocks, batch, drafts, Hq, Hkv, G, block_size, num_blocks, box_rows, q_box, checked;
     int32_t q_rows;          // rows that a Q tile has room for (a multiple of 8): the MMA reads on past them
     int32_t k_stages, v_stages;
+    int32_t shift;           // G = 1 << shift
     int32_t lanes;           // ranges side by side, each over Hkv / lanes of the heads
     float scale_log2;
     // Arrivals [3][kMaxGrid][2 row tiles]: of the first kFan parts of the item that
@@ -93,14 +96,19 @@ struct TreeArgs {
     DevError *err;
 };
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort, DevError *err,
-                                              int where) {
-    if (mbar_try_wait(smem_addr(bar), parity)) return true;
+// A wait that is not over at once.  (A call of its own: inlined in the 25 places
+// that wait, it takes the roles' loops apart in the instruction cache.)
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort, DevError *err, int where) {
     if (*abort) return false;
     if (mbar_wait(bar, parity)) return true;
     record_error(err, PA_DEV_TIMEOUT, where);
     *abort = 1;
     return false;
+}
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort, DevError *err,
+                                              int where) {
+    if (__builtin_expect(mbar_try_wait(smem_addr(bar), parity), 1)) return true;
+    return wait_on(bar, parity, abort, err, where);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -197,10 +205,34 @@ struct Walker {
     }
 };
 
-// Parts [p0, p1) of an item to combine, in steps of `step`: rows [row0, row0 +
-// live) of the item.  Part p is that of CTA c0 + p * lanes.
+// Adds the V values of drafts lo .. hi - 1 that are not finite to a thread's row (fp32,
+// or the bf16 output) where its mask has them.  Rare, and kept out of the loop's code.
+__device__ __noinline__ void add_hidden(void *row, bool bf16, unsigned long long mask, const __nv_bfloat16 *v,
+                                        int64_t v_row, const int32_t *bt, int block_size, int num_blocks, int first,
+                                        int lo, int hi, int lane) {
+    for (int j = lo; j < hi; ++j) {
+        const int p = first + j, blk = __ldg(bt + p / block_size);
+        if (blk < 0 || blk >= num_blocks) continue;
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(v + ((int64_t)blk * block_size + p % block_size) * v_row) + lane);
+        if (!__any_sync(FULL, not_finite2(w.x) || not_finite2(w.y))) continue;
+        for (int c = 0; c < D; ++c) {
+            const uint32_t t = __shfl_sync(FULL, (c & 2) ? w.y : w.x, c >> 2);
+            const float x = (c & 1) ? bf16hi(t) : bf16lo(t);
+            if (isfinite(x) || !((mask >> j) & 1)) continue;
+            if (bf16) {
+                __nv_bfloat16 *e = static_cast<__nv_bfloat16 *>(row) + c;
+                *e = __float2bfloat16(__bfloat162float(*e) + x);
+            } else {
+                static_cast<float *>(row)[c] += x;
+            }
+        }
+    }
+}
+
+// Part number `part` of `nparts`: rows [row0, row0 + live) of an item of which part p
+// is that of CTA c0 + p * lanes.
 struct Job {
-    int b, g, blk, row0, live, c0, nparts, p0;
+    int b, g, blk, row0, live, c0, nparts, part;
 };
 constexpr int kFan = 8;  // parts combined at a time
 
@@ -214,42 +246,42 @@ struct Merge {
     float *first, *rest;  // the first part; part i > 0 at rest + i * apart
     size_t apart;
     int part_rows, tr0, live, n;
-    // The output row of row r of the (sequence, kv head): out + (r / G) * token + r % G * D.
+    // The output row of row r of the (sequence, kv head): out + (r >> shift) * token + r % G * D, G = 1 << shift.
     __nv_bfloat16 *out;
     int64_t token;
-    int gr0, G;
+    int gr0, shift;
 };
 __device__ __noinline__ void merge_rows(Merge g, bool final, int w, int lane) {
     constexpr int RM = 4, PM = 4, PL = 32 / RM;  // rows, parts at a time, lanes of a row
     const int n = g.n, r = lane & (RM - 1), ps = lane / RM;
-    auto slot = [&](int i) -> float * { return i == 0 ? g.first : g.rest + (size_t)i * g.apart; };
+    auto part = [&](int i) -> float * { return i == 0 ? g.first : g.rest + (size_t)i * g.apart; };
+#pragma unroll 1
     for (int r0 = RM * w; r0 < g.live; r0 += 8 * RM) {
-        const int nr = min(RM, g.live - r0);
-        float4 v[PM][RM];
-        auto load = [&](int i0) {  // rows r0 .. of parts i0 ..
-#pragma unroll
-            for (int pp = 0; pp < PM; ++pp)
-#pragma unroll
-                for (int e = 0; e < RM; ++e)
-                    if (e < nr && i0 + pp < n)
-                        v[pp][e] =
-                            __ldcg(reinterpret_cast<const float4 *>(slot(i0 + pp) + (size_t)(g.tr0 + r0 + e) * D) + lane);
+        const int row = g.tr0 + r0, nr = min(RM, g.live - r0);
+        auto ml_of = [&](int i) -> float2 {  // of row r in the i-th part
+            return i < n && r < nr ? __ldcg(reinterpret_cast<const float2 *>(part(i) + (size_t)g.part_rows * D) + row + r)
+                                   : make_float2(-INFINITY, 0.f);
         };
-        auto ml_of = [&](int i) -> float2 {  // of row r0 + r in the i-th part
-            return i < n && r < nr
-                       ? __ldcg(reinterpret_cast<const float2 *>(slot(i) + (size_t)g.part_rows * D) + g.tr0 + r0 + r)
-                       : make_float2(-INFINITY, 0.f);
+        float4 v[PM][RM], acc[RM];
+        auto load = [&](int i0) {  // the rows of parts i0 .. i0 + 3 (a part or row past the last: the last again)
+#pragma unroll
+            for (int pp = 0; pp < PM; ++pp) {
+                const float4 *at = reinterpret_cast<const float4 *>(part(min(i0 + pp, n - 1)) + (size_t)row * D) + lane;
+#pragma unroll
+                for (int e = 0; e < RM; ++e) v[pp][e] = __ldcg(at + min(e, nr - 1) * (D / 4));
+            }
         };
-        const float2 ml0 = ml_of(ps);
+        float2 ml = ml_of(ps);
         load(0);
-        float m = ml0.x, l = ml0.y;
+        float m = ml.x, l = ml.y;
+#pragma unroll 1
         for (int i = ps + PL; i < n; i += PL) {
-            const float2 ml = ml_of(i);
-            const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-            l = l * fast_exp2(m - ref) + ml.y * fast_exp2(ml.x - ref);
+            const float2 t = ml_of(i);
+            const float mn = fmaxf(m, t.x), ref = mn == -INFINITY ? 0.f : mn;
+            l = l * fast_exp2(m - ref) + t.y * fast_exp2(t.x - ref);
             m = mn;
         }
-#pragma unroll
+#pragma unroll 1
         for (int o = RM; o < 32; o <<= 1) {
             const float m2 = __shfl_xor_sync(FULL, m, o), l2 = __shfl_xor_sync(FULL, l, o);
             const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn;
@@ -257,41 +289,40 @@ __device__ __noinline__ void merge_rows(Merge g, bool final, int w, int lane) {
             m = mn;
         }
         const float ref = m == -INFINITY ? 0.f : m, inv = l == 0.f ? 0.f : 1.f / l;
-        float4 acc[RM];
 #pragma unroll
         for (int e = 0; e < RM; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        float wgt = fast_exp2(ml0.x - ref);  // of row r in the part ps (of the eight under way)
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += PM) {
             if (i0 > 0) {
                 load(i0);
-                if (i0 % PL == 0) wgt = fast_exp2(ml_of(i0 + ps).x - ref);
+                if (i0 % PL == 0) ml = ml_of(i0 + ps);
             }
+            const float wgt = fast_exp2(ml.x - ref);  // of row r in the part ps of the eight under way
 #pragma unroll
-            for (int pp = 0; pp < PM; ++pp)
+            for (int pp = 0; pp < PM; ++pp) {
+                if (i0 + pp >= n) break;
 #pragma unroll
                 for (int e = 0; e < RM; ++e) {
-                    const float f = __shfl_sync(FULL, wgt, ((i0 + pp) % PL) * RM + e);
-                    if (e < nr && i0 + pp < n) {
-                        acc[e].x = fmaf(v[pp][e].x, f, acc[e].x);
-                        acc[e].y = fmaf(v[pp][e].y, f, acc[e].y);
-                        acc[e].z = fmaf(v[pp][e].z, f, acc[e].z);
-                        acc[e].w = fmaf(v[pp][e].w, f, acc[e].w);
-                    }
+                    const float f = __shfl_sync(FULL, wgt, ((i0 & PM) + pp) * RM + e);
+                    acc[e].x = fmaf(v[pp][e].x, f, acc[e].x);
+                    acc[e].y = fmaf(v[pp][e].y, f, acc[e].y);
+                    acc[e].z = fmaf(v[pp][e].z, f, acc[e].z);
+                    acc[e].w = fmaf(v[pp][e].w, f, acc[e].w);
                 }
+            }
         }
         if (!final && ps == 0 && r < nr)  // (every lane has read the rows' m and l)
-            reinterpret_cast<float2 *>(g.first + (size_t)g.part_rows * D)[g.tr0 + r0 + r] = make_float2(m, l);
+            reinterpret_cast<float2 *>(g.first + (size_t)g.part_rows * D)[row + r] = make_float2(m, l);
 #pragma unroll
         for (int e = 0; e < RM; ++e) {
             const float f = __shfl_sync(FULL, inv, e);
-            if (e >= nr) continue;
+            if (e >= nr) break;
             if (final) {
                 const int gr = g.gr0 + r0 + e;
-                reinterpret_cast<uint2 *>(g.out + (gr / g.G) * g.token + (gr % g.G) * D)[lane] =
+                reinterpret_cast<uint2 *>(g.out + (gr >> g.shift) * g.token + (gr & ((1 << g.shift) - 1)) * D)[lane] =
                     make_uint2(pack_bf16(acc[e].x * f, acc[e].y * f), pack_bf16(acc[e].z * f, acc[e].w * f));
             } else {
-                reinterpret_cast<float4 *>(g.first + (size_t)(g.tr0 + r0 + e) * D)[lane] = acc[e];
+                reinterpret_cast<float4 *>(g.first + (size_t)(row + e) * D)[lane] = acc[e];
             }
         }
     }
@@ -314,16 +345,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t *cum = reinterpret_cast<uint32_t *>(ctl + ARRAYS);
     int *ctx_s = reinterpret_cast<int *>(cum + (a.batch + 1));
     uint8_t *n_s = reinterpret_cast<uint8_t *>(ctx_s + (a.batch + 1));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform, and known to be)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NBAR; ++i) {
             // The four softmax warps of a row tile arrive one each.
-            const bool per_warp = (i >= PFULL && i < PFULL + 4) || (i >= OEMPTY && i < OEMPTY + 2) ||
-                                  (i >= WROTE && i < WROTE + 2);
-            mbar_init(&bar[i], i == ENDED || i == WROTE2 ? 8u : per_warp ? 4u : 1u);
+            const bool per_warp = (i >= PFULL && i < PFULL + 4) || (i >= OEMPTY && i < OEMPTY + 2);
+            mbar_init(&bar[i], i == ENDED || i == WROTE ? 8u : per_warp ? 4u : 1u);
         }
-        for (int i = 0; i < 7; ++i) abort[i] = 0;  // and the marks behind it
+        for (int i = 0; i < 9; ++i) abort[i] = 0;  // and the marks behind it
         fence_mbar_init();
         prefetch_tensormap(&tmq);
         prefetch_tensormap(&tmk);
@@ -333,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_alloc(tmem_slot, TMEM_COLS);
         tmem_relinquish();
     }
-    pdl_wait_then_release();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Lengths, and the running sum of the sequences' tiles.
     uint32_t carry = 0;
     for (int base = 0; base < a.batch; base += THREADS) {
@@ -383,6 +413,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Row tiles of segment number k.
     auto h_begin = [](int k) -> int { return PAIR ? 0 : k & 1; };
     auto h_end = [](int k, const Seg &s) -> int { return PAIR ? (s.rows + ROWS - 1) / ROWS : (k & 1) + 1; };
+    // The MMA warps run whole and one lane issues: descriptors and addresses then stay
+    // in uniform registers, where the instructions take them from.  (Issued by one lane
+    // of a diverged warp they took 50 to 200 cycles each, and the issuing threads were
+    // what bound the kernel: 64 drafts over 8 x 32768 keys 289 us instead of 252, the
+    // Qwen3-8B shape 291 instead of 266.)
+    uint32_t elected_;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(elected_));
+    const bool elected = elected_ != 0;
+    auto wwait = [&](int i, uint32_t parity, int where) -> bool {  // the warp as one
+        return __all_sync(FULL, wait_or_abort(&bar[i], parity, abort, a.err, where));
+    };
     Seg s;
     bool ok = true;
 
@@ -428,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (h < h_begin(k) || h >= h_end(k, s)) continue;
                     if (!(ok = wait_or_abort(&bar[QEMPTY + h], (uq[h] & 1u) ^ 1u, abort, a.err, 708))) break;
                     // Whole boxes, whatever the sequence's drafts: the rows past them are not live.
-                    const int token = s.b * a.drafts + (s.blk * BLOCK + (PAIR ? h * ROWS : 0)) / a.G;
+                    const int token = s.b * a.drafts + ((s.blk * BLOCK + (PAIR ? h * ROWS : 0)) >> a.shift);
                     mbar_arrive_expect_tx(&bar[QFULL + h], (uint32_t)(2 * a.q_box * a.G * 128));
                     tma_load_4d_plain(smem + h * qtile, &tmq, 0, s.g * a.G, token, 0, &bar[QFULL + h]);
                     tma_load_4d_plain(smem + h * qtile + qhalf, &tmq, 0, s.g * a.G, token, 1, &bar[QFULL + h]);
@@ -473,28 +514,27 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- S = Q K^T
-        if (lane == 0) {
-            Ring ring(a.k_stages);
-            uint32_t th[2] = {0, 0}, uq[2] = {0, 0};  // of each row tile: tiles, segments
-            bool issued = false;
-            for (int k = 0; ok && walk.next(s); ++k) {
-                const int h0 = h_begin(k), h1 = h_end(k, s);
-                for (int j = s.t0; ok && j < s.t1; ++j) {
-                    if (!(ok = wait_or_abort(&bar[KFULL + ring.st], ring.par, abort, a.err, 703))) break;
-                    const uint64_t kdesc = smem_desc_sw128(smem_addr(k_ring + ring.st * KV_BYTES), 16, SBO);
+        Ring ring(a.k_stages);
+        uint32_t th[2] = {0, 0}, uq[2] = {0, 0};  // of each row tile: tiles, segments
+        bool issued = false;
+        for (int k = 0; ok && walk.next(s); ++k) {
+            const int h0 = h_begin(k), h1 = h_end(k, s);
+            for (int j = s.t0; ok && j < s.t1; ++j) {
+                if (!(ok = wwait(KFULL + ring.st, ring.par, 703))) break;
+                const uint64_t kdesc = smem_desc_sw128(smem_addr(k_ring + ring.st * KV_BYTES), 16, SBO);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h < h0 || h >= h1) continue;
-                        const int b = th[h] & 1;
-                        if (j == s.t0) {
-                            if (!(ok = wait_or_abort(&bar[QFULL + h], uq[h] & 1u, abort, a.err, 702))) break;
-                            ++uq[h];
-                        }
-                        // The buffer is free once the P.V of two tiles ago has read it.
-                        if (!(ok = wait_or_abort(&bar[PDONE + 2 * h + b], ((th[h] >> 1) & 1u) ^ 1u, abort, a.err, 704)))
-                            break;
-                        tc_fence_after();
-                        const uint64_t qdesc = smem_desc_sw128(smem_addr(smem + h * qtile), 16, SBO);
+                for (int h = 0; h < 2; ++h) {
+                    if (h < h0 || h >= h1) continue;
+                    const int b = th[h] & 1;
+                    if (j == s.t0) {
+                        if (!(ok = wwait(QFULL + h, uq[h] & 1u, 702))) break;
+                        ++uq[h];
+                    }
+                    // The buffer is free once the P.V of two tiles ago has read it.
+                    if (!(ok = wwait(PDONE + 2 * h + b, ((th[h] >> 1) & 1u) ^ 1u, 704))) break;
+                    tc_fence_after();
+                    const uint64_t qdesc = smem_desc_sw128(smem_addr(smem + h * qtile), 16, SBO);
+                    if (elected) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             mma_bf16_ss(tmem + h * 128 + b * TILE,
@@ -503,58 +543,68 @@ __global__ void __launch_bounds__(THREADS, 1)
                                         kk > 0 ? 1u : 0u);
                         mma_commit(&bar[SFULL + 2 * h + b]);
                         if (j == s.t1 - 1) mma_commit(&bar[QEMPTY + h]);  // the segment's products have read Q
-                        issued = true;
-                        ++th[h];
                     }
-                    if (!ok) break;
-                    mma_commit(&bar[KEMPTY + ring.st]);
-                    ring.next();
+                    issued = true;
+                    ++th[h];
                 }
+                if (!ok) break;
+                if (elected) mma_commit(&bar[KEMPTY + ring.st]);
+                ring.next();
             }
-            if (issued && *abort) {
-                mma_commit(&bar[DRAIN]);
-                (void)mbar_wait(&bar[DRAIN], 0);
-            }
+        }
+        if (issued && elected && *abort) {
+            mma_commit(&bar[DRAIN]);
+            (void)mbar_wait(&bar[DRAIN], 0);
         }
     } else if (warp == 2) {
         // ---------------------------------------------------------------- O += P V
-        if (lane == 0) {
-            Ring ring(a.v_stages);
-            uint32_t th[2] = {0, 0}, uh[2] = {0, 0};
-            bool issued = false;
-            for (int k = 0; ok && walk.next(s); ++k) {
-                const int h0 = h_begin(k), h1 = h_end(k, s);
-                for (int j = s.t0; ok && j < s.t1; ++j) {
-                    if (!(ok = wait_or_abort(&bar[VFULL + ring.st], ring.par, abort, a.err, 705))) break;
-                    const int steps = (min(TILE, ctx_s[s.b] - j * TILE) + 15) / 16;  // keys past the last: P is 0
-                    const uint64_t vdesc = smem_desc_sw128(smem_addr(v_ring + ring.st * KV_BYTES), KV_HALF, SBO);
+        Ring ring(a.v_stages);
+        uint32_t th[2] = {0, 0}, uh[2] = {0, 0};
+        bool issued = false;
+        for (int k = 0; ok && walk.next(s); ++k) {
+            const int h0 = h_begin(k), h1 = h_end(k, s);
+            for (int j = s.t0; ok && j < s.t1; ++j) {
+                if (!(ok = wwait(VFULL + ring.st, ring.par, 705))) break;
+                const int steps = (min(TILE, ctx_s[s.b] - j * TILE) + 15) / 16;  // keys past the last: P is 0
+                const uint64_t vdesc = smem_desc_sw128(smem_addr(v_ring + ring.st * KV_BYTES), KV_HALF, SBO);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h < h0 || h >= h1) continue;
-                        const int b = th[h] & 1;
-                        if (j == s.t0) {  // O is free once the row tile's last segment was read
-                            if (!(ok = wait_or_abort(&bar[OEMPTY + h], (uh[h] & 1u) ^ 1u, abort, a.err, 706))) break;
-                            ++uh[h];
-                        }
-                        if (!(ok = wait_or_abort(&bar[PFULL + 2 * h + b], (th[h] >> 1) & 1u, abort, a.err, 707))) break;
-                        tc_fence_after();
-                        for (int kk = 0; kk < steps; ++kk)  // 16 keys a step = 8 TMEM columns of P
-                            mma_bf16_ts(tmem + COL_O + h * 128, tmem + h * 128 + b * TILE + kk * 8,
-                                        vdesc + (uint64_t)((kk * 16 * 128) >> 4), IDESC_PV,
-                                        (j > s.t0 || kk > 0) ? 1u : 0u);
-                        mma_commit(&bar[PDONE + 2 * h + b]);
-                        issued = true;
-                        ++th[h];
+                for (int h = 0; h < 2; ++h) {
+                    if (h < h0 || h >= h1) continue;
+                    const int b = th[h] & 1;
+                    if (j == s.t0) {  // O is free once the row tile's last segment was read
+                        if (!(ok = wwait(OEMPTY + h, (uh[h] & 1u) ^ 1u, 706))) break;
+                        ++uh[h];
                     }
-                    if (!ok) break;
-                    mma_commit(&bar[VEMPTY + ring.st]);
-                    ring.next();
+                    if (!(ok = wwait(PFULL + 2 * h + b, (th[h] >> 1) & 1u, 707))) break;
+                    tc_fence_after();
+                    if (elected) {
+                        // 16 keys a step = 8 TMEM columns of P; unrolled where it can be.
+                        if (steps == TILE / 16) {
+#pragma unroll
+                            for (int kk = 0; kk < TILE / 16; ++kk)
+                                mma_bf16_ts(tmem + COL_O + h * 128, tmem + h * 128 + b * TILE + kk * 8,
+                                            vdesc + (uint64_t)((kk * 16 * 128) >> 4), IDESC_PV,
+                                            (j > s.t0 || kk > 0) ? 1u : 0u);
+                        } else {
+#pragma unroll 1
+                            for (int kk = 0; kk < steps; ++kk)
+                                mma_bf16_ts(tmem + COL_O + h * 128, tmem + h * 128 + b * TILE + kk * 8,
+                                            vdesc + (uint64_t)((kk * 16 * 128) >> 4), IDESC_PV,
+                                            (j > s.t0 || kk > 0) ? 1u : 0u);
+                        }
+                        mma_commit(&bar[PDONE + 2 * h + b]);
+                    }
+                    issued = true;
+                    ++th[h];
                 }
+                if (!ok) break;
+                if (elected) mma_commit(&bar[VEMPTY + ring.st]);
+                ring.next();
             }
-            if (issued && *abort) {
-                mma_commit(&bar[DRAIN + 1]);
-                (void)mbar_wait(&bar[DRAIN + 1], 0);
-            }
+        }
+        if (issued && elected && *abort) {
+            mma_commit(&bar[DRAIN + 1]);
+            (void)mbar_wait(&bar[DRAIN + 1], 0);
         }
     } else {
         // ---------------------------------------------------------------- softmax, output
@@ -563,9 +613,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int wrow = quarter * 32, row = wrow + lane;  // row of the tile == TMEM lane
         const uint32_t t_s = tmem + ((uint32_t)wrow << 16) + h * 128, t_o = tmem + ((uint32_t)wrow << 16) + COL_O + h * 128;
         const float sl = a.scale_log2;
-        auto wwait = [&](int i, uint32_t parity, int where) -> bool {
-            return __all_sync(FULL, wait_or_abort(&bar[i], parity, abort, a.err, where));
-        };
         {
             // Tokens past a sequence's drafts: zeros.
             const int per = a.Hq * (D / 8);  // 16-byte chunks of a token
@@ -581,8 +628,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         // segment of its own ahead of another, as a segment's last product needs the
         // P of all of them.
         volatile int *marks = abort + 1;
-        volatile int *last = abort + 5;  // jobs of each row tile
-        Job *jobs = reinterpret_cast<Job *>(ctl + JOBS);
+        volatile int *held = abort + 5, *todo = abort + 7, *go_on = abort + 8;
+        Job *parts = reinterpret_cast<Job *>(ctl + JOBS);
+        int nparts_h = 0;  // parts of this row tile
         // The next segment that this row tile has rows in: its number, its first
         // tile's number, and (asked for ahead) this row's mask.
         int k_next = 0;
@@ -604,36 +652,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 o.m = 0;
                 const int row0 = PAIR ? h * ROWS : 0;
                 if (row0 + row < o.s.rows) {
-                    const int di = (o.s.blk * BLOCK + row0 + row) / a.G;
+                    const int di = (o.s.blk * BLOCK + row0 + row) >> a.shift;
                     o.m = a.mask ? __ldg(a.mask + (int64_t)o.s.b * a.drafts + di) : di >= 63 ? ~0ull : (2ull << di) - 1;
                 }
                 return true;
             }
             return false;
-        };
-        // The row tile's four warps have written: one of them counts it.  The one that
-        // brings the counter to `all` leaves it at zero, as it was found, and calls
-        // `then` before the others go on.
-        uint32_t ns = 0;
-        auto arrive = [&](int *cnt, int all, auto then) -> bool {
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[WROTE + h]);
-            if (quarter == 0) {
-                if (!wwait(WROTE + h, ns & 1u, 713)) return false;
-                if (lane == 0) {
-                    __threadfence();
-                    if (atomicAdd(cnt, 1) == all - 1) {
-                        __threadfence();
-                        *cnt = 0;
-                        then();
-                    }
-                    mbar_arrive(&bar[TOLD + h]);
-                }
-            }
-            if (!wwait(TOLD + h, ns & 1u, 714)) return false;
-            ++ns;
-            return true;
         };
         Own nx;
         bool have = fetch(nx);
@@ -654,7 +678,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int j = s.t0; ok && j < s.t1; ++j, ++gg, ++th) {
                 const int b = th & 1, kb = j * TILE;
                 const uint32_t cs = t_s + b * TILE;
+                if (!(ok = wwait(SFULL + 2 * h + b, (th >> 1) & 1u, 710))) break;
                 if (kb + TILE > first) {
+                    // (V's place in its ring is waited for after the scores: their product
+                    // followed the P.V of at most four tiles before, so that this tile's
+                    // round is the next to complete, as a wait by parity needs.)
                     // A tile with drafts: V's rows past the last key that the
                     // product reads become zeros, and drafts' values that are not
                     // finite too.  Each row tile of the item does it before its
@@ -679,7 +707,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                if (!(ok = wwait(SFULL + 2 * h + b, (th >> 1) & 1u, 710))) break;
                 tc_fence_after();
                 if (wlive) {
                     uint32_t r[TILE];
@@ -756,32 +783,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (wlive) {
                 const float inv = !whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;  // a row that sees nothing: zeros
-                const bool odd = *mark == k + 1;
                 const int gr = s.blk * BLOCK + row0 + row;  // row of the (sequence, kv head)
-                __nv_bfloat16 *dst = a.out + (((int64_t)s.b * a.drafts + gr / a.G) * a.Hq + s.g * a.G + gr % a.G) * D;
+                __nv_bfloat16 *dst = a.out + (((int64_t)s.b * a.drafts + (gr >> a.shift)) * a.Hq + s.g * a.G + (gr & (a.G - 1))) * D;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
                     tmem_ld32(t_o + c * 32, o);
                     tmem_ld_wait();
-                    if (odd) {
-                        // What was taken out of V: added to the rows that see it.
-                        const int lo = max(0, s.t0 * TILE - first), hi = min(n, s.t1 * TILE - first);
-                        for (int j = lo; j < hi; ++j) {
-                            const int p = first + j, blk = __ldg(a.bt + (int64_t)s.b * a.max_blocks + p / a.block_size);
-                            if (blk < 0 || blk >= a.num_blocks) continue;
-                            const uint16_t *v = reinterpret_cast<const uint16_t *>(
-                                a.v_cache + (((int64_t)blk * a.block_size + p % a.block_size) * a.Hkv + s.g) * D + c * 32);
-                            const float x = __uint_as_float((uint32_t)__ldg(v + lane) << 16);  // 32 values across the warp
-                            if (!__any_sync(FULL, !isfinite(x))) continue;
-                            const bool sees = mine && ((m64 >> j) & 1);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float y = __shfl_sync(FULL, x, e);
-                                if (sees && !isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-                            }
-                        }
-                    }
                     if (mine && whole) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -806,33 +814,60 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[OEMPTY + h]);
+            if (wlive && *mark == k + 1) {
+                // What was taken out of V: added to the rows that see it.
+                const int lo = max(0, s.t0 * TILE - first), hi = min(n, s.t1 * TILE - first);  // drafts of the segment
+                const int gr = s.blk * BLOCK + row0 + row;
+                void *at = whole ? static_cast<void *>(a.out + (((int64_t)s.b * a.drafts + (gr >> a.shift)) * a.Hq + s.g * a.G + (gr & (a.G - 1))) * D)
+                                 : static_cast<void *>(slot + (size_t)(row0 + row) * D);
+                add_hidden(at, whole, mine ? m64 : 0ull, a.v_cache + (int64_t)s.g * D, (int64_t)a.Hkv * D,
+                           a.bt + (int64_t)s.b * a.max_blocks, a.block_size, a.num_blocks, first, lo, hi, lane);
+            }
             if (whole) continue;
             if (mine) reinterpret_cast<float2 *>(slot + (size_t)a.part_rows * D)[row0 + row] = make_float2(m_run * sl, l_run);
-            // The part is counted among the kFan that are combined together; where it
-            // is the last of them, the CTA combines them after its walk.
-            const int p = (int)range - c0 / a.lanes, p0 = p / kFan * kFan;
-            int *cnt = a.count + 2 * ((c0 + p0 * a.lanes) + (p0 > 0 ? kMaxGrid : 0)) + (PAIR ? h : 0);
-            if (!(ok = arrive(cnt, min(kFan, nparts - p0), [&]() {
-                      jobs[2 * h + last[h]] = {s.b, s.g, s.blk, row0, live, c0, nparts, p0};
-                      last[h] = last[h] + 1;
-                  })))
-                break;
+            if (quarter == 0 && lane == 0)  // two parts at most: of the range's first and last item
+                parts[2 * h + nparts_h] = {s.b, s.g, s.blk, row0, live, c0, nparts, (int)range - c0 / a.lanes};
+            ++nparts_h;
         }
-        // The parts whose last was this CTA's (it has two parts at most): here, where
-        // nothing of the loop above is alive in registers, and by both row tiles' warps.
+        // The parts are written: they are counted, and those whose last this CTA's was
+        // are combined, by both row tiles' warps; here, where nothing of the loop above
+        // is alive in registers.
+        __threadfence();
+        if (quarter == 0 && lane == 0) held[h] = nparts_h;
+        __syncwarp();
         if (lane == 0) mbar_arrive(&bar[ENDED]);
         ok = ok && wwait(ENDED, 0u, 715);
-        const int njobs0 = ok ? last[0] : 0, njobs = ok ? njobs0 + last[1] : 0;
-        uint32_t nw = 0;  // combined parts counted
-        for (int i = 0; ok && i < njobs; ++i) {
-            const Job &job = jobs[i < njobs0 ? i : 2 + i - njobs0];
-            const int jh = PAIR && i >= njobs0 ? 1 : 0;
+        uint32_t told = 0;
+        if (ok && warp == 4) {
+            // Lane i counts part i & 1 of row tile i >> 1: among the kFan parts that are
+            // combined together.
+            bool mine_last = false;
+            if (lane < 4 && (lane & 1) < held[lane >> 1]) {
+                const Job p = parts[lane];
+                const int p0 = p.part / kFan * kFan;
+                int *cnt = a.count + 2 * ((p.c0 + p0 * a.lanes) + (p0 > 0 ? kMaxGrid : 0)) + (PAIR ? lane >> 1 : 0);
+                __threadfence();
+                mine_last = atomicAdd(cnt, 1) == min(kFan, p.nparts - p0) - 1;
+                if (mine_last) *cnt = 0;  // as it was found
+                __threadfence();
+            }
+            const unsigned m = __ballot_sync(FULL, mine_last);
+            if (lane == 0) {
+                *todo = (int)m;
+                mbar_arrive(&bar[TOLD]);
+            }
+        }
+        ok = ok && wwait(TOLD, told++ & 1u, 714);
+        uint32_t wrote = 0;
+        for (unsigned m = ok ? (unsigned)*todo : 0u; ok && m; m &= m - 1) {
+            const int at = __ffs(m) - 1;
+            const Job &job = parts[at];
             const bool one = job.nparts <= kFan;
             // More parts than that: they are combined by several CTAs, and the
             // combined ones by the last of these.
             for (bool final = one;; final = true) {
                 __threadfence();
-                const int p0 = final ? 0 : job.p0;
+                const int p0 = final ? 0 : job.part / kFan * kFan;
                 const int step = final && !one ? kFan : 1, p1 = final ? job.nparts : min(p0 + kFan, job.nparts);
                 const size_t slot_floats = slot_of(a.part_rows);
                 Merge g;
@@ -846,27 +881,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 g.token = (int64_t)a.Hq * D;
                 g.out = a.out + (int64_t)job.b * a.drafts * g.token + job.g * a.G * D;
                 g.gr0 = job.blk * BLOCK + job.row0;
-                g.G = a.G;
+                g.shift = a.shift;
                 merge_rows(g, final, warp - 4, lane);
                 if (final) break;
                 __threadfence();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[WROTE2]);
+                if (lane == 0) mbar_arrive(&bar[WROTE]);
                 if (warp == 4) {
-                    if (!(ok = wwait(WROTE2, nw & 1u, 716))) break;
+                    if (!(ok = wwait(WROTE, wrote++ & 1u, 716))) break;
                     if (lane == 0) {
-                        int *cnt = a.count + 2 * (job.c0 + 2 * kMaxGrid) + jh;
+                        int *cnt = a.count + 2 * (job.c0 + 2 * kMaxGrid) + (PAIR ? at >> 1 : 0);
                         __threadfence();
                         const bool is_last = atomicAdd(cnt, 1) == (job.nparts + kFan - 1) / kFan - 1;
-                        __threadfence();
                         if (is_last) *cnt = 0;
-                        marks[0] = is_last;  // (of the walk, and free now)
-                        mbar_arrive(&bar[TOLD2]);
+                        __threadfence();
+                        *go_on = is_last;
+                        mbar_arrive(&bar[TOLD]);
                     }
                 }
-                if (!(ok = wwait(TOLD2, nw & 1u, 717))) break;
-                ++nw;
-                if (!marks[0]) break;
+                if (!(ok = wwait(TOLD, told++ & 1u, 717))) break;
+                if (!*go_on) break;
             }
         }
     }
@@ -906,9 +940,13 @@ pa_status launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUte
         if (e != cudaSuccess) return cuda_fail(e, "decode_tree_kernel shared memory");
         g_attr_done[dev][PAIR].store(1, std::memory_order_release);
     }
-    return launch_pdl(decode_tree_kernel<PAIR>, dim3((unsigned)grid), dim3(THREADS),
-                      (size_t)4 * a.q_rows * 128 + (a.k_stages + a.v_stages) * KV_BYTES + fixed_smem(a.batch), stream,
-                      "decode_tree_kernel", tmq, tmk, tmv, a);
+    // A plain launch: as a programmatic dependent one its CTAs take the SMs in the
+    // order in which the kernel before leaves them, those of a range no longer sit
+    // side by side, and long calls lose more (Qwen3-8B shape, 4 drafts, 356 us
+    // instead of 312) than short ones gain (9.0 us, 8.0).
+    const size_t smem = (size_t)4 * a.q_rows * 128 + (size_t)(a.k_stages + a.v_stages) * KV_BYTES + fixed_smem(a.batch);
+    decode_tree_kernel<PAIR><<<dim3((unsigned)grid), dim3(THREADS), smem, stream>>>(tmq, tmk, tmv, a);
+    return check_launch("decode_tree_kernel");
 }
 
 }  // namespace
@@ -982,6 +1020,7 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     a.Hq = num_q_heads;
     a.Hkv = num_kv_heads;
     a.G = G;
+    while ((1 << a.shift) < G) ++a.shift;
     a.block_size = block_size;
     a.num_blocks = num_blocks;
     int r = TILE;
