@@ -442,7 +442,7 @@ def _placed(stream, first, *others):
         if stream.device_index != dev:
             raise ValueError(f"stream of device {stream.device_index}, tensors on {first.device}")
         return torch.cuda.stream(stream)  # makes its device current as well
-    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return None if dev == _current_device() else torch.cuda.device(dev)
 
 
 def _rows(t, name, n, heads, d):
@@ -678,28 +678,43 @@ def rope_frequencies(rotary_dim=128, theta=10000.0, scaling=None, interleaved=Fa
     return Rope(host.to(device), gain.value, bool(interleaved))
 
 
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+def _current_device():
+    get = getattr(torch._C, "_cuda_getDevice", None)  # (0.1 us; torch.cuda.current_device takes 0.5)
+    return torch.cuda.current_device() if get is None else get()
+
+
+def _stream_of(dev):
+    """The raw current stream of the current device, dev."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(dev)
+
+
 def _rope_args(q, k, positions, frequencies, q_norm, k_norm, out_q):
     """Checks what rope and rope_store_kvcache share; returns (tokens, q heads, kv heads, D, strides)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("q and k must be [N, heads, 128]")
     n, hq, d = q.shape
     hkv = k.shape[1]
-    for x, name in ((n, "number of tokens"), (hq, "number of q heads"), (hkv, "number of kv heads")):
-        _fits(x, name)
+    if n > 0x7fffffff or hq > 0x7fffffff or hkv > 0x7fffffff:
+        raise ValueError("number of tokens or heads does not fit 32 bits")
     qs, ks = _rows(q, "q", n, hq, d), _rows(k, "k", n, hkv, d)
-    _need(positions, torch.int32, "positions")
-    if positions.shape != (n,) or not positions.is_contiguous():
+    freqs = frequencies.freqs
+    if positions.dtype is not _I32 or freqs.dtype is not _I64:
+        raise TypeError(f"positions must be {_I32} and frequencies.freqs {_I64}, got {positions.dtype}, {freqs.dtype}")
+    if positions.dim() != 1 or positions.shape[0] != n or not positions.is_contiguous():
         raise ValueError("positions must be contiguous [N]")
-    _need(frequencies.freqs, torch.int64, "frequencies.freqs")
-    if frequencies.freqs.dim() != 1 or not frequencies.freqs.is_contiguous():
+    if freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("frequencies.freqs must be contiguous [rotary_dim / 2]")
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+    for w in (q_norm, k_norm):
         if w is not None:
-            _need(w, torch.bfloat16, name)
-            if w.shape != (d,) or not w.is_contiguous():
-                raise ValueError(f"{name} must be contiguous [{d}]")
-    oqs = hq * d if out_q is None else _rows(out_q, "out_q", n, hq, d)
-    return n, hq, hkv, d, qs, ks, oqs
+            if w.dtype is not _BF16:
+                raise TypeError(f"q_norm and k_norm must be {_BF16}, got {w.dtype}")
+            if w.dim() != 1 or w.shape[0] != d or not w.is_contiguous():
+                raise ValueError(f"q_norm and k_norm must be contiguous [{d}]")
+    return n, hq, hkv, d, qs, ks, hq * d if out_q is None else _rows(out_q, "out_q", n, hq, d)
 
 
 def rope(q, k, positions, frequencies, q_norm=None, k_norm=None, eps=1e-6, out_q=None, out_k=None, stream=None):
@@ -708,33 +723,33 @@ def rope(q, k, positions, frequencies, q_norm=None, k_norm=None, eps=1e-6, out_q
     (int32 [N]), frequencies from rope_frequencies.  Returns (out_q, out_k); out_q may be q itself, out_k may be k."""
     n, hq, hkv, d, qs, ks, oqs = _rope_args(q, k, positions, frequencies, q_norm, k_norm, out_q)
     oks = hkv * d if out_k is None else _rows(out_k, "out_k", n, hkv, d)
-    ctx = _placed(stream, q, k, positions, frequencies.freqs, q_norm, k_norm, out_q, out_k)
+    freqs = frequencies.freqs
+    ctx = _placed(stream, q, k, positions, freqs, q_norm, k_norm, out_q, out_k)
     if ctx is not None:
         with ctx:
             return rope(q, k, positions, frequencies, q_norm, k_norm, eps, out_q, out_k)
     if out_q is None:
-        out_q = torch.empty(n, hq, d, dtype=torch.bfloat16, device=q.device)
+        out_q = q.new_empty((n, hq, d))
     if out_k is None:
-        out_k = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=q.device)
+        out_k = k.new_empty((n, hkv, d))
     _check(lib().pa_rope(out_q.data_ptr(), oqs, out_k.data_ptr(), oks, q.data_ptr(), qs, k.data_ptr(), ks,
-                         positions.data_ptr(), frequencies.freqs.data_ptr(), 2 * frequencies.freqs.shape[0],
-                         1 if frequencies.interleaved else 0, frequencies.gain,
-                         None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
-                         float(eps), n, hq, hkv, d, _raw_stream()), "pa_rope")
+                         positions.data_ptr(), freqs.data_ptr(), 2 * freqs.shape[0],
+                         1 if frequencies.interleaved else 0, frequencies.gain, None if q_norm is None else q_norm.data_ptr(),
+                         None if k_norm is None else k_norm.data_ptr(), eps, n, hq, hkv, d, _stream_of(q.get_device())),
+           "pa_rope")
     return out_q, out_k
 
 
-def _bf16_caches(k_cache, v_cache, dims=(4,)):
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, torch.bfloat16, name)
-    if k_cache.dim() not in dims or v_cache.shape != k_cache.shape:
+def _bf16_pool(k_cache, v_cache):
+    """The shape of a bf16 pool [num_blocks, B, Hkv, 128]."""
+    shape = k_cache.shape
+    if k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16:
+        raise TypeError(f"caches must be {_BF16}, got {k_cache.dtype}, {v_cache.dtype}")
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be of one shape, [num_blocks, B, Hkv, 128]")
-    for t in (k_cache, v_cache):
-        if not (t if t.dim() == 4 else t[0] if t.shape[0] else t).is_contiguous():
-            raise ValueError("caches must be contiguous")
-    for x, name in zip(k_cache.shape, ("number of layers", "number of blocks", "block size", "number of kv heads")[
-            5 - k_cache.dim():]):
-        _fits(x, name)
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("caches must be contiguous")
+    return shape
 
 
 def rope_store_kvcache(q, key, value, positions, frequencies, k_cache, v_cache, slot_mapping, q_norm=None,
@@ -744,48 +759,50 @@ def rope_store_kvcache(q, key, value, positions, frequencies, k_cache, v_cache, 
     (int32 [N], negatives skipped).  Returns the rotated q (out_q may be q itself)."""
     n, hq, hkv, d, qs, ks, oqs = _rope_args(q, key, positions, frequencies, q_norm, k_norm, out_q)
     vs = _rows(value, "value", n, hkv, d)
-    _bf16_caches(k_cache, v_cache)
-    nb, B, ch, cd = k_cache.shape
-    if (ch, cd) != (hkv, d):
+    nb, B, ch, cd = _bf16_pool(k_cache, v_cache)
+    if ch != hkv or cd != d:
         raise ValueError(f"caches must be [num_blocks, B, {hkv}, {d}]")
     _slots(slot_mapping, n)
-    ctx = _placed(stream, q, key, value, positions, frequencies.freqs, k_cache, v_cache, slot_mapping, q_norm, k_norm,
-                  out_q)
+    freqs = frequencies.freqs
+    ctx = _placed(stream, q, key, value, positions, freqs, k_cache, v_cache, slot_mapping, q_norm, k_norm, out_q)
     if ctx is not None:
         with ctx:
             return rope_store_kvcache(q, key, value, positions, frequencies, k_cache, v_cache, slot_mapping, q_norm,
                                       k_norm, eps, out_q)
     if out_q is None:
-        out_q = torch.empty(n, hq, d, dtype=torch.bfloat16, device=q.device)
+        out_q = q.new_empty((n, hq, d))
     _check(lib().pa_rope_store_kvcache(
         out_q.data_ptr(), oqs, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, positions.data_ptr(),
-        frequencies.freqs.data_ptr(), 2 * frequencies.freqs.shape[0], 1 if frequencies.interleaved else 0,
-        frequencies.gain, None if q_norm is None else q_norm.data_ptr(),
-        None if k_norm is None else k_norm.data_ptr(), float(eps),
-        k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, hq, hkv, d, nb * B, _raw_stream()),
-        "pa_rope_store_kvcache")
+        freqs.data_ptr(), 2 * freqs.shape[0], 1 if frequencies.interleaved else 0, frequencies.gain,
+        None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(), eps,
+        k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, hq, hkv, d, nb * B,
+        _stream_of(q.get_device())), "pa_rope_store_kvcache")
     return out_q
 
 
-def _int_rows(t, name, shape, dtype=torch.int32):
-    """Checks a contiguous tensor that may be None."""
+def _int_rows(t, name, shape, dtype=_I32):
+    """The address of a contiguous tensor of this shape and type; None stays None."""
     if t is None:
         return None
-    _need(t, dtype, name)
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{name} must be a tensor of {dtype}")
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
 
 
 def _tables(block_tables, context_lens, batch):
-    _need(block_tables, torch.int32, "block_tables")
-    _need(context_lens, torch.int32, "context_lens")
+    """Checks a batch's tables and lengths; returns the tables' width."""
+    if block_tables.dtype is not _I32 or context_lens.dtype is not _I32:
+        raise TypeError(f"block_tables and context_lens must be {_I32}")
     if block_tables.dim() != 2 or block_tables.shape[0] != batch or context_lens.shape != (batch,):
         raise ValueError("block_tables must be [batch, max_blocks] and context_lens [batch]")
     if not (block_tables.is_contiguous() and context_lens.is_contiguous()):
         raise ValueError("block_tables and context_lens must be contiguous")
-    _fits(batch, "batch")
-    _fits(block_tables.shape[1], "width of block_tables")
+    width = block_tables.shape[1]
+    if batch > 0x7fffffff or width > 0x7fffffff:
+        raise ValueError("batch or width of block_tables does not fit 32 bits")
+    return width
 
 
 class TreeMetadata(NamedTuple):
@@ -801,7 +818,7 @@ def tree_metadata(parents, context_lens, block_tables, block_size, draft_lens=No
     int32 [batch] counts all keys, the step's nodes the last of them; draft_lens
     int32 [batch] or None (num_drafts everywhere)."""
     batch = context_lens.shape[0] if isinstance(context_lens, torch.Tensor) and context_lens.dim() == 1 else -1
-    _tables(block_tables, context_lens, batch)
+    width = _tables(block_tables, context_lens, batch)
     if parents is None:
         if num_drafts is None:
             raise ValueError("num_drafts is needed without parents")
@@ -819,13 +836,12 @@ def tree_metadata(parents, context_lens, block_tables, block_size, draft_lens=No
     if ctx is not None:
         with ctx:
             return tree_metadata(parents, context_lens, block_tables, block_size, draft_lens, t)
-    dev, size = context_lens.device, max(t, 0)
-    out = TreeMetadata(torch.empty(batch, size, dtype=torch.int64, device=dev),
-                       torch.empty(batch * size, dtype=torch.int32, device=dev),
-                       torch.empty(batch * size, dtype=torch.int32, device=dev))
+    size = max(t, 0)
+    out = TreeMetadata(torch.empty(batch, size, dtype=torch.int64, device=context_lens.device),
+                       *context_lens.new_empty((2, batch * size)).unbind())
     _check(lib().pa_tree_metadata(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), par,
-                                  context_lens.data_ptr(), lens, block_tables.data_ptr(), block_tables.shape[1], batch,
-                                  t, int(block_size), _raw_stream()), "pa_tree_metadata")
+                                  context_lens.data_ptr(), lens, block_tables.data_ptr(), width, batch, t,
+                                  int(block_size), _stream_of(context_lens.get_device())), "pa_tree_metadata")
     return out
 
 
@@ -845,27 +861,30 @@ def decode_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask=None,
     of them (stored before the call); tree_mask int64 [batch, num_drafts]: bit j
     where the draft sees draft j (None: chains); draft_lens int32 [batch] or None.
     Returns out, of q's shape; zeros for padding."""
-    _bf16_caches(k_cache, v_cache)
-    nb, B, hkv, d = k_cache.shape
+    nb, B, hkv, d = _bf16_pool(k_cache, v_cache)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError(f"q must be [batch, num_drafts, Hq, {d}]")
-    batch, t, hq, _ = q.shape
-    _need(q, torch.bfloat16, "q")
+    shape = q.shape
+    batch, t, hq, qd = shape
+    if q.dtype is not _BF16:
+        raise TypeError(f"q must be {_BF16}, got {q.dtype}")
     s0, s1, s2, s3 = q.stride()
-    if q.shape[3] != d or (d > 1 and s3 != 1) or (hq > 1 and s2 != d) or (batch > 1 and t > 1 and s0 != t * s1):
+    if qd != d or (d > 1 and s3 != 1) or (hq > 1 and s2 != d) or (batch > 1 and t > 1 and s0 != t * s1):
         raise ValueError(f"q must be [batch, num_drafts, Hq, {d}], each token contiguous and all evenly spaced")
     qs = s1 if t > 1 else s0 if batch > 1 else hq * d
-    _tables(block_tables, context_lens, batch)
-    _fits(t, "num_drafts")
-    mask = _int_rows(tree_mask, "tree_mask", (batch, t), torch.int64)
+    width = _tables(block_tables, context_lens, batch)
+    if t > 0x7fffffff or hq > 0x7fffffff:
+        raise ValueError("num_drafts or number of q heads does not fit 32 bits")
+    mask = _int_rows(tree_mask, "tree_mask", (batch, t), _I64)
     lens = _int_rows(draft_lens, "draft_lens", (batch,))
     if out is not None:
-        _need(out, torch.bfloat16, "out")
-        if out.shape != q.shape or not out.is_contiguous():
+        if out.dtype is not _BF16:
+            raise TypeError(f"out must be {_BF16}, got {out.dtype}")
+        if out.shape != shape or not out.is_contiguous():
             raise ValueError("out must be contiguous and of q's shape")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
+    scale = 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale
     ctx = _placed(stream, q, k_cache, v_cache, block_tables, context_lens, tree_mask, draft_lens, workspace, out)
     if ctx is not None:
         with ctx:
@@ -874,11 +893,11 @@ def decode_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask=None,
     if workspace is None:
         workspace = decode_tree_workspace(hq, hkv, d, t, q.device)
     if out is None:
-        out = torch.empty(batch, t, hq, d, dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty(shape)
     _check(lib().pa_decode_tree(out.data_ptr(), q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
-                                block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), lens, mask,
-                                batch, t, hq, hkv, d, B, nb, scale, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _raw_stream()), "pa_decode_tree")
+                                block_tables.data_ptr(), width, context_lens.data_ptr(), lens, mask, batch, t, hq, hkv,
+                                d, B, nb, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                _stream_of(q.get_device())), "pa_decode_tree")
     return out
 
 
@@ -910,31 +929,32 @@ def verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, dr
     that the nodes' children were drawn from, or None (chosen candidates);
     draft_lens int32 [batch], nodes of each tree, or None.  `out`, a Verified of
     contiguous tensors, is filled and returned."""
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.bfloat16, torch.float32):
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (_BF16, _F32):
         raise TypeError("logits must be a bfloat16 or float32 tensor")
     ls = _flat_rows(logits, "logits")
     batch, n, vocab = logits.shape
-    for x, name in ((batch, "batch"), (n, "number of nodes"), (vocab, "vocabulary")):
-        _fits(x, name)
-    ptr = [_int_rows(t, name, shape, dtype) for t, name, shape, dtype in (
-        (tokens, "tokens", (batch, n), torch.int32), (parents, "parents", (batch, n), torch.int32),
-        (uniforms, "uniforms", (batch, n), torch.float32), (temperatures, "temperatures", (batch,), torch.float32),
-        (draft_lens, "draft_lens", (batch,), torch.int32))]
-    _need(exp_noise, torch.float32, "exp_noise")
-    if tuple(exp_noise.shape) != (batch, vocab) or (vocab > 1 and exp_noise.stride(1) != 1):
+    if batch > 0x7fffffff or n > 0x7fffffff or vocab > 0x7fffffff:
+        raise ValueError("batch, number of nodes or vocabulary does not fit 32 bits")
+    rows = (batch, n)
+    tok, par = _int_rows(tokens, "tokens", rows), _int_rows(parents, "parents", rows)
+    uni, temp = _int_rows(uniforms, "uniforms", rows, _F32), _int_rows(temperatures, "temperatures", (batch,), _F32)
+    lens = _int_rows(draft_lens, "draft_lens", (batch,))
+    if exp_noise.dtype is not _F32:
+        raise TypeError(f"exp_noise must be {_F32}, got {exp_noise.dtype}")
+    if exp_noise.shape != (batch, vocab) or (vocab > 1 and exp_noise.stride(1) != 1):
         raise ValueError("exp_noise must be [batch, vocab] with contiguous rows")
     es = exp_noise.stride(0) if batch > 1 else -(-vocab // 4) * 4
-    ps, pr = 0, 0
+    probs, ps, pr = None, 0, 0
     if draft_probs is not None:
-        _need(draft_probs, torch.float32, "draft_probs")
+        if draft_probs.dtype is not _F32:
+            raise TypeError(f"draft_probs must be {_F32}, got {draft_probs.dtype}")
         ps = _flat_rows(draft_probs, "draft_probs")
-        if draft_probs.shape[0] != batch or draft_probs.shape[2] != vocab or draft_probs.shape[1] < n - 1:
+        pb, pr, pv = draft_probs.shape
+        if pb != batch or pv != vocab or not n - 1 <= pr <= 0x7fffffff:
             raise ValueError("draft_probs must be [batch, at least num_nodes - 1, vocab]")
-        pr = draft_probs.shape[1]
-        _fits(pr, "rows of draft_probs")
+        probs = draft_probs.data_ptr()
     if out is not None:
-        for t, shape, name in ((out[0], (batch, n), "tokens"), (out[1], (batch, n), "nodes"),
-                               (out[2], (batch,), "counts")):
+        for t, shape, name in ((out[0], rows, "tokens"), (out[1], rows, "nodes"), (out[2], (batch,), "counts")):
             if _int_rows(t, f"out.{name}", shape) is None:
                 raise TypeError(f"out.{name} must be a CUDA tensor")
     ctx = _placed(stream, logits, tokens, parents, uniforms, exp_noise, temperatures, draft_probs, draft_lens,
@@ -944,14 +964,10 @@ def verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, dr
             return verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, draft_probs, draft_lens,
                                  out)
     if out is None:
-        out = Verified(torch.empty(batch, n, dtype=torch.int32, device=logits.device),
-                       torch.empty(batch, n, dtype=torch.int32, device=logits.device),
-                       torch.empty(batch, dtype=torch.int32, device=logits.device))
+        out = Verified(*tokens.new_empty((2, batch, n)).unbind(), tokens.new_empty(batch))
     _check(lib().pa_verify_drafts(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), logits.data_ptr(), ls,
-                                  1 if logits.dtype is torch.float32 else 0, ptr[0], ptr[1], ptr[2],
-                                  exp_noise.data_ptr(), es, ptr[3],
-                                  None if draft_probs is None else draft_probs.data_ptr(), ps, pr, ptr[4], batch, n,
-                                  vocab, _raw_stream()), "pa_verify_drafts")
+                                  1 if logits.dtype is _F32 else 0, tok, par, uni, exp_noise.data_ptr(), es, temp,
+                                  probs, ps, pr, lens, batch, n, vocab, _stream_of(logits.get_device())), "pa_verify_drafts")
     return out
 
 
@@ -962,24 +978,33 @@ def compact_kvcache(k_cache, v_cache, block_tables, context_lens, nodes, counts,
     [layers, num_blocks, B, Hkv, 128] for all layers in one call (each layer
     contiguous); nodes int32 [batch, num_nodes] and counts int32 [batch] as
     verify_drafts returns them."""
-    _bf16_caches(k_cache, v_cache, (4, 5))
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
-    nb, B, hkv, d = k_cache.shape[-4:]
-    strides = [t.stride(0) if t.dim() == 5 and layers > 1 else 0 for t in (k_cache, v_cache)]
+    layers, ks, vs = 1, 0, 0
+    if k_cache.dim() == 5 and v_cache.dim() == 5:
+        layers, ks, vs = k_cache.shape[0], k_cache.stride(0), v_cache.stride(0)
+        if v_cache.shape[0] != layers or layers > 0x7fffffff:
+            raise ValueError("k_cache and v_cache must have the same layers")
+        if layers == 0:
+            return
+        nb, B, hkv, d = _bf16_pool(k_cache[0], v_cache[0])
+        if layers > 1 and min(ks, vs) < nb * B * hkv * d:
+            raise ValueError("layers overlap")
+    else:
+        nb, B, hkv, d = _bf16_pool(k_cache, v_cache)
     if not isinstance(nodes, torch.Tensor) or nodes.dim() != 2:
         raise ValueError("nodes must be [batch, num_nodes]")
     batch, n = nodes.shape
-    _tables(block_tables, context_lens, batch)
-    _fits(n, "number of nodes")
-    ptr = [_int_rows(t, name, shape) for t, name, shape in (
-        (draft_lens, "draft_lens", (batch,)), (nodes, "nodes", (batch, n)), (counts, "counts", (batch,)))]
+    width = _tables(block_tables, context_lens, batch)
+    if n > 0x7fffffff:
+        raise ValueError("number of nodes does not fit 32 bits")
+    lens, node_ptr = _int_rows(draft_lens, "draft_lens", (batch,)), _int_rows(nodes, "nodes", (batch, n))
+    count_ptr = _int_rows(counts, "counts", (batch,))
     ctx = _placed(stream, k_cache, v_cache, block_tables, context_lens, nodes, counts, draft_lens)
     if ctx is not None:
         with ctx:
             return compact_kvcache(k_cache, v_cache, block_tables, context_lens, nodes, counts, draft_lens)
-    _check(lib().pa_compact_kvcache(k_cache.data_ptr(), strides[0], v_cache.data_ptr(), strides[1],
-                                    block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), *ptr,
-                                    batch, n, layers, hkv, d, B, nb, _raw_stream()), "pa_compact_kvcache")
+    _check(lib().pa_compact_kvcache(k_cache.data_ptr(), ks, v_cache.data_ptr(), vs, block_tables.data_ptr(), width,
+                                    context_lens.data_ptr(), lens, node_ptr, count_ptr, batch, n, layers, hkv, d, B, nb,
+                                    _stream_of(k_cache.get_device())), "pa_compact_kvcache")
 
 
 def set_checked(enabled: bool):

@@ -177,8 +177,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) compact_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 // Verification
 // ---------------------------------------------------------------------------
-constexpr int VT = 256;           // threads of a CTA
-constexpr int VW = VT / 32;
+constexpr int V_MAX_THREADS = 512;
 constexpr int V_MAX_CLUSTER = 8;
 constexpr float E_MIN = 1e-10f;   // the sampler's clamp of the exponential numbers
 
@@ -198,11 +197,7 @@ struct VerifyArgs {
     DevError *err;
 };
 
-struct __align__(8) Best {
-    float key;
-    int idx;
-};
-__device__ __forceinline__ bool better(Best a, Best b) { return a.key > b.key || (a.key == b.key && a.idx < b.idx); }
+__device__ __forceinline__ bool better(float ka, int ia, float kb, int ib) { return ka > kb || (ka == kb && ia < ib); }
 
 __device__ __forceinline__ uint4 ld16(const void *p) {
     uint4 v;
@@ -210,6 +205,32 @@ __device__ __forceinline__ uint4 ld16(const void *p) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
+}
+
+// Pairs of fp32.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max8(const float (&x)[8]) {
+    return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
 }
 
 // A logit as it counts: NaN as -inf, +inf as the largest number.
@@ -222,7 +243,7 @@ __device__ __forceinline__ float logit_at(const VerifyArgs &a, int64_t row, int 
     return tame(__uint_as_float((uint32_t)h << 16));
 }
 
-// Eight logits from index i on (a multiple of 8).
+// Eight logits from index i on (a multiple of 8), as they stand.
 template <bool FP32>
 struct Raw {
     uint4 w[FP32 ? 2 : 1];
@@ -246,165 +267,176 @@ struct Raw {
             x[0] = bf16lo(v.x); x[1] = bf16hi(v.x); x[2] = bf16lo(v.y); x[3] = bf16hi(v.y);
             x[4] = bf16lo(v.z); x[5] = bf16hi(v.z); x[6] = bf16lo(v.w); x[7] = bf16hi(v.w);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = tame(x[e]);
     }
 };
+__device__ __forceinline__ void as8(const uint4 &v, const uint4 &t, float (&x)[8]) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+    x[4] = __uint_as_float(t.x); x[5] = __uint_as_float(t.y); x[6] = __uint_as_float(t.z); x[7] = __uint_as_float(t.w);
+}
+
+// 2^((x - m) k) of eight logits.
+__device__ __forceinline__ void powers(float (&x)[8], float m, float k) {
+    const float2 nm = make_float2(-m, -m), kk = make_float2(k, k);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const float2 y = mul2(add2(make_float2(x[e], x[e + 1]), nm), kk);
+        x[e] = fast_exp2(y.x);
+        x[e + 1] = fast_exp2(y.y);
+    }
+}
 
 struct VerifyShared {
     int32_t parent[kMaxNodes], token[kMaxNodes];
     float u[kMaxNodes], x[kMaxNodes], q[kMaxNodes], p[kMaxNodes];  // of the children of the current node: logit, q, p
-    int32_t gone[kMaxNodes];                                       // tokens of the rejected candidates
-    float2 warp[VW];
-    float2 all[2][V_MAX_CLUSTER];  // the CTAs' values, written by each into all
+    float2 all[2][V_MAX_CLUSTER * V_MAX_THREADS / 32];             // the warps' values, each written into every CTA
 };
 
-// Reductions over the cluster.  Each CTA's value goes to every CTA of the
-// cluster; two buffers in turn, so one barrier each: a buffer is written again
-// only after the barrier that follows its last reading.
-template <typename F>
-__device__ __forceinline__ float2 cluster_reduce(VerifyShared &s, float2 v, int S, int &turn, F combine) {
+// Reductions over the cluster.  Each warp's value goes to every CTA; two buffers in
+// turn, so one barrier each: a buffer is written again only after the barrier that
+// follows its last reading.  Every thread has the result, and every CTA the same bits.
+template <int THREADS, typename F>
+__device__ __forceinline__ float2 cluster_reduce(VerifyShared &s, float2 v, int S, int rank, int &turn, float2 nothing,
+                                                 F combine) {
+    constexpr int W = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto warp_reduce = [&]() {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        float2 t;
-        t.x = __shfl_xor_sync(FULL, v.x, o);
-        t.y = __shfl_xor_sync(FULL, v.y, o);
-        v = combine(v, t);
-    }
-    if (lane == 0) s.warp[warp] = v;
-    __syncthreads();
-    v = s.warp[0];
-#pragma unroll
-    for (int w = 1; w < VW; ++w) v = combine(v, s.warp[w]);
+        for (int o = 16; o > 0; o >>= 1) {
+            float2 t;
+            t.x = __shfl_xor_sync(FULL, v.x, o);
+            t.y = __shfl_xor_sync(FULL, v.y, o);
+            v = combine(v, t);
+        }
+    };
+    warp_reduce();
+    float2 *mine = &s.all[turn][rank * W + warp];
     if (S == 1) {
+        if (lane == 0) *mine = v;
         __syncthreads();
-        return v;
+    } else {
+        if (lane < S) {
+            uint32_t dst;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_addr(mine)), "r"((uint32_t)lane));
+            asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(__float_as_uint(v.x)),
+                         "r"(__float_as_uint(v.y))
+                         : "memory");
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
-    if ((int)threadIdx.x < S) {
-        uint32_t rank, dst;
-        asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(dst)
-                     : "r"(smem_addr(&s.all[turn][rank])), "r"((uint32_t)threadIdx.x));
-        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(__float_as_uint(v.x)),
-                     "r"(__float_as_uint(v.y))
-                     : "memory");
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    v = s.all[turn][0];
-    for (int c = 1; c < S; ++c) v = combine(v, s.all[turn][c]);
+    v = nothing;
+    for (int i = lane; i < S * W; i += 32) v = combine(v, s.all[turn][i]);
+    warp_reduce();
     turn ^= 1;
     return v;
 }
 
-template <bool FP32, bool PROBS>
-__global__ void __launch_bounds__(VT) verify_kernel(const __grid_constant__ VerifyArgs a) {
+template <bool FP32, bool PROBS, int THREADS>
+__global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__ VerifyArgs a) {
     pdl_wait_then_release();
     __shared__ VerifyShared s;
     // The cluster's CTAs have started before any of them writes into another
     // (waited for ahead of the first reduction).
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    const int b = blockIdx.y, S = a.cluster, rank = blockIdx.x, tid = threadIdx.x;
+    const int b = blockIdx.y, S = a.cluster, rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const bool lead = rank == 0 && tid == 0;
     const float T = __ldg(a.temperatures + b);
     int n = a.lens ? __ldg(a.lens + b) : a.nodes;
+    if (tid < a.nodes) {  // (all of them: the loads need not wait for the length)
+        const int64_t at = (int64_t)b * a.nodes + tid;
+        const int p = a.parents ? __ldg(a.parents + at) : tid - 1, x = __ldg(a.tokens + at);
+        s.u[tid] = __ldg(a.u + at);
+        const bool bad_p = tid > 0 && (p < 0 || p >= tid), bad_x = tid > 0 && (x < 0 || x >= a.vocab);
+        if (rank == 0 && tid < n && n <= a.nodes) {
+            if (bad_p) record_error(a.err, PA_DEV_BAD_TREE, at);
+            if (bad_x) record_error(a.err, PA_DEV_BAD_TOKEN, at);
+        }
+        s.parent[tid] = tid == 0 || tid >= n || bad_p || bad_x ? -1 : p;  // nobody's child: never kept, never subtracted
+        s.token[tid] = x;
+        if (rank == 0) {
+            a.out_tokens[at] = -1;
+            a.out_nodes[at] = -1;
+        }
+    }
     const bool bad_t = !(T > 1e-10f), bad_n = n < 0 || n > a.nodes;
     if (lead && bad_t) record_error(a.err, PA_DEV_BAD_TEMPERATURE, b);
     if (lead && bad_n) record_error(a.err, PA_DEV_BAD_CONTEXT, b);
     if (bad_n || bad_t) n = 0;
-    if (rank == 0)
-        for (int i = tid; i < a.nodes; i += VT) {
-            a.out_tokens[(int64_t)b * a.nodes + i] = -1;
-            a.out_nodes[(int64_t)b * a.nodes + i] = -1;
-        }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (n == 0) {  // a padded row: uniform over the cluster
         if (lead) a.out_counts[b] = 0;
         return;
     }
-    for (int i = tid; i < n; i += VT) {
-        const int p = a.parents ? __ldg(a.parents + (int64_t)b * a.nodes + i) : i - 1;
-        const int x = __ldg(a.tokens + (int64_t)b * a.nodes + i);
-        const bool bad_p = i > 0 && (p < 0 || p >= i), bad_x = i > 0 && (x < 0 || x >= a.vocab);
-        if (rank == 0 && bad_p) record_error(a.err, PA_DEV_BAD_TREE, (long long)b * a.nodes + i);
-        if (rank == 0 && bad_x) record_error(a.err, PA_DEV_BAD_TOKEN, (long long)b * a.nodes + i);
-        s.parent[i] = i == 0 || bad_p || bad_x ? -1 : p;  // nobody's child: never kept, never subtracted
-        s.token[i] = x;
-        s.u[i] = __ldg(a.u + (int64_t)b * a.nodes + i);
-    }
-    // log2(e) / T, the float and what it leaves.
-    const double kd = fmax(1.4426950408889634 / (double)T, 1e-37);
-    const float k = (float)kd, k_lo = (float)(kd - (double)k);
+    const double kd = fmax(1.4426950408889634 / (double)T, 1e-37);  // log2(e) / T
+    const float k = (float)kd;
     // This CTA's chunk of a row: whole groups of 8 logits, then the ragged end.
     const int chunk = ((a.vocab + S - 1) / S + 7) & ~7;
     const int lo = min(a.vocab, rank * chunk), hi = min(a.vocab, lo + chunk);
     const int nvec = (hi - lo) / 8, tail = lo + 8 * nvec;
     const float *er = a.noise + (int64_t)b * a.noise_stride;
-    int turn = 0, cur = 0, count = 1, gone = 0;
+    int turn = 0, cur = 0, count = 1;
     float m = 0.f, inv_l = 0.f, sub = 0.f;  // of the current node: maximum, 1 / sum, S
+    unsigned long long gone = 0;            // its children that were rejected (without probabilities)
     __syncthreads();
     while (true) {
         // ---- maximum and sum of the current node's row
         const int64_t row = (int64_t)b * a.nodes + cur;
         const float *qr = PROBS ? a.probs + ((int64_t)b * a.probs_rows + cur) * a.probs_stride : nullptr;
-        if (tid < n && s.parent[tid] == cur) {  // (n <= 64: the children's own entries, meanwhile)
+        const unsigned long long kids =
+            (unsigned long long)__ballot_sync(FULL, lane < n && s.parent[lane] == cur) |
+            (n > 32 ? (unsigned long long)__ballot_sync(FULL, lane + 32 < n && s.parent[lane + 32] == cur) << 32 : 0ull);
+        const bool kid = tid < kMaxNodes && ((kids >> tid) & 1);
+        if (kid) {  // (the children's own entries, meanwhile)
             s.x[tid] = logit_at<FP32>(a, row, s.token[tid]);
             s.q[tid] = PROBS ? __ldg(qr + s.token[tid]) : 1.f;
         }
         float tm = -INFINITY, ts = 0.f;
-        auto add = [&](float top, const float *x, int num) {
-            if (top > tm) {
-                ts *= tm == -INFINITY ? 0.f : fast_exp2((tm - top) * k);
-                tm = top;
-            }
-            if (tm == -INFINITY) return;
-            for (int e = 0; e < num; ++e) {
-                const float d = x[e] - tm;
-                ts += fast_exp2(fmaf(d, k, d * k_lo));
-            }
+        auto raise = [&](float top) {
+            ts *= tm == -INFINITY ? 0.f : fast_exp2((tm - top) * k);
+            tm = top;
         };
-        for (int v0 = tid; v0 < nvec; v0 += 4 * VT) {
-            Raw<FP32> w[4];
+        constexpr int U = FP32 ? 4 : 8;  // vectors under way: 128 bytes a thread
+        for (int v0 = tid; v0 < nvec; v0 += U * THREADS) {
+            Raw<FP32> w[U];
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-                if (v0 + h * VT < nvec) w[h].load(a, row, lo + 8 * (v0 + h * VT));
+            for (int h = 0; h < U; ++h)
+                if (v0 + h * THREADS < nvec) w[h].load(a, row, lo + 8 * (v0 + h * THREADS));
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                if (v0 + h * VT >= nvec) break;
+            for (int h = 0; h < U; ++h) {
+                if (v0 + h * THREADS >= nvec) break;
                 float x[8];
                 w[h].get(x);
-                const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-                if (top > tm) {
-                    ts *= tm == -INFINITY ? 0.f : fast_exp2((tm - top) * k);
-                    tm = top;
-                }
+                float top = max8(x);  // (of the numbers among them)
+                if (top > tm) raise(fminf(top, FLT_MAX));
                 if (tm == -INFINITY) continue;
-                float y[4] = {0.f, 0.f, 0.f, 0.f};
+                powers(x, tm, k);
+                const float2 y = add2(add2(make_float2(x[0], x[1]), make_float2(x[2], x[3])),
+                                      add2(make_float2(x[4], x[5]), make_float2(x[6], x[7])));
+                float part = y.x + y.y;
+                if (!(part < INFINITY)) {  // a NaN or +inf among them
+                    w[h].get(x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float d = x[e] - tm;
-                    y[e & 3] += fast_exp2(fmaf(d, k, d * k_lo));
+                    for (int e = 0; e < 8; ++e) x[e] = tame(x[e]);
+                    powers(x, tm, k);
+                    part = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
                 }
-                ts += (y[0] + y[1]) + (y[2] + y[3]);
+                ts += part;
             }
         }
-        for (int i = tail + tid; i < hi; i += VT) {
+        for (int i = tail + tid; i < hi; i += THREADS) {
             const float x = logit_at<FP32>(a, row, i);
-            add(x, &x, 1);
+            if (x > tm) raise(x);
+            if (tm != -INFINITY) ts += fast_exp2((x - tm) * k);
         }
-        const float2 st = cluster_reduce(s, make_float2(tm, ts), S, turn, [&](float2 p, float2 q) {
-            const float mm = fmaxf(p.x, q.x);
-            if (mm == -INFINITY) return make_float2(mm, 0.f);
-            return make_float2(mm, (p.x == -INFINITY ? 0.f : p.y * fast_exp2((p.x - mm) * k)) +
-                                       (q.x == -INFINITY ? 0.f : q.y * fast_exp2((q.x - mm) * k)));
-        });
+        const float2 st = cluster_reduce<THREADS>(
+            s, make_float2(tm, ts), S, rank, turn, make_float2(-INFINITY, 0.f), [&](float2 p, float2 q) {
+                const float mm = fmaxf(p.x, q.x), ref = mm == -INFINITY ? 0.f : mm;
+                return make_float2(mm, p.y * fast_exp2((p.x - ref) * k) + q.y * fast_exp2((q.x - ref) * k));
+            });
         m = st.x == -INFINITY ? 0.f : st.x;
         inv_l = st.y > 0.f ? 1.f / st.y : 0.f;  // a row of -inf alone: every probability 0
         // p of the children, with the exponent in 64 bits.
-        if (tid < n && s.parent[tid] == cur) {
+        if (kid) {
             const double y = fmax((double)(s.x[tid] - m) * kd, -1000.0);
             const double whole = rint(y);
             s.p[tid] = ldexpf(exp2f((float)(y - whole)), (int)whole) * inv_l;
@@ -415,16 +447,16 @@ __global__ void __launch_bounds__(VT) verify_kernel(const __grid_constant__ Veri
         sub = 0.f;
         gone = 0;
         int next = -1;
-        for (int c = cur + 1; c < n; ++c) {
-            if (s.parent[c] != cur) continue;
+        for (unsigned long long todo = kids; todo; todo &= todo - 1) {
+            const int c = __ffsll(todo) - 1;
             const float p = s.p[c], q = s.q[c];
             float w;
             if (PROBS) {
                 w = fmaxf(fmaf(-sub, q, p), 0.f);
             } else {
                 w = p;
-                for (int g = 0; g < gone; ++g)
-                    if (s.gone[g] == s.token[c]) w = 0.f;  // a candidate given twice
+                for (unsigned long long g = gone; g; g &= g - 1)
+                    if (s.token[__ffsll(g) - 1] == s.token[c]) w = 0.f;  // a candidate given twice
             }
             if (s.u[c] * q * left < w) {
                 next = c;
@@ -432,42 +464,34 @@ __global__ void __launch_bounds__(VT) verify_kernel(const __grid_constant__ Veri
             }
             if (!PROBS) {
                 left = fmaxf(left - w, 0.f);
-                __syncthreads();  // the list has been read
-                if (tid == 0) s.gone[gone] = s.token[c];
-                ++gone;
-                __syncthreads();
+                gone |= 1ull << c;
                 continue;
             }
             sub += left;
-            bool more = false;
-            for (int d = c + 1; d < n; ++d) more = more || s.parent[d] == cur;
-            if (!more) break;
+            if (!(todo & (todo - 1))) break;  // the last child: nobody asks for s
             // s <- sum of max(p - S q, 0)
             float acc = 0.f;
-            for (int v = tid; v < nvec; v += VT) {
+            for (int v = tid; v < nvec; v += THREADS) {
                 Raw<FP32> w8;
                 const int i = lo + 8 * v;
                 w8.load(a, row, i);
                 const uint4 q0 = ld16(qr + i), q1 = ld16(qr + i + 4);
-                float x[8];
+                float x[8], qq[8];
                 w8.get(x);
-                const float qq[8] = {__uint_as_float(q0.x), __uint_as_float(q0.y), __uint_as_float(q0.z),
-                                     __uint_as_float(q0.w), __uint_as_float(q1.x), __uint_as_float(q1.y),
-                                     __uint_as_float(q1.z), __uint_as_float(q1.w)};
+                as8(q0, q1, qq);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = tame(x[e]);
+                powers(x, m, k);
                 float part = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float d = x[e] - m;
-                    part += fmaxf(fmaf(-sub, qq[e], fast_exp2(fmaf(d, k, d * k_lo)) * inv_l), 0.f);
-                }
+                for (int e = 0; e < 8; ++e) part += fmaxf(fmaf(-sub, qq[e], x[e] * inv_l), 0.f);
                 acc += part;
             }
-            for (int i = tail + tid; i < hi; i += VT) {
-                const float d = logit_at<FP32>(a, row, i) - m;
-                acc += fmaxf(fmaf(-sub, __ldg(qr + i), fast_exp2(fmaf(d, k, d * k_lo)) * inv_l), 0.f);
-            }
-            left = cluster_reduce(s, make_float2(acc, 0.f), S, turn,
-                                  [](float2 p, float2 q) { return make_float2(p.x + q.x, 0.f); }).x;
+            for (int i = tail + tid; i < hi; i += THREADS)
+                acc += fmaxf(fmaf(-sub, __ldg(qr + i), fast_exp2((logit_at<FP32>(a, row, i) - m) * k) * inv_l), 0.f);
+            left = cluster_reduce<THREADS>(s, make_float2(acc, 0.f), S, rank, turn, make_float2(0.f, 0.f),
+                                           [](float2 p, float2 q) { return make_float2(p.x + q.x, 0.f); })
+                       .x;
         }
         if (next < 0) break;
         if (lead) {
@@ -481,63 +505,83 @@ __global__ void __launch_bounds__(VT) verify_kernel(const __grid_constant__ Veri
     // ---- the last token: argmax w / E, of p / E where nothing is left of w
     const int64_t row = (int64_t)b * a.nodes + cur;
     const float *qr = PROBS && sub > 0.f ? a.probs + ((int64_t)b * a.probs_rows + cur) * a.probs_stride : nullptr;
-    Best best;
+    float key;
+    int idx;
     for (int all = 0;; ++all) {
         if (all) {
             sub = 0.f;
             qr = nullptr;
             gone = 0;
         }
-        best = {0.f, 0x7fffffff};
-        auto offer = [&](float w, float e, int i) {
-            const Best t = {__fdividef(w, fmaxf(e, E_MIN)), i};
-            if (!(t.key > 0.f) || !better(t, best)) return;
+        key = 0.f;
+        idx = 0x7fffffff;
+        auto offer = [&](float r, int i) {  // i ascends: the first of equals stays
+            if (!(r > key)) return;
             if (!PROBS)
-                for (int g = 0; g < gone; ++g)
-                    if (s.gone[g] == i) return;
-            best = t;
+                for (unsigned long long g = gone; g; g &= g - 1)
+                    if (s.token[__ffsll(g) - 1] == i) return;
+            key = r;
+            idx = i;
         };
-        for (int v = tid; v < nvec; v += VT) {
-            Raw<FP32> w8;
-            const int i = lo + 8 * v;
-            w8.load(a, row, i);
-            const uint4 e0 = ld16(er + i), e1 = ld16(er + i + 4);
-            uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
-            if (PROBS && qr) {
-                q0 = ld16(qr + i);
-                q1 = ld16(qr + i + 4);
-            }
-            float x[8];
-            w8.get(x);
-            const float ee[8] = {__uint_as_float(e0.x), __uint_as_float(e0.y), __uint_as_float(e0.z),
-                                 __uint_as_float(e0.w), __uint_as_float(e1.x), __uint_as_float(e1.y),
-                                 __uint_as_float(e1.z), __uint_as_float(e1.w)};
-            const float qq[8] = {__uint_as_float(q0.x), __uint_as_float(q0.y), __uint_as_float(q0.z),
-                                 __uint_as_float(q0.w), __uint_as_float(q1.x), __uint_as_float(q1.y),
-                                 __uint_as_float(q1.z), __uint_as_float(q1.w)};
+        constexpr int U = FP32 ? 1 : 2;
+        for (int v0 = tid; v0 < nvec; v0 += U * THREADS) {
+            Raw<FP32> w[U];
+            uint4 e0[U], e1[U], q0[U], q1[U];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float d = x[e] - m;
-                float w = fast_exp2(fmaf(d, k, d * k_lo)) * inv_l;
-                if (PROBS) w = fmaf(-sub, qq[e], w);
-                offer(w, ee[e], i + e);
+            for (int h = 0; h < U; ++h) {
+                const int i = lo + 8 * (v0 + h * THREADS);
+                if (v0 + h * THREADS >= nvec) break;
+                w[h].load(a, row, i);
+                e0[h] = ld16(er + i);
+                e1[h] = ld16(er + i + 4);
+                if (PROBS && qr) {
+                    q0[h] = ld16(qr + i);
+                    q1[h] = ld16(qr + i + 4);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < U; ++h) {
+                if (v0 + h * THREADS >= nvec) break;
+                float x[8], ee[8], qq[8];
+                w[h].get(x);
+                as8(e0[h], e1[h], ee);
+                powers(x, m, k);
+                // NaN (of a NaN logit, or +inf less the largest number): out of the question
+                // but for the latter, which counts as the maximum.
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (!(x[e] < INFINITY)) {
+                        float y[8];
+                        w[h].get(y);
+                        x[e] = fast_exp2((tame(y[e]) - m) * k);
+                    }
+                if (PROBS && qr) {
+                    as8(q0[h], q1[h], qq);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = fmaf(-sub, qq[e], x[e] * inv_l);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = __fdividef(x[e], fmaxf(ee[e], E_MIN));
+                if (max8(x) > key)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) offer(x[e], lo + 8 * (v0 + h * THREADS) + e);
             }
         }
-        for (int i = tail + tid; i < hi; i += VT) {
-            const float d = logit_at<FP32>(a, row, i) - m;
-            float w = fast_exp2(fmaf(d, k, d * k_lo)) * inv_l;
-            if (PROBS && qr) w = fmaf(-sub, __ldg(qr + i), w);
-            offer(w, __ldg(er + i), i);
+        for (int i = tail + tid; i < hi; i += THREADS) {
+            float w = fast_exp2((logit_at<FP32>(a, row, i) - m) * k);
+            if (PROBS && qr) w = fmaf(-sub, __ldg(qr + i), w * inv_l);
+            offer(__fdividef(w, fmaxf(__ldg(er + i), E_MIN)), i);
         }
-        const float2 r = cluster_reduce(s, make_float2(best.key, __int_as_float(best.idx)), S, turn, [](float2 p, float2 q) {
-            const Best x = {p.x, __float_as_int(p.y)}, y = {q.x, __float_as_int(q.y)};
-            return better(y, x) ? q : p;
-        });
-        best = {r.x, __float_as_int(r.y)};
-        if (best.key > 0.f || all || (sub == 0.f && gone == 0)) break;  // uniform over the cluster
+        const float2 r = cluster_reduce<THREADS>(s, make_float2(key, __int_as_float(idx)), S, rank, turn,
+                                                 make_float2(0.f, __int_as_float(0x7fffffff)), [](float2 p, float2 q) {
+                                                     return better(q.x, __float_as_int(q.y), p.x, __float_as_int(p.y)) ? q : p;
+                                                 });
+        key = r.x;
+        idx = __float_as_int(r.y);
+        if (key > 0.f || all || (sub == 0.f && gone == 0)) break;  // uniform over the cluster
     }
     if (lead) {
-        a.out_tokens[(int64_t)b * a.nodes + count - 1] = best.idx == 0x7fffffff ? 0 : best.idx;
+        a.out_tokens[(int64_t)b * a.nodes + count - 1] = idx == 0x7fffffff ? 0 : idx;
         a.out_nodes[(int64_t)b * a.nodes] = 0;
         a.out_counts[b] = count;
     }
@@ -551,12 +595,11 @@ int ctas_per_seq(int batch, int vocab, int sms) {
     return S;
 }
 
-template <bool FP32, bool PROBS>
+template <bool FP32, bool PROBS, int THREADS>
 pa_status launch_verify(VerifyArgs &a, cudaStream_t stream) {
-    a.cluster = ctas_per_seq(a.batch, a.vocab, sm_count());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.cluster, (unsigned)a.batch);
-    cfg.blockDim = dim3(VT);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -567,9 +610,18 @@ pa_status launch_verify(VerifyArgs &a, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<FP32, PROBS>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<FP32, PROBS, THREADS>, a);
     if (e != cudaSuccess) return cuda_fail(e, "verify_kernel");
     return check_launch("verify_kernel");
+}
+
+template <bool FP32, bool PROBS>
+pa_status launch_verify(VerifyArgs &a, cudaStream_t stream) {
+    const int sms = sm_count();
+    a.cluster = ctas_per_seq(a.batch, a.vocab, sms);
+    // Few CTAs: twice the threads.
+    return (int64_t)a.batch * a.cluster <= 2LL * sms ? launch_verify<FP32, PROBS, 512>(a, stream)
+                                                     : launch_verify<FP32, PROBS, 256>(a, stream);
 }
 
 }  // namespace
