@@ -729,9 +729,9 @@ def rope(q, k, positions, frequencies, q_norm=None, k_norm=None, eps=1e-6, out_q
         with ctx:
             return rope(q, k, positions, frequencies, q_norm, k_norm, eps, out_q, out_k)
     if out_q is None:
-        out_q = q.new_empty((n, hq, d))
+        out_q = torch.empty(n, hq, d, dtype=_BF16, device=q.device)
     if out_k is None:
-        out_k = k.new_empty((n, hkv, d))
+        out_k = torch.empty(n, hkv, d, dtype=_BF16, device=k.device)
     _check(lib().pa_rope(out_q.data_ptr(), oqs, out_k.data_ptr(), oks, q.data_ptr(), qs, k.data_ptr(), ks,
                          positions.data_ptr(), freqs.data_ptr(), 2 * freqs.shape[0],
                          1 if frequencies.interleaved else 0, frequencies.gain, None if q_norm is None else q_norm.data_ptr(),
@@ -770,7 +770,7 @@ def rope_store_kvcache(q, key, value, positions, frequencies, k_cache, v_cache, 
             return rope_store_kvcache(q, key, value, positions, frequencies, k_cache, v_cache, slot_mapping, q_norm,
                                       k_norm, eps, out_q)
     if out_q is None:
-        out_q = q.new_empty((n, hq, d))
+        out_q = torch.empty(n, hq, d, dtype=_BF16, device=q.device)
     _check(lib().pa_rope_store_kvcache(
         out_q.data_ptr(), oqs, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, positions.data_ptr(),
         freqs.data_ptr(), 2 * freqs.shape[0], 1 if frequencies.interleaved else 0, frequencies.gain,
@@ -836,9 +836,10 @@ def tree_metadata(parents, context_lens, block_tables, block_size, draft_lens=No
     if ctx is not None:
         with ctx:
             return tree_metadata(parents, context_lens, block_tables, block_size, draft_lens, t)
-    size = max(t, 0)
-    out = TreeMetadata(torch.empty(batch, size, dtype=torch.int64, device=context_lens.device),
-                       *context_lens.new_empty((2, batch * size)).unbind())
+    size, dev = max(t, 0), context_lens.device
+    out = TreeMetadata(torch.empty(batch, size, dtype=_I64, device=dev),
+                       torch.empty(batch * size, dtype=_I32, device=dev),
+                       torch.empty(batch * size, dtype=_I32, device=dev))
     _check(lib().pa_tree_metadata(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), par,
                                   context_lens.data_ptr(), lens, block_tables.data_ptr(), width, batch, t,
                                   int(block_size), _stream_of(context_lens.get_device())), "pa_tree_metadata")
@@ -893,7 +894,7 @@ def decode_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask=None,
     if workspace is None:
         workspace = decode_tree_workspace(hq, hkv, d, t, q.device)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
     _check(lib().pa_decode_tree(out.data_ptr(), q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
                                 block_tables.data_ptr(), width, context_lens.data_ptr(), lens, mask, batch, t, hq, hkv,
                                 d, B, nb, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -909,13 +910,14 @@ class Verified(NamedTuple):
 
 
 def _flat_rows(t, name):
-    """Elements between the rows of a [batch, rows, vocab] tensor, evenly spaced."""
+    """Shape of a [batch, rows, vocab] tensor, and elements between its rows, evenly spaced."""
     if t.dim() != 3:
         raise ValueError(f"{name} must have three dimensions")
     b, r, v = t.shape
-    if (v > 1 and t.stride(2) != 1) or (b > 1 and r > 1 and t.stride(0) != r * t.stride(1)):
+    s0, s1, s2 = t.stride()
+    if (v > 1 and s2 != 1) or (b > 1 and r > 1 and s0 != r * s1):
         raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
-    return t.stride(1) if r > 1 else t.stride(0) if b > 1 else -(-v // 8) * 8
+    return b, r, v, s1 if r > 1 else s0 if b > 1 else -(-v // 8) * 8
 
 
 def verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, draft_probs=None, draft_lens=None,
@@ -931,8 +933,7 @@ def verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, dr
     contiguous tensors, is filled and returned."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (_BF16, _F32):
         raise TypeError("logits must be a bfloat16 or float32 tensor")
-    ls = _flat_rows(logits, "logits")
-    batch, n, vocab = logits.shape
+    batch, n, vocab, ls = _flat_rows(logits, "logits")
     if batch > 0x7fffffff or n > 0x7fffffff or vocab > 0x7fffffff:
         raise ValueError("batch, number of nodes or vocabulary does not fit 32 bits")
     rows = (batch, n)
@@ -948,8 +949,7 @@ def verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, dr
     if draft_probs is not None:
         if draft_probs.dtype is not _F32:
             raise TypeError(f"draft_probs must be {_F32}, got {draft_probs.dtype}")
-        ps = _flat_rows(draft_probs, "draft_probs")
-        pb, pr, pv = draft_probs.shape
+        pb, pr, pv, ps = _flat_rows(draft_probs, "draft_probs")
         if pb != batch or pv != vocab or not n - 1 <= pr <= 0x7fffffff:
             raise ValueError("draft_probs must be [batch, at least num_nodes - 1, vocab]")
         probs = draft_probs.data_ptr()
@@ -964,7 +964,8 @@ def verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, dr
             return verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, draft_probs, draft_lens,
                                  out)
     if out is None:
-        out = Verified(*tokens.new_empty((2, batch, n)).unbind(), tokens.new_empty(batch))
+        out = Verified(torch.empty_like(tokens), torch.empty_like(tokens),
+                       torch.empty(batch, dtype=_I32, device=tokens.device))
     _check(lib().pa_verify_drafts(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), logits.data_ptr(), ls,
                                   1 if logits.dtype is _F32 else 0, tok, par, uni, exp_noise.data_ptr(), es, temp,
                                   probs, ps, pr, lens, batch, n, vocab, _stream_of(logits.get_device())), "pa_verify_drafts")
@@ -980,12 +981,16 @@ def compact_kvcache(k_cache, v_cache, block_tables, context_lens, nodes, counts,
     verify_drafts returns them."""
     layers, ks, vs = 1, 0, 0
     if k_cache.dim() == 5 and v_cache.dim() == 5:
-        layers, ks, vs = k_cache.shape[0], k_cache.stride(0), v_cache.stride(0)
-        if v_cache.shape[0] != layers or layers > 0x7fffffff:
-            raise ValueError("k_cache and v_cache must have the same layers")
-        if layers == 0:
-            return
-        nb, B, hkv, d = _bf16_pool(k_cache[0], v_cache[0])
+        layers, nb, B, hkv, d = shape = k_cache.shape
+        if k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16:
+            raise TypeError(f"caches must be {_BF16}, got {k_cache.dtype}, {v_cache.dtype}")
+        if v_cache.shape != shape or layers > 0x7fffffff:
+            raise ValueError("k_cache and v_cache must be of one shape, [layers, num_blocks, B, Hkv, 128]")
+        if not (k_cache.is_contiguous() and v_cache.is_contiguous()):  # then each layer has to be
+            for t in (k_cache, v_cache):
+                if layers > 0 and not t[0].is_contiguous():
+                    raise ValueError("each layer must be contiguous")
+        ks, vs = k_cache.stride(0), v_cache.stride(0)
         if layers > 1 and min(ks, vs) < nb * B * hkv * d:
             raise ValueError("layers overlap")
     else:

@@ -43,8 +43,8 @@ struct RopeArgs {
     const unsigned long long *freqs;
     const __nv_bfloat16 *wq, *wk;          // null: no norm
     float gain, eps;
-    int32_t tokens, Hq, Hkv, heads;        // heads: all that a token moves
-    int32_t rotary, parts;                 // parts: units per token
+    int32_t tokens, Hq, Hkv, groups;       // groups of four heads of a token: of q, k, and (store) v
+    int32_t rotary, span, parts;           // groups of a unit, units of a token
     DevError *err;
 };
 
@@ -70,10 +70,33 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(pack2bf(x[0], x[1]), pack2bf(x[2], x[3]), pack2bf(x[4], x[5]), pack2bf(x[6], x[7]));
 }
 
-// A unit is one token and U groups of four heads: its q heads, then its k heads,
-// then (store) its v heads.
-template <bool INTER, int U>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ RopeArgs a) {
+// Two fp32 at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// A unit is one token and `span` of its groups of four heads: those of q, then of k,
+// then (store) of v.  A head's output is X P + X' Q and Y R + Y' S, times the norm's
+// factor, with X and Y the lane's two chunks, X' and Y' the pairs' other halves
+// (the other chunk, or the neighbours), and P, Q, R, S the angles' cosines and sines
+// times gain and weight: made once per token for all heads of q, and of k.  U groups
+// are under way at a time.
+template <bool INTER, bool NORM, int U>
+__global__ void __launch_bounds__(ROPE_THREADS, 2) rope_kernel(const __grid_constant__ RopeArgs a) {
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31, l = lane & 7, grp = lane >> 3;
     const bool rot = 16 * l < a.rotary;
@@ -81,32 +104,22 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
     const int c1 = (INTER || !rot) ? 16 * l + 8 : a.rotary / 2 + 8 * l;
     const uint32_t nunits = (uint32_t)a.tokens * (uint32_t)a.parts;
     const uint32_t wstride = gridDim.x * (ROPE_THREADS / 32);
+    const int gq = (a.Hq + 3) >> 2, gk = (a.Hkv + 3) >> 2;
     // The two pairs whose angle this lane evaluates.
     unsigned long long f[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) f[e] = rot ? __ldg(a.freqs + 8 * l + 2 * grp + e) : 0ull;
     for (uint32_t unit = blockIdx.x * (ROPE_THREADS / 32) + (threadIdx.x >> 5); unit < nunits; unit += wstride) {
-        const uint32_t token = unit / (uint32_t)a.parts;
-        const int h0 = (int)(unit - token * (uint32_t)a.parts) * (4 * U) + grp;
+        const uint32_t token = unit / (uint32_t)a.parts, part = unit - token * (uint32_t)a.parts;
+        const int g0 = (int)part * a.span, g1 = min(g0 + a.span, a.groups);
         const long long pos = __ldg(a.positions + token);
         int64_t slot = 0;
         if (a.k_cache != nullptr) {
             slot = __ldg(a.slots + token);
             if (slot >= a.num_slots) {
-                if (h0 == 0 && l == 0) record_error(a.err, PA_DEV_BAD_SLOT, token);
+                if (g0 == 0 && lane == 0) record_error(a.err, PA_DEV_BAD_SLOT, token);
                 slot = -1;
             }
-        }
-        uint4 w0[U], w1[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + 4 * u;
-            if (h >= a.heads || (h >= a.Hq && slot < 0)) continue;
-            const __nv_bfloat16 *src = h < a.Hq            ? a.q + token * a.q_stride + (int64_t)h * ROPE_D
-                                       : h < a.Hq + a.Hkv ? a.k + token * a.k_stride + (int64_t)(h - a.Hq) * ROPE_D
-                                                          : a.v + token * a.v_stride + (int64_t)(h - a.Hq - a.Hkv) * ROPE_D;
-            w0[u] = ld_row16(src + c0);
-            w1[u] = ld_row16(src + c1);
         }
         float cs[8], sn[8];
         {
@@ -116,94 +129,141 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
                 const long long turns = (long long)((unsigned long long)pos * f[e]);  // in 2^-64, -1/2 .. 1/2
                 sincospif((float)turns * 0x1p-63f, &s2[e], &c2[e]);
             }
+            const float g = rot ? a.gain : 1.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int from = (e >> 1) * 8 + l;
-                const float g = rot ? a.gain : 1.f;
                 cs[e] = __shfl_sync(FULL, c2[e & 1], from) * g;
                 sn[e] = __shfl_sync(FULL, s2[e & 1], from) * g;
             }
         }
+#pragma unroll 1
+        for (int kind = 0; kind < 2; ++kind) {  // q, k
+            const int b0 = kind ? gq : 0, b1 = kind ? gq + gk : gq, heads = kind ? a.Hkv : a.Hq;
+            const int from = max(g0, b0) - b0, to = min(g1, b1) - b0;
+            if (from >= to || (kind && slot < 0)) continue;
+            const __nv_bfloat16 *src = kind ? a.k + token * a.k_stride : a.q + token * a.q_stride;
+            __nv_bfloat16 *dst = !kind                     ? a.out_q + token * a.out_q_stride
+                                 : a.k_cache == nullptr ? a.out_k + token * a.out_k_stride
+                                                        : a.k_cache + slot * a.Hkv * ROPE_D;
+            const __nv_bfloat16 *weight = kind ? a.wk : a.wq;
+            const bool norm = NORM && weight != nullptr;
+            float2 P[4], Q[4], R[4], S[4];
+            {
+                float g0w[8], g1w[8];
+                if (norm) {
+                    unpack8(__ldg(reinterpret_cast<const uint4 *>(weight + c0)), g0w);
+                    unpack8(__ldg(reinterpret_cast<const uint4 *>(weight + c1)), g1w);
+                }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + 4 * u;
-            const bool live = h < a.heads && (h < a.Hq || slot >= 0);
-            const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-            const __nv_bfloat16 *w = is_q ? a.wq : a.wk;
-            uint4 y0, y1;
-            float x[8], y[8];
-            if (live && !is_v) {
-                unpack8(w0[u], x);
-                unpack8(w1[u], y);
-            }
-            if (a.wq != nullptr || a.wk != nullptr) {  // uniform: the sum below is a warp's
-                float ss = 0.f;
-                if (live && !is_v)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(FULL, ss, o);
-                if (live && !is_v && w != nullptr) {
-                    const float r = rsqrtf(fmaf(ss, 1.f / ROPE_D, a.eps));
-                    float g0[8], g1[8];
-                    unpack8(__ldg(reinterpret_cast<const uint4 *>(w + c0)), g0);
-                    unpack8(__ldg(reinterpret_cast<const uint4 *>(w + c1)), g1);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] *= r * g0[e];
-                        y[e] *= r * g1[e];
+                for (int e = 0; e < 4; ++e) {
+                    const float w0 = norm ? g0w[2 * e] : 1.f, w1 = norm ? g0w[2 * e + 1] : 1.f;
+                    const float v0 = norm ? g1w[2 * e] : 1.f, v1 = norm ? g1w[2 * e + 1] : 1.f;
+                    if (!rot) {
+                        P[e] = make_float2(w0, w1);
+                        R[e] = make_float2(v0, v1);
+                        Q[e] = S[e] = make_float2(0.f, 0.f);
+                    } else if (INTER) {  // pairs e of the first chunk, e + 4 of the second
+                        P[e] = make_float2(w0 * cs[e], w1 * cs[e]);
+                        Q[e] = make_float2(-w1 * sn[e], w0 * sn[e]);
+                        R[e] = make_float2(v0 * cs[e + 4], v1 * cs[e + 4]);
+                        S[e] = make_float2(-v1 * sn[e + 4], v0 * sn[e + 4]);
+                    } else {
+                        P[e] = make_float2(w0 * cs[2 * e], w1 * cs[2 * e + 1]);
+                        Q[e] = make_float2(-v0 * sn[2 * e], -v1 * sn[2 * e + 1]);
+                        R[e] = make_float2(v0 * cs[2 * e], v1 * cs[2 * e + 1]);
+                        S[e] = make_float2(w0 * sn[2 * e], w1 * sn[2 * e + 1]);
                     }
                 }
             }
-            if (!live) continue;
-            if (is_v) {
-                y0 = w0[u];
-                y1 = w1[u];
-            } else {
-                if (rot) {
-                    if (INTER) {
+#pragma unroll 1
+            for (int g = from; g < to; g += U) {
+                uint4 w0[U], w1[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int h = 4 * (g + u) + grp;
+                    if (g + u < to && h < heads) {
+                        w0[u] = ld_row16(src + h * ROPE_D + c0);
+                        w1[u] = ld_row16(src + h * ROPE_D + c1);
+                    } else {
+                        w0[u] = w1[u] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int h = 4 * (g + u) + grp;
+                    float x[8], y[8];
+                    unpack8(w0[u], x);
+                    unpack8(w1[u], y);
+                    float r = 1.f;
+                    if (NORM && norm) {
+                        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            const float2 X = make_float2(x[e], x[e + 1]), Y = make_float2(y[e], y[e + 1]);
+                            ss = fma2(X, X, fma2(Y, Y, ss));
+                        }
+                        float t = ss.x + ss.y;
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1) t += __shfl_xor_sync(FULL, t, o);
+                        r = rsqrtf(fmaf(t, 1.f / ROPE_D, a.eps));
+                    }
+                    if (g + u >= to || h >= heads) continue;
+                    if (rot || (NORM && norm)) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float p0 = x[2 * e], p1 = x[2 * e + 1], q0 = y[2 * e], q1 = y[2 * e + 1];
-                            x[2 * e] = fmaf(p0, cs[e], -p1 * sn[e]);
-                            x[2 * e + 1] = fmaf(p1, cs[e], p0 * sn[e]);
-                            y[2 * e] = fmaf(q0, cs[e + 4], -q1 * sn[e + 4]);
-                            y[2 * e + 1] = fmaf(q1, cs[e + 4], q0 * sn[e + 4]);
+                            const float2 X = make_float2(x[2 * e], x[2 * e + 1]), Y = make_float2(y[2 * e], y[2 * e + 1]);
+                            float2 X1 = mul2(X, P[e]), Y1 = mul2(Y, R[e]);
+                            if (rot) {
+                                X1 = fma2(INTER ? make_float2(X.y, X.x) : Y, Q[e], X1);
+                                Y1 = fma2(INTER ? make_float2(Y.y, Y.x) : X, S[e], Y1);
+                            }
+                            if (NORM) {
+                                X1 = mul2(X1, make_float2(r, r));
+                                Y1 = mul2(Y1, make_float2(r, r));
+                            }
+                            x[2 * e] = X1.x;
+                            x[2 * e + 1] = X1.y;
+                            y[2 * e] = Y1.x;
+                            y[2 * e + 1] = Y1.y;
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float p0 = x[e], p1 = y[e];
-                            x[e] = fmaf(p0, cs[e], -p1 * sn[e]);
-                            y[e] = fmaf(p1, cs[e], p0 * sn[e]);
-                        }
+                        w0[u] = pack8(x);
+                        w1[u] = pack8(y);
                     }
+                    *reinterpret_cast<uint4 *>(dst + h * ROPE_D + c0) = w0[u];
+                    *reinterpret_cast<uint4 *>(dst + h * ROPE_D + c1) = w1[u];
                 }
-                y0 = pack8(x);
-                y1 = pack8(y);
             }
-            __nv_bfloat16 *dst;
-            if (is_q) {
-                dst = a.out_q + token * a.out_q_stride + (int64_t)h * ROPE_D;
-            } else if (a.k_cache == nullptr) {
-                dst = a.out_k + token * a.out_k_stride + (int64_t)(h - a.Hq) * ROPE_D;
-            } else if (!is_v) {
-                dst = a.k_cache + (slot * a.Hkv + (h - a.Hq)) * ROPE_D;
-            } else {
-                dst = a.v_cache + (slot * a.Hkv + (h - a.Hq - a.Hkv)) * ROPE_D;
-            }
-            *reinterpret_cast<uint4 *>(dst + c0) = y0;
-            *reinterpret_cast<uint4 *>(dst + c1) = y1;
+        }
+        // v: copied
+        if (a.v == nullptr || slot < 0) continue;
+        const __nv_bfloat16 *src = a.v + token * a.v_stride;
+        __nv_bfloat16 *dst = a.v_cache + slot * a.Hkv * ROPE_D;
+        const int from = max(g0, gq + gk) - (gq + gk), to = g1 - (gq + gk);
+        for (int h = 4 * from + grp; h < min(4 * to, a.Hkv); h += 4) {
+            const uint4 t0 = ld_row16(src + h * ROPE_D + 16 * l), t1 = ld_row16(src + h * ROPE_D + 16 * l + 8);
+            *reinterpret_cast<uint4 *>(dst + h * ROPE_D + 16 * l) = t0;
+            *reinterpret_cast<uint4 *>(dst + h * ROPE_D + 16 * l + 8) = t1;
         }
     }
 }
 
-template <bool INTER, int U>
-pa_status launch_rope(RopeArgs &a, int sms, cudaStream_t stream) {
-    a.parts = (a.heads + 4 * U - 1) / (4 * U);
+template <bool INTER, bool NORM, int U>
+pa_status launch_rope(const RopeArgs &a, int sms, cudaStream_t stream) {
     const int64_t units = (int64_t)a.tokens * a.parts, warps = ROPE_THREADS / 32;
-    const int64_t grid = std::min<int64_t>((units + warps - 1) / warps, 8LL * sms);
-    return launch_pdl(rope_kernel<INTER, U>, dim3((unsigned)grid), dim3(ROPE_THREADS), 0, stream, "rope_kernel", a);
+    const int64_t grid = std::min<int64_t>((units + warps - 1) / warps, 2LL * sms);
+    return launch_pdl(rope_kernel<INTER, NORM, U>, dim3((unsigned)grid), dim3(ROPE_THREADS), 0, stream, "rope_kernel", a);
+}
+
+template <bool INTER, bool NORM>
+pa_status launch_rope(RopeArgs &a, int sms, cudaStream_t stream) {
+    // Units of a whole token, its angles evaluated once, while there are warps enough
+    // for the GPU (16 per SM); smaller ones, down to one group of heads, below that.
+    // Whole tokens take four groups of heads at a time (16384 tokens 72.8 us, two at
+    // a time 74.2), parts of them two (512 tokens 5.4 us, four at a time 6.5).
+    a.span = (int)std::max<int64_t>(1, std::min<int64_t>(a.groups, (int64_t)a.tokens * a.groups / (16LL * sms)));
+    a.parts = (a.groups + a.span - 1) / a.span;
+    return a.parts == 1 ? launch_rope<INTER, NORM, 4>(a, sms, stream) : launch_rope<INTER, NORM, 2>(a, sms, stream);
 }
 
 // Checks and launches what the two entry points share.
@@ -227,12 +287,13 @@ pa_status run_rope(RopeArgs &a, int32_t head_dim, int32_t interleaved, pa_stream
         !aligned16(a.k_cache) || !aligned16(a.v_cache) || !aligned16(a.wq) || !aligned16(a.wk))
         return fail(PA_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
     if (reinterpret_cast<uintptr_t>(a.freqs) & 7u) return fail(PA_ERR_INVALID_ARG, "freqs must be 8-byte aligned");
-    if ((int64_t)a.tokens * ((a.heads + 3) / 4) > 0x7fffffff) return fail(PA_ERR_INVALID_ARG, "num_tokens too large");
+    if ((int64_t)a.tokens * a.groups > 0x7fffffff) return fail(PA_ERR_INVALID_ARG, "num_tokens too large");
     const int sms = sm_count();
     if (sms <= 0) return fail(PA_ERR_CUDA, "no CUDA device");
     a.err = device_error_ptr();
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return interleaved ? launch_rope<true, 4>(a, sms, s) : launch_rope<false, 4>(a, sms, s);
+    if (a.wq || a.wk) return interleaved ? launch_rope<true, true>(a, sms, s) : launch_rope<false, true>(a, sms, s);
+    return interleaved ? launch_rope<true, false>(a, sms, s) : launch_rope<false, false>(a, sms, s);
 }
 
 }  // namespace
@@ -300,7 +361,7 @@ pa_status pa_rope(void *out_q, int64_t out_q_row_stride, void *out_k, int64_t ou
     a.tokens = num_tokens;
     a.Hq = num_q_heads;
     a.Hkv = num_kv_heads;
-    a.heads = num_q_heads + num_kv_heads;
+    a.groups = (num_q_heads + 3) / 4 + (num_kv_heads + 3) / 4;
     a.rotary = rotary_dim;
     return run_rope(a, head_dim, interleaved, stream);
 }
@@ -339,7 +400,7 @@ pa_status pa_rope_store_kvcache(void *out_q, int64_t out_q_row_stride, const voi
     a.tokens = num_tokens;
     a.Hq = num_q_heads;
     a.Hkv = num_kv_heads;
-    a.heads = num_q_heads + 2 * num_kv_heads;
+    a.groups = (num_q_heads + 3) / 4 + 2 * ((num_kv_heads + 3) / 4);
     a.rotary = rotary_dim;
     return run_rope(a, head_dim, interleaved, stream);
 }

@@ -634,6 +634,14 @@ def test_compact_all_layers():
     pa.compact_kvcache(mixed[:, 0], mixed[:, 1], dev_i32(t.bt), dev_i32(t.ctx), dev_i32(nodes), dev_i32(counts))
     assert torch.equal(mixed[:, 0], whole[0]) and torch.equal(mixed[:, 1], whole[1])
     assert pa.get_device_error() == (0, 0)
+    args = [dev_i32(x) for x in (t.bt, t.ctx, nodes, counts)]
+    pa.compact_kvcache(whole[0][:0], whole[1][:0], *args)
+    with pytest.raises(ValueError):
+        pa.compact_kvcache(whole[0][:1].expand(2, -1, -1, -1, -1), whole[1][:2], *args)
+    with pytest.raises(ValueError):
+        pa.compact_kvcache(whole[0].transpose(1, 2), whole[1].transpose(1, 2), *args)
+    with pytest.raises(TypeError):
+        pa.compact_kvcache(whole[0].float(), whole[1].float(), *args)
 
 
 def test_compact_records_bad_paths_blocks_and_lengths():
