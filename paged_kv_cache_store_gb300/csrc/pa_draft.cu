@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
         inv_l = st.y > 0.f ? 1.f / st.y : 0.f;  // a row of -inf alone: every probability 0
         // p of the children, the exponent as a sum of two numbers.
         if (kid) {
-            const float d = fmaxf(s.x[tid] - m, -FLT_MAX), y = d * k, rest = fmaf(d, k, -y) + d * k_lo;
+            const float d = s.x[tid] - m, y = d * k, rest = fmaf(d, k, -y) + d * k_lo;
             const float whole = rintf(y);
             s.p[tid] = y > -1000.f ? ldexpf(exp2f((y - whole) + rest), (int)whole) * inv_l : 0.f;
         }
