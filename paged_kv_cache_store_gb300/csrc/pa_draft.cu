@@ -18,7 +18,11 @@
 // How: a thread-block cluster per sequence walks its tree, so only the rows of
 // the nodes that are reached are read.  A node costs one pass over its logits
 // (maximum and sum), one more per rejected child that has a sibling after it, and
-// the last node one pass for the draw (its logits from L2).
+// the last node one pass for the draw (its logits from L2).  What bounds it is the
+// latency of that chain of passes, a cluster barrier each: 64 drawn chains of 6 nodes
+// and 151936 bf16 logits take 49 us, 23 us of them the bytes of the rows reached at the
+// copy's rate.  Small rows and short chains are therefore read all at once, ahead of
+// the walk (kAtOnceBytes).
 #include <float.h>
 #include <math.h>
 
@@ -178,7 +182,15 @@ __global__ void __launch_bounds__(MOVE_THREADS) compact_kernel(const __grid_cons
 // Verification
 // ---------------------------------------------------------------------------
 constexpr int V_MAX_THREADS = 512;
-constexpr int V_MAX_CLUSTER = 8;
+constexpr int V_MAX_CLUSTER = 16;
+// A sequence's rows are read all at once, ahead of the walk, where a CTA's share of them
+// is small (what a row costs is then latency: 32 chains of 6 nodes and 8000 logits 17.2
+// us one after the other, 11.6 at once) or where they are a short drawn chain, whose
+// path holds most of them (64 x 6 x 151936: 52.3 and 48.9 us; 32 x 6: 38.6 and 32.2;
+// 128 x 4: 66.9 and 67.3).  Trees of that size have most rows off the path (64 x 8:
+// 47.5 us one after the other, 63.6 at once).
+constexpr int64_t kAtOnceBytes = 128 << 10;
+constexpr int kAtOnceChain = 8;
 constexpr float E_MIN = 1e-10f;   // the sampler's clamp of the exponential numbers
 
 struct VerifyArgs {
@@ -291,6 +303,10 @@ struct VerifyShared {
     float u[kMaxNodes], x[kMaxNodes], q[kMaxNodes], p[kMaxNodes];  // of the children of the current node: logit, q, p
     float2 all[2][V_MAX_CLUSTER * V_MAX_THREADS / 32];             // the warps' values, each written into every CTA
 };
+// With all rows read at once: of each node maximum and sum, by warp, by CTA, and 1 / sum.
+struct RowsShared {
+    float2 warps[kMaxNodes][V_MAX_THREADS / 32], ctas[kMaxNodes][V_MAX_CLUSTER], rows[kMaxNodes];
+};
 
 // Reductions over the cluster.  Each warp's value goes to every CTA; two buffers in
 // turn, so one barrier each: a buffer is written again only after the barrier that
@@ -332,10 +348,48 @@ __device__ __forceinline__ float2 cluster_reduce(VerifyShared &s, float2 v, int 
     return v;
 }
 
+// A thread's maximum and sum, of 2^((x - maximum) k).
+struct Sum {
+    float tm = -INFINITY, ts = 0.f;
+    __device__ __forceinline__ void raise(float top, float k) {
+        ts *= tm == -INFINITY ? 0.f : fast_exp2((tm - top) * k);
+        tm = top;
+    }
+    template <bool FP32>
+    __device__ __forceinline__ void add(const Raw<FP32> &w, float k) {
+        float x[8];
+        w.get(x);
+        const float top = max8(x);  // (of the numbers among them)
+        if (top > tm) raise(fminf(top, FLT_MAX), k);
+        if (tm == -INFINITY) return;
+        powers(x, tm, k);
+        const float2 y = add2(add2(make_float2(x[0], x[1]), make_float2(x[2], x[3])),
+                              add2(make_float2(x[4], x[5]), make_float2(x[6], x[7])));
+        float part = y.x + y.y;
+        if (!(part < INFINITY)) {  // a NaN or +inf among them
+            w.get(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = tame(x[e]);
+            powers(x, tm, k);
+            part = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+        }
+        ts += part;
+    }
+    __device__ __forceinline__ void add(float x, float k) {
+        if (x > tm) raise(x, k);
+        if (tm != -INFINITY) ts += fast_exp2((x - tm) * k);
+    }
+};
+__device__ __forceinline__ float2 join(float2 p, float2 q, float k) {
+    const float mm = fmaxf(p.x, q.x), ref = mm == -INFINITY ? 0.f : mm;
+    return make_float2(mm, p.y * fast_exp2((p.x - ref) * k) + q.y * fast_exp2((q.x - ref) * k));
+}
+
 template <bool FP32, bool PROBS, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const __grid_constant__ VerifyArgs a) {
     pdl_wait_then_release();
     __shared__ VerifyShared s;
+    __shared__ RowsShared rs;
     // The cluster's CTAs have started before any of them writes into another
     // (waited for ahead of the first reduction).
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -388,6 +442,89 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
     };
     constexpr int SIZE = FP32 ? 4 : 2;
     if (a.ahead) fetch(er, 4);
+    // p of a child, the exponent as a sum of two numbers.
+    auto prob = [&](float x, float m, float inv_l) -> float {
+        const float d = x - m, y = d * k, rest = fmaf(d, k, -y) + d * k_lo;
+        const float whole = rintf(y);
+        return y > -1000.f ? ldexpf(exp2f((y - whole) + rest), (int)whole) * inv_l : 0.f;
+    };
+    const bool chain = __syncthreads_and(tid == 0 || tid >= n || s.parent[tid] == tid - 1);
+    const bool all = (int64_t)n * chunk * SIZE <= kAtOnceBytes || (PROBS && chain && n <= kAtOnceChain);
+    if (all) {
+        if (tid < n && s.parent[tid] >= 0) {
+            const int p = s.parent[tid], x = s.token[tid];
+            s.x[tid] = logit_at<FP32>(a, (int64_t)b * a.nodes + p, x);
+            s.q[tid] = PROBS ? __ldg(a.probs + ((int64_t)b * a.probs_rows + p) * a.probs_stride + x) : 1.f;
+        }
+        // ---- maximum and sum of every row: the warps share the rows' pieces, in order
+        constexpr int W = THREADS / 32, U = FP32 ? 2 : 4, PIECE = 32 * U;  // vectors
+        const int warp = tid >> 5, pieces = max(1, (nvec + PIECE - 1) / PIECE), total = n * pieces;
+        for (int i = tid; i < n * W; i += THREADS) rs.warps[i / W][i % W] = make_float2(-INFINITY, 0.f);
+        __syncthreads();
+        const int t0 = total * warp / W, t1 = total * (warp + 1) / W;
+        int node = t0 / pieces, piece = t0 - node * pieces;
+        Sum sum;
+        for (int t = t0; t < t1; ++t) {
+            const int64_t row = (int64_t)b * a.nodes + node;
+            const int v0 = piece * PIECE + lane;
+            Raw<FP32> w[U];
+#pragma unroll
+            for (int h = 0; h < U; ++h)
+                if (v0 + 32 * h < nvec) w[h].load(a, row, lo + 8 * (v0 + 32 * h));
+#pragma unroll
+            for (int h = 0; h < U; ++h)
+                if (v0 + 32 * h < nvec) sum.add(w[h], k);
+            ++piece;
+            if (piece == pieces)
+                for (int i = tail + lane; i < hi; i += 32) sum.add(logit_at<FP32>(a, row, i), k);
+            if (piece == pieces || t + 1 == t1) {
+                float2 v = make_float2(sum.tm, sum.ts);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    float2 other;
+                    other.x = __shfl_xor_sync(FULL, v.x, o);
+                    other.y = __shfl_xor_sync(FULL, v.y, o);
+                    v = join(v, other, k);
+                }
+                if (lane == 0) rs.warps[node][warp] = v;
+                sum = Sum();
+                piece = 0;
+                ++node;
+            }
+        }
+        __syncthreads();
+        if (tid < n) {
+            float2 v = rs.warps[tid][0];
+#pragma unroll 1
+            for (int i = 1; i < W; ++i) v = join(v, rs.warps[tid][i], k);
+            if (S == 1) {
+                rs.ctas[tid][0] = v;
+            } else {
+                for (int c = 0; c < S; ++c) {
+                    uint32_t dst;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst)
+                                 : "r"(smem_addr(&rs.ctas[tid][rank])), "r"((uint32_t)c));
+                    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(__float_as_uint(v.x)),
+                                 "r"(__float_as_uint(v.y))
+                                 : "memory");
+                }
+            }
+        }
+        if (S > 1) {
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        }
+        if (tid < n) {
+            float2 v = rs.ctas[tid][0];
+            for (int c = 1; c < S; ++c) v = join(v, rs.ctas[tid][c], k);
+            rs.rows[tid] = make_float2(v.x == -INFINITY ? 0.f : v.x, v.y > 0.f ? 1.f / v.y : 0.f);
+        }
+        __syncthreads();
+        if (tid < n && s.parent[tid] >= 0) {
+            const float2 r = rs.rows[s.parent[tid]];
+            s.p[tid] = prob(s.x[tid], r.x, r.y);
+        }
+    }
     __syncthreads();
     while (true) {
         // ---- maximum and sum of the current node's row
@@ -396,66 +533,40 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
         const unsigned long long kids =
             (unsigned long long)__ballot_sync(FULL, lane < n && s.parent[lane] == cur) |
             (n > 32 ? (unsigned long long)__ballot_sync(FULL, lane + 32 < n && s.parent[lane + 32] == cur) << 32 : 0ull);
-        const bool kid = tid < kMaxNodes && ((kids >> tid) & 1);
-        if (kid) {  // (the children's own entries, meanwhile)
-            s.x[tid] = logit_at<FP32>(a, row, s.token[tid]);
-            s.q[tid] = PROBS ? __ldg(qr + s.token[tid]) : 1.f;
-        }
-        if (a.ahead && kids)
-            fetch(static_cast<const char *>(a.logits) +
-                      ((int64_t)b * a.nodes + __ffsll(kids) - 1) * a.logits_stride * SIZE, SIZE);
-        float tm = -INFINITY, ts = 0.f;
-        auto raise = [&](float top) {
-            ts *= tm == -INFINITY ? 0.f : fast_exp2((tm - top) * k);
-            tm = top;
-        };
-        constexpr int U = FP32 ? 4 : 5;  // vectors under way
-        for (int v0 = tid; v0 < nvec; v0 += U * THREADS) {
-            Raw<FP32> w[U];
-#pragma unroll
-            for (int h = 0; h < U; ++h)
-                if (v0 + h * THREADS < nvec) w[h].load(a, row, lo + 8 * (v0 + h * THREADS));
-#pragma unroll
-            for (int h = 0; h < U; ++h) {
-                if (v0 + h * THREADS >= nvec) break;
-                float x[8];
-                w[h].get(x);
-                float top = max8(x);  // (of the numbers among them)
-                if (top > tm) raise(fminf(top, FLT_MAX));
-                if (tm == -INFINITY) continue;
-                powers(x, tm, k);
-                const float2 y = add2(add2(make_float2(x[0], x[1]), make_float2(x[2], x[3])),
-                                      add2(make_float2(x[4], x[5]), make_float2(x[6], x[7])));
-                float part = y.x + y.y;
-                if (!(part < INFINITY)) {  // a NaN or +inf among them
-                    w[h].get(x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = tame(x[e]);
-                    powers(x, tm, k);
-                    part = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-                }
-                ts += part;
+        if (all) {
+            m = rs.rows[cur].x;
+            inv_l = rs.rows[cur].y;
+        } else {
+            const bool kid = tid < kMaxNodes && ((kids >> tid) & 1);
+            if (kid) {  // (the children's own entries, meanwhile)
+                s.x[tid] = logit_at<FP32>(a, row, s.token[tid]);
+                s.q[tid] = PROBS ? __ldg(qr + s.token[tid]) : 1.f;
             }
+            if (a.ahead && kids)
+                fetch(static_cast<const char *>(a.logits) +
+                          ((int64_t)b * a.nodes + __ffsll(kids) - 1) * a.logits_stride * SIZE, SIZE);
+            Sum sum;
+            constexpr int U = FP32 ? 4 : 5;  // vectors under way
+            for (int v0 = tid; v0 < nvec; v0 += U * THREADS) {
+                Raw<FP32> w[U];
+#pragma unroll
+                for (int h = 0; h < U; ++h)
+                    if (v0 + h * THREADS < nvec) w[h].load(a, row, lo + 8 * (v0 + h * THREADS));
+#pragma unroll
+                for (int h = 0; h < U; ++h) {
+                    if (v0 + h * THREADS >= nvec) break;
+                    sum.add(w[h], k);
+                }
+            }
+            for (int i = tail + tid; i < hi; i += THREADS) sum.add(logit_at<FP32>(a, row, i), k);
+            const float2 st = cluster_reduce<THREADS>(s, make_float2(sum.tm, sum.ts), S, rank, turn,
+                                                      make_float2(-INFINITY, 0.f),
+                                                      [&](float2 p, float2 q) { return join(p, q, k); });
+            m = st.x == -INFINITY ? 0.f : st.x;
+            inv_l = st.y > 0.f ? 1.f / st.y : 0.f;  // a row of -inf alone: every probability 0
+            if (kid) s.p[tid] = prob(s.x[tid], m, inv_l);
+            __syncthreads();
         }
-        for (int i = tail + tid; i < hi; i += THREADS) {
-            const float x = logit_at<FP32>(a, row, i);
-            if (x > tm) raise(x);
-            if (tm != -INFINITY) ts += fast_exp2((x - tm) * k);
-        }
-        const float2 st = cluster_reduce<THREADS>(
-            s, make_float2(tm, ts), S, rank, turn, make_float2(-INFINITY, 0.f), [&](float2 p, float2 q) {
-                const float mm = fmaxf(p.x, q.x), ref = mm == -INFINITY ? 0.f : mm;
-                return make_float2(mm, p.y * fast_exp2((p.x - ref) * k) + q.y * fast_exp2((q.x - ref) * k));
-            });
-        m = st.x == -INFINITY ? 0.f : st.x;
-        inv_l = st.y > 0.f ? 1.f / st.y : 0.f;  // a row of -inf alone: every probability 0
-        // p of the children, the exponent as a sum of two numbers.
-        if (kid) {
-            const float d = s.x[tid] - m, y = d * k, rest = fmaf(d, k, -y) + d * k_lo;
-            const float whole = rintf(y);
-            s.p[tid] = y > -1000.f ? ldexpf(exp2f((y - whole) + rest), (int)whole) * inv_l : 0.f;
-        }
-        __syncthreads();
         // ---- its children in order
         float left = 1.f;  // s
         sub = 0.f;
@@ -514,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
         }
         ++count;
         cur = next;
-        __syncthreads();  // the children's entries are written again
+        if (!all) __syncthreads();  // the children's entries are written again
     }
     // ---- the last token: argmax w / E, of p / E where nothing is left of w
     const int64_t row = (int64_t)b * a.nodes + cur;
@@ -602,11 +713,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
 }
 
 // CTAs per sequence: as many as leave all sequences room to run at once (1024
-// threads per SM, with a tenth to spare for clusters that do not fit), at most 8 (a
-// portable cluster) and 2048 logits a CTA at least.
+// threads per SM, with a tenth to spare for clusters that do not fit), at most 8 and
+// 2048 logits a CTA at least; 16 (no portable size) for up to four sequences, where one
+// SM's loads and exponentials are what a row waits for (1 x 6 x 151936: 17.4 us with
+// 8, 14.9 with 16; 4 x 32: 20.1 and 16.5; but 8 x 32: 26.0 and 27.7).
 int ctas_per_seq(int batch, int vocab, int sms) {
     int S = 1;
-    while (S < V_MAX_CLUSTER && 20LL * batch * S <= 36LL * sms && vocab / (2 * S) >= 2048) S *= 2;
+    if (32LL * batch <= sms && vocab / 16 >= 2048) return V_MAX_CLUSTER;
+    while (S < 8 && 20LL * batch * S <= 36LL * sms && vocab / (2 * S) >= 2048) S *= 2;
     return S;
 }
 
@@ -625,6 +739,11 @@ pa_status launch_verify(VerifyArgs &a, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    if (a.cluster > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(verify_kernel<FP32, PROBS, THREADS>,
+                                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return cuda_fail(e, "verify_kernel");
+    }
     const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<FP32, PROBS, THREADS>, a);
     if (e != cudaSuccess) return cuda_fail(e, "verify_kernel");
     return check_launch("verify_kernel");
@@ -638,8 +757,8 @@ pa_status launch_verify(VerifyArgs &a, cudaStream_t stream) {
     // the GPU (64 sequences 52 us without, 56 with; 16: 28.8 and 27.3).
     a.ahead = 8LL * a.batch <= sms;
     // Few CTAs: twice the threads.
-    return (int64_t)a.batch * a.cluster <= 2LL * sms ? launch_verify<FP32, PROBS, 512>(a, stream)
-                                                     : launch_verify<FP32, PROBS, 256>(a, stream);
+    const bool few = (int64_t)a.batch * a.cluster <= 2LL * sms;
+    return few ? launch_verify<FP32, PROBS, 512>(a, stream) : launch_verify<FP32, PROBS, 256>(a, stream);
 }
 
 }  // namespace

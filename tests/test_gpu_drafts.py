@@ -458,6 +458,46 @@ def test_verify_batches(batch):
     check_verify(verify_case(batch, batch, 4, 20011, torch.bfloat16, batch % 2 == 0))
 
 
+@pytest.mark.parametrize("batch,T,vocab,chain,drawn,dtype", [
+    (1, 8, 151936, True, True, torch.bfloat16),      # a short drawn chain: its rows at once
+    (3, 9, 151936, True, True, torch.bfloat16),      # one node more: one after the other
+    (5, 8, 151936, True, False, torch.bfloat16), (2, 8, 151936, False, True, torch.float32),
+    (40, 6, 50021, True, True, torch.float32), (5, 33, 40000, False, False, torch.bfloat16),
+    (4, 64, 32768, False, True, torch.bfloat16), (20, 64, 1100, False, True, torch.float32),
+    (20, 64, 1027, False, False, torch.bfloat16)])
+def test_verify_rows_at_once_and_one_after_the_other(batch, T, vocab, chain, drawn, dtype):
+    check_verify(verify_case(batch + T, batch, T, vocab, dtype, drawn, chain=chain, close=0.1 if chain else 0.3))
+
+
+def test_verify_a_sequence_has_the_same_result_in_either_way():
+    """Trees and chains, long and short ones, in one batch; and a bad node, which leaves no chain."""
+    s = verify_case(61, 6, 12, 40000, torch.bfloat16, True, chain=True, close=0.1,
+                    lens=np.array([8, 9, 12, 1, 0, 8], np.int32))
+    s["parents"][2, 6:] = 3
+    counts = check_verify(s)
+    assert counts[:2].max() > 2
+    s["parents"][5, 7] = 9                    # past the node itself: out of the tree
+    r = run_verify(s)
+    assert pa.get_device_error() == (pa.PA_DEV_BAD_TREE, 5 * 12 + 7)
+    t = dict(s, lens=np.array([8, 9, 12, 1, 0, 7], np.int32))
+    want = run_verify(t)
+    assert all(torch.equal(x, y) for x, y in zip(r, want))
+
+
+def test_verify_masked_logits_of_many_rows():
+    """The same masks where rows are read one after the other."""
+    low = float(torch.finfo(torch.bfloat16).min)
+    for mask in (-np.inf, low):
+        for dtype in (torch.bfloat16, torch.float32):
+            s = verify_case(62, 6, 64, 1203, dtype, False)
+            s["logits"][:, :, ::3] = mask
+            s["logits"][0] = mask
+            s["logits"][1, :, 1:] = mask
+            s["logits"][2, :, 5] = float("nan")
+            s["logits"][3, :, 7] = float("inf")
+            check_verify(s)
+
+
 def test_verify_many_siblings():
     """Residuals of many rejected children, drawn and chosen: all under the root."""
     for drawn in (True, False):
