@@ -710,7 +710,7 @@ PA_API pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, 
  *   draft_lens   int32 [batch], nodes of each sequence (0: padding, count 0), or NULL.
  * NaN logits count as -inf, +inf as the largest number.  num_nodes <= 64, batch <=
  * 65535, vocab <= 2^30; logits, exp_noise and draft_probs 16-byte aligned.  A small
- * temperature (1e-6) gives greedy verification.
+ * temperature (1e-6) gives greedy verification.  The outputs overlap no input.
  */
 PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *out_nodes, int32_t *out_counts, const void *logits,
                                   int64_t logits_row_stride, int32_t logits_is_fp32, const int32_t *tokens,
@@ -726,7 +726,8 @@ PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *out_nodes, int32
  * written.  nodes / counts are pa_verify_drafts' out_nodes / out_counts: nodes[b][0]
  * = 0, ascending, below n; the first one that is not ends its row's moves
  * (PA_DEV_BAD_TREE).  The context is then base + counts[b] keys long.  Rows of other
- * positions stay as they are.  A block id outside [0, num_blocks): that row is not
+ * positions stay as they are.  The rows from base on are the sequence's own: no other
+ * sequence of the call holds their slots (a shared prefix lies before them).  A block id outside [0, num_blocks): that row is not
  * moved (PA_DEV_BAD_BLOCK).
  *   k_cache, v_cache  the first layer's pools; the next layer's follow
  *                     k_layer_stride / v_layer_stride elements on (multiples of 8).

@@ -734,9 +734,9 @@ def rope(q, k, positions, frequencies, q_norm=None, k_norm=None, eps=1e-6, out_q
         out_k = torch.empty(n, hkv, d, dtype=_BF16, device=k.device)
     _check(lib().pa_rope(out_q.data_ptr(), oqs, out_k.data_ptr(), oks, q.data_ptr(), qs, k.data_ptr(), ks,
                          positions.data_ptr(), freqs.data_ptr(), 2 * freqs.shape[0],
-                         1 if frequencies.interleaved else 0, frequencies.gain, None if q_norm is None else q_norm.data_ptr(),
-                         None if k_norm is None else k_norm.data_ptr(), eps, n, hq, hkv, d, _stream_of(q.get_device())),
-           "pa_rope")
+                         1 if frequencies.interleaved else 0, frequencies.gain,
+                         None if q_norm is None else q_norm.data_ptr(), None if k_norm is None else k_norm.data_ptr(),
+                         eps, n, hq, hkv, d, _stream_of(q.get_device())), "pa_rope")
     return out_q, out_k
 
 
@@ -968,7 +968,8 @@ def verify_drafts(logits, tokens, parents, uniforms, exp_noise, temperatures, dr
                        torch.empty(batch, dtype=_I32, device=tokens.device))
     _check(lib().pa_verify_drafts(out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), logits.data_ptr(), ls,
                                   1 if logits.dtype is _F32 else 0, tok, par, uni, exp_noise.data_ptr(), es, temp,
-                                  probs, ps, pr, lens, batch, n, vocab, _stream_of(logits.get_device())), "pa_verify_drafts")
+                                  probs, ps, pr, lens, batch, n, vocab, _stream_of(logits.get_device())),
+           "pa_verify_drafts")
     return out
 
 

@@ -19,8 +19,17 @@
 // Of the 128 rows of an MMA only the live ones are loaded and read back; the
 // others hold whatever the memory held, which cannot reach a live row.
 //
-// An item cut between CTAs leaves (m, l, o) in fp32 in the workspace; the warp
-// that arrives last at its 32 rows combines the parts in order.
+// An item cut between CTAs leaves (m, l, o) in fp32 in the workspace.  After the
+// walk each CTA counts its parts in; the one whose part completes eight in a row
+// combines those, in order, and the last of such groups the groups, so that the
+// result does not depend on who comes last.
+//
+// What bounds it: up to 128 rows per kv head the bytes of K and V (Qwen3-8B shape,
+// 256 sequences x 4 drafts: 264 us, 6.6 TB/s); two row tiles the chain of products
+// and softmax (64 drafts over 8 x 32768 keys: 252 us, 1.09 PFLOP/s, 64 % of the
+// bytes' floor), in which a product's 64 keys re-read 128 rows of Q from shared
+// memory.  Products of 128 keys halve that but leave one score buffer a row tile:
+// 288 us.
 //
 // l is summed from the rounded P that the product uses, so that the weights sum
 // to one as they are.
@@ -238,8 +247,8 @@ constexpr int kFan = 8;  // parts combined at a time
 
 // Combines parts p0, p0 + step, ... < p1 of a job's rows.  `final`: writes the rows out;
 // otherwise leaves the combined part in p0's place.  Eight warps, w of them; four rows
-// per warp and four parts at a time, 16 row loads in flight.  A part's m of -inf has seen nothing; NaN
-// in l or o goes on.
+// per warp and four parts at a time, 16 row loads in flight.  A part's m of -inf has
+// seen nothing; NaN in l or o goes on.
 // A call of its own, with scalars alone: inlined, or with the arguments' address
 // taken, it costs the softmax loop its registers (64 drafts 311 -> 350 us).
 struct Merge {
@@ -784,7 +793,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (wlive) {
                 const float inv = !whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;  // a row that sees nothing: zeros
                 const int gr = s.blk * BLOCK + row0 + row;  // row of the (sequence, kv head)
-                __nv_bfloat16 *dst = a.out + (((int64_t)s.b * a.drafts + (gr >> a.shift)) * a.Hq + s.g * a.G + (gr & (a.G - 1))) * D;
+                __nv_bfloat16 *dst =
+                    a.out + (((int64_t)s.b * a.drafts + (gr >> a.shift)) * a.Hq + s.g * a.G + (gr & (a.G - 1))) * D;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
@@ -818,7 +828,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // What was taken out of V: added to the rows that see it.
                 const int lo = max(0, s.t0 * TILE - first), hi = min(n, s.t1 * TILE - first);  // drafts of the segment
                 const int gr = s.blk * BLOCK + row0 + row;
-                void *at = whole ? static_cast<void *>(a.out + (((int64_t)s.b * a.drafts + (gr >> a.shift)) * a.Hq + s.g * a.G + (gr & (a.G - 1))) * D)
+                const int64_t head = ((int64_t)s.b * a.drafts + (gr >> a.shift)) * a.Hq + s.g * a.G + (gr & (a.G - 1));
+                void *at = whole ? static_cast<void *>(a.out + head * D)
                                  : static_cast<void *>(slot + (size_t)(row0 + row) * D);
                 add_hidden(at, whole, mine ? m64 : 0ull, a.v_cache + (int64_t)s.g * D, (int64_t)a.Hkv * D,
                            a.bt + (int64_t)s.b * a.max_blocks, a.block_size, a.num_blocks, first, lo, hi, lane);
@@ -929,7 +940,8 @@ Layout layout_of(int drafts, int G) {
 std::atomic<int> g_attr_done[64][2];
 
 template <bool PAIR>
-pa_status launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const TreeArgs &a, int grid, cudaStream_t stream) {
+pa_status launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const TreeArgs &a,
+                      int grid, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");

@@ -264,3 +264,53 @@ def test_infinite_temperatures_and_numbers_at_their_ends():
                          torch.from_numpy(noise).cuda(), torch.full((3,), float("inf"), device="cuda"))
     # Equal probabilities to all but the -inf: token 0 is never kept, 3 is at u = 0.
     assert r.tokens.tolist() == [[17, -1], [3, 17], [17, -1]] and r.counts.tolist() == [1, 2, 1]
+
+
+@pytest.mark.parametrize("batch,n,vocab", [(2, 12, 40000), (3, 5, 40000), (12, 6, 20000)])
+def test_verification_captured_and_on_two_streams_at_once(batch, n, vocab):
+    """Wide clusters too: replays follow what the buffers hold, and calls on two
+    streams at once do not meet."""
+    def inputs(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        logits = torch.randn(batch, n, vocab, device="cuda", generator=g) * 3
+        q = torch.softmax(logits[:, :n - 1] + torch.randn(batch, n - 1, vocab, device="cuda", generator=g) * 0.3, -1)
+        tok = torch.zeros(batch, n, dtype=torch.int32, device="cuda")
+        for c in range(1, n):
+            tok[:, c] = torch.multinomial(q[:, c - 1], 1, generator=g)[:, 0].int()
+        return [logits, tok, torch.rand(batch, n, device="cuda", generator=g),
+                torch.empty(batch, vocab, device="cuda").exponential_(generator=g),
+                torch.ones(batch, device="cuda"), q]
+
+    def run(x, out=None):
+        return pa.verify_drafts(x[0], x[1], None, x[2], x[3], x[4], draft_probs=x[5], out=out)
+
+    sets = [inputs(s) for s in (1, 2, 3)]
+    want = [run(x) for x in sets]
+    assert any(int(w.counts.max()) > 2 for w in want)
+    held = [t.clone() for t in sets[0]]
+    out = pa.Verified(*(torch.empty_like(t) for t in want[0]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(held, out)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            run(held, out)
+    torch.cuda.current_stream().wait_stream(side)
+    for x, w in zip(sets, want):
+        for t, s in zip(held, x):
+            t.copy_(s)
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[] for _ in sets]
+    for _ in range(8):
+        for i, (s, x) in enumerate(zip(streams, sets)):
+            with torch.cuda.stream(s):
+                got[i].append(run(x))
+    torch.cuda.synchronize()
+    for gs, w in zip(got, want):
+        assert all(torch.equal(a, b) for r in gs for a, b in zip(r, w))
+    assert pa.get_device_error() == (0, 0)
