@@ -664,10 +664,9 @@ PA_API pa_status pa_tree_metadata(int64_t *tree_mask, int32_t *positions, int32_
  *   tree_mask     int64 [batch, num_drafts].
  *   draft_lens    int32 [batch] or NULL.  Lengths that do not fit (ctx < n among
  *                 them) are recorded as PA_DEV_BAD_CONTEXT and give zeros.
- *   workspace     >= pa_decode_tree_workspace_size(...) bytes, 32-byte aligned,
- *                 ZERO-FILLED before its first use; contract as for pa_decode.  It
- *                 serves calls of any shape for which it is large enough, in turn,
- *                 and no other entry point.
+ *   workspace     >= pa_decode_tree_workspace_size(...) bytes, 32-byte aligned.  It
+ *                 holds nothing between calls, and serves calls of any shape for
+ *                 which it is large enough, one after the other.
  * num_drafts <= 64, batch <= 2048; other arguments and limits as pa_decode, and
  * batch * num_kv_heads * max_blocks_per_seq * block_size / 64 (twice that above 256
  * query heads times drafts per kv head) < 2^31.

@@ -847,11 +847,11 @@ def tree_metadata(parents, context_lens, block_tables, block_size, draft_lens=No
 
 
 def decode_tree_workspace(num_q_heads, num_kv_heads, head_dim=128, num_drafts=64, device="cuda"):
-    """Zero-filled workspace for decode_tree (its size depends on the query heads
-    per kv head and on num_drafts; a larger one serves smaller calls too); the
-    calls leave it ready for the next one on the same stream."""
+    """Workspace for decode_tree (its size depends on the query heads per kv head
+    and on num_drafts; a larger one serves smaller calls too).  It holds nothing
+    between calls; calls that may run at the same time need one each."""
     n = int(lib().pa_decode_tree_workspace_size(num_q_heads, num_kv_heads, head_dim, num_drafts))
-    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
 def decode_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask=None, softmax_scale=None, draft_lens=None,

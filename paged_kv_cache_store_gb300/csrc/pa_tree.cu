@@ -19,17 +19,17 @@
 // Of the 128 rows of an MMA only the live ones are loaded and read back; the
 // others hold whatever the memory held, which cannot reach a live row.
 //
-// An item cut between CTAs leaves (m, l, o) in fp32 in the workspace.  After the
-// walk each CTA counts its parts in; the one whose part completes eight in a row
-// combines those, in order, and the last of such groups the groups, so that the
-// result does not depend on who comes last.
+// An item cut between CTAs leaves (m, l, o) of its parts in fp32 in the workspace, and
+// the CTA in whose range it begins a note of it; a second kernel combines the parts, a
+// CTA for 32 rows, in order.  (Combined by the CTA whose part came last, 256 rows of
+// four parts took it 12 to 23 us, while the others were idle: 64 drafts over 8 x 32768
+// keys 243 us instead of 229, over 4 x 2900 50 instead of 30.)  Short items are not cut.
 //
 // What bounds it: up to 128 rows per kv head the bytes of K and V (Qwen3-8B shape,
-// 256 sequences x 4 drafts: 264 us, 6.6 TB/s); two row tiles the chain of products
-// and softmax (64 drafts over 8 x 32768 keys: 252 us, 1.09 PFLOP/s, 64 % of the
-// bytes' floor), in which a product's 64 keys re-read 128 rows of Q from shared
-// memory.  Products of 128 keys halve that but leave one score buffer a row tile:
-// 288 us.
+// 256 sequences x 4 drafts: 262 us, 6.6 TB/s); two row tiles the chain of products
+// and softmax (64 drafts over 8 x 32768 keys: 229 us, 1.2 PFLOP/s, 71 % of the bytes'
+// floor), in which a product's 64 keys re-read 128 rows of Q from shared memory.
+// Products of 128 keys halve that but leave one score buffer a row tile: 34 us more.
 //
 // l is summed from the rounded P that the product uses, so that the weights sum
 // to one as they are.
@@ -59,6 +59,9 @@ constexpr int kMaxBatch = 2048;
 constexpr int kMaxDrafts = 64;
 constexpr int kMaxGrid = 256;
 constexpr int kMinTiles = 2;             // a CTA's share at least
+// What cutting items costs, in tiles: the parts' way through the workspace and the second
+// kernel.  Items are left whole where that costs less.
+__host__ __device__ constexpr int cut_tiles(bool pair) { return pair ? 10 : 6; }
 constexpr float kLazy = 8.f;             // log2 headroom before the running maximum must move
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -71,19 +74,25 @@ constexpr int KMAX = 6, VMAX = 8;                // ring stages at most
 enum {  // barriers: rings, then per row tile [2] (and score buffer [2])
     KFULL = 0, KEMPTY = KFULL + KMAX, VFULL = KEMPTY + KMAX, VEMPTY = VFULL + VMAX, SFULL = VEMPTY + VMAX,
     PFULL = SFULL + 4, PDONE = PFULL + 4, OEMPTY = PDONE + 4, QFULL = OEMPTY + 2, QEMPTY = QFULL + 2,
-    ENDED = QEMPTY + 2, WROTE, TOLD, DRAIN, NBAR = DRAIN + 2
+    DRAIN = QEMPTY + 2, NBAR = DRAIN + 2
 };
 // Shared memory: Q [2], the rings, then from off_bar on the barriers, a few words
-// (TMEM address, abort, marks [4], parts held [2], two words of the parts' count, scan
-// scratch [12]), the parts [2][2],
-// and per sequence the running sum of tiles, the length (int) and the drafts (byte).
-constexpr int MISC = (NBAR * 8 + 15) / 16 * 16, JOBS = MISC + 128, ARRAYS = JOBS + 4 * 32;
+// (TMEM address, abort, marks [4], the longest item's tiles, scan scratch [12]), and per
+// sequence the running sum of tiles, the length (int) and the drafts (byte).
+constexpr int MISC = (NBAR * 8 + 15) / 16 * 16, ARRAYS = MISC + 128;
 constexpr uint32_t TMEM_COLS = 512, COL_O = 256;               // S(h, b) at h * 128 + b * 64, O(h) at COL_O + h * 128
 constexpr int kMaxSmem = 232448;
 constexpr int fixed_smem(int batch) { return 1024 + ARRAYS + 9 * (batch + 1); }
 
-// Floats of a part: o [rows][D], (m, l) [rows], a multiple of 32 bytes.
+// Floats of a part: o [D / 4][rows][4], so that the lanes of a warp, a row each, write and
+// read whole lines, then (m, l) [rows]; a multiple of 32 bytes.
 __host__ __device__ constexpr size_t slot_of(int rows) { return ((size_t)rows * (D + 2) + 7) / 8 * 8; }
+
+// What CTA c leaves of the item that begins in its range and ends behind it: its output
+// and rows, and the parts, the first in slot 2 c + 1, the others in 2 (c + i lanes).
+struct TreeJob {
+    int b, g, row0, rows, nparts, pad[3];  // nparts 0: none
+};
 
 struct TreeArgs {
     __nv_bfloat16 *out;
@@ -96,10 +105,7 @@ struct TreeArgs {
     int32_t shift;           // G = 1 << shift
     int32_t lanes;           // ranges side by side, each over Hkv / lanes of the heads
     float scale_log2;
-    // Arrivals [3][kMaxGrid][2 row tiles]: of the first kFan parts of the item that
-    // begins in a CTA's range and ends in a later one; of the kFan parts that begin
-    // with this CTA's; of such groups of the item that begins here.
-    int *count;
+    TreeJob *jobs;  // [grid]
     float *parts;  // [grid][2] of slot_of(part_rows)
     int32_t part_rows;
     DevError *err;
@@ -181,15 +187,25 @@ struct Walker {
     int G, g0;  // the lane's first head
     uint32_t x, x1;
     int b;
-    __device__ __forceinline__ void start(uint32_t x0, uint32_t xe, int batch) {
-        x = x0;
-        x1 = xe;
-        int lo = 0, hi = batch - 1;  // the last b with cum[b] <= x
+    __device__ __forceinline__ int find(uint32_t at, int batch) const {
+        int lo = 0, hi = batch - 1;  // the last b with cum[b] <= at
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (cum[mid] <= x) lo = mid; else hi = mid - 1;
+            if (cum[mid] <= at) lo = mid; else hi = mid - 1;
         }
-        b = lo;
+        return lo;
+    }
+    // The first item's begin from `at` on.
+    __device__ __forceinline__ uint32_t begin(uint32_t at, int batch) const {
+        if (at >= cum[batch]) return cum[batch];
+        const int i = find(at, batch);
+        const uint32_t nt = (uint32_t)(ctx_s[i] + TILE - 1) / TILE;
+        return cum[i] + (at - cum[i] + nt - 1) / nt * nt;
+    }
+    __device__ __forceinline__ void start(uint32_t x0, uint32_t xe, int batch, bool uncut) {
+        x = uncut ? begin(x0, batch) : x0;
+        x1 = uncut ? begin(xe, batch) : xe;
+        b = find(x, batch);
     }
     // The next item in the range.
     __device__ __forceinline__ bool next(Seg &s) {
@@ -214,124 +230,28 @@ struct Walker {
     }
 };
 
-// Adds the V values of drafts lo .. hi - 1 that are not finite to a thread's row (fp32,
-// or the bf16 output) where its mask has them.  Rare, and kept out of the loop's code.
-__device__ __noinline__ void add_hidden(void *row, bool bf16, unsigned long long mask, const __nv_bfloat16 *v,
-                                        int64_t v_row, const int32_t *bt, int block_size, int num_blocks, int first,
-                                        int lo, int hi, int lane) {
+// Adds the V values of drafts lo .. hi - 1 that are not finite to a thread's row where its
+// mask has them; element c of the row is at row[c / 4 * apart + c % 4] (fp32, or the bf16
+// output).  Rare, and kept out of the loop's code.
+__device__ __noinline__ void add_hidden(void *row, bool bf16, int apart, unsigned long long mask,
+                                        const __nv_bfloat16 *v, int64_t v_row, const int32_t *bt, int block_size,
+                                        int num_blocks, int first, int lo, int hi, int lane) {
     for (int j = lo; j < hi; ++j) {
         const int p = first + j, blk = __ldg(bt + p / block_size);
         if (blk < 0 || blk >= num_blocks) continue;
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(v + ((int64_t)blk * block_size + p % block_size) * v_row) + lane);
+        const int64_t slot = (int64_t)blk * block_size + p % block_size;
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(v + slot * v_row) + lane);
         if (!__any_sync(FULL, not_finite2(w.x) || not_finite2(w.y))) continue;
         for (int c = 0; c < D; ++c) {
             const uint32_t t = __shfl_sync(FULL, (c & 2) ? w.y : w.x, c >> 2);
             const float x = (c & 1) ? bf16hi(t) : bf16lo(t);
             if (isfinite(x) || !((mask >> j) & 1)) continue;
+            const int at = (c >> 2) * apart + (c & 3);
             if (bf16) {
-                __nv_bfloat16 *e = static_cast<__nv_bfloat16 *>(row) + c;
+                __nv_bfloat16 *e = static_cast<__nv_bfloat16 *>(row) + at;
                 *e = __float2bfloat16(__bfloat162float(*e) + x);
             } else {
-                static_cast<float *>(row)[c] += x;
-            }
-        }
-    }
-}
-
-// Part number `part` of `nparts`: rows [row0, row0 + live) of an item of which part p
-// is that of CTA c0 + p * lanes.
-struct Job {
-    int b, g, blk, row0, live, c0, nparts, part;
-};
-constexpr int kFan = 8;  // parts combined at a time
-
-// Combines parts p0, p0 + step, ... < p1 of a job's rows.  `final`: writes the rows out;
-// otherwise leaves the combined part in p0's place.  Eight warps, w of them; four rows
-// per warp and four parts at a time, 16 row loads in flight.  A part's m of -inf has
-// seen nothing; NaN in l or o goes on.
-// A call of its own, with scalars alone: inlined, or with the arguments' address
-// taken, it costs the softmax loop its registers (64 drafts 311 -> 350 us).
-struct Merge {
-    float *first, *rest;  // the first part; part i > 0 at rest + i * apart
-    size_t apart;
-    int part_rows, tr0, live, n;
-    // The output row of row r of the (sequence, kv head): out + (r >> shift) * token + r % G * D, G = 1 << shift.
-    __nv_bfloat16 *out;
-    int64_t token;
-    int gr0, shift;
-};
-__device__ __noinline__ void merge_rows(Merge g, bool final, int w, int lane) {
-    constexpr int RM = 4, PM = 4, PL = 32 / RM;  // rows, parts at a time, lanes of a row
-    const int n = g.n, r = lane & (RM - 1), ps = lane / RM;
-    auto part = [&](int i) -> float * { return i == 0 ? g.first : g.rest + (size_t)i * g.apart; };
-#pragma unroll 1
-    for (int r0 = RM * w; r0 < g.live; r0 += 8 * RM) {
-        const int row = g.tr0 + r0, nr = min(RM, g.live - r0);
-        auto ml_of = [&](int i) -> float2 {  // of row r in the i-th part
-            return i < n && r < nr ? __ldcg(reinterpret_cast<const float2 *>(part(i) + (size_t)g.part_rows * D) + row + r)
-                                   : make_float2(-INFINITY, 0.f);
-        };
-        float4 v[PM][RM], acc[RM];
-        auto load = [&](int i0) {  // the rows of parts i0 .. i0 + 3 (a part or row past the last: the last again)
-#pragma unroll
-            for (int pp = 0; pp < PM; ++pp) {
-                const float4 *at = reinterpret_cast<const float4 *>(part(min(i0 + pp, n - 1)) + (size_t)row * D) + lane;
-#pragma unroll
-                for (int e = 0; e < RM; ++e) v[pp][e] = __ldcg(at + min(e, nr - 1) * (D / 4));
-            }
-        };
-        float2 ml = ml_of(ps);
-        load(0);
-        float m = ml.x, l = ml.y;
-#pragma unroll 1
-        for (int i = ps + PL; i < n; i += PL) {
-            const float2 t = ml_of(i);
-            const float mn = fmaxf(m, t.x), ref = mn == -INFINITY ? 0.f : mn;
-            l = l * fast_exp2(m - ref) + t.y * fast_exp2(t.x - ref);
-            m = mn;
-        }
-#pragma unroll 1
-        for (int o = RM; o < 32; o <<= 1) {
-            const float m2 = __shfl_xor_sync(FULL, m, o), l2 = __shfl_xor_sync(FULL, l, o);
-            const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn;
-            l = l * fast_exp2(m - ref) + l2 * fast_exp2(m2 - ref);
-            m = mn;
-        }
-        const float ref = m == -INFINITY ? 0.f : m, inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < RM; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += PM) {
-            if (i0 > 0) {
-                load(i0);
-                if (i0 % PL == 0) ml = ml_of(i0 + ps);
-            }
-            const float wgt = fast_exp2(ml.x - ref);  // of row r in the part ps of the eight under way
-#pragma unroll
-            for (int pp = 0; pp < PM; ++pp) {
-                if (i0 + pp >= n) break;
-#pragma unroll
-                for (int e = 0; e < RM; ++e) {
-                    const float f = __shfl_sync(FULL, wgt, ((i0 & PM) + pp) * RM + e);
-                    acc[e].x = fmaf(v[pp][e].x, f, acc[e].x);
-                    acc[e].y = fmaf(v[pp][e].y, f, acc[e].y);
-                    acc[e].z = fmaf(v[pp][e].z, f, acc[e].z);
-                    acc[e].w = fmaf(v[pp][e].w, f, acc[e].w);
-                }
-            }
-        }
-        if (!final && ps == 0 && r < nr)  // (every lane has read the rows' m and l)
-            reinterpret_cast<float2 *>(g.first + (size_t)g.part_rows * D)[row + r] = make_float2(m, l);
-#pragma unroll
-        for (int e = 0; e < RM; ++e) {
-            const float f = __shfl_sync(FULL, inv, e);
-            if (e >= nr) break;
-            if (final) {
-                const int gr = g.gr0 + r0 + e;
-                reinterpret_cast<uint2 *>(g.out + (gr >> g.shift) * g.token + (gr & ((1 << g.shift) - 1)) * D)[lane] =
-                    make_uint2(pack_bf16(acc[e].x * f, acc[e].y * f), pack_bf16(acc[e].z * f, acc[e].w * f));
-            } else {
-                reinterpret_cast<float4 *>(g.first + (size_t)(row + e) * D)[lane] = acc[e];
+                static_cast<float *>(row)[at] += x;
             }
         }
     }
@@ -356,14 +276,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t *n_s = reinterpret_cast<uint8_t *>(ctx_s + (a.batch + 1));
     const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform, and known to be)
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NBAR; ++i) {
-            // The four softmax warps of a row tile arrive one each.
-            const bool per_warp = (i >= PFULL && i < PFULL + 4) || (i >= OEMPTY && i < OEMPTY + 2);
-            mbar_init(&bar[i], i == ENDED || i == WROTE ? 8u : per_warp ? 4u : 1u);
-        }
-        for (int i = 0; i < 9; ++i) abort[i] = 0;  // and the marks behind it
+    static_assert(NBAR <= 64, "a thread of warps 2 and 3 each");
+    if (threadIdx.x >= 64 && threadIdx.x < 64 + NBAR) {
+        const int i = threadIdx.x - 64;
+        // The four softmax warps of a row tile arrive one each.
+        const bool per_warp = (i >= PFULL && i < PFULL + 4) || (i >= OEMPTY && i < OEMPTY + 2);
+        mbar_init(&bar[i], per_warp ? 4u : 1u);
         fence_mbar_init();
+    }
+    if (threadIdx.x < 6) abort[threadIdx.x] = 0;  // and the words behind it
+    if (threadIdx.x == 0) {
+        a.jobs[blockIdx.x].nparts = 0;
         prefetch_tensormap(&tmq);
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
@@ -375,6 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // Lengths, and the running sum of the sequences' tiles.
     uint32_t carry = 0;
+    int longest = 0;
     for (int base = 0; base < a.batch; base += THREADS) {
         const int b = base + threadIdx.x;
         uint32_t u = 0;
@@ -389,6 +313,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             ctx_s[b] = ctx;
             n_s[b] = (uint8_t)n;
             const int blocks = (n * a.G + BLOCK - 1) / BLOCK;
+            longest = max(longest, (ctx + TILE - 1) / TILE);
             u = (uint32_t)((ctx + TILE - 1) / TILE) * (uint32_t)(a.Hkv / a.lanes * blocks);
         }
         uint32_t inc = u;
@@ -409,16 +334,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncthreads();
     }
     if (threadIdx.x == 0) cum[a.batch] = carry;
+    longest = __reduce_max_sync(FULL, longest);
+    if (lane == 0) atomicMax(const_cast<int *>(abort) + 5, longest);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // The lane's tiles, its ranges, and this CTA's.
-    const uint32_t P = carry, W = min(gridDim.x / (uint32_t)a.lanes, max(1u, P / kMinTiles));
+    // The lane's tiles, its ranges, and this CTA's.  Items stay whole where that is shorter,
+    // as if all were as long as the longest (16 sequences of 1000 keys, 8 heads of 4 x 64
+    // rows: 31 us whole, 37 cut; 4 of 1900: 40 and 27): a range then goes from the first
+    // item that begins in it to the first that begins behind it.
+    const uint32_t P = carry, W0 = gridDim.x / (uint32_t)a.lanes, most = (uint32_t)abort[5];
+    const uint64_t round = (uint64_t)most * W0;
+    const uint32_t rounds = round >= P ? 1u : (P + (uint32_t)round - 1) / (uint32_t)round;
+    const bool uncut = rounds * most <= P / W0 + cut_tiles(PAIR);
+    const uint32_t W = min(W0, max(1u, uncut ? P : P / kMinTiles));
     const uint32_t range = blockIdx.x / (uint32_t)a.lanes, side = blockIdx.x - range * (uint32_t)a.lanes;
     Walker<PAIR> walk{ctx_s, n_s, cum, a.G, (int)side * (a.Hkv / a.lanes), 0u, 0u, 0};
     if (range < W && P > 0)
-        walk.start((uint32_t)((uint64_t)range * P / W), (uint32_t)((uint64_t)(range + 1) * P / W), a.batch);
+        walk.start((uint32_t)((uint64_t)range * P / W), (uint32_t)((uint64_t)(range + 1) * P / W), a.batch, uncut);
     // Row tiles of segment number k.
     auto h_begin = [](int k) -> int { return PAIR ? 0 : k & 1; };
     auto h_end = [](int k, const Seg &s) -> int { return PAIR ? (s.rows + ROWS - 1) / ROWS : (k & 1) + 1; };
@@ -637,9 +571,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         // segment of its own ahead of another, as a segment's last product needs the
         // P of all of them.
         volatile int *marks = abort + 1;
-        volatile int *held = abort + 5, *todo = abort + 7, *go_on = abort + 8;
-        Job *parts = reinterpret_cast<Job *>(ctl + JOBS);
-        int nparts_h = 0;  // parts of this row tile
         // The next segment that this row tile has rows in: its number, its first
         // tile's number, and (asked for ahead) this row's mask.
         int k_next = 0;
@@ -782,7 +713,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_after();
             const bool whole = s.t0 == 0 && s.t1 == s.nt;
             // A part: slot 1 of the item's first CTA, slot 0 of the others.
-            int c0 = 0, nparts = 1;
+            int c0 = 0, nparts = 0;
             float *slot = nullptr;
             if (!whole) {  // the range that holds tile x: ((x + 1) W - 1) / P
                 const int r0 = (int)(((uint64_t)(s.first + 1) * W - 1) / P);
@@ -812,12 +743,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     } else if (mine) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)  // 32 bytes a store: whole sectors
-                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                                             slot + (size_t)(row0 + row) * D + 32 * c + 8 * e),
-                                         "r"(o[8 * e]), "r"(o[8 * e + 1]), "r"(o[8 * e + 2]), "r"(o[8 * e + 3]),
-                                         "r"(o[8 * e + 4]), "r"(o[8 * e + 5]), "r"(o[8 * e + 6]), "r"(o[8 * e + 7])
-                                         : "memory");
+                        for (int e = 0; e < 8; ++e)  // a warp's stores: 512 bytes in a row
+                            reinterpret_cast<uint4 *>(slot)[(size_t)(8 * c + e) * a.part_rows + row0 + row] =
+                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
             }
@@ -830,89 +758,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int gr = s.blk * BLOCK + row0 + row;
                 const int64_t head = ((int64_t)s.b * a.drafts + (gr >> a.shift)) * a.Hq + s.g * a.G + (gr & (a.G - 1));
                 void *at = whole ? static_cast<void *>(a.out + head * D)
-                                 : static_cast<void *>(slot + (size_t)(row0 + row) * D);
-                add_hidden(at, whole, mine ? m64 : 0ull, a.v_cache + (int64_t)s.g * D, (int64_t)a.Hkv * D,
-                           a.bt + (int64_t)s.b * a.max_blocks, a.block_size, a.num_blocks, first, lo, hi, lane);
+                                 : static_cast<void *>(slot + (size_t)(row0 + row) * 4);
+                add_hidden(at, whole, whole ? 4 : a.part_rows * 4, mine ? m64 : 0ull, a.v_cache + (int64_t)s.g * D,
+                           (int64_t)a.Hkv * D, a.bt + (int64_t)s.b * a.max_blocks, a.block_size, a.num_blocks, first, lo,
+                           hi, lane);
             }
             if (whole) continue;
             if (mine) reinterpret_cast<float2 *>(slot + (size_t)a.part_rows * D)[row0 + row] = make_float2(m_run * sl, l_run);
-            if (quarter == 0 && lane == 0)  // two parts at most: of the range's first and last item
-                parts[2 * h + nparts_h] = {s.b, s.g, s.blk, row0, live, c0, nparts, (int)range - c0 / a.lanes};
-            ++nparts_h;
-        }
-        // The parts are written: they are counted, and those whose last this CTA's was
-        // are combined, by both row tiles' warps; here, where nothing of the loop above
-        // is alive in registers.
-        __threadfence();
-        if (quarter == 0 && lane == 0) held[h] = nparts_h;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[ENDED]);
-        ok = ok && wwait(ENDED, 0u, 715);
-        uint32_t told = 0;
-        if (ok && warp == 4) {
-            // Lane i counts part i & 1 of row tile i >> 1: among the kFan parts that are
-            // combined together.
-            bool mine_last = false;
-            if (lane < 4 && (lane & 1) < held[lane >> 1]) {
-                const Job p = parts[lane];
-                const int p0 = p.part / kFan * kFan;
-                int *cnt = a.count + 2 * ((p.c0 + p0 * a.lanes) + (p0 > 0 ? kMaxGrid : 0)) + (PAIR ? lane >> 1 : 0);
-                __threadfence();
-                mine_last = atomicAdd(cnt, 1) == min(kFan, p.nparts - p0) - 1;
-                if (mine_last) *cnt = 0;  // as it was found
-                __threadfence();
-            }
-            const unsigned m = __ballot_sync(FULL, mine_last);
-            if (lane == 0) {
-                *todo = (int)m;
-                mbar_arrive(&bar[TOLD]);
-            }
-        }
-        ok = ok && wwait(TOLD, told++ & 1u, 714);
-        uint32_t wrote = 0;
-        for (unsigned m = ok ? (unsigned)*todo : 0u; ok && m; m &= m - 1) {
-            const int at = __ffs(m) - 1;
-            const Job &job = parts[at];
-            const bool one = job.nparts <= kFan;
-            // More parts than that: they are combined by several CTAs, and the
-            // combined ones by the last of these.
-            for (bool final = one;; final = true) {
-                __threadfence();
-                const int p0 = final ? 0 : job.part / kFan * kFan;
-                const int step = final && !one ? kFan : 1, p1 = final ? job.nparts : min(p0 + kFan, job.nparts);
-                const size_t slot_floats = slot_of(a.part_rows);
-                Merge g;
-                g.rest = a.parts + (size_t)(2 * (job.c0 + p0 * a.lanes)) * slot_floats;
-                g.first = g.rest + (p0 == 0 ? slot_floats : 0);
-                g.apart = (size_t)(2 * step * a.lanes) * slot_floats;
-                g.part_rows = a.part_rows;
-                g.tr0 = job.row0;
-                g.live = job.live;
-                g.n = (p1 - p0 + step - 1) / step;
-                g.token = (int64_t)a.Hq * D;
-                g.out = a.out + (int64_t)job.b * a.drafts * g.token + job.g * a.G * D;
-                g.gr0 = job.blk * BLOCK + job.row0;
-                g.shift = a.shift;
-                merge_rows(g, final, warp - 4, lane);
-                if (final) break;
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[WROTE]);
-                if (warp == 4) {
-                    if (!(ok = wwait(WROTE, wrote++ & 1u, 716))) break;
-                    if (lane == 0) {
-                        int *cnt = a.count + 2 * (job.c0 + 2 * kMaxGrid) + (PAIR ? at >> 1 : 0);
-                        __threadfence();
-                        const bool is_last = atomicAdd(cnt, 1) == (job.nparts + kFan - 1) / kFan - 1;
-                        if (is_last) *cnt = 0;
-                        __threadfence();
-                        *go_on = is_last;
-                        mbar_arrive(&bar[TOLD]);
-                    }
-                }
-                if (!(ok = wwait(TOLD, told++ & 1u, 717))) break;
-                if (!*go_on) break;
-            }
+            if (quarter == 0 && lane == 0 && blockIdx.x == c0 && (!PAIR || h == 0))
+                a.jobs[c0] = {s.b, s.g, s.blk * BLOCK, s.rows, nparts, {}};
         }
     }
     tc_fence_before();
@@ -921,7 +775,107 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-// Counters (at the same place for every shape), then the parts.
+// Combines the parts of the items that were cut: a CTA for 32 rows (blockIdx.y) of the item
+// of blockIdx.x and D / Z of its columns; a warp 16 columns of every Z-th part, four parts
+// under way.  A part's m of -inf has seen nothing; NaN in l or o goes on.
+struct CombineArgs {
+    __nv_bfloat16 *out;
+    const TreeJob *jobs;
+    const float *parts;
+    int part_rows, lanes, drafts, Hq, G, shift;
+};
+struct Sums {
+    float m = -INFINITY, l = 0.f;
+    float4 o[4] = {};
+    // Scales to a maximum of mn; returns what -inf counts as.
+    __device__ __forceinline__ float raise(float mn) {
+        const float ref = mn == -INFINITY ? 0.f : mn, f = fast_exp2(m - ref);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = make_float4(o[e].x * f, o[e].y * f, o[e].z * f, o[e].w * f);
+        return ref;
+    }
+    __device__ __forceinline__ void add(float mp, float lp, const float4 (&v)[4], float ref) {
+        const float f = fast_exp2(mp - ref);
+        l = fmaf(lp, f, l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = make_float4(fmaf(v[e].x, f, o[e].x), fmaf(v[e].y, f, o[e].y), fmaf(v[e].z, f, o[e].z),
+                               fmaf(v[e].w, f, o[e].w));
+    }
+};
+constexpr int CTHREADS = 256;
+template <int Z>
+__global__ void __launch_bounds__(CTHREADS) combine_kernel(const __grid_constant__ CombineArgs a) {
+    pdl_wait_then_release();
+    constexpr int SETS = 8 / Z, PM = 4;  // sets of 16 columns; parts at a time
+    const int4 job = __ldcg(reinterpret_cast<const int4 *>(a.jobs + blockIdx.x));
+    const int nparts = __ldcg(&a.jobs[blockIdx.x].nparts);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y * 32 + lane;
+    if (nparts == 0 || (int)blockIdx.y * 32 >= job.w) return;
+    const int set = warp % SETS + blockIdx.z * SETS, p0 = warp / SETS;
+    const bool mine = row < job.w;
+    const size_t slot = slot_of(a.part_rows);
+    const float *rest = a.parts + (size_t)2 * blockIdx.x * slot;
+    Sums sum;
+#pragma unroll 1
+    for (int i0 = p0; i0 < nparts; i0 += PM * Z) {
+        float4 v[PM][4];
+        float2 ml[PM];
+        float mn = sum.m;
+#pragma unroll
+        for (int p = 0; p < PM; ++p) {
+            const int i = i0 + p * Z;
+            ml[p] = make_float2(-INFINITY, 0.f);
+            if (i < nparts && mine) {
+                const float *from = i == 0 ? rest + slot : rest + (size_t)(2 * i * a.lanes) * slot;
+                ml[p] = __ldcg(reinterpret_cast<const float2 *>(from + (size_t)a.part_rows * D) + row);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[p][e] = __ldcg(reinterpret_cast<const float4 *>(from) + (size_t)(4 * set + e) * a.part_rows + row);
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < PM; ++p) mn = fmaxf(mn, ml[p].x);
+        const float ref = sum.raise(mn);
+#pragma unroll
+        for (int p = 0; p < PM; ++p)
+            if (i0 + p * Z < nparts) sum.add(ml[p].x, ml[p].y, v[p], ref);
+    }
+    if (Z > 1) {
+        __shared__ float4 os[8][4][32];
+        __shared__ float2 mls[8][32];
+        if (p0 > 0) {
+            mls[warp][lane] = make_float2(sum.m, sum.l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) os[warp][e][lane] = sum.o[e];
+        }
+        __syncthreads();
+        if (p0 > 0) return;
+#pragma unroll 1
+        for (int w = warp + SETS; w < 8 && w / SETS < nparts; w += SETS) {
+            const float2 ml = mls[w][lane];
+            float4 v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = os[w][e][lane];
+            const float ref = sum.raise(fmaxf(sum.m, ml.x));
+            sum.add(ml.x, ml.y, v, ref);
+        }
+    }
+    if (!mine) return;
+    const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+    const int gr = job.z + row;
+    uint4 *dst = reinterpret_cast<uint4 *>(
+        a.out + (((int64_t)job.x * a.drafts + (gr >> a.shift)) * a.Hq + job.y * a.G + (gr & (a.G - 1))) * D + 16 * set);
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+        dst[e / 2] = make_uint4(pack_bf16(sum.o[e].x * inv, sum.o[e].y * inv), pack_bf16(sum.o[e].z * inv, sum.o[e].w * inv),
+                                pack_bf16(sum.o[e + 1].x * inv, sum.o[e + 1].y * inv),
+                                pack_bf16(sum.o[e + 1].z * inv, sum.o[e + 1].w * inv));
+}
+
+// Notes of the items that were cut, then the parts.
 struct Layout {
     bool pair;
     int part_rows;  // rows of an item at most
@@ -931,7 +885,7 @@ Layout layout_of(int drafts, int G) {
     Layout l;
     l.pair = drafts * G > ROWS;
     l.part_rows = std::min(drafts * G, 2 * ROWS);
-    l.parts = (size_t)3 * kMaxGrid * 2 * sizeof(int);
+    l.parts = (size_t)kMaxGrid * sizeof(TreeJob);
     l.bytes = l.parts + (size_t)kMaxGrid * 2 * slot_of(l.part_rows) * sizeof(float);
     return l;
 }
@@ -1040,7 +994,7 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     a.box_rows = r;
     a.checked = checked_mode() ? 1 : 0;
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
-    a.count = static_cast<int *>(workspace);
+    a.jobs = static_cast<TreeJob *>(workspace);
     a.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + l.parts);
     a.part_rows = l.part_rows;
     a.err = device_error_ptr();
@@ -1067,7 +1021,19 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     for (int n = 2; n <= num_kv_heads && n <= grid; ++n)
         if (num_kv_heads % n == 0 && grid / n * n * 10 >= grid * 9) a.lanes = n;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    return l.pair ? launch_tree<true>(tmq, tmk, tmv, a, (int)grid, cs) : launch_tree<false>(tmq, tmk, tmv, a, (int)grid, cs);
+    st = l.pair ? launch_tree<true>(tmq, tmk, tmv, a, (int)grid, cs) : launch_tree<false>(tmq, tmk, tmv, a, (int)grid, cs);
+    if (st != PA_OK || (keys + TILE - 1) / TILE <= cut_tiles(l.pair)) return st;  // none is cut
+    const CombineArgs c = {a.out, a.jobs, a.parts, a.part_rows, a.lanes, a.drafts, a.Hq, a.G, a.shift};
+    // Many parts an item: its columns over more CTAs, and the parts over more warps.  (CTAs
+    // without work cost too: Qwen3-0.6B shape, 8 drafts, 84.6 us with one CTA a note, 89.8
+    // with 8.)
+    const int64_t rows32 = (l.part_rows + 31) / 32, parts = grid / (num_kv_heads * blocks * batch);
+    const int z = l.pair || parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
+    const auto kernel = z == 8   ? combine_kernel<8>
+                        : z == 4 ? combine_kernel<4>
+                        : z == 2 ? combine_kernel<2>
+                                 : combine_kernel<1>;
+    return launch_pdl(kernel, dim3((unsigned)grid, (unsigned)rows32, z), dim3(CTHREADS), 0, cs, "combine_kernel", c);
 }
 
 }  // extern "C"

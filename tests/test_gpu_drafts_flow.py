@@ -192,7 +192,6 @@ def test_steps_captured_into_graphs_that_share_a_workspace():
                 pool = len(d["kc"])
                 s.kc, s.vc = (np.concatenate([c, c[:max(0, pool - len(c))]])[:pool] for c in (s.kc, s.vc))
                 check(s, d, *o)
-    assert not ws[:6144].any()
 
 
 def test_the_same_call_gives_the_same_bits():
