@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "pa_internal.cuh"
 
@@ -739,10 +740,17 @@ pa_status launch_verify(VerifyArgs &a, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (a.cluster > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(verify_kernel<FP32, PROBS, THREADS>,
-                                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return cuda_fail(e, "verify_kernel");
+    if (a.cluster > 8) {  // per (device, variant): the attribute has been set (setting it takes 3 us)
+        static std::atomic<int> done[64];
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+        if (dev < 0 || dev >= 64) return fail(PA_ERR_UNSUPPORTED, "device %d", dev);
+        if (!done[dev].load(std::memory_order_acquire)) {
+            e = cudaFuncSetAttribute(verify_kernel<FP32, PROBS, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return cuda_fail(e, "verify_kernel");
+            done[dev].store(1, std::memory_order_release);
+        }
     }
     const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<FP32, PROBS, THREADS>, a);
     if (e != cudaSuccess) return cuda_fail(e, "verify_kernel");
