@@ -762,8 +762,9 @@ pa_status launch_verify(VerifyArgs &a, cudaStream_t stream) {
     const int sms = sm_count();
     a.cluster = ctas_per_seq(a.batch, a.vocab, sms);
     // A row read ahead in vain costs more than the wait it saves once the sequences fill
-    // the GPU (64 sequences 52 us without, 56 with; 16: 28.8 and 27.3).
-    a.ahead = 8LL * a.batch <= sms;
+    // the GPU (64 sequences 52 us without, 56 with; 32 trees of 12 nodes 39.5 and 38.3; 16
+    // sequences 28.8 and 27.3).
+    a.ahead = 8LL * a.batch <= 2LL * sms;
     // Few CTAs: twice the threads.
     const bool few = (int64_t)a.batch * a.cluster <= 2LL * sms;
     return few ? launch_verify<FP32, PROBS, 512>(a, stream) : launch_verify<FP32, PROBS, 256>(a, stream);

@@ -181,6 +181,28 @@ def test_items_cut_between_many_ctas(hq, hkv, before):
         Tree(T + hq, before, T, hq, hkv, 256).check()
 
 
+@pytest.mark.parametrize("T,hq,hkv,tiles", [(5, 8, 2, 6), (5, 8, 2, 7), (40, 8, 2, 10), (40, 8, 2, 11), (3, 4, 4, 17)])
+def test_short_items_whole_and_cut(T, hq, hkv, tiles):
+    """Block tables too short for a cut, so that one kernel does it all, and just long enough."""
+    rng = np.random.default_rng(tiles)
+    for batch in (1, 3, 19, 40, 77):
+        before = rng.integers(0, 64 * tiles - T + 1, batch)
+        before[0] = 64 * tiles - T
+        t = Tree(tiles + batch, before, T, hq, hkv, 64)
+        t.bt = np.ascontiguousarray(t.bt[:, :tiles])
+        t.check()
+
+
+def test_the_workspace_may_hold_anything():
+    for T, hq, hkv, before in ((5, 8, 2, [9000, 40, 700]), (40, 8, 2, [5000, 3]), (64, 8, 1, [300, 9000])):
+        t = Tree(T, before, T, hq, hkv, 64)
+        ws = pa.decode_tree_workspace(hq, hkv, 128, T)
+        want = t.check(workspace=ws.fill_(0))
+        assert torch.equal(t.run(workspace=ws), want)
+        assert torch.equal(t.run(workspace=ws.fill_(255)), want)
+        assert torch.equal(t.run(workspace=ws.random_()), want)
+
+
 def test_ragged_batches_and_padding():
     rng = np.random.default_rng(3)
     lens = rng.integers(0, 17, 40)
