@@ -286,7 +286,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (threadIdx.x < 6) abort[threadIdx.x] = 0;  // and the words behind it
     if (threadIdx.x == 0) {
-        a.jobs[blockIdx.x].nparts = 0;
         prefetch_tensormap(&tmq);
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
@@ -295,7 +294,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_alloc(tmem_slot, TMEM_COLS);
         tmem_relinquish();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    pdl_wait_then_release();
+    if (threadIdx.x == 0) a.jobs[blockIdx.x].nparts = 0;
     // Lengths, and the running sum of the sequences' tiles.
     uint32_t carry = 0;
     int longest = 0;
@@ -895,7 +895,7 @@ std::atomic<int> g_attr_done[64][2];
 
 template <bool PAIR>
 pa_status launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const TreeArgs &a,
-                      int grid, cudaStream_t stream) {
+                      int grid, bool is_short, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -906,11 +906,14 @@ pa_status launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUte
         if (e != cudaSuccess) return cuda_fail(e, "decode_tree_kernel shared memory");
         g_attr_done[dev][PAIR].store(1, std::memory_order_release);
     }
-    // A plain launch: as a programmatic dependent one its CTAs take the SMs in the
-    // order in which the kernel before leaves them, those of a range no longer sit
-    // side by side, and long calls lose more (Qwen3-8B shape, 4 drafts, 356 us
-    // instead of 312) than short ones gain (9.0 us, 8.0).
     const size_t smem = (size_t)4 * a.q_rows * 128 + (size_t)(a.k_stages + a.v_stages) * KV_BYTES + fixed_smem(a.batch);
+    // Short calls: the set-up beside the end of the kernel before (1 x 1000 keys 11.1 us,
+    // 10.6 so).  Long ones have a plain launch: as programmatic dependents their CTAs take
+    // the SMs in the order in which the kernel before leaves them, and those of a range
+    // need not sit side by side (Qwen3-8B shape, an earlier state: 312 us, 356 so).
+    if (is_short)
+        return launch_pdl(decode_tree_kernel<PAIR>, dim3((unsigned)grid), dim3(THREADS), smem, stream,
+                          "decode_tree_kernel", tmq, tmk, tmv, a);
     decode_tree_kernel<PAIR><<<dim3((unsigned)grid), dim3(THREADS), smem, stream>>>(tmq, tmk, tmv, a);
     return check_launch("decode_tree_kernel");
 }
@@ -1021,7 +1024,9 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     for (int n = 2; n <= num_kv_heads && n <= grid; ++n)
         if (num_kv_heads % n == 0 && grid / n * n * 10 >= grid * 9) a.lanes = n;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    st = l.pair ? launch_tree<true>(tmq, tmk, tmv, a, (int)grid, cs) : launch_tree<false>(tmq, tmk, tmv, a, (int)grid, cs);
+    const bool is_short = a_seq * batch <= 16 * grid;  // tiles a CTA at most
+    st = l.pair ? launch_tree<true>(tmq, tmk, tmv, a, (int)grid, is_short, cs)
+                : launch_tree<false>(tmq, tmk, tmv, a, (int)grid, is_short, cs);
     if (st != PA_OK || (keys + TILE - 1) / TILE <= cut_tiles(l.pair)) return st;  // none is cut
     const CombineArgs c = {a.out, a.jobs, a.parts, a.part_rows, a.lanes, a.drafts, a.Hq, a.G, a.shift};
     // Many parts an item: its columns over more CTAs, and the parts over more warps.  (CTAs
