@@ -907,10 +907,12 @@ pa_status launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUte
         g_attr_done[dev][PAIR].store(1, std::memory_order_release);
     }
     const size_t smem = (size_t)4 * a.q_rows * 128 + (size_t)(a.k_stages + a.v_stages) * KV_BYTES + fixed_smem(a.batch);
-    // Short calls: the set-up beside the end of the kernel before (1 x 1000 keys 11.1 us,
-    // 10.6 so).  Long ones have a plain launch: as programmatic dependents their CTAs take
-    // the SMs in the order in which the kernel before leaves them, and those of a range
-    // need not sit side by side (Qwen3-8B shape, an earlier state: 312 us, 356 so).
+    // The set-up beside the end of the kernel before: after a pa_rope_store_kvcache on a
+    // stream, Qwen3-0.6B shape with 8 drafts 94.8 us for both, 96.8 with a plain launch; 1 x
+    // 1000 keys 10.6 and 11.1.  But the CTAs then take the SMs in the order in which the
+    // kernel before leaves them, and those of a range need not sit side by side, which
+    // long calls feel (Qwen3-8B shape in a graph 273.3 us for both, 271.8 so): they have a
+    // plain launch.
     if (is_short)
         return launch_pdl(decode_tree_kernel<PAIR>, dim3((unsigned)grid), dim3(THREADS), smem, stream,
                           "decode_tree_kernel", tmq, tmk, tmv, a);
@@ -1024,7 +1026,7 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     for (int n = 2; n <= num_kv_heads && n <= grid; ++n)
         if (num_kv_heads % n == 0 && grid / n * n * 10 >= grid * 9) a.lanes = n;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const bool is_short = a_seq * batch <= 16 * grid;  // tiles a CTA at most
+    const bool is_short = a_seq * batch <= 512 * grid;  // tiles a CTA at most
     st = l.pair ? launch_tree<true>(tmq, tmk, tmv, a, (int)grid, is_short, cs)
                 : launch_tree<false>(tmq, tmk, tmv, a, (int)grid, is_short, cs);
     if (st != PA_OK || (keys + TILE - 1) / TILE <= cut_tiles(l.pair)) return st;  // none is cut
