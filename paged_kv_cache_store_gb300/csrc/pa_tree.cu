@@ -104,6 +104,7 @@ struct TreeArgs {
     int32_t k_stages, v_stages;
     int32_t shift;           // G = 1 << shift
     int32_t lanes;           // ranges side by side, each over Hkv / lanes of the heads
+    int32_t whole;           // no item is cut
     float scale_log2;
     TreeJob *jobs;  // [grid]
     float *parts;  // [grid][2] of slot_of(part_rows)
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t P = carry, W0 = gridDim.x / (uint32_t)a.lanes, most = (uint32_t)abort[5];
     const uint64_t round = (uint64_t)most * W0;
     const uint32_t rounds = round >= P ? 1u : (P + (uint32_t)round - 1) / (uint32_t)round;
-    const bool uncut = rounds * most <= P / W0 + cut_tiles(PAIR);
+    const bool uncut = a.whole || rounds * most <= P / W0 + cut_tiles(PAIR);
     const uint32_t W = min(W0, max(1u, uncut ? P : P / kMinTiles));
     const uint32_t range = blockIdx.x / (uint32_t)a.lanes, side = blockIdx.x - range * (uint32_t)a.lanes;
     Walker<PAIR> walk{ctx_s, n_s, cum, a.G, (int)side * (a.Hkv / a.lanes), 0u, 0u, 0};
@@ -1026,10 +1027,16 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     for (int n = 2; n <= num_kv_heads && n <= grid; ++n)
         if (num_kv_heads % n == 0 && grid / n * n * 10 >= grid * 9) a.lanes = n;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    // Tables too short for a cut: one launch.  So too where every item can have a CTA of its
+    // own and at most twice that length (4 sequences of up to 600 keys, 5 drafts: 12.0 us
+    // instead of 11.4, but 14.9 instead of 18.1 a call from Python, which the launches bound).
+    const int64_t longest = (keys + TILE - 1) / TILE;
+    a.whole = longest <= cut_tiles(l.pair) ||
+              (longest <= 2 * cut_tiles(l.pair) && (int64_t)batch * num_kv_heads * blocks <= grid);
     const bool is_short = a_seq * batch <= 512 * grid;  // tiles a CTA at most
     st = l.pair ? launch_tree<true>(tmq, tmk, tmv, a, (int)grid, is_short, cs)
                 : launch_tree<false>(tmq, tmk, tmv, a, (int)grid, is_short, cs);
-    if (st != PA_OK || (keys + TILE - 1) / TILE <= cut_tiles(l.pair)) return st;  // none is cut
+    if (st != PA_OK || a.whole) return st;
     const CombineArgs c = {a.out, a.jobs, a.parts, a.part_rows, a.lanes, a.drafts, a.Hq, a.G, a.shift};
     // Many parts an item: its columns over more CTAs, and the parts over more warps.  (CTAs
     // without work cost too: Qwen3-0.6B shape, 8 drafts, 84.6 us with one CTA a note, 89.8
