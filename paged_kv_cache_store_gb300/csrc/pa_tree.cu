@@ -77,7 +77,7 @@ enum {  // barriers: rings, then per row tile [2] (and score buffer [2])
     DRAIN = QEMPTY + 2, NBAR = DRAIN + 2
 };
 // Shared memory: Q [2], the rings, then from off_bar on the barriers, a few words
-// (TMEM address, abort, marks [4], the longest item's tiles, scan scratch [12]), and per
+// (TMEM address, abort, mark, the longest item's tiles, scan scratch [12]), and per
 // sequence the running sum of tiles, the length (int) and the drafts (byte).
 constexpr int MISC = (NBAR * 8 + 15) / 16 * 16, ARRAYS = MISC + 128;
 constexpr uint32_t TMEM_COLS = 512, COL_O = 256;               // S(h, b) at h * 128 + b * 64, O(h) at COL_O + h * 128
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(&bar[i], per_warp ? 4u : 1u);
         fence_mbar_init();
     }
-    if (threadIdx.x < 6) abort[threadIdx.x] = 0;  // and the words behind it
+    if (threadIdx.x < 3) abort[threadIdx.x] = 0;  // and the words behind it
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tmq);
         prefetch_tensormap(&tmk);
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (threadIdx.x == 0) cum[a.batch] = carry;
     longest = __reduce_max_sync(FULL, longest);
-    if (lane == 0) atomicMax(const_cast<int *>(abort) + 5, longest);
+    if (lane == 0) atomicMax(const_cast<int *>(abort) + 2, longest);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // as if all were as long as the longest (16 sequences of 1000 keys, 8 heads of 4 x 64
     // rows: 31 us whole, 37 cut; 4 of 1900: 40 and 27): a range then goes from the first
     // item that begins in it to the first that begins behind it.
-    const uint32_t P = carry, W0 = gridDim.x / (uint32_t)a.lanes, most = (uint32_t)abort[5];
+    const uint32_t P = carry, W0 = gridDim.x / (uint32_t)a.lanes, most = (uint32_t)abort[2];
     const uint64_t round = (uint64_t)most * W0;
     const uint32_t rounds = round >= P ? 1u : (P + (uint32_t)round - 1) / (uint32_t)round;
     const bool uncut = a.whole || rounds * most <= P / W0 + cut_tiles(PAIR);
@@ -567,18 +567,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int c = lane; c < per; c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        // A mark of segment number k (k + 1 in its place): a draft's V held
-        // something not finite.  Two places in turn: no warp is more than one
-        // segment of its own ahead of another, as a segment's last product needs the
-        // P of all of them.
-        volatile int *marks = abort + 1;
-        // The next segment that this row tile has rows in: its number, its first
-        // tile's number, and (asked for ahead) this row's mask.
+        // Set once a draft's V held something not finite, and never taken back: from then
+        // on each segment looks for such values of its own.  (A mark per segment would need
+        // a place that no warp writes again before the slowest has read it, and a warp
+        // without live rows runs segments ahead of one that still stores its own.)
+        volatile int *mark = abort + 1;
+        // The next segment that this row tile has rows in: its first tile's number, and
+        // (asked for ahead) this row's mask.
         int k_next = 0;
         uint32_t g_next = 0;
         struct Own {
             Seg s;
-            int k;
             uint32_t g;
             unsigned long long m;
         };
@@ -588,7 +587,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t g = g_next;
                 g_next += o.s.t1 - o.s.t0;
                 if (h < h_begin(k) || h >= h_end(k, o.s)) continue;
-                o.k = k;
                 o.g = g;
                 o.m = 0;
                 const int row0 = PAIR ? h * ROWS : 0;
@@ -605,7 +603,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t th = 0;  // tiles of this row tile
         while (ok && have) {
             s = nx.s;
-            const int k = nx.k;
             uint32_t gg = nx.g;
             unsigned long long m64 = nx.m;
             have = fetch(nx);
@@ -614,7 +611,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int ctx = ctx_s[s.b], n = n_s[s.b], first = ctx - n;
             const bool mine = row < live, wlive = wrow < live;
             if (n < 64) m64 &= (1ull << n) - 1;
-            volatile int *mark = marks + (PAIR ? k & 1 : 2 * h + ((k >> 1) & 1));
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = s.t0; ok && j < s.t1; ++j, ++gg, ++th) {
                 const int b = th & 1, kb = j * TILE;
@@ -640,7 +636,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             if (w.x | w.y | w.z | w.w) st_shared_u4(at, make_uint4(0u, 0u, 0u, 0u));
                         } else if (not_finite2(w.x) || not_finite2(w.y) || not_finite2(w.z) || not_finite2(w.w)) {
                             // Seen by every warp at the segment's end: its P follows this.
-                            *mark = k + 1;
+                            *mark = 1;
                             __threadfence_block();
                             st_shared_u4(at, make_uint4(finite_only(w.x), finite_only(w.y), finite_only(w.z),
                                                         finite_only(w.w)));
@@ -753,7 +749,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[OEMPTY + h]);
-            if (wlive && *mark == k + 1) {
+            if (wlive && *mark) {
                 // What was taken out of V: added to the rows that see it.
                 const int lo = max(0, s.t0 * TILE - first), hi = min(n, s.t1 * TILE - first);  // drafts of the segment
                 const int gr = s.blk * BLOCK + row0 + row;
