@@ -311,7 +311,9 @@ struct RowsShared {
 
 // Reductions over the cluster.  Each warp's value goes to every CTA; two buffers in
 // turn, so one barrier each: a buffer is written again only after the barrier that
-// follows its last reading.  Every thread has the result, and every CTA the same bits.
+// follows its last reading.  Every thread of every CTA has the same bits, as the walk
+// needs (each CTA decides for itself, and they meet at the next barrier): `combine` has to
+// give the same for (p, q) as for (q, p), which the two lanes of an exchange evaluate.
 template <int THREADS, typename F>
 __device__ __forceinline__ float2 cluster_reduce(VerifyShared &s, float2 v, int S, int rank, int &turn, float2 nothing,
                                                  F combine) {
@@ -383,7 +385,8 @@ struct Sum {
 };
 __device__ __forceinline__ float2 join(float2 p, float2 q, float k) {
     const float mm = fmaxf(p.x, q.x), ref = mm == -INFINITY ? 0.f : mm;
-    return make_float2(mm, p.y * fast_exp2((p.x - ref) * k) + q.y * fast_exp2((q.x - ref) * k));
+    // Both products rounded: fused, p.y a + q.y b would not be what q.y b + p.y a is.
+    return make_float2(mm, __fadd_rn(__fmul_rn(p.y, fast_exp2((p.x - ref) * k)), __fmul_rn(q.y, fast_exp2((q.x - ref) * k))));
 }
 
 template <bool FP32, bool PROBS, int THREADS>

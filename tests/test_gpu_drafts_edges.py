@@ -35,3 +35,56 @@ def test_infinite_values_of_drafts_in_runs_of_short_sequences(T, hq, lens):
         out = t.run()
         assert pa.get_device_error() == (0, 0)
         near(host_f64(out), want, tol)
+
+
+# ---------------------------------------------------------------- verification
+
+@pytest.mark.parametrize("batch,n,vocab,dtype", [(1, 12, 151936, torch.bfloat16), (48, 12, 151936, torch.bfloat16),
+                                                 (48, 9, 40000, torch.float32), (200, 64, 2000, torch.float32)])
+def test_verify_lowest_index_of_equal_weights(batch, n, vocab, dtype):
+    """The only child is rejected, and some 200 entries all over the row share the largest
+    weight over noise: the first of them is the token, whichever thread met it."""
+    for seed in range(4 if batch > 1 else 40):
+        rng = np.random.default_rng(seed)
+        logits = torch.from_numpy(rng.standard_normal((batch, 1, vocab)).astype(np.float32)).to(dtype).cuda()
+        noise = torch.full((batch, vocab), 1e6, device="cuda")
+        probs = torch.zeros(batch, 1, vocab, device="cuda")
+        first = []
+        for b in range(batch):
+            at = rng.choice(np.arange(1, vocab), 200, replace=False)
+            logits[b, 0, at], noise[b, at] = 3.0, 1.0
+            first.append(int(at.min()))
+        probs[:, :, 0] = 1.0
+        tokens = torch.zeros(batch, n, dtype=torch.int32, device="cuda")
+        r = pa.verify_drafts(logits.repeat(1, n, 1), tokens, None, torch.full((batch, n), 0.99, device="cuda"), noise,
+                             torch.ones(batch, device="cuda"), draft_probs=probs.repeat(1, n, 1))
+        assert r.counts.tolist() == [1] * batch and r.tokens[:, 0].tolist() == first
+    assert pa.get_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("batch,n,vocab,drawn", [(4, 12, 151936, True), (48, 12, 40000, True), (48, 12, 40000, False),
+                                                 (1, 64, 40000, False), (8, 7, 40000, True)])
+def test_verify_decisions_next_to_the_border(batch, n, vocab, drawn):
+    """u q within a few units in the last place of w at every node: either way is right,
+    but all CTAs of a sequence have to go the same (they would wait for each other else)."""
+    rng = np.random.default_rng(batch + n)
+    logits = torch.from_numpy(rng.standard_normal((batch, n, vocab)).astype(np.float32)).cuda()
+    p = torch.softmax(logits.double(), -1)
+    tokens = torch.from_numpy(rng.integers(0, vocab, (batch, n)).astype(np.int32)).cuda()
+    at = tokens[:, 1:].long().unsqueeze(-1)
+    px = p[:, :-1].gather(2, at)[..., 0]           # of each node's child, in a chain
+    nudge = torch.from_numpy(1 + rng.integers(-4, 5, (batch, n - 1)) * 2.0 ** -24).cuda()
+    u, probs = torch.zeros(batch, n, device="cuda"), None
+    if drawn:
+        u[:, 1:] = 0.5
+        probs = torch.zeros(batch, n - 1, vocab, device="cuda").scatter_(2, at, (2 * px * nudge).float().unsqueeze(-1))
+    else:
+        u[:, 1:] = (px * nudge).float()
+    for seed in range(5):
+        noise = torch.from_numpy(rng.exponential(size=(batch, vocab)).astype(np.float32)).cuda()
+        r = pa.verify_drafts(logits, tokens, None, u, noise, torch.ones(batch, device="cuda"), draft_probs=probs)
+        assert pa.get_device_error() == (0, 0)
+        for b in range(batch):
+            c = int(r.counts[b])
+            assert 1 <= c <= n and r.nodes[b].tolist() == list(range(c)) + [-1] * (n - c)
+            assert r.tokens[b, :c - 1].tolist() == tokens[b, 1:c].tolist() and 0 <= int(r.tokens[b, c - 1]) < vocab
