@@ -530,6 +530,21 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
         }
     }
     __syncthreads();
+    // The sum of the probabilities of all but the rejected candidates.  (Seldom asked for:
+    // one logit a thread.)
+    auto rest = [&](int64_t row) -> float {
+        float acc = 0.f;
+#pragma unroll 1
+        for (int i = lo + tid; i < hi; i += THREADS) {
+            bool out = false;
+#pragma unroll 1
+            for (unsigned long long g = gone; g; g &= g - 1) out = out || s.token[__ffsll(g) - 1] == i;
+            if (!out) acc += fast_exp2((logit_at<FP32>(a, row, i) - m) * k);
+        }
+        return cluster_reduce<THREADS>(s, make_float2(acc, 0.f), S, rank, turn, make_float2(0.f, 0.f),
+                                       [](float2 p, float2 q) { return make_float2(p.x + q.x, 0.f); })
+                   .x * inv_l;
+    };
     while (true) {
         // ---- maximum and sum of the current node's row
         const int64_t row = (int64_t)b * a.nodes + cur;
@@ -572,7 +587,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
             __syncthreads();
         }
         // ---- its children in order
-        float left = 1.f;  // s
+        float left = 1.f, from = 1.f;  // s; what it was when it was last a sum
         sub = 0.f;
         gone = 0;
         int next = -1;
@@ -594,6 +609,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
             if (!PROBS) {
                 left = fmaxf(left - w, 0.f);
                 gone |= 1ull << c;
+                // Five bits of s lost to the difference (it is then off by 2^-17 or so): summed anew.
+                if (left < from * (1.f / 32.f) && (todo & (todo - 1))) left = from = rest(row);
                 continue;
             }
             sub += left;

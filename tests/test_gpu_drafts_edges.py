@@ -7,7 +7,7 @@ import torch
 import paged_kv_cache_store_gb300 as pa
 from oracle import drafts as OD
 from gpu_util import host_f64
-from test_gpu_drafts import Tree, f64, near
+from test_gpu_drafts import Tree, f64, near, place
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,48 @@ def test_verify_decisions_next_to_the_border(batch, n, vocab, drawn):
             c = int(r.counts[b])
             assert 1 <= c <= n and r.nodes[b].tolist() == list(range(c)) + [-1] * (n - c)
             assert r.tokens[b, :c - 1].tolist() == tokens[b, 1:c].tolist() and 0 <= int(r.tokens[b, c - 1]) < vocab
+
+
+@pytest.mark.parametrize("vocab,n,dtype", [(500, 5, torch.float32), (20011, 5, torch.float32), (5003, 40, torch.float32),
+                                           (151936, 9, torch.float32), (1203, 7, torch.bfloat16)])
+def test_verify_candidates_behind_one_that_held_nearly_everything(vocab, n, dtype):
+    """The first candidate, rejected, has probability 1 - 2^-8 .. 1 - 2^-20; the others'
+    decisions are about what is left, of which u w are 4 % from the border.
+
+    What is left is a sum of its own, not the difference from 1: the kernel's probabilities
+    are off by under 2^-17, and 2^-14 is asked of a margin elsewhere."""
+    batch = 40
+    rng = np.random.default_rng(vocab + n)
+    logits = rng.standard_normal((batch, n, vocab)) * 2
+    tokens = np.stack([rng.permutation(vocab)[:n] for _ in range(batch)]).astype(np.int32)
+    parents = np.zeros((batch, n), np.int32)
+    parents[:, 0] = -1
+    u = np.full((batch, n), 1 - 2.0 ** -24, np.float32)
+    for b in range(batch):
+        left = 2.0 ** -rng.uniform(8, 20)
+        logits[b, 0, tokens[b, 2:]] = 6 + rng.standard_normal(n - 2)
+        others = np.delete(np.arange(vocab), tokens[b, 1])
+        logits[b, 0, tokens[b, 1]] = np.log(np.exp(logits[b, 0, others]).sum() * (1 - left) / left)
+    lg = place(logits.astype(np.float32), dtype)
+    z = lg[:, 0].double().cpu().numpy()
+    for b in range(batch):
+        w = np.exp(z[b] - z[b].max())
+        for c in range(2, n):
+            w[tokens[b, c - 1]] = 0
+            ratio = w[tokens[b, c]] / w.sum()
+            if c == n - 1 or rng.random() < 0.5 / n:
+                u[b, c] = ratio * 0.96              # kept
+                break
+            u[b, c] = min(ratio * 1.04, 1 - 2.0 ** -24)
+    noise = rng.exponential(size=(batch, vocab)).astype(np.float32)
+    # The oracle without that candidate: the same residual, and margins of the others alone.
+    z = lg.double().cpu().numpy()
+    z[np.arange(batch), 0, tokens[:, 1]] = -np.inf
+    want = OD.verify(z, tokens, parents, u, noise, np.ones(batch))
+    r = pa.verify_drafts(lg, torch.from_numpy(tokens).cuda(), torch.from_numpy(parents).cuda(),
+                         torch.from_numpy(u).cuda(), place(noise, torch.float32), torch.ones(batch, device="cuda"))
+    assert pa.get_device_error() == (0, 0)
+    sure = want[3] > 2.0 ** -14
+    assert sure.mean() > 0.9 and np.all(want[2] <= 2) and want[2].sum() > batch
+    for got, w in zip(r, want):
+        assert np.array_equal(got.cpu().numpy()[sure], w[sure])
