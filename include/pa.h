@@ -639,7 +639,8 @@ PA_API pa_status pa_rope_store_kvcache(void *out_q, int64_t out_q_row_stride, co
  *   tree_mask     bit j set where j is i or an ancestor of i
  *   positions     context_lens[b] - n + depth of i (the root's depth is 0)
  *   slot_mapping  slot of position context_lens[b] - n + i (-1 where the table
- *                 holds none); padding: mask 0, position 0, slot -1
+ *                 holds none, or one whose slots do not fit int32, recorded as
+ *                 PA_DEV_BAD_BLOCK); padding: mask 0, position 0, slot -1
  * parents int32 [batch, num_drafts] (entry 0 of a row is not read), NULL: chains.
  * A parent that is not an earlier node ends the walk up (PA_DEV_BAD_TREE); lengths
  * that do not fit make the row padding (PA_DEV_BAD_CONTEXT).

@@ -25,6 +25,7 @@
 // the walk (kAtOnceBytes).
 #include <float.h>
 #include <math.h>
+#include <stdint.h>
 
 #include <algorithm>
 #include <atomic>
@@ -87,7 +88,9 @@ __global__ void __launch_bounds__(128) tree_metadata_kernel(const __grid_constan
     a.mask[t] = m;
     a.positions[t] = ctx - n + depth;
     const int p = ctx - n + i, blk = __ldg(a.bt + (int64_t)b * a.max_blocks + p / a.block_size);
-    a.slots[t] = blk < 0 ? -1 : blk * a.block_size + p % a.block_size;
+    const int64_t slot = (int64_t)blk * a.block_size + p % a.block_size;
+    if (slot > INT32_MAX) record_error(a.err, PA_DEV_BAD_BLOCK, (long long)b * a.max_blocks + p / a.block_size);
+    a.slots[t] = slot < 0 || slot > INT32_MAX ? -1 : (int32_t)slot;
 }
 
 // ---------------------------------------------------------------------------

@@ -6,7 +6,7 @@ import torch
 
 import paged_kv_cache_store_gb300 as pa
 from oracle import drafts as OD
-from gpu_util import host_f64
+from gpu_util import dev_i32, host_f64
 from test_gpu_drafts import Tree, f64, near, place
 
 pytestmark = pytest.mark.gpu
@@ -35,6 +35,24 @@ def test_infinite_values_of_drafts_in_runs_of_short_sequences(T, hq, lens):
         out = t.run()
         assert pa.get_device_error() == (0, 0)
         near(host_f64(out), want, tol)
+
+
+def test_metadata_of_block_ids_whose_slots_do_not_fit():
+    """No slot, rather than one that wraps into another sequence's rows."""
+    for bad, B in ((1 << 28, 16), (1 << 27, 16), ((1 << 31) - 1, 256), ((1 << 28) + 3, 48)):
+        bt = np.array([[5, 7], [4, bad]], np.int32)
+        ctx = np.array([B + 2, B + 2], np.int32)
+        m = pa.tree_metadata(None, dev_i32(ctx), dev_i32(bt), B, num_drafts=4)
+        assert pa.get_device_error() == (pa.PA_DEV_BAD_BLOCK, 3)
+        slots = m.slot_mapping.view(2, 4).tolist()
+        assert slots[0] == [5 * B + B - 2, 5 * B + B - 1, 7 * B, 7 * B + 1]
+        assert slots[1] == [4 * B + B - 2, 4 * B + B - 1, -1, -1]
+        assert m.positions.view(2, 4)[1].tolist() == [B - 2, B - 1, B, B + 1]
+    # The last slot that fits.
+    last = dev_i32([[(1 << 27) - 1]])
+    m = pa.tree_metadata(None, dev_i32([16]), last, 16, num_drafts=2)
+    assert m.slot_mapping.tolist() == [(1 << 31) - 2, (1 << 31) - 1]
+    assert pa.get_device_error() == (0, 0)
 
 
 # ---------------------------------------------------------------- verification
