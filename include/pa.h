@@ -584,8 +584,9 @@ PA_API pa_status pa_decode_store_q8(void *out, const void *q, int64_t q_row_stri
 /*
  * pa_rope_frequencies -- rotary frequencies (host code; freqs and gain are host
  * pointers).  freqs[i], i < rotary_dim/2, are turns per position as fractions of
- * 2^64, so that position * freqs[i] modulo 2^64 is the exact turn whatever the
- * position: f_i = theta^(-2i/R) radians per position, and with `factor` s:
+ * 2^64, rounded to the nearest, so that position * freqs[i] modulo 2^64 is the turn to
+ * within 2^-34 at the farthest position: f_i = theta^(-2i/R) radians per position, and
+ * with `factor` s:
  *   PA_ROPE_LINEAR  f_i / s
  *   PA_ROPE_NTK     theta * s^(R/(R-2)) in place of theta
  *   PA_ROPE_YARN    f_i (1 - r_i) + f_i / s * r_i, r_i = clamp((i - lo)/(hi - lo), 0, 1)

@@ -8,10 +8,11 @@
 //   (x1 cos a - x2 sin a, x2 cos a + x1 sin a) * gain,  a = 2 pi p f_i,
 // f_i in turns per position; everything in fp32, rounded once to bf16.
 //
-// The angle: f_i is a fraction of 2^64 and p * f_i is taken modulo 2^64, so the
-// turns are exact for every 32-bit position; the signed result is rounded once
-// to fp32 (an angle error of at most 2^-25 pi) before sincospif.  The product in
-// fp32 would be off by 4e-3 at position 10^5 and by 3e-2 at 10^6.
+// The angle: f_i is a fraction of 2^64, rounded to the nearest, and p * f_i is taken
+// modulo 2^64, so the turns are off by |p| 2^-65 (2^-34 at the farthest 32-bit
+// position); the signed result is rounded once to fp32 (an angle error of at most
+// 2^-25 pi) before sincospif.  The product in fp32 would be off by 4e-3 at position 10^5
+// and by 3e-2 at 10^6.
 //
 // Layout: eight lanes per head, two 16-byte chunks a lane, chosen so that both
 // halves of a pair are in one lane: chunks 8l and R/2 + 8l of the rotated part
@@ -252,6 +253,39 @@ __global__ void __launch_bounds__(ROPE_THREADS, 2) rope_kernel(const __grid_cons
     }
 }
 
+// Numbers of some 105 bits, the sum of two doubles: a frequency's 64 bits are more than one
+// holds.  (A sum's and a product's rounding error is a double, which fma and differences
+// give exactly.)
+struct Wide {
+    double hi, lo;
+};
+Wide norm(double a, double b) {  // |a| >= |b|
+    const double s = a + b;
+    return {s, b - (s - a)};
+}
+Wide add(Wide a, Wide b) {
+    const double s = a.hi + b.hi, t = s - a.hi;
+    return norm(s, (a.hi - (s - t)) + (b.hi - t) + a.lo + b.lo);
+}
+Wide mul(Wide a, Wide b) {
+    const double p = a.hi * b.hi;
+    return norm(p, fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+Wide div(Wide a, double b) {
+    const double q = a.hi / b, rest = fma(-q, b, a.hi) + a.lo;
+    return norm(q, rest / b);
+}
+// a^(-1/n): the root of a x^n = 1, by Newton's steps from double's.
+Wide inverse_root(double a, int n) {
+    Wide x = {pow(a, -1.0 / n), 0.0};
+    for (int step = 0; step < 2; ++step) {
+        Wide y = {-a, 0.0};  // to -a x^n, from the large end, so that nothing underflows
+        for (int i = 0; i < n; ++i) y = mul(y, x);
+        x = add(x, div(mul(x, add({1.0, 0.0}, y)), n));
+    }
+    return x;
+}
+
 template <bool INTER, bool NORM, int U>
 pa_status launch_rope(const RopeArgs &a, int sms, cudaStream_t stream) {
     const int64_t units = (int64_t)a.tokens * a.parts, warps = ROPE_THREADS / 32;
@@ -324,15 +358,23 @@ pa_status pa_rope_frequencies(uint64_t *freqs, float *gain, int32_t rotary_dim, 
         lo = std::max(floor(r * log(original_context / (beta_fast * two_pi)) / (2 * log(theta))), 0.0);
         hi = std::min(ceil(r * log(original_context / (beta_slow * two_pi)) / (2 * log(theta))), r - 1);
     }
-    if (scaling == PA_ROPE_NTK) theta *= pow(factor, r / (r - 2));
-    for (int i = 0; i < rotary_dim / 2; ++i) {
-        double f = pow(theta, -2.0 * i / r);
-        if (scaling == PA_ROPE_LINEAR) f /= factor;
-        if (scaling == PA_ROPE_YARN) {
-            const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
-            f = f * (1 - ramp) + f / factor * ramp;
+    // f_i is the i-th power of theta^(-2/R), for ntk times s^(-2/(R-2)).
+    Wide step = inverse_root(theta, rotary_dim / 2);
+    if (scaling == PA_ROPE_NTK) step = mul(step, inverse_root(factor, rotary_dim / 2 - 1));
+    Wide f = {0.15915494309189535, -9.839338337591243e-18};  // 1 / (2 pi)
+    for (int i = 0; i < rotary_dim / 2; ++i, f = mul(f, step)) {
+        Wide x = f;
+        if (scaling == PA_ROPE_LINEAR) x = div(f, factor);
+        if (scaling == PA_ROPE_YARN) {  // f (1 - ramp) + f / s * ramp
+            if (i >= hi) {
+                x = i > lo ? div(f, factor) : f;
+            } else if (i > lo) {
+                const Wide short_part = div(mul(f, {hi - i, 0.0}), hi - lo);
+                x = add(short_part, div(div(mul(f, {i - lo, 0.0}), hi - lo), factor));
+            }
         }
-        freqs[i] = static_cast<uint64_t>(f / two_pi * 18446744073709551616.0);  // f <= 1: below 2^62
+        const double whole = rint(x.hi * 0x1p64);  // (f <= 1: below 2^62)
+        freqs[i] = static_cast<uint64_t>(whole) + static_cast<uint64_t>(llrint((x.hi * 0x1p64 - whole) + x.lo * 0x1p64));
     }
     *gain = static_cast<float>(scaling == PA_ROPE_YARN ? 0.1 * log(factor) + 1.0 : 1.0);
     return PA_OK;
