@@ -1023,12 +1023,16 @@ pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, const v
     for (int n = 2; n <= num_kv_heads && n <= grid; ++n)
         if (num_kv_heads % n == 0 && grid / n * n * 10 >= grid * 9) a.lanes = n;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    // Tables too short for a cut: one launch.  So too where every item can have a CTA of its
-    // own and at most twice that length (4 sequences of up to 600 keys, 5 drafts: 12.0 us
-    // instead of 11.4, but 14.9 instead of 18.1 a call from Python, which the launches bound).
+    // Tables too short for a cut: one launch.  So too two tiles more, which is what the second
+    // launch costs, where every item has a CTA of its own (whatever the lengths: the
+    // table's width may be one sequence's alone).  Device us, one launch and two, the second
+    // of which combines nothing up to here: 1 and 4 sequences, 8 kv heads, 5 drafts, 512 keys
+    // 10.4 and 11.4, 10.9 and 12.0; 64 drafts, 768 keys 19.9 and 21.5.  A tile more, which
+    // is cut: 5 drafts, 576 keys 11.1 and 10.0, 11.6 and 11.5; 64 drafts, 832 keys 20.9 and
+    // 15.2, 21.3 and 23.2.
     const int64_t longest = (keys + TILE - 1) / TILE;
     a.whole = longest <= cut_tiles(l.pair) ||
-              (longest <= 2 * cut_tiles(l.pair) && (int64_t)batch * num_kv_heads * blocks <= grid);
+              (longest <= cut_tiles(l.pair) + 2 && (int64_t)batch * num_kv_heads * blocks <= grid);
     const bool is_short = a_seq * batch <= 512 * grid;  // tiles a CTA at most
     st = l.pair ? launch_tree<true>(tmq, tmk, tmv, a, (int)grid, is_short, cs)
                 : launch_tree<false>(tmq, tmk, tmv, a, (int)grid, is_short, cs);

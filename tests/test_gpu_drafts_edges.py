@@ -37,6 +37,21 @@ def test_infinite_values_of_drafts_in_runs_of_short_sequences(T, hq, lens):
         near(host_f64(out), want, tol)
 
 
+@pytest.mark.parametrize("T,hq,hkv,tiles", [(5, 8, 2, 8), (5, 8, 2, 9), (5, 8, 2, 12), (5, 8, 2, 13), (40, 8, 2, 12),
+                                            (40, 8, 2, 13), (64, 8, 1, 12), (64, 8, 1, 13), (40, 8, 2, 20),
+                                            (40, 8, 2, 21)])
+def test_block_tables_around_the_width_that_one_launch_serves(T, hq, hkv, tiles):
+    """Every item with a CTA of its own, and more items than CTAs; one sequence of the
+    table's width, others shorter."""
+    rng = np.random.default_rng(tiles)
+    for batch in (1, 2, 5, 80):
+        before = rng.integers(0, 64 * tiles - T + 1, batch)
+        before[0] = 64 * tiles - T
+        t = Tree(tiles + batch, before, T, hq, hkv, 64)
+        t.bt = np.ascontiguousarray(t.bt[:, :tiles])
+        t.check()
+
+
 def test_metadata_of_block_ids_whose_slots_do_not_fit():
     """No slot, rather than one that wraps into another sequence's rows."""
     for bad, B in ((1 << 28, 16), (1 << 27, 16), ((1 << 31) - 1, 256), ((1 << 28) + 3, 48)):
