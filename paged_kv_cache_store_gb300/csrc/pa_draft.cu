@@ -533,16 +533,32 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
         }
     }
     __syncthreads();
-    // The sum of the probabilities of all but the rejected candidates.  (Seldom asked for:
-    // one logit a thread.)
+    // The sum of the probabilities of all but the rejected candidates, 16 bytes at a time.
     auto rest = [&](int64_t row) -> float {
+        constexpr int N = 16 / SIZE;
+        const char *r = static_cast<const char *>(a.logits) + row * a.logits_stride * SIZE;
         float acc = 0.f;
 #pragma unroll 1
-        for (int i = lo + tid; i < hi; i += THREADS) {
-            bool out = false;
+        for (int i = lo + N * tid; i < hi; i += N * THREADS) {
+            float x[N];
+            if (i + N <= hi) {
+                const uint4 w = ld16(r + (int64_t)i * SIZE);
+                const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < N; ++e) x[e] = tame(FP32 ? __uint_as_float(q[e % 4]) : (e & 1) ? bf16hi(q[e / 2]) : bf16lo(q[e / 2]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) x[e] = i + e < hi ? logit_at<FP32>(a, row, i + e) : -INFINITY;
+            }
 #pragma unroll 1
-            for (unsigned long long g = gone; g; g &= g - 1) out = out || s.token[__ffsll(g) - 1] == i;
-            if (!out) acc += fast_exp2((logit_at<FP32>(a, row, i) - m) * k);
+            for (unsigned long long g = gone; g; g &= g - 1) {
+                const int at = s.token[__ffsll(g) - 1] - i;
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (at == e) x[e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc += fast_exp2((x[e] - m) * k);
         }
         return cluster_reduce<THREADS>(s, make_float2(acc, 0.f), S, rank, turn, make_float2(0.f, 0.f),
                                        [](float2 p, float2 q) { return make_float2(p.x + q.x, 0.f); })
@@ -612,8 +628,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
             if (!PROBS) {
                 left = fmaxf(left - w, 0.f);
                 gone |= 1ull << c;
-                // Five bits of s lost to the difference (it is then off by 2^-17 or so): summed anew.
-                if (left < from * (1.f / 32.f) && (todo & (todo - 1))) left = from = rest(row);
+                // Seven bits of s lost to the difference, which is off by some 2^-23 of what it
+                // was taken from: summed anew.
+                if (left < from * (1.f / 128.f) && (todo & (todo - 1))) left = from = rest(row);
                 continue;
             }
             sub += left;
