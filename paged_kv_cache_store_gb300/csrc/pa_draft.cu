@@ -190,11 +190,16 @@ constexpr int V_MAX_CLUSTER = 16;
 // A sequence's rows are read all at once, ahead of the walk, where a CTA's share of them
 // is small (what a row costs is then latency: 32 chains of 6 nodes and 8000 logits 17.2
 // us one after the other, 11.6 at once) or where they are a short drawn chain, whose
-// path holds most of them (64 x 6 x 151936: 52.3 and 48.9 us; 32 x 6: 38.6 and 32.2;
-// 128 x 4: 66.9 and 67.3).  Trees of that size have most rows off the path (64 x 8:
-// 47.5 us one after the other, 63.6 at once).
+// path holds most of them, of so few sequences that each has eight CTAs at least.  Chains
+// of 151936 logits, 70 % of the drafts kept, one after the other and at once: 8 x 8 32.3
+// and 26.4 us, 16 x 8 32.4 and 32.6, 32 x 6 35.9 and 31.8, 64 x 6 50.5 and 49.1, 64 x 8
+// 58.8 and 56.8; with four CTAs and two 128 x 6 81.7 and 85.5, 128 x 8 94.1 and 100.5,
+// 256 x 8 164.8 and 185.4, as HBM then brings the rows behind a rejected draft at the cost
+// of others.  All kept, 64 x 6 55.2 and 48.7, 256 x 8 187.7 and 178.5; all rejected 27.9
+// and 48.7, 89.1 and 186.1.  Trees of that size have most rows off the path (64 x 8: 47.5
+// us one after the other, 63.6 at once).
 constexpr int64_t kAtOnceBytes = 128 << 10;
-constexpr int kAtOnceChain = 8;
+constexpr int kAtOnceChain = 8, kAtOnceCtas = 8;
 constexpr float E_MIN = 1e-10f;   // the sampler's clamp of the exponential numbers
 
 struct VerifyArgs {
@@ -456,7 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
         return y > -1000.f ? ldexpf(exp2f((y - whole) + rest), (int)whole) * inv_l : 0.f;
     };
     const bool chain = __syncthreads_and(tid == 0 || tid >= n || s.parent[tid] == tid - 1);
-    const bool all = (int64_t)n * chunk * SIZE <= kAtOnceBytes || (PROBS && chain && n <= kAtOnceChain);
+    const bool all = (int64_t)n * chunk * SIZE <= kAtOnceBytes || (PROBS && chain && n <= kAtOnceChain && S >= kAtOnceCtas);
     if (all) {
         if (tid < n && s.parent[tid] >= 0) {
             const int p = s.parent[tid], x = s.token[tid];

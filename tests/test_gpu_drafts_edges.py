@@ -7,7 +7,7 @@ import torch
 import paged_kv_cache_store_gb300 as pa
 from oracle import drafts as OD
 from gpu_util import dev_i32, host_f64
-from test_gpu_drafts import Tree, f64, near, place
+from test_gpu_drafts import Tree, check_verify, f64, near, place, verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +166,12 @@ def test_verify_candidates_behind_one_that_held_nearly_everything(vocab, n, dtyp
     assert sure.mean() > 0.9 and np.all(want[2] <= 2) and want[2].sum() > batch
     for got, w in zip(r, want):
         assert np.array_equal(got.cpu().numpy()[sure], w[sure])
+
+
+@pytest.mark.parametrize("batch,n,vocab,dtype", [(30, 8, 32000, torch.bfloat16), (70, 8, 32000, torch.bfloat16),
+                                                 (130, 7, 32000, torch.float32), (310, 6, 40000, torch.bfloat16)])
+def test_verify_drawn_chains_of_few_and_many_sequences(batch, n, vocab, dtype):
+    """Chains whose rows are read at once while each sequence has several CTAs, and one
+    after the other above that; drafts that are mostly kept, and mostly rejected."""
+    for close in (0.1, 3.0):
+        check_verify(verify_case(batch + n, batch, n, vocab, dtype, True, chain=True, close=close))
