@@ -772,29 +772,42 @@ int ctas_per_seq(int batch, int vocab, int sms) {
 
 template <bool FP32, bool PROBS, int THREADS>
 pa_status launch_verify(VerifyArgs &a, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.cluster, (unsigned)a.batch);
     cfg.blockDim = dim3(THREADS);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)a.cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (a.cluster > 8) {  // per (device, variant): the attribute has been set (setting it takes 3 us)
-        static std::atomic<int> done[64];
+    if (a.cluster > 8) {
+        // Allowed once per (device, variant), which takes 3 us, and the device asked whether
+        // it can run such a cluster: where its SMs lie in smaller groups (a partitioned
+        // device) the portable size serves.
+        static std::atomic<int> known[64];  // 0: not asked, 1: it can, 2: it cannot
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
         if (dev < 0 || dev >= 64) return fail(PA_ERR_UNSUPPORTED, "device %d", dev);
-        if (!done[dev].load(std::memory_order_acquire)) {
+        int can = known[dev].load(std::memory_order_acquire);
+        if (can == 0) {
+            int clusters = 0;
+            cfg.numAttrs = 1;
             e = cudaFuncSetAttribute(verify_kernel<FP32, PROBS, THREADS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return cuda_fail(e, "verify_kernel");
-            done[dev].store(1, std::memory_order_release);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, verify_kernel<FP32, PROBS, THREADS>, &cfg);
+            cfg.numAttrs = 2;
+            if (e != cudaSuccess) (void)cudaGetLastError();
+            can = e == cudaSuccess && clusters > 0 ? 1 : 2;
+            known[dev].store(can, std::memory_order_release);
+        }
+        if (can == 2) {
+            a.cluster = 8;
+            cfg.gridDim.x = attr[0].val.clusterDim.x = 8;
         }
     }
     const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<FP32, PROBS, THREADS>, a);

@@ -1,11 +1,17 @@
 """Speculative decoding where it can go wrong: calls that the documentation allows
 and that the tests of each entry point's ordinary range do not reach."""
+import ctypes as C
+import glob
+import os
+import subprocess
+
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_cache_store_gb300 as pa
 from oracle import drafts as OD
+from paged_kv_cache_store_gb300 import build as pabuild
 from gpu_util import dev_i32, host_f64
 from test_gpu_drafts import Tree, check_verify, f64, near, place, verify_case
 
@@ -175,3 +181,54 @@ def test_verify_drawn_chains_of_few_and_many_sequences(batch, n, vocab, dtype):
     after the other above that; drafts that are mostly kept, and mostly rejected."""
     for close in (0.1, 3.0):
         check_verify(verify_case(batch + n, batch, n, vocab, dtype, True, chain=True, close=close))
+
+
+NO_WIDE_CLUSTERS = """
+#include <cuda_runtime.h>
+template <typename K>
+cudaError_t fake_max_clusters(int *n, K *, const cudaLaunchConfig_t *cfg) {
+    *n = 1;
+    for (unsigned i = 0; i < cfg->numAttrs; ++i)
+        if (cfg->attrs[i].id == cudaLaunchAttributeClusterDimension && cfg->attrs[i].val.clusterDim.x > 8) *n = 0;
+    return cudaSuccess;
+}
+template <typename... E, typename... A>
+cudaError_t fake_launch(const cudaLaunchConfig_t *cfg, void (*kernel)(E...), A &&...args) {
+    int n = 0;
+    fake_max_clusters(&n, kernel, cfg);
+    return n ? cudaLaunchKernelEx(cfg, kernel, static_cast<A &&>(args)...) : cudaErrorInvalidClusterSize;
+}
+#define cudaOccupancyMaxActiveClusters fake_max_clusters
+#define cudaLaunchKernelEx fake_launch
+"""
+
+
+def test_verify_on_a_device_without_clusters_of_16(tmp_path):
+    """The calls that ask for such clusters are faked, to say that the device has none: up to
+    four sequences of a large vocabulary are then served by clusters of eight."""
+    pabuild.build()
+    fake, obj, lib = tmp_path / "fake.h", tmp_path / "pa_draft.o", tmp_path / "libpa_fake.so"
+    fake.write_text(NO_WIDE_CLUSTERS)
+    nvcc = [pabuild.nvcc()] + pabuild.ARCH
+    subprocess.run(nvcc + pabuild.NVCC_FLAGS + ["-include", str(fake), "-c", os.path.join(pabuild.CSRC, "pa_draft.cu"),
+                                                "-o", str(obj)], check=True, capture_output=True)
+    others = [o for o in glob.glob(os.path.join(pabuild.BUILD, "*.o")) if os.path.basename(o) != "pa_draft.o"]
+    subprocess.run(nvcc + ["-shared", "-o", str(lib), str(obj)] + others, check=True, capture_output=True)
+    call = C.CDLL(str(lib)).pa_verify_drafts
+    call.restype, call.argtypes = pa.SIGNATURES["pa_verify_drafts"]
+    for batch, n, drawn in ((1, 6, True), (4, 20, False), (3, 12, True)):
+        s = verify_case(batch * n, batch, n, 50000, torch.bfloat16, drawn, close=0.2)
+        want = check_verify(s)
+        lg, noise = s["logits"], place(s["noise"], torch.float32)
+        tok, par = dev_i32(s["tokens"]), dev_i32(s["parents"])
+        u, temps = torch.from_numpy(s["u"]).cuda(), torch.from_numpy(s["temps"]).cuda()
+        q = place(s["probs"], torch.float32) if drawn else None
+        out = [torch.empty_like(tok), torch.empty_like(tok), torch.empty(batch, dtype=torch.int32, device="cuda")]
+        for _ in range(2):  # asked, and known
+            rc = call(*(x.data_ptr() for x in out), lg.data_ptr(), lg.stride(1), 0, tok.data_ptr(), par.data_ptr(),
+                      u.data_ptr(), noise.data_ptr(), noise.stride(0), temps.data_ptr(), q.data_ptr() if drawn else None,
+                      q.stride(1) if drawn else 0, n if drawn else 0, None, batch, n, 50000,
+                      torch.cuda.current_stream().cuda_stream)
+            assert rc == pa.PA_OK
+            r = pa.verify_drafts(lg, tok, par, u, noise, temps, draft_probs=q)
+            assert all(torch.equal(x, y) for x, y in zip(out, r)) and out[2].tolist() == want.tolist()
