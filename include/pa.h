@@ -604,7 +604,8 @@ PA_API pa_status pa_rope_frequencies(uint64_t *freqs, float *gain, int32_t rotar
  *   x <- x / sqrt(mean(x^2) + eps) * weight,
  * then the pairs (x[i], x[i + R/2]), or (x[2i], x[2i+1]) when interleaved, i < R/2,
  * R = rotary_dim, are rotated by positions[t] * f_i and multiplied by gain; the
- * values from R on are not rotated.  fp32 throughout, one rounding to bf16.
+ * values from R on are not rotated.  fp32 throughout, one rounding to bf16; the squares
+ * too, so that a normed head holds values below 10^18, and above 10^-18 if eps is 0.
  *   out_q, out_k    bf16; token t's Hq*128 (Hkv*128) values at out + t*stride.
  *                   out_q may be q itself with its stride, out_k may be key.
  *   q, key          bf16, row strides in elements: >= a token's values, multiples
@@ -661,7 +662,8 @@ PA_API pa_status pa_tree_metadata(int64_t *tree_mask, int32_t *positions, int32_
  * matter, NaN and infinities included.  The weights are rounded to bf16, and
  * normalised by the sum of the rounded ones.  The same call gives the same bits
  * again; a row's last bits depend on the batch, by which the keys are cut.
- *   out           bf16 [batch, num_drafts, Hq, 128] contiguous; zeros for i >= n.
+ *   out           bf16 [batch, num_drafts, Hq, 128] contiguous, overlaps no input;
+ *                 zeros for i >= n.
  *   q             bf16; the Hq*128 values of (b, i) at q + (b*num_drafts + i)*q_row_stride.
  *   tree_mask     int64 [batch, num_drafts].
  *   draft_lens    int32 [batch] or NULL.  Lengths that do not fit (ctx < n among
@@ -709,9 +711,13 @@ PA_API pa_status pa_decode_tree(void *out, const void *q, int64_t q_row_stride, 
  *   draft_probs  fp32, row (b*probs_rows + v), row stride a multiple of 4, or NULL;
  *                probs_rows >= num_nodes - 1 (the last node has no children).
  *   draft_lens   int32 [batch], nodes of each sequence (0: padding, count 0), or NULL.
- * NaN logits count as -inf, +inf as the largest number.  num_nodes <= 64, batch <=
- * 65535, vocab <= 2^30; logits, exp_noise and draft_probs 16-byte aligned.  A small
- * temperature (1e-6) gives greedy verification.  The outputs overlap no input.
+ * NaN logits count as -inf, +inf as the largest number; a row of -inf alone keeps no
+ * child and draws token 0, as pa_sample_gumbel does.  exp_noise holds no NaN (one
+ * counts as 1e-10).  p, w and s are in fp32: a decision whose two sides differ by less
+ * than 2^-14 of the larger (of p(x), where w is a difference) may go either way.
+ * num_nodes <= 64, batch <= 65535, vocab <= 2^30; logits, exp_noise and draft_probs
+ * 16-byte aligned.  A small temperature (1e-6) gives greedy verification.  The outputs
+ * overlap no input.
  */
 PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *out_nodes, int32_t *out_counts, const void *logits,
                                   int64_t logits_row_stride, int32_t logits_is_fp32, const int32_t *tokens,
@@ -728,8 +734,8 @@ PA_API pa_status pa_verify_drafts(int32_t *out_tokens, int32_t *out_nodes, int32
  * = 0, ascending, below n; the first one that is not ends its row's moves
  * (PA_DEV_BAD_TREE).  The context is then base + counts[b] keys long.  Rows of other
  * positions stay as they are.  The rows from base on are the sequence's own: no other
- * sequence of the call holds their slots (a shared prefix lies before them).  A block id outside [0, num_blocks): that row is not
- * moved (PA_DEV_BAD_BLOCK).
+ * sequence of the call holds their slots (a shared prefix lies before them).  A block
+ * id outside [0, num_blocks): that row is not moved (PA_DEV_BAD_BLOCK).
  *   k_cache, v_cache  the first layer's pools; the next layer's follow
  *                     k_layer_stride / v_layer_stride elements on (multiples of 8).
  * Bit-exact.  num_nodes <= 64.
