@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_kernel(const _
         }
     }
     const bool bad_t = !(T > 1e-10f), bad_n = n < 0 || n > a.nodes;
-    if (lead && bad_t) record_error(a.err, PA_DEV_BAD_TEMPERATURE, b);
+    if (lead && bad_t && n > 0) record_error(a.err, PA_DEV_BAD_TEMPERATURE, b);  // (a padded row's may be anything)
     if (lead && bad_n) record_error(a.err, PA_DEV_BAD_CONTEXT, b);
     if (bad_n || bad_t) n = 0;
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -13,7 +13,7 @@ import paged_kv_cache_store_gb300 as pa
 from oracle import drafts as OD
 from paged_kv_cache_store_gb300 import build as pabuild
 from gpu_util import dev_i32, host_f64
-from test_gpu_drafts import Tree, check_verify, f64, near, place, verify_case
+from test_gpu_drafts import Tree, check_verify, f64, near, place, run_verify, verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -181,6 +181,24 @@ def test_verify_drawn_chains_of_few_and_many_sequences(batch, n, vocab, dtype):
     after the other above that; drafts that are mostly kept, and mostly rejected."""
     for close in (0.1, 3.0):
         check_verify(verify_case(batch + n, batch, n, vocab, dtype, True, chain=True, close=close))
+
+
+def test_verify_padded_rows_may_hold_anything():
+    """No error of a row that takes part in nothing, whatever its buffers hold."""
+    for drawn, T, vocab in ((True, 6, 5003), (False, 12, 50000)):
+        lens = np.array([T, 0, 3, 0, 0, 0], np.int32)
+        s = verify_case(T, 6, T, vocab, torch.float32, drawn, lens=lens)
+        check_verify(s)
+        want = run_verify(s)
+        pad = lens == 0
+        s["temps"][pad] = [0.0, float("nan"), -1.0, float("inf")]
+        s["tokens"][pad], s["parents"][pad] = 1 << 30, 77
+        s["u"][pad] = s["noise"][pad] = np.nan
+        s["logits"][torch.from_numpy(pad).cuda()] = float("nan")
+        r = run_verify(s)
+        assert pa.get_device_error() == (0, 0)
+        assert all(torch.equal(x, y) for x, y in zip(r, want))
+        assert r.counts[torch.from_numpy(pad).cuda()].tolist() == [0] * 4
 
 
 NO_WIDE_CLUSTERS = """
