@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[OEMPTY + h]);
-            if (wlive && *mark) {
+            if (wlive && __any_sync(FULL, *mark != 0)) {  // (the lanes as one: another warp may set it now)
                 // What was taken out of V: added to the rows that see it.
                 const int lo = max(0, s.t0 * TILE - first), hi = min(n, s.t1 * TILE - first);  // drafts of the segment
                 const int gr = s.blk * BLOCK + row0 + row;
