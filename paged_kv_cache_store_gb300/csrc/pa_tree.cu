@@ -26,13 +26,16 @@
 // keys 243 us instead of 229, over 4 x 2900 50 instead of 30.)  Short items are not cut.
 //
 // What bounds it: up to 128 rows per kv head the bytes of K and V (Qwen3-8B shape,
-// 256 sequences x 4 drafts: 262 us, 6.6 TB/s); two row tiles the chain of products
-// and softmax (64 drafts over 8 x 32768 keys: 229 us, 1.2 PFLOP/s, 71 % of the bytes'
-// floor), in which a product's 64 keys re-read 128 rows of Q from shared memory.
-// Products of 128 keys halve that but leave one score buffer a row tile: 34 us more.
+// 256 sequences x 4 drafts: 264 us, 6.6 TB/s); two row tiles the chain of products
+// and softmax (64 drafts over 8 x 32768 keys: 230 us in a dozen calls, 252 in calls over
+// some hundred milliseconds, 1.2 and 1.1 PFLOP/s, 70 and 64 % of the bytes' floor), in
+// which a product's 64 keys re-read 128 rows of Q from shared memory.  Products of 128
+// keys halve that but leave one score buffer a row tile: 34 us more.
 //
-// l is summed from the rounded P that the product uses, so that the weights sum
-// to one as they are.
+// P is rounded to bf16, V's type, as the instruction takes both operands in one: an
+// output is then off by 2.3e-3 of itself (root mean square, against 64 bits), 1.7e-3 by
+// its own rounding.  l is summed from the rounded P that the product uses, so that the
+// weights sum to one as they are.
 //
 // What a mask hides may be anything: scores are replaced before the maximum,
 // and a draft's V values that are not finite are taken out of the tile (0 times
